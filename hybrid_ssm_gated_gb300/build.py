@@ -38,7 +38,7 @@ def sources() -> list[str]:
 
 def _deps() -> list[str]:
     return sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) + \
-        [os.path.join(INCLUDE, "gdn.h"), __file__]
+        [os.path.join(INCLUDE, "gdn.h"), os.path.join(INCLUDE, "kv.h"), __file__]
 
 
 def _paths(debug: bool) -> tuple[str, str]:

@@ -10,10 +10,13 @@
 
 #include "../../include/gdn.h"
 #include "gdn_dispatch.h"
+#include "gdn_error.h"
+
+namespace gdn {
 
 namespace {
-
 thread_local std::string g_last_error;
+}
 
 int fail(int code, const char* fmt, ...) {
     char buf[512];
@@ -33,6 +36,15 @@ int launched(cudaError_t e, const char* what) {
     if (e == cudaErrorNotSupported) return fail(GDN_ERR_SHAPE, "%s: no kernel for this dtype/dk", what);
     return fail(GDN_ERR_LAUNCH, "%s: %s", what, cudaGetErrorString(e));
 }
+
+const char* last_error() { return g_last_error.c_str(); }
+
+}  // namespace gdn
+
+namespace {
+
+using gdn::fail;
+using gdn::launched;
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool aligned_to(const void* p, int n) { return (reinterpret_cast<uintptr_t>(p) % (uintptr_t)n) == 0; }
@@ -393,7 +405,7 @@ int mamba2_rollback(const mamba2_dims* dims, const gdn_replay_cache* cache, cons
     return gdn_rollback(&d, cache, slots, accepted, T, dev_err, stream);
 }
 
-const char* gdn_last_error_string(void) { return g_last_error.c_str(); }
+const char* gdn_last_error_string(void) { return gdn::last_error(); }
 
 int32_t gdn_abi_version(void) { return GDN_ABI_VERSION; }
 

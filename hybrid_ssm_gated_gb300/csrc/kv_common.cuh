@@ -1,0 +1,216 @@
+// kv_common.cuh -- what the key/value-cache kernels share: launch arguments,
+// addresses of cache entries, and the division of a batch's key tiles over a
+// persistent grid.
+//
+// Division. A sequence of a call is a row of units (key head, block of query
+// rows), each a run of key tiles; all units of all sequences in order make one
+// line of W tiles, and CTA c of G takes tiles [W c / G, W (c + 1) / G). So
+// every CTA streams the same number of tiles whatever the lengths, with no
+// host knowledge of them; a unit that spans several CTAs leaves one partial
+// result (unnormalised output, running maximum and sum) a CTA, joined
+// afterwards by kv_join_kernel. A CTA holds at most two partials: that of the
+// unit it starts in and that of the unit it ends in.
+#pragma once
+
+#include "../../include/kv.h"
+#include "gdn_device.cuh"
+
+namespace gdn {
+
+constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
+
+struct KvPages {  // one of k, v: base address and strides in elements
+    const void* p;
+    int64_t page, head, token;
+};
+
+struct KvRows {
+    const void* p;
+    int64_t seq, node, head;
+};
+
+struct KvArgs {
+    KvPages k, v;
+    const int32_t* page_table;
+    const int32_t* slots;
+    int32_t* lengths;
+    int32_t* counts;
+    float* weights;
+    int32_t* stamps;
+    int32_t* dev_err;
+    int64_t num_pages, num_slots;
+    int B, T, P, Hq, Hkv, G;  // G: query heads a key head
+    int d, page_size, max_pages, dtype;
+    // attention and accumulation
+    KvRows q, kn, vn;
+    const uint64_t* mask;
+    const int32_t* num_nodes;  // attention: nodes of each sequence
+    const int32_t* path;
+    const int32_t* n_path;
+    const float* lse_in;
+    float scale, decay;
+    void* out;
+    float* lse;
+    float* part;  // partials: [CTA][2] blocks of row_block x (d + 2) floats
+    int row_block, row_blocks;  // query rows a unit, units a key head
+    // eviction
+    int budget, recent;
+    int32_t* moves;
+};
+
+// Entry e of a sequence with page-table row `row`: its page and place.
+__device__ __forceinline__ int64_t kv_at(const KvPages& c, int page, int head, int place) {
+    return (int64_t)page * c.page + (int64_t)head * c.head + (int64_t)place * c.token;
+}
+
+struct KvSeq {
+    int slot;   // -1: padding, or refused with an error bit
+    int len;    // entries
+    int nodes;  // live nodes (attention), path length (accumulation)
+    int err;
+};
+
+// Sequence b of the call, checked. ATTN: nodes from num_nodes; else from n_path.
+template <bool ATTN>
+__device__ __forceinline__ KvSeq kv_seq(const KvArgs& a, int b) {
+    KvSeq s{-1, 0, 0, 0};
+    const int slot = a.slots[b];
+    if (slot < 0) return s;
+    if (slot >= a.num_slots) {
+        s.err = GDN_DEVERR_SLOT;
+        return s;
+    }
+    const int len = a.lengths[slot];
+    const int n = ATTN ? (a.num_nodes ? a.num_nodes[b] : a.T) : a.n_path[b];
+    if (len < 0 || (int64_t)len > (int64_t)a.max_pages * a.page_size || (!ATTN && len < n)) s.err = KV_DEVERR_LENGTH;
+    if (n < 0 || n > (ATTN ? a.T : a.P)) s.err |= KV_DEVERR_NODES;
+    if (s.err) return s;
+    s.slot = slot, s.len = len, s.nodes = n;
+    return s;
+}
+
+// Key tiles of one unit of the sequence: the cache's, and for attention one of the drafted nodes.
+template <bool ATTN, int KT>
+__device__ __forceinline__ int kv_tiles(const KvSeq& s) {
+    if (s.slot < 0 || s.nodes == 0) return 0;
+    return (s.len + KT - 1) / KT + (ATTN ? 1 : 0);
+}
+
+// A place in the line of tiles: sequence, unit of it, tile of the unit.
+struct KvPlace {
+    int b, unit, tile;
+};
+
+// Number of CTAs that take part: none gets less than `least` tiles, so that small calls are not cut
+// into partials that cost more to join than they save.
+__device__ __forceinline__ int kv_parts(int64_t W, int grid, int least) {
+    const int64_t most = W / least;
+    return (int)(most < 1 ? 1 : (most < grid ? most : grid));
+}
+
+// The CTA of `parts` whose range holds tile t, and where CTA c's range starts.
+__device__ __forceinline__ int64_t kv_start(int64_t W, int parts, int c) { return W * c / parts; }
+__device__ __forceinline__ int kv_owner(int64_t W, int parts, int64_t t) {
+    int c = (int)(t * parts / W);
+    while (c + 1 < parts && kv_start(W, parts, c + 1) <= t) ++c;
+    while (c > 0 && kv_start(W, parts, c) > t) --c;
+    return c;
+}
+
+// Scratch of the scan over sequences.
+template <int NT>
+struct KvScan {
+    long long warp_sum[NT / 32];
+    long long total, before;  // all tiles; tiles of the sequences before the found one
+    int b;
+};
+
+// Total number of tiles, and (by the whole block of NT threads) the sequence whose tiles hold tile
+// `at(total)`. Each thread sums a run of sequences; a scan over the block places the runs.
+template <bool ATTN, int KT, int NT, typename At>
+__device__ __forceinline__ void kv_locate(const KvArgs& a, KvScan<NT>& sc, At at) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int run = (a.B + NT - 1) / NT;
+    const int b0 = tid * run, b1 = min(a.B, b0 + run);
+    const int units = a.Hkv * a.row_blocks;
+    long long sum = 0;
+    for (int b = b0; b < b1; ++b) sum += (long long)kv_tiles<ATTN, KT>(kv_seq<ATTN>(a, b)) * units;
+    long long inc = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(FULL_MASK, inc, o);
+        if (lane >= o) inc += y;
+    }
+    if (lane == 31) sc.warp_sum[warp] = inc;
+    __syncthreads();
+    long long before = 0, total = 0;
+    for (int w = 0; w < NT / 32; ++w) {
+        if (w < warp) before += sc.warp_sum[w];
+        total += sc.warp_sum[w];
+    }
+    before += inc - sum;
+    if (tid == 0) sc.total = total, sc.b = a.B;
+    const long long want = at(total);
+    if (want >= before && want < before + sum) {
+        int b = b0;
+        for (; b < b1; ++b) {
+            const long long n = (long long)kv_tiles<ATTN, KT>(kv_seq<ATTN>(a, b)) * units;
+            if (want < before + n) break;
+            before += n;
+        }
+        sc.b = b, sc.before = before;
+    }
+    __syncthreads();
+}
+
+// Every page of the sequence's entries is a page of the pool (all threads of a group of `n` ask, each
+// a part; the caller joins the answers).
+__device__ __forceinline__ bool kv_pages_ok(const KvArgs& a, const KvSeq& s, int tid, int n) {
+    const int32_t* row = a.page_table + (int64_t)s.slot * a.max_pages;
+    const int used = (s.len + a.page_size - 1) / a.page_size;
+    bool ok = true;
+    for (int i = tid; i < used; i += n) ok = ok && (uint32_t)row[i] < (uint64_t)a.num_pages;
+    return ok;
+}
+
+// Outputs of rows that no unit computes: padding, refused sequences, nodes past a sequence's count.
+// Error bits of refused sequences are set here, once a call.
+template <int NT>
+__device__ __forceinline__ void kv_empty_rows(const KvArgs& a) {
+    for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
+        const KvSeq s = kv_seq<true>(a, b);
+        if (s.err && threadIdx.x == 0) set_error(a.dev_err, s.err);
+        const int64_t r0 = ((int64_t)b * a.T + s.nodes) * a.Hq, r1 = ((int64_t)b + 1) * a.T * a.Hq;
+        const int esz = dtype_size(a.dtype);
+        char* o = static_cast<char*>(a.out);
+        // 2-byte words: a 16-bit output of odd d starts its rows on 2-byte boundaries
+        uint16_t* o16 = reinterpret_cast<uint16_t*>(o + r0 * a.d * esz);
+        const int64_t words = (r1 - r0) * a.d * (esz / 2);
+        for (int64_t i = threadIdx.x; i < words; i += NT) o16[i] = 0;
+        if (a.lse)
+            for (int64_t r = r0 + threadIdx.x; r < r1; r += NT) a.lse[r] = -INFINITY;
+    }
+}
+
+__device__ __forceinline__ float kv_ex2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// Floats of one partial: row_block rows of d outputs, their maxima and their sums.
+__host__ __device__ inline int64_t kv_part_floats(int row_block, int d) { return (int64_t)row_block * (d + 2); }
+
+// Eviction's move lists in the workspace: for unit (b, h) a count (-1: the sequence stays as it is),
+// and after four words up to `cap` holes and as many fillers.
+__host__ __device__ inline int64_t kv_moves_at(int64_t unit, int cap) {
+    return unit * (4 + 2 * (int64_t)align_up(cap, 4));
+}
+// Most moves of a unit: a hole lies below the budget, a filler at or above it.
+__host__ __device__ inline int kv_moves_cap(int max_pages, int page_size, int budget) {
+    const int room = max_pages * page_size;
+    const int over = room > budget ? room - budget : 0;
+    return over < budget ? over : budget;
+}
+
+}  // namespace gdn
