@@ -76,7 +76,7 @@ gdn::KvArgs args_of(const kv_cache* c, int32_t B, const int32_t* slots, int32_t*
     a.lengths = c->lengths, a.counts = c->counts, a.weights = c->weights, a.stamps = c->stamps;
     a.num_pages = c->num_pages, a.num_slots = c->num_slots;
     a.B = B, a.Hkv = c->Hkv, a.d = c->d, a.page_size = c->page_size, a.max_pages = c->max_pages, a.dtype = c->dtype;
-    a.row_block = 1, a.row_blocks = 1;
+    a.row_block = 1;
     return a;
 }
 
@@ -85,6 +85,16 @@ gdn::KvArgs args_of(const kv_cache* c, int32_t B, const int32_t* slots, int32_t*
 bool vec_rows(const void* p, int64_t s0, int64_t s1, int64_t s2, int d, int esz) {
     return aligned_to(p, 16) && s0 * esz % 16 == 0 && s1 * esz % 16 == 0 && s2 * esz % 16 == 0 && d * esz % 16 == 0;
 }
+// Workspace of either attention kernel: the caller's rows decide at the call which one runs.
+cudaError_t attention_workspace(gdn::KvArgs& a, int64_t& bytes) {
+    cudaError_t e = gdn::kv_attn_workspace(a, bytes);
+    if (e != cudaSuccess || !gdn::kv_attn_tc_fits(a)) return e;
+    int64_t more = 0;
+    e = gdn::kv_attn_tc_workspace(a, more);
+    if (more > bytes) bytes = more;
+    return e;
+}
+
 bool vec_pages(const gdn::KvPages& c, int d, int esz) { return vec_rows(c.p, c.page, c.head, c.token, d, esz); }
 bool vec_rows(const gdn::KvRows& r, int d, int esz) { return vec_rows(r.p, r.seq, r.node, r.head, d, esz); }
 
@@ -101,7 +111,7 @@ int64_t kv_tree_attention_workspace(const kv_cache* cache, int32_t B, int32_t T,
     gdn::KvArgs a = args_of(cache, B, nullptr, nullptr);
     a.T = T, a.Hq = Hq, a.G = Hq / cache->Hkv;
     int64_t bytes = 0;
-    const cudaError_t e = gdn::kv_attn_workspace(a, bytes);
+    const cudaError_t e = attention_workspace(a, bytes);
     if (e != cudaSuccess) return launched(e, fn);
     return bytes;
 }
@@ -129,7 +139,7 @@ int kv_tree_attention(const kv_cache* cache, int32_t B, int32_t T, int32_t Hq, c
     a.mask = mask, a.num_nodes = num_nodes, a.scale = scale, a.out = out, a.lse = lse;
     a.part = static_cast<float*>(workspace);
     int64_t need = 0;
-    const cudaError_t e = gdn::kv_attn_workspace(a, need);
+    cudaError_t e = attention_workspace(a, need);
     if (e != cudaSuccess) return launched(e, fn);
     if (workspace_bytes < need)
         return fail(GDN_ERR_SHAPE, "%s: workspace of %lld bytes, %lld needed", fn, (long long)workspace_bytes,
@@ -137,7 +147,9 @@ int kv_tree_attention(const kv_cache* cache, int32_t B, int32_t T, int32_t Hq, c
     const int esz = gdn::dtype_size(cache->dtype);
     const bool vec = vec_pages(a.k, a.d, esz) && vec_pages(a.v, a.d, esz) && vec_rows(a.q, a.d, esz) &&
                      vec_rows(a.kn, a.d, esz) && vec_rows(a.vn, a.d, esz);
-    return launched(gdn::launch_kv_attn(a, vec, static_cast<cudaStream_t>(stream)), fn);
+    e = vec && gdn::kv_attn_tc_fits(a) ? gdn::launch_kv_attn_tc(a, static_cast<cudaStream_t>(stream)) : cudaErrorNotSupported;
+    if (e == cudaErrorNotSupported) e = gdn::launch_kv_attn(a, vec, static_cast<cudaStream_t>(stream));
+    return launched(e, fn);
 }
 
 int kv_commit(const kv_cache* cache, int32_t B, int32_t T, int32_t P, const int32_t* slots, const kv_rows* k_new,

@@ -96,18 +96,13 @@ __global__ void __launch_bounds__(kvg::NT) kv_attn_kernel(const KvArgs a, const 
     const int parts = kv_parts(W, gridDim.x, LEAST);
     if (W == 0 || blockIdx.x >= parts) return;
     const long long w0 = kv_start(W, parts, blockIdx.x), w1 = kv_start(W, parts, blockIdx.x + 1);
-    const int units = a.Hkv * a.row_blocks;
-    long long at = w0;
-    int b = scan.b, unit, tile, checked = -1;
+    int checked = -1;
     bool pages_ok = true;
-    KvSeq s = kv_seq<true>(a, b);
-    int nt = kv_tiles<true, KT>(s);
-    unit = (int)((at - scan.before) / nt), tile = (int)((at - scan.before) - (long long)unit * nt);
-
-    while (at < w1) {
-        const int t_first = tile, t_end = (int)min((long long)nt, tile + (w1 - at));
-        const int h = unit / a.row_blocks, r0 = (unit - h * a.row_blocks) * RB;
-        const int rows = min(RB, s.nodes * a.G - r0);  // <= 0: rows of nodes past the count only
+    KvWalk<true, KT> w(a, w0, w1, scan.b, scan.before);
+    do {
+        const KvSeq& s = w.s;
+        const int b = w.b, h = w.h, nt = w.nt, r0 = w.rb * RB;
+        const int rows = min(RB, s.nodes * a.G - r0);
         const int32_t* table = a.page_table + (int64_t)s.slot * a.max_pages;
         if (checked != b) {
             pages_ok = __syncthreads_and(kv_pages_ok(a, s, tid, NT));
@@ -115,7 +110,7 @@ __global__ void __launch_bounds__(kvg::NT) kv_attn_kernel(const KvArgs a, const 
             checked = b;
         }
         // queries, row state
-        kv_load_rows<ST, NT>(sq, L.dp, L.dp, RB, max(rows, 0), a.q.p, a.d, vec, [&](int r) {
+        kv_load_rows<ST, NT>(sq, L.dp, L.dp, RB, rows, a.q.p, a.d, vec, [&](int r) {
             const int node = (r0 + r) / a.G, hq = h * a.G + (r0 + r) - node * a.G;
             return (int64_t)b * a.q.seq + (int64_t)node * a.q.node + (int64_t)hq * a.q.head;
         });
@@ -131,7 +126,7 @@ __global__ void __launch_bounds__(kvg::NT) kv_attn_kernel(const KvArgs a, const 
 #pragma unroll
             for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
 
-        for (int t = t_first; t < t_end && pages_ok && rows > 0; ++t) {
+        for (int t = w.t0; t < w.t1 && pages_ok; ++t) {
             const bool tree = t == nt - 1;
             const int n = tree ? s.nodes : min(KT, s.len - t * KT);
             __syncthreads();  // the last tile is read
@@ -184,7 +179,7 @@ __global__ void __launch_bounds__(kvg::NT) kv_attn_kernel(const KvArgs a, const 
                 // fmaxf drops a NaN; the weights below keep it
                 float m = fmaxf(x0, x1);
 #pragma unroll
-                for (int w = 16; w; w >>= 1) m = fmaxf(m, __shfl_xor_sync(FULL_MASK, m, w));
+                for (int x = 16; x; x >>= 1) m = fmaxf(m, __shfl_xor_sync(FULL_MASK, m, x));
                 const float old = sm[r];
                 m = fmaxf(m, old);
                 const float base = m == -INFINITY ? 0.f : m;  // a row without a key yet
@@ -218,14 +213,13 @@ __global__ void __launch_bounds__(kvg::NT) kv_attn_kernel(const KvArgs a, const 
             }
         }
         __syncthreads();
-        const bool whole = t_first == 0 && t_end == nt;
         if (rg < groups) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int r = rg + i * groups;
-                if (r >= min(RB, rows)) break;
+                if (r >= rows) break;
                 const float l = sl[r];
-                if (whole) {
+                if (w.whole()) {
                     const float inv = l == 0.f ? 0.f : 1.f / l;
                     const int node = (r0 + r) / a.G, hq = h * a.G + (r0 + r) - node * a.G;
                     const int64_t row = ((int64_t)b * a.T + node) * a.Hq + hq;
@@ -234,7 +228,7 @@ __global__ void __launch_bounds__(kvg::NT) kv_attn_kernel(const KvArgs a, const 
                         if (4 * run + e < a.d) store_elem(a.out, row * a.d + 4 * run + e, a.dtype, o[i][e] * inv);
                     if (run == 0 && a.lse) a.lse[row] = l == 0.f ? -INFINITY : (sm[r] + log2f(l)) * LN2;
                 } else {
-                    float* part = a.part + ((int64_t)blockIdx.x * 2 + (at > w0)) * kv_part_floats(RB, a.d);
+                    float* part = a.part + ((int64_t)blockIdx.x * 2 + w.later) * kv_part_floats(RB, a.d);
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
                         if (4 * run + e < a.d) part[r * a.d + 4 * run + e] = o[i][e];
@@ -243,15 +237,7 @@ __global__ void __launch_bounds__(kvg::NT) kv_attn_kernel(const KvArgs a, const 
             }
         }
         __syncthreads();
-        at += t_end - t_first, tile = 0;
-        if (t_end == nt && ++unit == units && at < w1) {
-            unit = 0;
-            do {
-                s = kv_seq<true>(a, ++b);
-                nt = kv_tiles<true, KT>(s);
-            } while (nt == 0);
-        }
-    }
+    } while (w.next());
 }
 
 // Joins the partials of units that span CTAs: block i stands at the border between the ranges of CTAs i
@@ -276,7 +262,7 @@ __global__ void __launch_bounds__(128) kv_join_kernel(const KvArgs a, const int 
     const long long u0 = scan.before + (long long)unit * nt;
     if (border == u0) return;  // the border lies between two units
     const int c0 = kv_owner(W, parts, u0), c1 = kv_owner(W, parts, u0 + nt - 1);
-    const int RB = a.row_block, h = unit / a.row_blocks, r0 = (unit - h * a.row_blocks) * RB;
+    const int RB = a.row_block, blocks = kv_row_blocks<true>(a, s), h = unit / blocks, r0 = (unit - h * blocks) * RB;
     const int rows = min(RB, s.nodes * a.G - r0);
     const int64_t size = kv_part_floats(RB, a.d);
     for (int r = (i - c0) * (NT / 32) + warp; r < rows; r += (c1 - c0) * (NT / 32)) {

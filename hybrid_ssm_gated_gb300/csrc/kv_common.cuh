@@ -52,7 +52,7 @@ struct KvArgs {
     void* out;
     float* lse;
     float* part;  // partials: [CTA][2] blocks of row_block x (d + 2) floats
-    int row_block, row_blocks;  // query rows a unit, units a key head
+    int row_block;  // query rows a unit at most
     // eviction
     int budget, recent;
     int32_t* moves;
@@ -96,10 +96,15 @@ __device__ __forceinline__ int kv_tiles(const KvSeq& s) {
     return (s.len + KT - 1) / KT + (ATTN ? 1 : 0);
 }
 
-// A place in the line of tiles: sequence, unit of it, tile of the unit.
-struct KvPlace {
-    int b, unit, tile;
-};
+// Blocks of query rows, and units, of the sequence (accumulation takes all rows of a tile at once).
+template <bool ATTN>
+__device__ __forceinline__ int kv_row_blocks(const KvArgs& a, const KvSeq& s) {
+    return ATTN ? (s.nodes * a.G + a.row_block - 1) / a.row_block : 1;
+}
+template <bool ATTN, int KT>
+__device__ __forceinline__ long long kv_seq_tiles(const KvArgs& a, const KvSeq& s) {
+    return (long long)kv_tiles<ATTN, KT>(s) * kv_row_blocks<ATTN>(a, s) * a.Hkv;
+}
 
 // Number of CTAs that take part: none gets less than `least` tiles, so that small calls are not cut
 // into partials that cost more to join than they save.
@@ -132,9 +137,8 @@ __device__ __forceinline__ void kv_locate(const KvArgs& a, KvScan<NT>& sc, At at
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int run = (a.B + NT - 1) / NT;
     const int b0 = tid * run, b1 = min(a.B, b0 + run);
-    const int units = a.Hkv * a.row_blocks;
     long long sum = 0;
-    for (int b = b0; b < b1; ++b) sum += (long long)kv_tiles<ATTN, KT>(kv_seq<ATTN>(a, b)) * units;
+    for (int b = b0; b < b1; ++b) sum += kv_seq_tiles<ATTN, KT>(a, kv_seq<ATTN>(a, b));
     long long inc = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -154,7 +158,7 @@ __device__ __forceinline__ void kv_locate(const KvArgs& a, KvScan<NT>& sc, At at
     if (want >= before && want < before + sum) {
         int b = b0;
         for (; b < b1; ++b) {
-            const long long n = (long long)kv_tiles<ATTN, KT>(kv_seq<ATTN>(a, b)) * units;
+            const long long n = kv_seq_tiles<ATTN, KT>(a, kv_seq<ATTN>(a, b));
             if (want < before + n) break;
             before += n;
         }
@@ -162,6 +166,50 @@ __device__ __forceinline__ void kv_locate(const KvArgs& a, KvScan<NT>& sc, At at
     }
     __syncthreads();
 }
+
+// A walk along a CTA's tiles, segment by segment: a segment is the run of tiles of one unit (key head h,
+// row block rb of sequence b) within the CTA's range. Every warp role of a kernel walks by itself.
+template <bool ATTN, int KT>
+struct KvWalk {
+    const KvArgs& a;
+    long long at, end;  // next tile of the line, end of the range
+    int b, unit, units, blocks, nt;
+    KvSeq s;
+    int h, rb, t0, t1;  // the segment: tiles t0 .. t1 - 1 of nt
+    bool later;         // it does not begin the CTA's range: its partial is the second one
+
+    // From tile w0 of the line, which lies in sequence b0, whose tiles begin at `before`.
+    __device__ __forceinline__ KvWalk(const KvArgs& a_, long long w0, long long w1, int b0, long long before)
+        : a(a_), at(w0), end(w1), b(b0), later(false) {
+        load();
+        const long long off = w0 - before;
+        unit = (int)(off / nt);
+        segment((int)(off - (long long)unit * nt));
+    }
+    __device__ __forceinline__ void load() {
+        s = kv_seq<ATTN>(a, b);
+        nt = kv_tiles<ATTN, KT>(s), blocks = kv_row_blocks<ATTN>(a, s), units = a.Hkv * blocks;
+    }
+    __device__ __forceinline__ void segment(int tile) {
+        h = unit / blocks, rb = unit - h * blocks;
+        t0 = tile, t1 = (int)min((long long)nt, tile + (end - at));
+    }
+    __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == nt; }
+    // The next segment; false at the end of the range.
+    __device__ __forceinline__ bool next() {
+        at += t1 - t0, later = true;
+        if (at >= end) return false;
+        if (++unit == units) {
+            unit = 0;
+            do {
+                ++b;
+                load();
+            } while (nt == 0);
+        }
+        segment(0);
+        return true;
+    }
+};
 
 // Every page of the sequence's entries is a page of the pool (all threads of a group of `n` ask, each
 // a part; the caller joins the answers).

@@ -28,7 +28,8 @@ cudaError_t wave(Kernel kern, const KvArgs& a, int smem, int least, int64_t& gri
     if ((e = prepare_kernel(kern, kvg::NT, smem, bps)) != cudaSuccess) return e;
     grid = (int64_t)di.sms * bps;
     const int64_t cap = (int64_t)a.max_pages * a.page_size;
-    const int64_t most = (int64_t)a.B * a.Hkv * a.row_blocks * ((cap + kvg::KT - 1) / kvg::KT + 1) / least;
+    const int64_t blocks = ((int64_t)a.T * a.G + a.row_block - 1) / a.row_block;
+    const int64_t most = (int64_t)a.B * a.Hkv * blocks * ((cap + kvg::KT - 1) / kvg::KT + 1) / least;
     if (grid > most) grid = most;
     if (grid < 1) grid = 1;
     return cudaSuccess;
@@ -36,15 +37,9 @@ cudaError_t wave(Kernel kern, const KvArgs& a, int smem, int least, int64_t& gri
 
 }  // namespace
 
-namespace {
-
-void set_rows(KvArgs& a) { a.row_block = kvg::RB, a.row_blocks = (a.T * a.G + kvg::RB - 1) / kvg::RB; }
-
-}  // namespace
-
 cudaError_t kv_attn_workspace(KvArgs& a, int64_t& bytes) {
     int64_t grid = 0;
-    set_rows(a);
+    a.row_block = kvg::RB;
     const cudaError_t e = wave(attn_kernel(a.dtype), a, kvg::layout(a.d).bytes, kvg::LEAST, grid);
     bytes = grid * 2 * kv_part_floats(kvg::RB, a.d) * 4;
     return e;
@@ -53,7 +48,7 @@ cudaError_t kv_attn_workspace(KvArgs& a, int64_t& bytes) {
 cudaError_t launch_kv_attn(KvArgs& a, bool vec, cudaStream_t stream) {
     const int smem = kvg::layout(a.d).bytes;
     int64_t grid = 0;
-    set_rows(a);
+    a.row_block = kvg::RB;
     cudaError_t e = wave(attn_kernel(a.dtype), a, smem, kvg::LEAST, grid);
     if (e != cudaSuccess) return e;
     attn_kernel(a.dtype)<<<(unsigned)grid, kvg::NT, smem, stream>>>(a, vec);

@@ -1,0 +1,134 @@
+// Instantiations and launch of the tensor-core attention kernel, and its tensor maps.
+#include "gdn_launch.cuh"
+#include "kv_attn.cuh"
+#include "kv_dispatch.h"
+#include "kv_tc.cuh"
+
+namespace gdn {
+
+namespace {
+
+using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                            const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                            CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// The driver's encoder, found once (the library links no driver library); NULL where there is none.
+Encode encoder() {
+    static const Encode fn = [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult r;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &r) != cudaSuccess ||
+            r != cudaDriverEntryPointSuccess)
+            p = nullptr;
+        return reinterpret_cast<Encode>(p);
+    }();
+    return fn;
+}
+
+// 16-bit rows [n3][n2][n1][d] with strides s3, s2, s1 (elements), boxes of `rows` x 64 elements in the
+// 128-byte swizzle; past the ends zeros are read.
+bool encode(CUtensorMap& m, int dtype, const void* p, int d, int64_t n1, int64_t s1, int64_t n2, int64_t s2, int64_t n3,
+            int64_t s3, int rows) {
+    const cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)n1, (cuuint64_t)n2, (cuuint64_t)n3};
+    const cuuint64_t strides[3] = {(cuuint64_t)s1 * 2, (cuuint64_t)s2 * 2, (cuuint64_t)s3 * 2};
+    const cuuint32_t box[4] = {kvt::BOX, (cuuint32_t)rows, 1, 1}, unit[4] = {1, 1, 1, 1};
+    return encoder()(&m, dtype == GDN_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
+                     const_cast<void*>(p), dims, strides, box, unit, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                     CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+int boxes_of(int d) { return (d + kvt::BOX - 1) / kvt::BOX; }
+
+// Keys of one box: the largest power of two that divides the page (so that a box lies in one page), up
+// to the tile; 0 where it is under the swizzle's eight rows.
+int box_rows_of(int page_size) {
+    int r = page_size & -page_size;
+    if (r > kvt::KT) r = kvt::KT;
+    return r >= 8 ? r : 0;
+}
+
+// Query rows a unit: the smallest block that holds them all, up to 128 (64 where the outputs of two
+// halves of d share tensor memory with the scores).
+int row_block_of(int64_t rows, int boxes) {
+    const int most = boxes > 2 ? 64 : 128;
+    int nr = 16;
+    while (nr < rows && nr < most) nr *= 2;
+    return nr;
+}
+
+template <int NR>
+int stages_of(int boxes, int smem_optin) {
+    const int one = (boxes > 1 ? 2 : 1) * kvt::BOX_BYTES;
+    const int n = (smem_optin - kvt::smem_bytes<NR>(boxes, 0)) / one;
+    return n < kvt::MAX_STAGES ? n : kvt::MAX_STAGES;
+}
+
+template <typename ST, int NR>
+cudaError_t launch(KvArgs& a, const kvt::Maps& maps, int boxes, int box_rows, int grid, int optin, cudaStream_t stream) {
+    auto kern = kv_attn_tc_kernel<ST, NR>;
+    const int stages = stages_of<NR>(boxes, optin), smem = kvt::smem_bytes<NR>(boxes, stages);
+    int bps = 0;
+    cudaError_t e = prepare_kernel(kern, kvt::NT, smem, bps);
+    if (e != cudaSuccess) return e;
+    kern<<<grid, kvt::NT, smem, stream>>>(a, maps, boxes, stages, box_rows);
+    return cudaGetLastError();
+}
+
+template <typename ST>
+cudaError_t launch_rows(KvArgs& a, const kvt::Maps& maps, int boxes, int box_rows, int grid, int optin, cudaStream_t s) {
+    switch (a.row_block) {
+        case 16: return launch<ST, 16>(a, maps, boxes, box_rows, grid, optin, s);
+        case 32: return launch<ST, 32>(a, maps, boxes, box_rows, grid, optin, s);
+        case 64: return launch<ST, 64>(a, maps, boxes, box_rows, grid, optin, s);
+        default: return launch<ST, 128>(a, maps, boxes, box_rows, grid, optin, s);
+    }
+}
+
+cudaError_t wave(const KvArgs& a, DeviceInfo& di, int64_t& grid) {
+    const cudaError_t e = device_info(di);
+    if (e != cudaSuccess) return e;
+    const int64_t cap = (int64_t)a.max_pages * a.page_size, blocks = ((int64_t)a.T * a.G + a.row_block - 1) / a.row_block;
+    const int64_t most = (int64_t)a.B * a.Hkv * blocks * ((cap + kvt::KT - 1) / kvt::KT + 1);
+    grid = di.sms < most ? di.sms : most;
+    if (grid < 1) grid = 1;
+    return cudaSuccess;
+}
+
+}  // namespace
+
+bool kv_attn_tc_fits(const KvArgs& a) {
+    return a.dtype != GDN_F32 && a.d % 8 == 0 && box_rows_of(a.page_size) > 0 && a.num_pages > 0;
+}
+
+cudaError_t kv_attn_tc_workspace(KvArgs& a, int64_t& bytes) {
+    DeviceInfo di;
+    int64_t grid = 0;
+    a.row_block = row_block_of((int64_t)a.T * a.G, boxes_of(a.d));
+    const cudaError_t e = wave(a, di, grid);
+    bytes = grid * 2 * kv_part_floats(a.row_block, a.d) * 4;
+    return e;
+}
+
+cudaError_t launch_kv_attn_tc(KvArgs& a, cudaStream_t stream) {
+    const int boxes = boxes_of(a.d), box_rows = box_rows_of(a.page_size);
+    kvt::Maps maps;
+    if (!encoder() ||
+        !encode(maps.k, a.dtype, a.k.p, a.d, a.page_size, a.k.token, a.Hkv, a.k.head, a.num_pages, a.k.page, box_rows) ||
+        !encode(maps.v, a.dtype, a.v.p, a.d, a.page_size, a.v.token, a.Hkv, a.v.head, a.num_pages, a.v.page, box_rows) ||
+        !encode(maps.kn, a.dtype, a.kn.p, a.d, a.T, a.kn.node, a.Hkv, a.kn.head, a.B, a.kn.seq, a.T) ||
+        !encode(maps.vn, a.dtype, a.vn.p, a.d, a.T, a.vn.node, a.Hkv, a.vn.head, a.B, a.vn.seq, a.T))
+        return cudaErrorNotSupported;
+    a.row_block = row_block_of((int64_t)a.T * a.G, boxes);
+    DeviceInfo di;
+    int64_t grid = 0;
+    cudaError_t e = wave(a, di, grid);
+    if (e != cudaSuccess) return e;
+    e = a.dtype == GDN_BF16 ? launch_rows<__nv_bfloat16>(a, maps, boxes, box_rows, (int)grid, di.smem_optin, stream)
+                            : launch_rows<__half>(a, maps, boxes, box_rows, (int)grid, di.smem_optin, stream);
+    if (e != cudaSuccess || grid == 1) return e;
+    kv_join_kernel<kvt::KT, kvt::LEAST><<<(unsigned)grid - 1, 128, 0, stream>>>(a, (int)grid);
+    return cudaGetLastError();
+}
+
+}  // namespace gdn

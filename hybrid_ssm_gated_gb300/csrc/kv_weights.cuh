@@ -38,12 +38,12 @@ __global__ void __launch_bounds__(kvg::NT) kv_weights_kernel(const KvArgs a, con
     const int parts = (int)min(W, (long long)gridDim.x);
     if (blockIdx.x >= parts) return;
     const long long w0 = kv_start(W, parts, blockIdx.x), w1 = kv_start(W, parts, blockIdx.x + 1);
-    int b = scan.b, checked = -1;
+    int checked = -1;
     bool ok = true;
-    KvSeq s = kv_seq<false>(a, b);
-    int nt = kv_tiles<false, KT>(s);
-    int h = (int)((w0 - scan.before) / nt), tile = (int)((w0 - scan.before) - (long long)h * nt);
-    for (long long at = w0; at < w1; ++at) {
+    KvWalk<false, KT> w(a, w0, w1, scan.b, scan.before);
+    do {
+        const KvSeq& s = w.s;
+        const int b = w.b, h = w.h;
         const int32_t* table = a.page_table + (int64_t)s.slot * a.max_pages;
         if (checked != b) {
             bool nodes_ok = true;
@@ -55,7 +55,7 @@ __global__ void __launch_bounds__(kvg::NT) kv_weights_kernel(const KvArgs a, con
                 set_error(a.dev_err, (nodes_ok ? 0 : KV_DEVERR_NODES) | (pages_ok ? 0 : KV_DEVERR_PAGE));
             checked = b;
         }
-        if (ok) {
+        for (int tile = w.t0; tile < w.t1 && ok; ++tile) {
             const int e0 = tile * KT, n = min(KT, s.len - e0), rows = s.nodes * a.G;
             const int key = tid & (KT - 1), g = tid / KT;
             __syncthreads();  // the last tile's sums and keys are read
@@ -102,21 +102,11 @@ __global__ void __launch_bounds__(kvg::NT) kv_weights_kernel(const KvArgs a, con
             __syncthreads();
             if (tid < n) {
                 const int e = e0 + tid, pg = e / a.page_size;
-                float* w = a.weights + ((int64_t)table[pg] * a.Hkv + h) * a.page_size + (e - pg * a.page_size);
-                *w = fmaf(*w, a.decay, sp[tid] + sp[KT + tid] + sp[2 * KT + tid] + sp[3 * KT + tid]);
+                float* x = a.weights + ((int64_t)table[pg] * a.Hkv + h) * a.page_size + (e - pg * a.page_size);
+                *x = fmaf(*x, a.decay, sp[tid] + sp[KT + tid] + sp[2 * KT + tid] + sp[3 * KT + tid]);
             }
         }
-        if (++tile == nt) {
-            tile = 0;
-            if (++h == a.Hkv && at + 1 < w1) {
-                h = 0;
-                do {
-                    s = kv_seq<false>(a, ++b);
-                    nt = kv_tiles<false, KT>(s);
-                } while (nt == 0);
-            }
-        }
-    }
+    } while (w.next());
 }
 
 }  // namespace gdn
