@@ -87,6 +87,7 @@ __global__ void __launch_bounds__(kvg::NT) kv_attn_kernel(const KvArgs a, const 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const float c2 = a.scale * LOG2E;
 
+    kv_grid_launch();
     kv_empty_rows<NT>(a);
     kv_locate<true, KT, NT>(a, scan, [&](long long W) -> long long {
         const int parts = kv_parts(W, gridDim.x, LEAST);
@@ -238,55 +239,6 @@ __global__ void __launch_bounds__(kvg::NT) kv_attn_kernel(const KvArgs a, const 
         }
         __syncthreads();
     } while (w.next());
-}
-
-// Joins the partials of units that span CTAs: block i stands at the border between the ranges of CTAs i
-// and i + 1; the blocks at a unit's inner borders share its rows, a warp a row.
-template <int KT, int LEAST>
-__global__ void __launch_bounds__(128) kv_join_kernel(const KvArgs a, const int grid) {
-    constexpr int NT = 128;
-    __shared__ KvScan<NT> scan;
-    const int i = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    kv_locate<true, KT, NT>(a, scan, [&](long long W) -> long long {
-        const int parts = kv_parts(W, grid, LEAST);
-        return W > 0 && i + 1 < parts ? kv_start(W, parts, i + 1) : -1;
-    });
-    const long long W = scan.total;
-    const int parts = kv_parts(W, grid, LEAST);
-    if (W == 0 || i + 1 >= parts) return;
-    const long long border = kv_start(W, parts, i + 1);
-    const int b = scan.b;
-    const KvSeq s = kv_seq<true>(a, b);
-    const int nt = kv_tiles<true, KT>(s);
-    const int unit = (int)((border - scan.before) / nt);
-    const long long u0 = scan.before + (long long)unit * nt;
-    if (border == u0) return;  // the border lies between two units
-    const int c0 = kv_owner(W, parts, u0), c1 = kv_owner(W, parts, u0 + nt - 1);
-    const int RB = a.row_block, blocks = kv_row_blocks<true>(a, s), h = unit / blocks, r0 = (unit - h * blocks) * RB;
-    const int rows = min(RB, s.nodes * a.G - r0);
-    const int64_t size = kv_part_floats(RB, a.d);
-    for (int r = (i - c0) * (NT / 32) + warp; r < rows; r += (c1 - c0) * (NT / 32)) {
-        const auto part = [&](int c) { return a.part + ((int64_t)c * 2 + (kv_start(W, parts, c) < u0)) * size; };
-        float m = -INFINITY, l = 0.f;
-        for (int c = c0; c <= c1; ++c) m = fmaxf(m, part(c)[RB * a.d + r]);
-        const float base = m == -INFINITY ? 0.f : m;
-        for (int c = c0; c <= c1; ++c) {
-            const float* p = part(c);
-            l += p[RB * a.d + RB + r] * kv_ex2(p[RB * a.d + r] - base);
-        }
-        const float inv = l == 0.f ? 0.f : 1.f / l;
-        const int node = (r0 + r) / a.G, hq = h * a.G + (r0 + r) - node * a.G;
-        const int64_t row = ((int64_t)b * a.T + node) * a.Hq + hq;
-        for (int e = lane; e < a.d; e += 32) {
-            float o = 0.f;
-            for (int c = c0; c <= c1; ++c) {
-                const float* p = part(c);
-                o = fmaf(p[r * a.d + e], kv_ex2(p[RB * a.d + r] - base), o);
-            }
-            store_elem(a.out, row * a.d + e, a.dtype, o * inv);
-        }
-        if (lane == 0 && a.lse) a.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * LN2;
-    }
 }
 
 }  // namespace gdn

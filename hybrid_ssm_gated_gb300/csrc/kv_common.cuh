@@ -246,8 +246,14 @@ __device__ __forceinline__ float kv_ex2(float x) {
     return r;
 }
 
-// Floats of one partial: row_block rows of d outputs, their maxima and their sums.
-__host__ __device__ inline int64_t kv_part_floats(int row_block, int d) { return (int64_t)row_block * (d + 2); }
+// Floats of one partial: row_block rows of d outputs, their maxima and their sums (16-byte blocks).
+__host__ __device__ inline int64_t kv_part_floats(int row_block, int d) { return ((int64_t)row_block * (d + 2) + 3) / 4 * 4; }
+
+// The join kernel is launched while the attention kernel runs (programmatic launch): the attention
+// kernel's blocks let it start, and every block of it waits here until the attention kernel has ended
+// and its writes are visible.
+__device__ __forceinline__ void kv_grid_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void kv_grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // Eviction's move lists in the workspace: for unit (b, h) a count (-1: the sequence stays as it is),
 // and after four words up to `cap` holes and as many fillers.

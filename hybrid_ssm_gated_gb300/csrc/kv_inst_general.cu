@@ -2,6 +2,7 @@
 #include "gdn_launch.cuh"
 #include "kv_attn.cuh"
 #include "kv_dispatch.h"
+#include "kv_launch_join.cuh"
 #include "kv_weights.cuh"
 
 namespace gdn {
@@ -53,8 +54,7 @@ cudaError_t launch_kv_attn(KvArgs& a, bool vec, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     attn_kernel(a.dtype)<<<(unsigned)grid, kvg::NT, smem, stream>>>(a, vec);
     if ((e = cudaGetLastError()) != cudaSuccess || grid == 1) return e;
-    kv_join_kernel<kvg::KT, kvg::LEAST><<<(unsigned)grid - 1, 128, 0, stream>>>(a, (int)grid);
-    return cudaGetLastError();
+    return launch_join<kvg::KT, kvg::LEAST>(a, (int)grid, stream);
 }
 
 cudaError_t launch_kv_weights(KvArgs& a, bool vec, cudaStream_t stream) {

@@ -1,7 +1,7 @@
 // Instantiations and launch of the tensor-core attention kernel, and its tensor maps.
 #include "gdn_launch.cuh"
-#include "kv_attn.cuh"
 #include "kv_dispatch.h"
+#include "kv_launch_join.cuh"
 #include "kv_tc.cuh"
 
 namespace gdn {
@@ -127,8 +127,7 @@ cudaError_t launch_kv_attn_tc(KvArgs& a, cudaStream_t stream) {
     e = a.dtype == GDN_BF16 ? launch_rows<__nv_bfloat16>(a, maps, boxes, box_rows, (int)grid, di.smem_optin, stream)
                             : launch_rows<__half>(a, maps, boxes, box_rows, (int)grid, di.smem_optin, stream);
     if (e != cudaSuccess || grid == 1) return e;
-    kv_join_kernel<kvt::KT, kvt::LEAST><<<(unsigned)grid - 1, 128, 0, stream>>>(a, (int)grid);
-    return cudaGetLastError();
+    return launch_join<kvt::KT, kvt::LEAST>(a, (int)grid, stream);
 }
 
 }  // namespace gdn

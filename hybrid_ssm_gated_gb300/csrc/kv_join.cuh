@@ -1,0 +1,115 @@
+// kv_join.cuh -- joins the partial results of units whose key tiles span CTAs:
+// with m = max m_c, out = sum_c 2^{m_c - m} O_c / sum_c 2^{m_c - m} l_c.
+//
+// Bound by latency: a few hundred KB at most, read once. So a job is one row's
+// 128 outputs (16 bytes a lane), the parts of a unit with many are split over
+// the warps of a block, and the loads of a lane do not depend on one another.
+// (With one warp a row and the factors formed at every load it took 55 us of
+// a 63 us call: 32 rows of d = 256 in 7 parts.)
+#pragma once
+
+#include "kv_common.cuh"
+
+namespace gdn {
+
+namespace kvj {
+
+constexpr int NT = 256, WARPS = NT / 32;
+constexpr int SHARE = 4;  // blocks a border
+
+}  // namespace kvj
+
+// Blocks SHARE i .. SHARE i + SHARE - 1 stand at the border between the ranges of CTAs i and i + 1 of an
+// attention kernel of `grid` CTAs; the blocks at a unit's inner borders share its jobs.
+template <int KT, int LEAST>
+__global__ void __launch_bounds__(kvj::NT) kv_join_kernel(const __grid_constant__ KvArgs a, const int grid) {
+    using namespace kvj;
+    __shared__ KvScan<NT> scan;
+    __shared__ float4 sums[WARPS][32];
+    const int i = blockIdx.x / SHARE, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    kv_locate<true, KT, NT>(a, scan, [&](long long W) -> long long {
+        const int parts = kv_parts(W, grid, LEAST);
+        return W > 0 && i + 1 < parts ? kv_start(W, parts, i + 1) : -1;
+    });
+    kv_grid_wait();  // the partials are written
+    const long long W = scan.total;
+    const int parts = kv_parts(W, grid, LEAST);
+    if (W == 0 || i + 1 >= parts) return;
+    const long long border = kv_start(W, parts, i + 1);
+    const int b = scan.b;
+    const KvSeq s = kv_seq<true>(a, b);
+    const int nt = kv_tiles<true, KT>(s);
+    const int unit = (int)((border - scan.before) / nt);
+    const long long u0 = scan.before + (long long)unit * nt;
+    if (border == u0) return;  // the border lies between two units
+    const int c0 = kv_owner(W, parts, u0), c1 = kv_owner(W, parts, u0 + nt - 1), n = c1 - c0 + 1;
+    const int RB = a.row_block, blocks = kv_row_blocks<true>(a, s), h = unit / blocks, r0 = (unit - h * blocks) * RB;
+    const int rows = min(RB, s.nodes * a.G - r0);
+    const int64_t size = kv_part_floats(RB, a.d);
+    // partial of CTA c0 + j: the first one of a CTA that begins inside the unit, the second of the one
+    // in which the unit begins after another
+    const auto part = [&](int j) { return a.part + ((int64_t)(c0 + j) * 2 + (kv_start(W, parts, c0 + j) < u0)) * size; };
+    const bool vec = a.d % 4 == 0;
+    const int cols = (a.d + 127) / 128, jobs = rows * cols;
+    int team = 1;  // warps a job
+    while (team < WARPS && team * 4 < n) team *= 2;
+    const int teams = WARPS / team, mine = warp / team, me = warp - mine * team;
+    const int rank = (i - c0) * SHARE + blockIdx.x % SHARE, ranks = (c1 - c0) * SHARE;
+    for (int first = rank * teams; first < jobs; first += ranks * teams) {
+        const int job = first + mine;
+        const bool live = job < jobs;
+        const int r = live ? job / cols : 0, e = live ? (job - r * cols) * 128 + lane * 4 : 0;
+        float m = -INFINITY, l = 0.f;
+        for (int j = lane; j < n; j += 32) m = fmaxf(m, part(j)[RB * a.d + r]);
+#pragma unroll
+        for (int x = 16; x; x >>= 1) m = fmaxf(m, __shfl_xor_sync(FULL_MASK, m, x));
+        const float base = m == -INFINITY ? 0.f : m;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int j0 = 0; j0 < n; j0 += 32) {
+            float f = 0.f;
+            if (j0 + lane < n) {
+                const float* p = part(j0 + lane);
+                f = kv_ex2(p[RB * a.d + r] - base);
+                l += p[RB * a.d + RB + r] * f;
+            }
+            const int end = min(32, n - j0);
+#pragma unroll 4
+            for (int j = me; j < end; j += team) {
+                const float w = __shfl_sync(FULL_MASK, f, j);
+                const float* p = part(j0 + j) + (int64_t)r * a.d + e;
+                float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (vec) {
+                    if (e < a.d) x = *reinterpret_cast<const float4*>(p);
+                } else {
+                    if (e < a.d) x.x = p[0];
+                    if (e + 1 < a.d) x.y = p[1];
+                    if (e + 2 < a.d) x.z = p[2];
+                    if (e + 3 < a.d) x.w = p[3];
+                }
+                o.x = fmaf(x.x, w, o.x), o.y = fmaf(x.y, w, o.y), o.z = fmaf(x.z, w, o.z), o.w = fmaf(x.w, w, o.w);
+            }
+        }
+        l = group_sum<32>(l);
+        if (team > 1) {
+            sums[warp][lane] = o;
+            __syncthreads();
+            for (int x = 1; x < team && me == 0; ++x) {
+                const float4 y = sums[warp + x][lane];
+                o.x += y.x, o.y += y.y, o.z += y.z, o.w += y.w;
+            }
+            __syncthreads();
+        }
+        if (live && me == 0) {
+            const float inv = l == 0.f ? 0.f : 1.f / l;
+            const int node = (r0 + r) / a.G, hq = h * a.G + (r0 + r) - node * a.G;
+            const int64_t row = ((int64_t)b * a.T + node) * a.Hq + hq;
+            const float y[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+                if (e + x < a.d) store_elem(a.out, row * a.d + e + x, a.dtype, l == 0.f ? 0.f : y[x] * inv);
+            if (e == 0 && a.lse) a.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * LN2;
+        }
+    }
+}
+
+}  // namespace gdn

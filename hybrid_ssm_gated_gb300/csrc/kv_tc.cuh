@@ -207,6 +207,7 @@ __global__ void __launch_bounds__(kvt::NT, 1)
     constexpr uint32_t TM_S = 0, TM_O = 2 * NR;  // tensor memory: two buffers of S^T, then O^T by halves of d
     constexpr uint32_t tm_cols = NR * 4;
 
+    kv_grid_launch();
     if (tid == 0) {
         for (int i = 0; i < stages; ++i) mbar_init(&st.full[i], 1), mbar_init(&st.empty[i], 1);
         for (int i = 0; i < 2; ++i) {
