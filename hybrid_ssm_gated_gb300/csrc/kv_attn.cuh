@@ -89,17 +89,14 @@ __global__ void __launch_bounds__(kvg::NT) kv_attn_kernel(const KvArgs a, const 
 
     kv_grid_launch();
     kv_empty_rows<NT>(a);
-    kv_locate<true, KT, NT>(a, scan, [&](long long W) -> long long {
-        const int parts = kv_parts(W, gridDim.x, LEAST);
-        return blockIdx.x < parts && W > 0 ? kv_start(W, parts, blockIdx.x) : -1;
-    });
-    const long long W = scan.total;
-    const int parts = kv_parts(W, gridDim.x, LEAST);
-    if (W == 0 || blockIdx.x >= parts) return;
-    const long long w0 = kv_start(W, parts, blockIdx.x), w1 = kv_start(W, parts, blockIdx.x + 1);
+    const KvSplit split = kv_locate<true, KT, NT>(a, scan, gridDim.x, LEAST);
+    if (!split.busy(blockIdx.x)) {
+        if (tid == 0) static_cast<KvBorder*>(a.border)[blockIdx.x].rows = 0;
+        return;
+    }
     int checked = -1;
     bool pages_ok = true;
-    KvWalk<true, KT> w(a, w0, w1, scan.b, scan.before);
+    KvWalk<true, KT> w(a, split, scan);
     do {
         const KvSeq& s = w.s;
         const int b = w.b, h = w.h, nt = w.nt, r0 = w.rb * RB;
@@ -238,6 +235,7 @@ __global__ void __launch_bounds__(kvg::NT) kv_attn_kernel(const KvArgs a, const 
             }
         }
         __syncthreads();
+        if (tid == 0 && w.last()) static_cast<KvBorder*>(a.border)[blockIdx.x] = kv_border(a, split, w);
     } while (w.next());
 }
 

@@ -52,6 +52,7 @@ struct KvArgs {
     void* out;
     float* lse;
     float* part;  // partials: [CTA][2] blocks of row_block x (d + 2) floats
+    void* border;  // a KvBorder a CTA
     int row_block;  // query rows a unit at most
     // eviction
     int budget, recent;
@@ -106,46 +107,61 @@ __device__ __forceinline__ long long kv_seq_tiles(const KvArgs& a, const KvSeq& 
     return (long long)kv_tiles<ATTN, KT>(s) * kv_row_blocks<ATTN>(a, s) * a.Hkv;
 }
 
-// Number of CTAs that take part: none gets less than `least` tiles, so that small calls are not cut
-// into partials that cost more to join than they save.
-__device__ __forceinline__ int kv_parts(int64_t W, int grid, int least) {
-    const int64_t most = W / least;
-    return (int)(most < 1 ? 1 : (most < grid ? most : grid));
+__device__ __forceinline__ long long kv_div(long long a, long long b) {  // a, b >= 0; mostly both fit 32 bits
+    return ((a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
 }
 
-// The CTA of `parts` whose range holds tile t, and where CTA c's range starts.
-__device__ __forceinline__ int64_t kv_start(int64_t W, int parts, int c) { return W * c / parts; }
-__device__ __forceinline__ int kv_owner(int64_t W, int parts, int64_t t) {
-    int c = (int)(t * parts / W);
-    while (c + 1 < parts && kv_start(W, parts, c + 1) <= t) ++c;
-    while (c > 0 && kv_start(W, parts, c) > t) --c;
-    return c;
-}
+// The line of W tiles cut into ranges of W / parts tiles, the first W % parts of them one longer. No
+// CTA gets less than `least` tiles, so that small calls are not cut into partials that cost more to
+// join than they save.
+struct KvSplit {
+    long long W, q;
+    int parts, r;
+    __device__ __forceinline__ KvSplit(long long W_, int grid, int least) : W(W_) {
+        const long long most = kv_div(W, least);
+        parts = (int)(most < 1 ? 1 : (most < grid ? most : grid));
+        q = kv_div(W, parts), r = (int)(W - q * parts);
+    }
+    __device__ __forceinline__ bool busy(int c) const { return W > 0 && c < parts; }
+    __device__ __forceinline__ long long start(int c) const { return q * c + min(c, r); }
+    __device__ __forceinline__ int owner(long long t) const {
+        const long long head = (q + 1) * r;
+        return (int)(t < head ? kv_div(t, q + 1) : r + kv_div(t - head, q));
+    }
+};
 
-// Scratch of the scan over sequences.
+// What the scan over sequences leaves in shared memory.
 template <int NT>
 struct KvScan {
+    KvSeq seq[NT];  // the batch's sequences, where there are at most NT
     long long warp_sum[NT / 32];
-    long long total, before;  // all tiles; tiles of the sequences before the found one
+    long long before;  // tiles of the sequences before the found one
     int b;
 };
 
-// Total number of tiles, and (by the whole block of NT threads) the sequence whose tiles hold tile
-// `at(total)`. Each thread sums a run of sequences; a scan over the block places the runs.
-template <bool ATTN, int KT, int NT, typename At>
-__device__ __forceinline__ void kv_locate(const KvArgs& a, KvScan<NT>& sc, At at) {
+// The split of the batch's tiles and (by the whole block of NT threads) the sequence in which this CTA's
+// range begins. Each thread sums a run of sequences; a scan over the block places the runs.
+template <bool ATTN, int KT, int NT>
+__device__ __forceinline__ KvSplit kv_locate(const KvArgs& a, KvScan<NT>& sc, int grid, int least) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int run = (a.B + NT - 1) / NT;
-    const int b0 = tid * run, b1 = min(a.B, b0 + run);
+    const int run = a.B <= NT ? 1 : (a.B + NT - 1) / NT;
+    const int b0 = min(a.B, tid * run), b1 = min(a.B, b0 + run);
     long long sum = 0;
-    for (int b = b0; b < b1; ++b) sum += kv_seq_tiles<ATTN, KT>(a, kv_seq<ATTN>(a, b));
-    long long inc = sum;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(FULL_MASK, inc, o);
-        if (lane >= o) inc += y;
+    for (int b = b0; b < b1; ++b) {
+        const KvSeq s = kv_seq<ATTN>(a, b);
+        if (run == 1) sc.seq[b] = s;
+        sum += kv_seq_tiles<ATTN, KT>(a, s);
     }
-    if (lane == 31) sc.warp_sum[warp] = inc;
+    long long inc = sum;
+    if (a.B > 1) {
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long y = __shfl_up_sync(FULL_MASK, inc, o);
+            if (lane >= o) inc += y;
+        }
+    }
+    const long long in_warp = __shfl_sync(FULL_MASK, inc, a.B > 1 ? 31 : 0);
+    if (lane == 0) sc.warp_sum[warp] = in_warp;
     __syncthreads();
     long long before = 0, total = 0;
     for (int w = 0; w < NT / 32; ++w) {
@@ -153,18 +169,21 @@ __device__ __forceinline__ void kv_locate(const KvArgs& a, KvScan<NT>& sc, At at
         total += sc.warp_sum[w];
     }
     before += inc - sum;
-    if (tid == 0) sc.total = total, sc.b = a.B;
-    const long long want = at(total);
-    if (want >= before && want < before + sum) {
-        int b = b0;
-        for (; b < b1; ++b) {
-            const long long n = kv_seq_tiles<ATTN, KT>(a, kv_seq<ATTN>(a, b));
-            if (want < before + n) break;
-            before += n;
+    const KvSplit split(total, grid, least);
+    if (split.busy(blockIdx.x)) {
+        const long long want = split.start(blockIdx.x);
+        if (want >= before && want < before + sum) {
+            int b = b0;
+            for (; run > 1 && b < b1; ++b) {
+                const long long n = kv_seq_tiles<ATTN, KT>(a, kv_seq<ATTN>(a, b));
+                if (want < before + n) break;
+                before += n;
+            }
+            sc.b = b, sc.before = before;
         }
-        sc.b = b, sc.before = before;
     }
     __syncthreads();
+    return split;
 }
 
 // A walk along a CTA's tiles, segment by segment: a segment is the run of tiles of one unit (key head h,
@@ -172,22 +191,25 @@ __device__ __forceinline__ void kv_locate(const KvArgs& a, KvScan<NT>& sc, At at
 template <bool ATTN, int KT>
 struct KvWalk {
     const KvArgs& a;
+    const KvSeq* seq;   // the batch's sequences in shared memory, or NULL
     long long at, end;  // next tile of the line, end of the range
     int b, unit, units, blocks, nt;
     KvSeq s;
     int h, rb, t0, t1;  // the segment: tiles t0 .. t1 - 1 of nt
     bool later;         // it does not begin the CTA's range: its partial is the second one
 
-    // From tile w0 of the line, which lies in sequence b0, whose tiles begin at `before`.
-    __device__ __forceinline__ KvWalk(const KvArgs& a_, long long w0, long long w1, int b0, long long before)
-        : a(a_), at(w0), end(w1), b(b0), later(false) {
+    // This CTA's range, which begins in sequence sc.b.
+    template <int NT>
+    __device__ __forceinline__ KvWalk(const KvArgs& a_, const KvSplit& split, const KvScan<NT>& sc)
+        : a(a_), seq(a_.B <= NT ? sc.seq : nullptr), at(split.start(blockIdx.x)), end(split.start(blockIdx.x + 1)),
+          b(sc.b), later(false) {
         load();
-        const long long off = w0 - before;
-        unit = (int)(off / nt);
+        const long long off = at - sc.before;
+        unit = (int)kv_div(off, nt);
         segment((int)(off - (long long)unit * nt));
     }
     __device__ __forceinline__ void load() {
-        s = kv_seq<ATTN>(a, b);
+        s = seq ? seq[b] : kv_seq<ATTN>(a, b);
         nt = kv_tiles<ATTN, KT>(s), blocks = kv_row_blocks<ATTN>(a, s), units = a.Hkv * blocks;
     }
     __device__ __forceinline__ void segment(int tile) {
@@ -195,6 +217,7 @@ struct KvWalk {
         t0 = tile, t1 = (int)min((long long)nt, tile + (end - at));
     }
     __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == nt; }
+    __device__ __forceinline__ bool last() const { return at + (t1 - t0) >= end; }
     // The next segment; false at the end of the range.
     __device__ __forceinline__ bool next() {
         at += t1 - t0, later = true;
@@ -210,6 +233,26 @@ struct KvWalk {
         return true;
     }
 };
+
+// A unit that goes on past the end of a CTA's range: what the join needs, one record a CTA.
+struct KvBorder {
+    int b, h, r0, rows;  // rows 0: the range ends between units
+    int c0, n;           // the unit's CTAs are c0 .. c0 + n - 1
+    int second;          // the unit begins within CTA c0's range, after another: its partial there is the second
+    int pad;
+};
+
+// Record of this CTA's last segment, by one thread.
+template <bool ATTN, int KT>
+__device__ __forceinline__ KvBorder kv_border(const KvArgs& a, const KvSplit& split, const KvWalk<ATTN, KT>& w) {
+    KvBorder k{};
+    if (w.t1 == w.nt) return k;
+    const long long u0 = w.at - w.t0;
+    k.b = w.b, k.h = w.h, k.r0 = w.rb * a.row_block, k.rows = min(a.row_block, w.s.nodes * a.G - k.r0);
+    k.c0 = split.owner(u0), k.n = split.owner(u0 + w.nt - 1) - k.c0 + 1;
+    k.second = split.start(k.c0) < u0;
+    return k;
+}
 
 // Every page of the sequence's entries is a page of the pool (all threads of a group of `n` ask, each
 // a part; the caller joins the answers).
@@ -248,6 +291,10 @@ __device__ __forceinline__ float kv_ex2(float x) {
 
 // Floats of one partial: row_block rows of d outputs, their maxima and their sums (16-byte blocks).
 __host__ __device__ inline int64_t kv_part_floats(int row_block, int d) { return ((int64_t)row_block * (d + 2) + 3) / 4 * 4; }
+
+__host__ __device__ inline int64_t kv_part_bytes(int64_t grid, int row_block, int d) {
+    return grid * 2 * kv_part_floats(row_block, d) * 4;
+}
 
 // The join kernel is launched while the attention kernel runs (programmatic launch): the attention
 // kernel's blocks let it start, and every block of it waits here until the attention kernel has ended

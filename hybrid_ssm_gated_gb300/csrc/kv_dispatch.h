@@ -19,6 +19,9 @@ bool kv_attn_tc_fits(const KvArgs& a);
 cudaError_t launch_kv_attn_tc(KvArgs& a, cudaStream_t stream);
 cudaError_t kv_attn_tc_workspace(KvArgs& a, int64_t& bytes);
 
+// Joins the partials of an attention kernel of `grid` CTAs, on the same stream.
+cudaError_t launch_kv_join(const KvArgs& a, int grid, cudaStream_t stream);
+
 cudaError_t launch_kv_commit(const KvArgs& a, bool vec, cudaStream_t stream);
 cudaError_t launch_kv_evict(const KvArgs& a, int cap, bool vec, cudaStream_t stream);
 

@@ -2,7 +2,6 @@
 #include "gdn_launch.cuh"
 #include "kv_attn.cuh"
 #include "kv_dispatch.h"
-#include "kv_launch_join.cuh"
 #include "kv_weights.cuh"
 
 namespace gdn {
@@ -42,7 +41,7 @@ cudaError_t kv_attn_workspace(KvArgs& a, int64_t& bytes) {
     int64_t grid = 0;
     a.row_block = kvg::RB;
     const cudaError_t e = wave(attn_kernel(a.dtype), a, kvg::layout(a.d).bytes, kvg::LEAST, grid);
-    bytes = grid * 2 * kv_part_floats(kvg::RB, a.d) * 4;
+    bytes = kv_part_bytes(grid, kvg::RB, a.d) + grid * (int64_t)sizeof(KvBorder);
     return e;
 }
 
@@ -52,9 +51,10 @@ cudaError_t launch_kv_attn(KvArgs& a, bool vec, cudaStream_t stream) {
     a.row_block = kvg::RB;
     cudaError_t e = wave(attn_kernel(a.dtype), a, smem, kvg::LEAST, grid);
     if (e != cudaSuccess) return e;
+    a.border = reinterpret_cast<char*>(a.part) + kv_part_bytes(grid, kvg::RB, a.d);
     attn_kernel(a.dtype)<<<(unsigned)grid, kvg::NT, smem, stream>>>(a, vec);
-    if ((e = cudaGetLastError()) != cudaSuccess || grid == 1) return e;
-    return launch_join<kvg::KT, kvg::LEAST>(a, (int)grid, stream);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    return launch_kv_join(a, (int)grid, stream);
 }
 
 cudaError_t launch_kv_weights(KvArgs& a, bool vec, cudaStream_t stream) {

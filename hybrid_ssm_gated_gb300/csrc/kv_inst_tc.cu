@@ -1,7 +1,6 @@
 // Instantiations and launch of the tensor-core attention kernel, and its tensor maps.
 #include "gdn_launch.cuh"
 #include "kv_dispatch.h"
-#include "kv_launch_join.cuh"
 #include "kv_tc.cuh"
 
 namespace gdn {
@@ -69,9 +68,9 @@ cudaError_t launch(KvArgs& a, const kvt::Maps& maps, int boxes, int box_rows, in
     auto kern = kv_attn_tc_kernel<ST, NR>;
     const int stages = stages_of<NR>(boxes, optin), smem = kvt::smem_bytes<NR>(boxes, stages);
     int bps = 0;
-    cudaError_t e = prepare_kernel(kern, kvt::NT, smem, bps);
+    cudaError_t e = prepare_kernel(kern, kvt::threads(NR), smem, bps);
     if (e != cudaSuccess) return e;
-    kern<<<grid, kvt::NT, smem, stream>>>(a, maps, boxes, stages, box_rows);
+    kern<<<grid, kvt::threads(NR), smem, stream>>>(a, maps, boxes, stages, box_rows);
     return cudaGetLastError();
 }
 
@@ -106,7 +105,7 @@ cudaError_t kv_attn_tc_workspace(KvArgs& a, int64_t& bytes) {
     int64_t grid = 0;
     a.row_block = row_block_of((int64_t)a.T * a.G, boxes_of(a.d));
     const cudaError_t e = wave(a, di, grid);
-    bytes = grid * 2 * kv_part_floats(a.row_block, a.d) * 4;
+    bytes = kv_part_bytes(grid, a.row_block, a.d) + grid * (int64_t)sizeof(KvBorder);
     return e;
 }
 
@@ -124,10 +123,11 @@ cudaError_t launch_kv_attn_tc(KvArgs& a, cudaStream_t stream) {
     int64_t grid = 0;
     cudaError_t e = wave(a, di, grid);
     if (e != cudaSuccess) return e;
+    a.border = reinterpret_cast<char*>(a.part) + kv_part_bytes(grid, a.row_block, a.d);
     e = a.dtype == GDN_BF16 ? launch_rows<__nv_bfloat16>(a, maps, boxes, box_rows, (int)grid, di.smem_optin, stream)
                             : launch_rows<__half>(a, maps, boxes, box_rows, (int)grid, di.smem_optin, stream);
-    if (e != cudaSuccess || grid == 1) return e;
-    return launch_join<kvt::KT, kvt::LEAST>(a, (int)grid, stream);
+    if (e != cudaSuccess) return e;
+    return launch_kv_join(a, (int)grid, stream);
 }
 
 }  // namespace gdn

@@ -19,42 +19,26 @@ constexpr int SHARE = 4;  // blocks a border
 
 }  // namespace kvj
 
-// Blocks SHARE i .. SHARE i + SHARE - 1 stand at the border between the ranges of CTAs i and i + 1 of an
-// attention kernel of `grid` CTAs; the blocks at a unit's inner borders share its jobs.
-template <int KT, int LEAST>
-__global__ void __launch_bounds__(kvj::NT) kv_join_kernel(const __grid_constant__ KvArgs a, const int grid) {
+// Blocks SHARE i .. SHARE i + SHARE - 1 stand at the end of CTA i's range (`parts` is known on the device
+// only, so there are blocks for every CTA of the attention kernel but the last); those at a unit's inner
+// borders share its jobs.
+__global__ void __launch_bounds__(kvj::NT) kv_join_kernel(const __grid_constant__ KvArgs a) {
     using namespace kvj;
-    __shared__ KvScan<NT> scan;
     __shared__ float4 sums[WARPS][32];
     const int i = blockIdx.x / SHARE, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    kv_locate<true, KT, NT>(a, scan, [&](long long W) -> long long {
-        const int parts = kv_parts(W, grid, LEAST);
-        return W > 0 && i + 1 < parts ? kv_start(W, parts, i + 1) : -1;
-    });
     kv_grid_wait();  // the partials are written
-    const long long W = scan.total;
-    const int parts = kv_parts(W, grid, LEAST);
-    if (W == 0 || i + 1 >= parts) return;
-    const long long border = kv_start(W, parts, i + 1);
-    const int b = scan.b;
-    const KvSeq s = kv_seq<true>(a, b);
-    const int nt = kv_tiles<true, KT>(s);
-    const int unit = (int)((border - scan.before) / nt);
-    const long long u0 = scan.before + (long long)unit * nt;
-    if (border == u0) return;  // the border lies between two units
-    const int c0 = kv_owner(W, parts, u0), c1 = kv_owner(W, parts, u0 + nt - 1), n = c1 - c0 + 1;
-    const int RB = a.row_block, blocks = kv_row_blocks<true>(a, s), h = unit / blocks, r0 = (unit - h * blocks) * RB;
-    const int rows = min(RB, s.nodes * a.G - r0);
+    const KvBorder k = static_cast<const KvBorder*>(a.border)[i];
+    if (k.rows == 0) return;
+    const int RB = a.row_block, rows = k.rows, r0 = k.r0, h = k.h, b = k.b, c0 = k.c0, n = k.n;
     const int64_t size = kv_part_floats(RB, a.d);
-    // partial of CTA c0 + j: the first one of a CTA that begins inside the unit, the second of the one
-    // in which the unit begins after another
-    const auto part = [&](int j) { return a.part + ((int64_t)(c0 + j) * 2 + (kv_start(W, parts, c0 + j) < u0)) * size; };
+    // a unit's partial is the first of a CTA's two, but for the CTA in which it begins after another
+    const auto part = [&](int j) { return a.part + ((int64_t)(c0 + j) * 2 + (j == 0 ? k.second : 0)) * size; };
     const bool vec = a.d % 4 == 0;
     const int cols = (a.d + 127) / 128, jobs = rows * cols;
     int team = 1;  // warps a job
     while (team < WARPS && team * 4 < n) team *= 2;
     const int teams = WARPS / team, mine = warp / team, me = warp - mine * team;
-    const int rank = (i - c0) * SHARE + blockIdx.x % SHARE, ranks = (c1 - c0) * SHARE;
+    const int rank = (i - c0) * SHARE + blockIdx.x % SHARE, ranks = (n - 1) * SHARE;
     for (int first = rank * teams; first < jobs; first += ranks * teams) {
         const int job = first + mine;
         const bool live = job < jobs;

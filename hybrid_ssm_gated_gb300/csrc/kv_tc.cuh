@@ -18,15 +18,17 @@
 // tensor memory, happen on a unit's first tile and where the maximum really
 // moves; otherwise a tile costs one barrier, which carries the vote.
 //
-// Kernel shape: persistent, one CTA per SM, 10 warps:
-//   warps 0-7  softmax: two groups of four warps; group g owns query rows
-//              g NR/2 .. (g+1) NR/2 - 1 (columns of S^T and O^T), thread key
+// Kernel shape: persistent, one CTA per SM:
+//   softmax    NG groups of four warps (two up to 32 rows, four above: 16 or 32
+//              rows a thread keep scores and sums in registers); group g owns
+//              NR / NG query rows (columns of S^T and O^T), thread key
 //              (warp % 4) * 32 + lane = its tensor-memory lane;
-//   warp 8     TMA: K and V tiles into a ring of stages of 128 keys x 128
-//              elements (64 where d <= 64), 128-byte swizzle, boxes of as many
-//              keys as a page and the tile share; page indices two tiles ahead;
-//   warp 9     one thread issues the MMAs: S^T of tile i + 1 before O^T of tile
-//              i, so that the tensor cores work while tile i's weights form.
+//   loads      one warp: K and V tiles by TMA into a ring of stages of 128 keys
+//              x 128 elements (64 where d <= 64), 128-byte swizzle, boxes of as
+//              many keys as a page and the tile share; page indices two tiles
+//              ahead;
+//   MMAs       one thread issues them: S^T of tile i + 1 before O^T of tile i,
+//              so that the tensor cores work while tile i's weights form.
 // K is the A operand as it lies (K-major); V is the A operand of the second
 // product transposed (MN-major); P^T is written by its threads, 16 bytes for
 // eight rows, in the unswizzled MN-major layout, which a warp fills without
@@ -43,8 +45,9 @@ namespace gdn {
 namespace kvt {
 
 constexpr int KT = 128;       // keys a tile
-constexpr int NT = 320;       // threads
-constexpr int SM_WARPS = 8;   // softmax warps
+// groups of softmax warps, and all warps, for a block of NR rows
+__host__ __device__ constexpr int groups(int NR) { return NR > 32 ? 4 : 2; }
+__host__ __device__ constexpr int threads(int NR) { return (4 * groups(NR) + 2) * 32; }
 constexpr int LEAST = 1;      // tiles a CTA at least
 constexpr int BOX = 64;       // elements of d in one TMA box (128 bytes)
 constexpr int BOX_BYTES = KT * BOX * 2;
@@ -59,15 +62,16 @@ struct Maps {
 // Small shared-memory state of a CTA.
 template <int NR>
 struct __align__(16) State {
-    float ref[NR];            // reference m of each row
+    float nref[NR];           // reference of each row, negated: -m
     float factor[NR];         // rescaling factor of a moved reference; at the end 1 / l
     float warp_max[4][NR];    // maxima by warp quadrant; at the end sums
     uint32_t mask[2][NR];     // mask words of each row
     int64_t row[NR];          // row of out and lse, -1 where the unit has none
     uint64_t full[MAX_STAGES], empty[MAX_STAGES];
     uint64_t s_full[2], s_empty[2], p_full[2], p_empty[2], q_full, v_ok, drain;
-    KvScan<NT> scan;
-    int gave_up[2], v_stage;
+    int64_t q_at[NR];         // element offset of each row's query
+    KvScan<threads(NR)> scan;
+    int gave_up[4], v_stage;
     uint32_t tmem;
 };
 
@@ -139,11 +143,13 @@ template <>
 struct Half16<__nv_bfloat16> {
     static constexpr uint32_t type = 1, exp_mask = 0x7f80u;
     __device__ static __forceinline__ uint32_t pack(float lo, float hi) { return pack_bf16x2(lo, hi); }
+    __device__ static __forceinline__ __nv_bfloat16 round(float x) { return __float2bfloat16_rn(x); }
 };
 template <>
 struct Half16<__half> {
     static constexpr uint32_t type = 0, exp_mask = 0x7c00u;
     __device__ static __forceinline__ uint32_t pack(float lo, float hi) { return pack_f16x2(lo, hi); }
+    __device__ static __forceinline__ __half round(float x) { return __float2half_rn(x); }
 };
 
 // Row sums of 32 (or N < 32) rows over a warp's threads: lane r holds row r's.
@@ -172,32 +178,62 @@ __device__ __forceinline__ uint4 clear_odd(uint4 x) {
     return make_uint4(u[0], u[1], u[2], u[3]);
 }
 
-// The values that clear_odd took out, added to the eight rows' outputs where the row attends the node.
+// Whether this thread's share of the nodes' values (all 128 threads of a group ask) is not all finite.
 template <typename ST>
+__device__ __forceinline__ bool odd_values(const KvArgs& a, int nodes, int b, int h, int gt) {
+    constexpr uint32_t m = Half16<ST>::exp_mask;
+    const ST* v = static_cast<const ST*>(a.vn.p) + (int64_t)b * a.vn.seq + (int64_t)h * a.vn.head;
+    bool odd = false;
+    const int per = (a.d + 63) / 64 * 8, n = nodes * per;
+#pragma unroll 4
+    for (int i = gt; i < n; i += 128) {
+        const int j = i / per, e = (i - j * per) * 8;
+        uint4 x = make_uint4(0, 0, 0, 0);
+        if (e < a.d) x = *reinterpret_cast<const uint4*>(v + (int64_t)j * a.vn.node + e);
+        const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int y = 0; y < 4; ++y) odd = odd || (u[y] & m) == m || (u[y] >> 16 & m) == m;
+    }
+    return odd;
+}
+
+// The values that clear_odd took out, added to the rows' outputs where the row attends the node.
+template <typename ST, int N>
 __device__ __noinline__ void add_odd(const KvArgs& a, int nodes, int b, int h, int e, const uint32_t* lo, const uint32_t* hi,
                                      float* o) {
     for (int j = 0; j < nodes; ++j) {
         const float v = load_elem(a.vn.p, (int64_t)b * a.vn.seq + (int64_t)j * a.vn.node + (int64_t)h * a.vn.head + e,
                                   Store<ST>::code);
         if (isfinite(v)) continue;
-        for (int x = 0; x < 8; ++x)
+        for (int x = 0; x < N; ++x)
             if ((j < 32 ? lo[x] >> j : hi[x] >> (j - 32)) & 1) o[x] += v;
     }
+}
+
+// x * c + y on two values at a time
+__device__ __forceinline__ float2 fma2(float2 x, float2 c, float2 y) {
+    float2 r;
+    asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+        "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(x.x), "f"(x.y), "f"(c.x), "f"(c.y), "f"(y.x), "f"(y.y));
+    return r;
 }
 
 }  // namespace kvt
 
 // boxes: 64-element boxes of d; stages: of the ring; box_rows: keys of one TMA box.
 template <typename ST, int NR>
-__global__ void __launch_bounds__(kvt::NT, 1)
+__global__ void __launch_bounds__(kvt::threads(NR), 1)
     kv_attn_tc_kernel(const __grid_constant__ KvArgs a, const __grid_constant__ kvt::Maps maps, const int boxes,
                       const int stages, const int box_rows) {
     using namespace kvt;
     using H = Half16<ST>;
-    constexpr int NRH = NR / 2;
+    constexpr int NG = groups(NR), NRH = NR / NG, NT = threads(NR), SM_WARPS = 4 * NG;
+    constexpr int LOAD_WARP = SM_WARPS, MMA_WARP = SM_WARPS + 1;
     extern __shared__ unsigned char smem_raw[];
     unsigned char* smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
-    const int pairs = (boxes + 1) >> 1;                    // 128-element halves of d
+    const int pairs = (boxes + 1) >> 1;  // 128-element halves of d
     const int stage_bytes = (boxes > 1 ? 2 : 1) * BOX_BYTES;
     unsigned char* sQ = smem;
     unsigned char* sP = sQ + boxes * NR * 128;
@@ -205,40 +241,38 @@ __global__ void __launch_bounds__(kvt::NT, 1)
     State<NR>& st = *reinterpret_cast<State<NR>*>(ring + stages * stage_bytes);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     constexpr uint32_t TM_S = 0, TM_O = 2 * NR;  // tensor memory: two buffers of S^T, then O^T by halves of d
-    constexpr uint32_t tm_cols = NR * 4;
+    constexpr uint32_t TM_COLS = NR * 4;
 
     kv_grid_launch();
-    if (tid == 0) {
-        for (int i = 0; i < stages; ++i) mbar_init(&st.full[i], 1), mbar_init(&st.empty[i], 1);
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&st.s_full[i], 1), mbar_init(&st.s_empty[i], SM_WARPS);
-            mbar_init(&st.p_full[i], SM_WARPS), mbar_init(&st.p_empty[i], 1);
-            st.gave_up[i] = 0;
+    if (warp == LOAD_WARP) {
+        if (lane < 4) {
+            const CUtensorMap* m = lane == 0 ? &maps.k : lane == 1 ? &maps.v : lane == 2 ? &maps.kn : &maps.vn;
+            asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory");
         }
-        mbar_init(&st.q_full, SM_WARPS), mbar_init(&st.v_ok, 1), mbar_init(&st.drain, 1);
+        if (lane < stages) mbar_init(&st.full[lane], 1), mbar_init(&st.empty[lane], 1);
+        if (lane < 2) {
+            mbar_init(&st.s_full[lane], 1), mbar_init(&st.s_empty[lane], SM_WARPS);
+            mbar_init(&st.p_full[lane], SM_WARPS), mbar_init(&st.p_empty[lane], 1);
+        }
+        if (lane == 2) mbar_init(&st.q_full, SM_WARPS), mbar_init(&st.v_ok, 1), mbar_init(&st.drain, 1);
+        if (lane < 4) st.gave_up[lane] = 0;
         fence_barrier_init();
     }
-    if (warp == 9) {
+    if (warp == MMA_WARP) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&st.tmem)),
-                     "r"(tm_cols)
+                     "r"(TM_COLS)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
     tc::fence_before();
-    kv_locate<true, KT, NT>(a, st.scan, [&](long long W) -> long long {
-        const int parts = kv_parts(W, gridDim.x, LEAST);
-        return W > 0 && blockIdx.x < parts ? kv_start(W, parts, blockIdx.x) : -1;
-    });
+    const KvSplit split = kv_locate<true, KT, NT>(a, st.scan, gridDim.x, LEAST);
     tc::fence_after();
     const uint32_t tmem = st.tmem;
-    const long long W = st.scan.total;
-    const int parts = kv_parts(W, gridDim.x, LEAST);
-    const bool busy = W > 0 && blockIdx.x < parts;
-    const long long w0 = busy ? kv_start(W, parts, blockIdx.x) : 0, w1 = busy ? kv_start(W, parts, blockIdx.x + 1) : 0;
+    const bool busy = split.busy(blockIdx.x);
 
-    if (warp == 8 && busy) {
+    if (warp == LOAD_WARP && busy) {
         // ------------------------------------------------------------ loads
-        KvWalk<true, KT> w(a, w0, w1, st.scan.b, st.scan.before);
+        KvWalk<true, KT> w(a, split, st.scan);
         uint32_t n_block = 0;
         int stage = 0, round = 0;
         bool ok = true;
@@ -266,7 +300,8 @@ __global__ void __launch_bounds__(kvt::NT, 1)
                         mbar_arrive_expect_tx(&st.full[stage], (tree ? a.T : used * box_rows) * 128 * nb);
                     __syncwarp();
                     if (tree) {
-                        if (lane < nb) tma_load(dst + lane * BOX_BYTES, map_new, (2 * p + lane) * BOX, 0, w.h, w.b, &st.full[stage]);
+                        if (lane < nb)
+                            tma_load(dst + lane * BOX_BYTES, map_new, (2 * p + lane) * BOX, 0, w.h, w.b, &st.full[stage]);
                     } else if (lane < used) {
                         for (int x = 0; x < nb; ++x)
                             tma_load(dst + x * BOX_BYTES + lane * box_rows * 128, map, (2 * p + x) * BOX, place, w.h, page,
@@ -294,10 +329,10 @@ __global__ void __launch_bounds__(kvt::NT, 1)
                 mbar_wait(&st.full[blk % stages], (blk / stages) & 1);
             }
         }
-    } else if (warp == 9 && busy) {
+    } else if (warp == MMA_WARP && busy) {
         // ------------------------------------------------------------ MMAs
         if (lane == 0) {
-            KvWalk<true, KT> w(a, w0, w1, st.scan.b, st.scan.before);
+            KvWalk<true, KT> w(a, split, st.scan);
             const uint32_t id_s = idesc(H::type, false, false, NR), id_o = idesc(H::type, true, true, NR);
             const uint32_t aQ = smem_addr(sQ), aP = smem_addr(sP), aR = smem_addr(ring);
             int stage = 0, round = 0;
@@ -374,38 +409,46 @@ __global__ void __launch_bounds__(kvt::NT, 1)
         __syncwarp();
     } else if (warp < SM_WARPS && busy) {
         // ------------------------------------------------------------ softmax
-        const int g = warp >> 2, quad = warp & 3, key = quad * 32 + lane, gt = tid & 127;
+        const int g = warp >> 2, quad = warp & 3, key = quad * 32 + lane, gt = tid & 127, g0 = g * NRH;
         const uint32_t lane_base = (uint32_t)(quad * 32) << 16;
         const float c2 = a.scale * LOG2E;
         const int64_t part_floats = kv_part_floats(NR, a.d);
-        KvWalk<true, KT> w(a, w0, w1, st.scan.b, st.scan.before);
+        KvWalk<true, KT> w(a, split, st.scan);
         uint32_t n_t = 0, n_v = 0;  // tiles so far, v_ok rounds so far
         int checked = -1;
         bool pages_bad = false, failed = false, stop = false;  // stop: the whole group gives up
         float l[NRH];
         do {
             const int rows = min(NR, w.s.nodes * a.G - w.rb * NR), r_first = w.rb * NR, n = w.t1 - w.t0;
-            const bool has_tree = w.t1 == w.nt;
-            // ---- row tables and queries (rows g NRH ..), checks of pages and of the nodes' values
-            for (int r = g * NRH + gt; r < (g + 1) * NRH; r += 128) {
-                st.ref[r] = REF_NONE;
-                const int node = (r_first + r) / a.G, x = w.h * a.G + (r_first + r) - node * a.G;
+            // ---- row tables and queries of the group's rows
+            if (gt < NRH) {
+                const int r = g0 + gt, node = (r_first + r) / a.G, x = w.h * a.G + (r_first + r) - node * a.G;
                 const bool in = r < rows;
+                st.nref[r] = -REF_NONE;
                 st.row[r] = in ? ((int64_t)w.b * a.T + node) * a.Hq + x : -1;
+                st.q_at[r] = (int64_t)w.b * a.q.seq + (int64_t)node * a.q.node + (int64_t)x * a.q.head;
                 const uint64_t m = in ? a.mask[(int64_t)w.b * a.T + node] : 0;
                 st.mask[0][r] = (uint32_t)m, st.mask[1][r] = (uint32_t)(m >> 32);
             }
+            group_sync(g);
             {
-                const int per = boxes * 8;  // 16-byte pieces of a row
-                for (int i = gt; i < NRH * per; i += 128) {
-                    const int rr = i / per, c = i - rr * per, r = g * NRH + rr;
-                    uint4 x = make_uint4(0, 0, 0, 0);
-                    if (r < rows && c * 8 < a.d) {
-                        const int node = (r_first + r) / a.G, hq = w.h * a.G + (r_first + r) - node * a.G;
-                        x = *reinterpret_cast<const uint4*>(static_cast<const ST*>(a.q.p) + (int64_t)w.b * a.q.seq +
-                                                            (int64_t)node * a.q.node + (int64_t)hq * a.q.head + c * 8);
+                // 16-byte pieces, eight of a row's box; a thread's loads all go out before the first is stored
+                constexpr int N = (NRH * 8 + 127) / 128;
+                for (int x = 0; x < boxes; ++x) {
+                    uint4 v[N];
+#pragma unroll
+                    for (int y = 0; y < N; ++y) {
+                        const int i = gt + y * 128, r = g0 + (i >> 3), e = x * BOX + (i & 7) * 8;
+                        v[y] = make_uint4(0, 0, 0, 0);
+                        if (i < NRH * 8 && r < rows && e < a.d)
+                            v[y] = *reinterpret_cast<const uint4*>(static_cast<const ST*>(a.q.p) + st.q_at[r] + e);
                     }
-                    *reinterpret_cast<uint4*>(sQ + (c >> 3) * NR * 128 + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = x;
+#pragma unroll
+                    for (int y = 0; y < N; ++y) {
+                        const int i = gt + y * 128, r = g0 + (i >> 3);
+                        if (i < NRH * 8)
+                            *reinterpret_cast<uint4*>(sQ + x * NR * 128 + r * 128 + (((i & 7) ^ (r & 7)) << 4)) = v[y];
+                    }
                 }
             }
             tc::fence_async_smem();
@@ -417,17 +460,6 @@ __global__ void __launch_bounds__(kvt::NT, 1)
                 checked = w.b;
             }
             bool odd = false;  // a node's value is not finite
-            if (has_tree) {
-                for (int i = gt; i < w.s.nodes * (a.d / 8); i += 128) {
-                    const int j = i / (a.d / 8), c = i - j * (a.d / 8);
-                    const uint4 x = *reinterpret_cast<const uint4*>(static_cast<const ST*>(a.vn.p) + (int64_t)w.b * a.vn.seq +
-                                                                    (int64_t)j * a.vn.node + (int64_t)w.h * a.vn.head + c * 8);
-                    const uint32_t e = H::exp_mask, u[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-                    for (int y = 0; y < 4; ++y) odd = odd || (u[y] & e) == e || (u[y] >> 16 & e) == e;
-                }
-            }
-            odd = group_any(g, odd);  // the tables above are complete, too
 #pragma unroll
             for (int r = 0; r < NRH; ++r) l[r] = 0.f;
 
@@ -435,32 +467,31 @@ __global__ void __launch_bounds__(kvt::NT, 1)
                 const int t = w.t0 + i, buf = n_t & 1;
                 const bool tree = t == w.nt - 1;
                 const int live = tree ? w.s.nodes : min(KT, w.s.len - t * KT);
+                if (tree) odd = group_any(g, odd_values<ST>(a, w.s.nodes, w.b, w.h, gt));
                 float s[NRH];
                 failed = failed || !mbar_wait(&st.s_full[buf], (n_t >> 1) & 1);
                 tc::fence_after();
-                tc::tmem_ld<NRH>(tmem + lane_base + TM_S + buf * NR + g * NRH, s);
+                tc::tmem_ld<NRH>(tmem + lane_base + TM_S + buf * NR + g0, s);
                 tc::fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&st.s_empty[buf]);
-                if (tree) {
+                float c = c2;
+                if (live < KT) {  // the scaled scores, -inf where the row does not see the key
+                    c = 1.f;
 #pragma unroll
                     for (int r = 0; r < NRH; ++r) {
-                        const uint32_t word = st.mask[quad & 1][g * NRH + r];
-                        if (key >= live || !(word >> lane & 1)) s[r] = -INFINITY;
-                        else s[r] *= c2;
+                        const bool seen = key < live && (!tree || (st.mask[quad & 1][g0 + r] >> lane & 1));
+                        s[r] = seen ? s[r] * c2 : -INFINITY;
                     }
-                } else if (key >= live) {
-#pragma unroll
-                    for (int r = 0; r < NRH; ++r) s[r] = -INFINITY;
-                } else {
-#pragma unroll
-                    for (int r = 0; r < NRH; ++r) s[r] *= c2;
                 }
-                float over = -INFINITY;
+                const float2 cc = make_float2(c, c);
+                float over = -INFINITY;  // the largest exponent against the references
 #pragma unroll
                 for (int r = 0; r < NRH; r += 4) {
-                    const float4 m = *reinterpret_cast<const float4*>(&st.ref[g * NRH + r]);
-                    over = fmaxf(over, fmaxf(fmaxf(s[r] - m.x, s[r + 1] - m.y), fmaxf(s[r + 2] - m.z, s[r + 3] - m.w)));
+                    const float4 m = *reinterpret_cast<const float4*>(&st.nref[g0 + r]);
+                    const float2 x = fma2(make_float2(s[r], s[r + 1]), cc, make_float2(m.x, m.y));
+                    const float2 y = fma2(make_float2(s[r + 2], s[r + 3]), cc, make_float2(m.z, m.w));
+                    over = fmaxf(over, fmaxf(fmaxf(x.x, x.y), fmaxf(y.x, y.y)));
                 }
                 if (failed) st.gave_up[g] = 1;
                 if (group_any(g, failed || over > REF_SLACK)) {
@@ -471,21 +502,24 @@ __global__ void __launch_bounds__(kvt::NT, 1)
                     // the tile's maxima, new references
 #pragma unroll
                     for (int r = 0; r < NRH; ++r) {
-                        const float x = warp_max(s[r]);
-                        if (lane == (r & 31)) st.warp_max[quad][g * NRH + r] = x;
+                        const float x = warp_max(s[r] * c);
+                        if (lane == (r & 31)) st.warp_max[quad][g0 + r] = x;
                     }
                     group_sync(g);
                     if (gt < NRH) {
-                        const int r = g * NRH + gt;
-                        const float old = st.ref[r];
+                        const int r = g0 + gt;
+                        const float old = -st.nref[r];
                         const float m = fmaxf(fmaxf(fmaxf(st.warp_max[0][r], st.warp_max[1][r]),
                                                     fmaxf(st.warp_max[2][r], st.warp_max[3][r])), old);
-                        st.factor[r] = kv_ex2(old - m), st.ref[r] = m;
+                        st.factor[r] = kv_ex2(old - m), st.nref[r] = -m;
                     }
                     group_sync(g);
+                    if (i > 0) {  // the sums and the accumulator, once the last tile's product is in it
 #pragma unroll
-                    for (int r = 0; r < NRH; ++r) l[r] *= st.factor[g * NRH + r];
-                    if (i > 0) {  // the accumulator too, once the last tile's product is in it
+                        for (int r = 0; r < NRH; r += 4) {
+                            const float4 f = *reinterpret_cast<const float4*>(&st.factor[g0 + r]);
+                            l[r] *= f.x, l[r + 1] *= f.y, l[r + 2] *= f.z, l[r + 3] *= f.w;
+                        }
                         const uint32_t p = n_t - 1;
                         failed = failed || !mbar_wait(&st.p_empty[p & 1], (p >> 1) & 1);
                         tc::fence_after();
@@ -493,10 +527,12 @@ __global__ void __launch_bounds__(kvt::NT, 1)
 #pragma unroll
                             for (int r = 0; r < NRH; r += 8) {
                                 float o[8];
-                                const uint32_t at = tmem + lane_base + TM_O + hf * NR + g * NRH + r;
+                                const uint32_t at = tmem + lane_base + TM_O + hf * NR + g0 + r;
                                 tc::tmem_ld<8>(at, o);
-#pragma unroll
-                                for (int x = 0; x < 8; ++x) o[x] *= st.factor[g * NRH + r + x];
+                                const float4 f0 = *reinterpret_cast<const float4*>(&st.factor[g0 + r]);
+                                const float4 f1 = *reinterpret_cast<const float4*>(&st.factor[g0 + r + 4]);
+                                o[0] *= f0.x, o[1] *= f0.y, o[2] *= f0.z, o[3] *= f0.w;
+                                o[4] *= f1.x, o[5] *= f1.y, o[6] *= f1.z, o[7] *= f1.w;
                                 tc::tmem_st<8>(at, o);
                             }
                         tc::fence_before();
@@ -507,29 +543,31 @@ __global__ void __launch_bounds__(kvt::NT, 1)
                 unsigned char* dst = sP + buf * p_bytes<NR>() + g * (NRH / 8) * (KT * 16) + key * 16;
 #pragma unroll
                 for (int r = 0; r < NRH; r += 8) {
-                    const float4 m0 = *reinterpret_cast<const float4*>(&st.ref[g * NRH + r]);
-                    const float4 m1 = *reinterpret_cast<const float4*>(&st.ref[g * NRH + r + 4]);
-                    const float p0 = kv_ex2(s[r] - m0.x), p1 = kv_ex2(s[r + 1] - m0.y), p2 = kv_ex2(s[r + 2] - m0.z),
-                                p3 = kv_ex2(s[r + 3] - m0.w), p4 = kv_ex2(s[r + 4] - m1.x), p5 = kv_ex2(s[r + 5] - m1.y),
-                                p6 = kv_ex2(s[r + 6] - m1.z), p7 = kv_ex2(s[r + 7] - m1.w);
-                    l[r] += p0, l[r + 1] += p1, l[r + 2] += p2, l[r + 3] += p3;
-                    l[r + 4] += p4, l[r + 5] += p5, l[r + 6] += p6, l[r + 7] += p7;
-                    *reinterpret_cast<uint4*>(dst + (r / 8) * (KT * 16)) =
-                        make_uint4(H::pack(p0, p1), H::pack(p2, p3), H::pack(p4, p5), H::pack(p6, p7));
+                    uint32_t u[4];
+#pragma unroll
+                    for (int x = 0; x < 8; x += 4) {
+                        const float4 m = *reinterpret_cast<const float4*>(&st.nref[g0 + r + x]);
+                        const float2 y = fma2(make_float2(s[r + x], s[r + x + 1]), cc, make_float2(m.x, m.y));
+                        const float2 z = fma2(make_float2(s[r + x + 2], s[r + x + 3]), cc, make_float2(m.z, m.w));
+                        const float p0 = kv_ex2(y.x), p1 = kv_ex2(y.y), p2 = kv_ex2(z.x), p3 = kv_ex2(z.y);
+                        l[r + x] += p0, l[r + x + 1] += p1, l[r + x + 2] += p2, l[r + x + 3] += p3;
+                        u[x / 2] = H::pack(p0, p1), u[x / 2 + 1] = H::pack(p2, p3);
+                    }
+                    *reinterpret_cast<uint4*>(dst + (r / 8) * (KT * 16)) = make_uint4(u[0], u[1], u[2], u[3]);
                 }
                 if (live < KT) {
                     // Rows of V past the last key become zero (0 x NaN would reach the sums), and so do a
                     // node's values that are not finite: the epilogue adds them to the rows that attend it.
                     failed = failed || !mbar_wait(&st.v_ok, n_v & 1);
                     ++n_v;
-                    for (int x = g; x < boxes; x += 2) {
+                    for (int x = g; x < boxes; x += NG) {
                         int stage = st.v_stage + (x >> 1);
                         if (stage >= stages) stage -= stages;
                         uint4* row = reinterpret_cast<uint4*>(ring + stage * stage_bytes + (x & 1) * BOX_BYTES + key * 128);
 #pragma unroll
-                        for (int c = 0; c < 8; ++c) {
-                            if (key >= live) row[c] = make_uint4(0, 0, 0, 0);
-                            else if (tree && odd) row[c] = clear_odd<ST>(row[c]);
+                        for (int y = 0; y < 8; ++y) {
+                            if (key >= live) row[y ^ (lane & 7)] = make_uint4(0, 0, 0, 0);  // (order against bank conflicts)
+                            else if (tree && odd) row[y] = clear_odd<ST>(row[y]);
                         }
                     }
                 }
@@ -541,23 +579,19 @@ __global__ void __launch_bounds__(kvt::NT, 1)
             if (stop) break;
             // ---- row sums over the group's threads, then the outputs
             const float own = sum_rows<NRH>(l, lane);
-            if constexpr (NRH == 64) {
-                const float hi = sum_rows<NRH>(l + 32, lane);
-                st.warp_max[quad][g * NRH + lane] = own, st.warp_max[quad][g * NRH + 32 + lane] = hi;
-            } else if (lane < NRH) {
-                st.warp_max[quad][g * NRH + lane] = own;
-            }
+            if (lane < NRH) st.warp_max[quad][g0 + lane] = own;
             group_sync(g);
+            const bool whole = w.whole();
             float* part = a.part + ((int64_t)blockIdx.x * 2 + w.later) * part_floats;
             if (gt < NRH) {
-                const int r = g * NRH + gt;
+                const int r = g0 + gt;
                 const float sum = pages_bad ? 0.f : st.warp_max[0][r] + st.warp_max[1][r] + st.warp_max[2][r] + st.warp_max[3][r];
-                st.factor[r] = w.whole() ? (sum == 0.f ? 0.f : 1.f / sum) : 1.f;
+                st.factor[r] = pages_bad ? 0.f : whole ? (sum == 0.f ? 0.f : 1.f / sum) : 1.f;
                 if (st.row[r] >= 0) {
-                    if (!w.whole())
-                        part[NR * a.d + r] = st.ref[r], part[NR * a.d + NR + r] = sum;
+                    if (!whole)
+                        part[NR * a.d + r] = -st.nref[r], part[NR * a.d + NR + r] = sum;
                     else if (a.lse)
-                        a.lse[st.row[r]] = sum == 0.f ? -INFINITY : (st.ref[r] + log2f(sum)) * LN2;
+                        a.lse[st.row[r]] = sum == 0.f ? -INFINITY : (log2f(sum) - st.nref[r]) * LN2;
                 }
             }
             group_sync(g);
@@ -565,38 +599,40 @@ __global__ void __launch_bounds__(kvt::NT, 1)
             tc::fence_after();
             for (int hf = 0; hf < pairs; ++hf) {
                 const int e = hf * 128 + key;
+                float o[NRH];
+                __syncwarp();
+                tc::tmem_ld<NRH>(tmem + lane_base + TM_O + hf * NR + g0, o);
+                if (e < a.d) {
+                    if (odd) add_odd<ST, NRH>(a, w.s.nodes, w.b, w.h, e, &st.mask[0][g0], &st.mask[1][g0], o);
+                    if (whole) {
+                        ST* out = static_cast<ST*>(a.out) + e;
 #pragma unroll
-                for (int r = 0; r < NRH; r += 8) {
-                    const int r1 = g * NRH + r;
-                    float o[8];
-                    __syncwarp();
-                    tc::tmem_ld<8>(tmem + lane_base + TM_O + hf * NR + r1, o);
-                    if (e >= a.d) continue;
-                    if (odd) add_odd<ST>(a, w.s.nodes, w.b, w.h, e, &st.mask[0][r1], &st.mask[1][r1], o);
+                        for (int r = 0; r < NRH; ++r) {
+                            const int64_t row = st.row[g0 + r];
+                            const float f = st.factor[g0 + r];
+                            if (row >= 0) out[row * a.d] = H::round(f == 0.f ? 0.f : o[r] * f);
+                        }
+                    } else {
+                        float* x = part + (int64_t)g0 * a.d + e;
 #pragma unroll
-                    for (int x = 0; x < 8; ++x) {
-                        const int64_t row = st.row[r1 + x];
-                        if (row < 0) continue;
-                        const float f = st.factor[r1 + x];
-                        const float y = f == 0.f || pages_bad ? 0.f : o[x] * f;
-                        if (w.whole())
-                            store_elem(a.out, row * a.d + e, Store<ST>::code, y);
-                        else
-                            part[(r1 + x) * a.d + e] = y;
+                        for (int r = 0; r < NRH; ++r)
+                            if (g0 + r < rows) x[r * a.d] = st.factor[g0 + r] == 0.f ? 0.f : o[r];
                     }
                 }
             }
             tc::fence_before();
+            if (tid == 0 && w.last()) static_cast<KvBorder*>(a.border)[blockIdx.x] = kv_border(a, split, w);
             group_sync(g);  // the row tables are read
         } while (w.next());
         if (failed && lane == 0) set_error(a.dev_err, GDN_DEVERR_TIMEOUT);
     }
+    if (!busy && tid == 0) static_cast<KvBorder*>(a.border)[blockIdx.x].rows = 0;
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
     kv_empty_rows<NT>(a);
-    if (warp == 9)
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(tm_cols) : "memory");
+    if (warp == MMA_WARP)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(TM_COLS) : "memory");
 }
 
 }  // namespace gdn

@@ -31,16 +31,11 @@ __global__ void __launch_bounds__(kvg::NT) kv_weights_kernel(const KvArgs a, con
         const KvSeq s = kv_seq<false>(a, b);
         if (s.err && tid == 0) set_error(a.dev_err, s.err);
     }
-    kv_locate<false, KT, NT>(a, scan, [&](long long W) -> long long {
-        return W > 0 ? (blockIdx.x < W ? kv_start(W, (int)min(W, (long long)gridDim.x), blockIdx.x) : -1) : -1;
-    });
-    const long long W = scan.total;
-    const int parts = (int)min(W, (long long)gridDim.x);
-    if (blockIdx.x >= parts) return;
-    const long long w0 = kv_start(W, parts, blockIdx.x), w1 = kv_start(W, parts, blockIdx.x + 1);
+    const KvSplit split = kv_locate<false, KT, NT>(a, scan, gridDim.x, 1);
+    if (!split.busy(blockIdx.x)) return;
     int checked = -1;
     bool ok = true;
-    KvWalk<false, KT> w(a, w0, w1, scan.b, scan.before);
+    KvWalk<false, KT> w(a, split, scan);
     do {
         const KvSeq& s = w.s;
         const int b = w.b, h = w.h;
