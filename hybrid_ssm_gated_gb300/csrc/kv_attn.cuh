@@ -88,7 +88,7 @@ __global__ void __launch_bounds__(kvg::NT) kv_attn_kernel(const KvArgs a, const 
     const float c2 = a.scale * LOG2E;
 
     kv_grid_launch();
-    kv_empty_rows<NT>(a);
+    kv_empty_rows(a, nullptr, tid, NT);
     const KvSplit split = kv_locate<true, KT, NT>(a, scan, gridDim.x, LEAST);
     if (!split.busy(blockIdx.x)) {
         if (tid == 0) static_cast<KvBorder*>(a.border)[blockIdx.x].rows = 0;

