@@ -88,7 +88,7 @@ bool vec_rows(const void* p, int64_t s0, int64_t s1, int64_t s2, int d, int esz)
 // Workspace of either attention kernel: the caller's rows decide at the call which one runs.
 cudaError_t attention_workspace(gdn::KvArgs& a, int64_t& bytes) {
     cudaError_t e = gdn::kv_attn_workspace(a, bytes);
-    if (e != cudaSuccess || !gdn::kv_attn_tc_fits(a)) return e;
+    if (e != cudaSuccess || !gdn::kv_tc_fits(a)) return e;
     int64_t more = 0;
     e = gdn::kv_attn_tc_workspace(a, more);
     if (more > bytes) bytes = more;
@@ -147,7 +147,7 @@ int kv_tree_attention(const kv_cache* cache, int32_t B, int32_t T, int32_t Hq, c
     const int esz = gdn::dtype_size(cache->dtype);
     const bool vec = vec_pages(a.k, a.d, esz) && vec_pages(a.v, a.d, esz) && vec_rows(a.q, a.d, esz) &&
                      vec_rows(a.kn, a.d, esz) && vec_rows(a.vn, a.d, esz);
-    e = vec && gdn::kv_attn_tc_fits(a) ? gdn::launch_kv_attn_tc(a, static_cast<cudaStream_t>(stream)) : cudaErrorNotSupported;
+    e = vec && gdn::kv_tc_fits(a) ? gdn::launch_kv_attn_tc(a, static_cast<cudaStream_t>(stream)) : cudaErrorNotSupported;
     if (e == cudaErrorNotSupported) e = gdn::launch_kv_attn(a, vec, static_cast<cudaStream_t>(stream));
     return launched(e, fn);
 }
@@ -193,7 +193,10 @@ int kv_accumulate(const kv_cache* cache, int32_t B, int32_t T, int32_t P, int32_
     a.lse_in = lse, a.path = path, a.n_path = n_path, a.scale = scale, a.decay = decay;
     const int esz = gdn::dtype_size(cache->dtype);
     const bool vec = vec_pages(a.k, a.d, esz) && vec_rows(a.q, a.d, esz);
-    return launched(gdn::launch_kv_weights(a, vec, static_cast<cudaStream_t>(stream)), fn);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    cudaError_t e = vec && gdn::kv_tc_fits(a) ? gdn::launch_kv_weights_tc(a, s) : cudaErrorNotSupported;
+    if (e == cudaErrorNotSupported) e = gdn::launch_kv_weights(a, vec, s);
+    return launched(e, fn);
 }
 
 int64_t kv_evict_workspace(const kv_cache* cache, int32_t B, int32_t budget) {

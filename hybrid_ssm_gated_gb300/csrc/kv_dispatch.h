@@ -13,11 +13,12 @@ cudaError_t launch_kv_weights(KvArgs& a, bool vec, cudaStream_t stream);
 // Bytes of partials that launch_kv_attn may write.
 cudaError_t kv_attn_workspace(KvArgs& a, int64_t& bytes);
 
-// Attention on the tensor cores: whether the cache's type and sizes fit, the launch (cudaErrorNotSupported
+// Attention and accumulation on the tensor cores: whether the cache's type and sizes fit, the launches (cudaErrorNotSupported
 // where the rows' addresses have no tensor map: the caller takes the other kernel), and its partials.
-bool kv_attn_tc_fits(const KvArgs& a);
+bool kv_tc_fits(const KvArgs& a);
 cudaError_t launch_kv_attn_tc(KvArgs& a, cudaStream_t stream);
 cudaError_t kv_attn_tc_workspace(KvArgs& a, int64_t& bytes);
+cudaError_t launch_kv_weights_tc(const KvArgs& a, cudaStream_t stream);
 
 // Joins the partials of an attention kernel of `grid` CTAs, on the same stream.
 cudaError_t launch_kv_join(const KvArgs& a, int grid, cudaStream_t stream);

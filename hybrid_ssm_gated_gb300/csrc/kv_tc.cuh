@@ -233,6 +233,15 @@ __device__ __forceinline__ float2 add2(float2 x, float2 y) {
     return r;
 }
 
+__device__ __forceinline__ float2 mul2(float2 x, float2 y) {
+    float2 r;
+    asm("{\n\t.reg .b64 a, b, c;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmul.rn.f32x2 c, a, b;\n\t"
+        "mov.b64 {%0, %1}, c;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y));
+    return r;
+}
+
 // The largest of three (a NaN among them is dropped).
 __device__ __forceinline__ float max3(float x, float y, float z) {
     float r;
