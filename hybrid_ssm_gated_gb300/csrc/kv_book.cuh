@@ -8,58 +8,67 @@
 
 namespace gdn {
 
-// Copy one row of d elements (esz bytes each); 16 bytes a lane where both ends allow it.
-__device__ __forceinline__ void kv_copy_row(char* dst, const char* src, int bytes, bool vec, int lane, int lanes) {
-    if (vec) {
-        for (int i = lane * 16; i < bytes; i += lanes * 16)
-            *reinterpret_cast<uint4*>(dst + i) = *reinterpret_cast<const uint4*>(src + i);
-    } else {
-        for (int i = lane * 2; i < bytes; i += lanes * 2)
-            *reinterpret_cast<uint16_t*>(dst + i) = *reinterpret_cast<const uint16_t*>(src + i);
-    }
-}
-
-// One CTA a sequence: checks the whole path first, then copies, a warp a row. vec: every row of the
-// cache and of the activations can be copied 16 bytes at a time.
-constexpr int KV_COMMIT_NT = 256;
-__global__ void __launch_bounds__(KV_COMMIT_NT) kv_commit_kernel(const KvArgs a, const int vec) {
-    const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int slot = a.slots[b];
+// One CTA a sequence: the whole path is checked first, and its entries' places are left in shared memory;
+// then every thread copies 16-byte pieces (2-byte ones where the rows allow no more) that do not depend
+// on one another, four in flight (a warp a row, one after the other, took 9 us for six tokens of eight
+// heads; bound by latency, three loads deep).
+constexpr int KV_COMMIT_NT = 256, KV_COMMIT_AHEAD = 4;
+template <typename Piece>
+__global__ void __launch_bounds__(KV_COMMIT_NT) kv_commit_kernel(const __grid_constant__ KvArgs a) {
+    constexpr int NT = KV_COMMIT_NT;
+    __shared__ int s_node[KV_MAX_NODES], s_page[KV_MAX_NODES], s_place[KV_MAX_NODES];
+    const int b = blockIdx.x, tid = threadIdx.x;
+    const int slot = a.slots[b], n = a.n_path[b];
+    const int node0 = tid < a.P ? a.path[(int64_t)b * a.P + tid] : 0;  // (asked for before the slot is known)
     if (slot < 0) return;
     if (slot >= a.num_slots) {
         if (tid == 0) set_error(a.dev_err, GDN_DEVERR_SLOT);
         return;
     }
-    const int len = a.lengths[slot], n = a.n_path[b];
-    const int count = a.counts ? a.counts[slot] : 0;
-    const int32_t* table = a.page_table + (int64_t)slot * a.max_pages;
+    const int len = a.lengths[slot], count = a.counts ? a.counts[slot] : 0;
     int err = 0;
     if (n < 0 || n > a.P) err |= KV_DEVERR_NODES;
     if (len < 0 || (int64_t)len + (n > 0 ? n : 0) > (int64_t)a.max_pages * a.page_size) err |= KV_DEVERR_LENGTH;
-    if (!err)
-        for (int j = tid; j < n; j += KV_COMMIT_NT) {
-            if ((uint32_t)a.path[(int64_t)b * a.P + j] >= (uint32_t)a.T) err |= KV_DEVERR_NODES;
-            if ((uint32_t)table[(len + j) / a.page_size] >= (uint64_t)a.num_pages) err |= KV_DEVERR_PAGE;
-        }
+    if (!err && tid < n) {
+        const int e = len + tid, pg = e / a.page_size, page = a.page_table[(int64_t)slot * a.max_pages + pg];
+        if ((uint32_t)node0 >= (uint32_t)a.T) err |= KV_DEVERR_NODES;
+        if ((uint32_t)page >= (uint64_t)a.num_pages) err |= KV_DEVERR_PAGE;
+        s_node[tid] = node0, s_page[tid] = page, s_place[tid] = e - pg * a.page_size;
+    }
     if (err) set_error(a.dev_err, err);
     if (__syncthreads_or(err)) return;  // the lengths were read by every thread: they may change now
-    const int esz = dtype_size(a.dtype), bytes = a.d * esz;
-    const int rows = n * a.Hkv;
-    for (int i = warp; i < 2 * rows; i += KV_COMMIT_NT / 32) {
-        const bool val = i >= rows;
-        const int r = val ? i - rows : i, j = r / a.Hkv, h = r - j * a.Hkv;
-        const int e = len + j, pg = e / a.page_size, place = e - pg * a.page_size;
-        const KvPages& c = val ? a.v : a.k;
-        const KvRows& x = val ? a.vn : a.kn;
-        const int node = a.path[(int64_t)b * a.P + j];
-        const int64_t from = (int64_t)b * x.seq + (int64_t)node * x.node + (int64_t)h * x.head;
-        char* dst = static_cast<char*>(const_cast<void*>(c.p)) + kv_at(c, table[pg], h, place) * esz;
-        kv_copy_row(dst, static_cast<const char*>(x.p) + from * esz, bytes, vec, lane, 32);
-        if (!val && lane == 0 && a.weights) {
-            const int64_t w = ((int64_t)table[pg] * a.Hkv + h) * a.page_size + place;
+    const int esz = dtype_size(a.dtype), per = a.d * esz / (int)sizeof(Piece);
+    const int rows = n * a.Hkv, total = 2 * rows * per;
+    for (int i0 = tid; i0 < total; i0 += NT * KV_COMMIT_AHEAD) {
+        Piece x[KV_COMMIT_AHEAD];
+        Piece* to[KV_COMMIT_AHEAD];
+#pragma unroll
+        for (int y = 0; y < KV_COMMIT_AHEAD; ++y) {
+            const int i = i0 + y * NT;
+            to[y] = nullptr;
+            if (i < total) {
+                const int q = i / per, p = i - q * per;
+                const bool val = q >= rows;
+                const int r = val ? q - rows : q, j = r / a.Hkv, h = r - j * a.Hkv;
+                const KvPages& c = val ? a.v : a.k;
+                const KvRows& from = val ? a.vn : a.kn;
+                to[y] = reinterpret_cast<Piece*>(static_cast<char*>(const_cast<void*>(c.p)) +
+                                                 kv_at(c, s_page[j], h, s_place[j]) * esz) + p;
+                x[y] = reinterpret_cast<const Piece*>(static_cast<const char*>(from.p) +
+                                                      ((int64_t)b * from.seq + (int64_t)s_node[j] * from.node +
+                                                       (int64_t)h * from.head) * esz)[p];
+            }
+        }
+#pragma unroll
+        for (int y = 0; y < KV_COMMIT_AHEAD; ++y)
+            if (to[y]) *to[y] = x[y];
+    }
+    if (a.weights)
+        for (int i = tid; i < rows; i += NT) {
+            const int j = i / a.Hkv, h = i - j * a.Hkv;
+            const int64_t w = ((int64_t)s_page[j] * a.Hkv + h) * a.page_size + s_place[j];
             a.weights[w] = 0.f, a.stamps[w] = count + j;
         }
-    }
     if (tid == 0 && n > 0) {
         a.lengths[slot] = len + n;
         if (a.counts) a.counts[slot] = count + n;

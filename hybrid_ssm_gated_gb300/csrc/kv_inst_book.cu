@@ -6,7 +6,10 @@
 namespace gdn {
 
 cudaError_t launch_kv_commit(const KvArgs& a, bool vec, cudaStream_t stream) {
-    kv_commit_kernel<<<(unsigned)a.B, KV_COMMIT_NT, 0, stream>>>(a, vec);
+    if (vec)
+        kv_commit_kernel<uint4><<<(unsigned)a.B, KV_COMMIT_NT, 0, stream>>>(a);
+    else
+        kv_commit_kernel<uint16_t><<<(unsigned)a.B, KV_COMMIT_NT, 0, stream>>>(a);
     return cudaGetLastError();
 }
 

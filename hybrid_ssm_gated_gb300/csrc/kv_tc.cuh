@@ -546,8 +546,10 @@ __global__ void __launch_bounds__(kvt::threads(NR), 1)
                     if (gt < NRH) {
                         const int r = g0 + gt;
                         const float old = -st.nref[r];
-                        const float m = fmaxf(fmaxf(fmaxf(st.warp_max[0][r], st.warp_max[1][r]),
-                                                    fmaxf(st.warp_max[2][r], st.warp_max[3][r])), old);
+                        float m = fmaxf(fmaxf(st.warp_max[0][r], st.warp_max[1][r]),
+                                        fmaxf(st.warp_max[2][r], st.warp_max[3][r]));
+                        // an ulp up: the weights' exponents come from one fused rounding, the maximum from two
+                        m = fmaxf(fmaf(fabsf(m), 1.1920929e-7f, m), old);
                         st.factor[r] = kv_ex2(old - m), st.nref[r] = -m;
                     }
                     group_sync(g);
