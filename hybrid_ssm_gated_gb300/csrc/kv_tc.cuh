@@ -512,18 +512,23 @@ __global__ void __launch_bounds__(kvt::threads(NR), 1)
                         tc::tmem_st<8>(tm_s + r, x);
                     }
                 }
-                float s[NRH];
-                tc::tmem_ld<NRH>(tm_s, s);
+                // sixteen scores at a time: 32 beside the 32 sums do not fit the registers of 20 warps, and are
+                // read from tensor memory a second time below
+                constexpr int CH = NRH < 16 ? NRH : 16;
+                float s[CH];
                 float over = -INFINITY;  // the largest exponent against the references
-                if (!dead) {
 #pragma unroll
-                    for (int r = 0; r < NRH; r += 4) {
-                        const float4 m = *reinterpret_cast<const float4*>(&st.nref[g0 + r]);
+                for (int r0 = 0; r0 < NRH; r0 += CH) {
+                    tc::tmem_ld<CH>(tm_s + r0, s);
+#pragma unroll
+                    for (int r = 0; r < CH; r += 4) {
+                        const float4 m = *reinterpret_cast<const float4*>(&st.nref[g0 + r0 + r]);
                         const float2 x = fma2(make_float2(s[r], s[r + 1]), cc, make_float2(m.x, m.y));
                         const float2 y = fma2(make_float2(s[r + 2], s[r + 3]), cc, make_float2(m.z, m.w));
                         over = max3(max3(over, x.x, x.y), y.x, y.y);
                     }
                 }
+                if (dead) over = -INFINITY;
                 if (failed) st.gave_up[g] = 1;
                 if (group_any(g, failed || over > REF_SLACK)) {
                     if (st.gave_up[g]) {
@@ -577,32 +582,39 @@ __global__ void __launch_bounds__(kvt::threads(NR), 1)
                             }
                     }
                 }
-                tc::fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&st.s_empty[buf]);
                 // weights: FP32 sums, rounded once to the cache's type for the product with the values
                 const int pbuf = n_t & pb;
                 if (n_t >= (uint32_t)p_bufs) failed = failed || !mbar_wait(&st.p_empty[pbuf], ((n_t >> pb) - 1) & 1);
                 unsigned char* dst = sP + pbuf * p_bytes<NR>() + g * (NRH / 8) * (KT * 16) + key * 16;
-                if (!dead) {
 #pragma unroll
-                    for (int r = 0; r < NRH; r += 8) {
-                        uint32_t u[4];
-#pragma unroll
-                        for (int x = 0; x < 8; x += 4) {
-                            const float4 m = *reinterpret_cast<const float4*>(&st.nref[g0 + r + x]);
-                            float2 y = fma2(make_float2(s[r + x], s[r + x + 1]), cc, make_float2(m.x, m.y));
-                            float2 z = fma2(make_float2(s[r + x + 2], s[r + x + 3]), cc, make_float2(m.z, m.w));
-                            y = make_float2(kv_ex2(y.x), kv_ex2(y.y)), z = make_float2(kv_ex2(z.x), kv_ex2(z.y));
-                            l[(r + x) / 2] = add2(l[(r + x) / 2], y), l[(r + x) / 2 + 1] = add2(l[(r + x) / 2 + 1], z);
-                            u[x / 2] = H::pack(y.x, y.y), u[x / 2 + 1] = H::pack(z.x, z.y);
-                        }
-                        *reinterpret_cast<uint4*>(dst + (r / 8) * (KT * 16)) = make_uint4(u[0], u[1], u[2], u[3]);
+                for (int r0 = 0; r0 < NRH; r0 += CH) {
+                    if (NRH > CH) tc::tmem_ld<CH>(tm_s + r0, s);
+                    if (r0 + CH >= NRH) {  // the scores are read
+                        tc::fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&st.s_empty[buf]);
                     }
-                } else {
-#pragma unroll 1
-                    for (int r = 0; r < NRH; r += 8)
-                        *reinterpret_cast<uint4*>(dst + (r / 8) * (KT * 16)) = make_uint4(0, 0, 0, 0);
+                    if (!dead) {
+#pragma unroll
+                        for (int r = 0; r < CH; r += 8) {
+                            uint32_t u[4];
+#pragma unroll
+                            for (int x = 0; x < 8; x += 4) {
+                                const int i2 = (r0 + r + x) / 2;
+                                const float4 m = *reinterpret_cast<const float4*>(&st.nref[g0 + r0 + r + x]);
+                                float2 y = fma2(make_float2(s[r + x], s[r + x + 1]), cc, make_float2(m.x, m.y));
+                                float2 z = fma2(make_float2(s[r + x + 2], s[r + x + 3]), cc, make_float2(m.z, m.w));
+                                y = make_float2(kv_ex2(y.x), kv_ex2(y.y)), z = make_float2(kv_ex2(z.x), kv_ex2(z.y));
+                                l[i2] = add2(l[i2], y), l[i2 + 1] = add2(l[i2 + 1], z);
+                                u[x / 2] = H::pack(y.x, y.y), u[x / 2 + 1] = H::pack(z.x, z.y);
+                            }
+                            *reinterpret_cast<uint4*>(dst + ((r0 + r) / 8) * (KT * 16)) = make_uint4(u[0], u[1], u[2], u[3]);
+                        }
+                    } else {
+#pragma unroll
+                        for (int r = 0; r < CH; r += 8)
+                            *reinterpret_cast<uint4*>(dst + ((r0 + r) / 8) * (KT * 16)) = make_uint4(0, 0, 0, 0);
+                    }
                 }
                 if (live < KT) {
                     // Rows of V past the last key become zero (0 x NaN would reach the sums), and so do a
