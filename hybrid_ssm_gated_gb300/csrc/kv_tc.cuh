@@ -107,12 +107,29 @@ __device__ __forceinline__ uint32_t idesc(uint32_t type, bool a_mn, bool b_mn, i
            ((uint32_t)(N >> 3) << 17) | ((uint32_t)(KT >> 4) << 24);
 }
 
+// Issued by one thread of a converged warp (all of whose threads call it with the same operands, which
+// so stay in uniform registers: a lone thread needed 110 cycles a product).
 __device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t id, bool accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "{\n\t.reg .pred p, e;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
         "l"(a), "l"(b), "r"(id), "r"((uint32_t)accumulate)
         : "memory");
+}
+// The barrier's arrival once the products issued so far by the same thread are done (as mma).
+__device__ __forceinline__ void commit(uint64_t* bar) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_addr(bar))
+        : "memory");
+}
+// A value that every thread of the warp holds, as one the compiler knows to be so.
+template <typename T>
+__device__ __forceinline__ T uniform(T x) {
+    return __shfl_sync(FULL_MASK, x, 0);
+}
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
+    return __all_sync(FULL_MASK, mbar_wait(bar, parity));
 }
 
 __device__ __forceinline__ void tma_load(void* dst, const CUtensorMap* map, int x, int y, int z, int w, uint64_t* bar) {
@@ -358,76 +375,77 @@ __global__ void __launch_bounds__(kvt::threads(NR), 1)
         }
     } else if ((warp == S_WARP || warp == O_WARP) && busy) {
         // ------------------------------------------------------------ MMAs
-        if (lane == 0) {
-            const bool outs = warp == O_WARP;
-            KvWalk<true, KT> w(a, split, st.scan);
-            const uint32_t id = outs ? idesc(H::type, true, true, NR) : idesc(H::type, false, false, NR);
-            const uint32_t aQ = smem_addr(sQ), aP = smem_addr(sP), aR = smem_addr(ring);
-            const int first = outs ? k_stages : 0, end = outs ? stages : k_stages;
-            int stage = first;
-            uint32_t round = 0, n_t = 0, seg = 0;
-            bool ok = true;
-            do {
-                const int n = w.t1 - w.t0;
-                if (!outs) ok = mbar_wait(&st.q_full, seg & 1);
-                ++seg;
+        const bool outs = warp == O_WARP;
+        KvWalk<true, KT> w(a, split, st.scan);
+        const uint32_t id = outs ? idesc(H::type, true, true, NR) : idesc(H::type, false, false, NR);
+        const uint32_t aQ = smem_addr(sQ), aP = smem_addr(sP), aR = smem_addr(ring), tm = uniform(tmem);
+        const int first = outs ? k_stages : 0, end = outs ? stages : k_stages;
+        int stage = first;
+        uint32_t round = 0, n_t = 0, seg = 0;
+        bool ok = true;
+        do {
+            const int n = uniform(w.t1 - w.t0);
+            // the tile whose V has rows that the softmax threads clear: the cache's last one, if it is not
+            // full, and the nodes'
+            const int t0 = uniform(w.t0), short_t = uniform(w.s.len % KT ? w.nt - 2 : w.nt - 1), tree_t = uniform(w.nt - 1);
+            if (!outs) ok = warp_wait(&st.q_full, seg & 1);
+            ++seg;
 #pragma unroll 1
-                for (int i = 0; i < n && ok; ++i, ++n_t) {
-                    const int buf = n_t & (outs ? pb : 1), t = w.t0 + i;
-                    if (outs) {
-                        if (t == w.nt - 1 || w.s.len - t * KT < KT) {  // the softmax threads clear rows of V
-                            int s2 = stage;
-                            uint32_t r2 = round;
+            for (int i = 0; i < n && ok; ++i, ++n_t) {
+                const int buf = n_t & (outs ? pb : 1), t = t0 + i;
+                if (outs) {
+                    if (t == tree_t || t == short_t) {
+                        int s2 = stage;
+                        uint32_t r2 = round;
 #pragma unroll 1
-                            for (int p = 0; p < pairs && ok; ++p) {
-                                ok = mbar_wait(&st.full[s2], r2 & 1);
-                                if (++s2 == end) s2 = first, ++r2;
-                            }
-                            st.v_stage = stage;
-                            if (ok) mbar_arrive(&st.v_ok);
+                        for (int p = 0; p < pairs && ok; ++p) {
+                            ok = warp_wait(&st.full[s2], r2 & 1);
+                            if (++s2 == end) s2 = first, ++r2;
                         }
-                        ok = ok && mbar_wait(&st.p_full[buf], (n_t >> pb) & 1);
-                    } else if (n_t >= 2) {
-                        ok = mbar_wait(&st.s_empty[buf], ((n_t >> 1) - 1) & 1);
+                        if (ok && lane == 0) st.v_stage = stage, mbar_arrive(&st.v_ok);
+                        __syncwarp();
                     }
-#pragma unroll 1
-                    for (int p = 0; p < pairs && ok; ++p) {
-                        ok = mbar_wait(&st.full[stage], round & 1);
-                        if (!ok) break;
-                        tc::fence_after();
-                        const uint32_t in = aR + stage * stage_bytes;
-                        const int nb = min(2, boxes - 2 * p);
-                        if (outs) {
-                            // A: 128 elements of d (the second 64 in the stage's second box; where there is
-                            // none, the first again: its lanes are not read)
-                            const uint64_t da = desc(in, nb > 1 ? BOX_BYTES : 0, 1024, SW128);
-                            const uint64_t db = desc(aP + buf * p_bytes<NR>(), 128, KT * 16, SW_NONE);
-#pragma unroll
-                            for (int k = 0; k < KT / 16; ++k)
-                                mma(tmem + TM_O + p * NR, da + k * (2048 >> 4), db + k * (256 >> 4), id, i + k > 0);
-                        } else {
-                            const uint64_t da = desc(in, 16, 1024, SW128), db = desc(aQ + 2 * p * NR * 128, 16, 1024, SW128);
-#pragma unroll
-                            for (int k = 0; k < BOX / 16; ++k)  // (past the end of d both operands are zero)
-                                mma(tmem + TM_S + buf * NR, da + k * (32 >> 4), db + k * (32 >> 4), id, p + k > 0);
-                            if (nb > 1) {
-#pragma unroll
-                                for (int k = 0; k < BOX / 16; ++k)
-                                    mma(tmem + TM_S + buf * NR, da + (BOX_BYTES >> 4) + k * (32 >> 4),
-                                        db + (NR * 128 >> 4) + k * (32 >> 4), id, true);
-                            }
-                        }
-                        tc::commit(&st.empty[stage]);
-                        if (++stage == end) stage = first, ++round;
-                    }
-                    if (ok) tc::commit(outs ? &st.p_empty[buf] : &st.s_full[buf]);
+                    ok = ok && warp_wait(&st.p_full[buf], (n_t >> pb) & 1);
+                } else if (n_t >= 2) {
+                    ok = warp_wait(&st.s_empty[buf], ((n_t >> 1) - 1) & 1);
                 }
-            } while (ok && w.next());
-            if (!ok) {
-                set_error(a.dev_err, GDN_DEVERR_TIMEOUT);
-                tc::commit(&st.drain[outs]);  // MMAs in flight end before tensor memory is freed
-                mbar_wait(&st.drain[outs], 0);
+#pragma unroll 1
+                for (int p = 0; p < pairs && ok; ++p) {
+                    ok = warp_wait(&st.full[stage], round & 1);
+                    if (!ok) break;
+                    tc::fence_after();
+                    const uint32_t in = aR + stage * stage_bytes;
+                    const int nb = min(2, boxes - 2 * p);
+                    if (outs) {
+                        // A: 128 elements of d (the second 64 in the stage's second box; where there is
+                        // none, the first again: its lanes are not read)
+                        const uint64_t da = desc(in, nb > 1 ? BOX_BYTES : 0, 1024, SW128);
+                        const uint64_t db = desc(aP + buf * p_bytes<NR>(), 128, KT * 16, SW_NONE);
+#pragma unroll
+                        for (int k = 0; k < KT / 16; ++k)
+                            mma(tm + TM_O + p * NR, da + k * (2048 >> 4), db + k * (256 >> 4), id, i + k > 0);
+                    } else {
+                        const uint64_t da = desc(in, 16, 1024, SW128), db = desc(aQ + 2 * p * NR * 128, 16, 1024, SW128);
+#pragma unroll
+                        for (int k = 0; k < BOX / 16; ++k)  // (past the end of d both operands are zero)
+                            mma(tm + TM_S + buf * NR, da + k * (32 >> 4), db + k * (32 >> 4), id, p + k > 0);
+                        if (nb > 1) {
+#pragma unroll
+                            for (int k = 0; k < BOX / 16; ++k)
+                                mma(tm + TM_S + buf * NR, da + (BOX_BYTES >> 4) + k * (32 >> 4),
+                                    db + (NR * 128 >> 4) + k * (32 >> 4), id, true);
+                        }
+                    }
+                    commit(&st.empty[stage]);
+                    if (++stage == end) stage = first, ++round;
+                }
+                if (ok) commit(outs ? &st.p_empty[buf] : &st.s_full[buf]);
             }
+        } while (ok && w.next());
+        if (!ok) {
+            if (lane == 0) set_error(a.dev_err, GDN_DEVERR_TIMEOUT);
+            commit(&st.drain[outs]);  // MMAs in flight end before tensor memory is freed
+            mbar_wait(&st.drain[outs], 0);
         }
         __syncwarp();
     } else if (warp < SM_WARPS && busy) {
@@ -584,8 +602,8 @@ __global__ void __launch_bounds__(kvt::threads(NR), 1)
                 }
                 // weights: FP32 sums, rounded once to the cache's type for the product with the values
                 const int pbuf = n_t & pb;
-                if (n_t >= (uint32_t)p_bufs) failed = failed || !mbar_wait(&st.p_empty[pbuf], ((n_t >> pb) - 1) & 1);
                 unsigned char* dst = sP + pbuf * p_bytes<NR>() + g * (NRH / 8) * (KT * 16) + key * 16;
+                uint32_t u[NRH / 2];
 #pragma unroll
                 for (int r0 = 0; r0 < NRH; r0 += CH) {
                     if (NRH > CH) tc::tmem_ld<CH>(tm_s + r0, s);
@@ -597,7 +615,6 @@ __global__ void __launch_bounds__(kvt::threads(NR), 1)
                     if (!dead) {
 #pragma unroll
                         for (int r = 0; r < CH; r += 8) {
-                            uint32_t u[4];
 #pragma unroll
                             for (int x = 0; x < 8; x += 4) {
                                 const int i2 = (r0 + r + x) / 2;
@@ -606,16 +623,20 @@ __global__ void __launch_bounds__(kvt::threads(NR), 1)
                                 float2 z = fma2(make_float2(s[r + x + 2], s[r + x + 3]), cc, make_float2(m.z, m.w));
                                 y = make_float2(kv_ex2(y.x), kv_ex2(y.y)), z = make_float2(kv_ex2(z.x), kv_ex2(z.y));
                                 l[i2] = add2(l[i2], y), l[i2 + 1] = add2(l[i2 + 1], z);
-                                u[x / 2] = H::pack(y.x, y.y), u[x / 2 + 1] = H::pack(z.x, z.y);
+                                u[i2] = H::pack(y.x, y.y), u[i2 + 1] = H::pack(z.x, z.y);
                             }
-                            *reinterpret_cast<uint4*>(dst + ((r0 + r) / 8) * (KT * 16)) = make_uint4(u[0], u[1], u[2], u[3]);
                         }
                     } else {
 #pragma unroll
-                        for (int r = 0; r < CH; r += 8)
-                            *reinterpret_cast<uint4*>(dst + ((r0 + r) / 8) * (KT * 16)) = make_uint4(0, 0, 0, 0);
+                        for (int r = 0; r < CH / 2; ++r) u[r0 / 2 + r] = 0;
                     }
                 }
+                // the buffer is free once the product of the tile that used it is done: with one buffer that
+                // product runs beside the exponentials above
+                if (n_t >= (uint32_t)p_bufs) failed = failed || !mbar_wait(&st.p_empty[pbuf], ((n_t >> pb) - 1) & 1);
+#pragma unroll
+                for (int r = 0; r < NRH / 2; r += 4)
+                    *reinterpret_cast<uint4*>(dst + (r / 4) * (KT * 16)) = make_uint4(u[r], u[r + 1], u[r + 2], u[r + 3]);
                 if (live < KT) {
                     // Rows of V past the last key become zero (0 x NaN would reach the sums), and so do a
                     // node's values that are not finite: the epilogue adds them to the rows that attend it.

@@ -130,52 +130,50 @@ __global__ void __launch_bounds__(kvw::NT, 1)
         }
     } else if (warp == S_WARP && busy) {
         // ------------------------------------------------------------ MMAs
-        if (lane == 0) {
-            KvWalk<false, KT> w(a, split, st.scan);
-            const uint32_t id = kvt::idesc(H::type, false, false, NR);
-            const uint32_t aQ = smem_addr(sQ), aR = smem_addr(ring);
-            int stage = 0;
-            uint32_t round = 0, n_t = 0, seg = 0;
-            bool ok = true;
-            do {
-                const int blocks = (w.s.nodes * a.G + NR - 1) / NR;
+        KvWalk<false, KT> w(a, split, st.scan);
+        const uint32_t id = kvt::idesc(H::type, false, false, NR);
+        const uint32_t aQ = smem_addr(sQ), aR = smem_addr(ring), tm = kvt::uniform(tmem);
+        int stage = 0;
+        uint32_t round = 0, n_t = 0, seg = 0;
+        bool ok = true;
+        do {
+            const int blocks = kvt::uniform((w.s.nodes * a.G + NR - 1) / NR), n = kvt::uniform(w.t1 - w.t0);
 #pragma unroll 1
-                for (int rb = 0; rb < blocks && ok; ++rb) {
-                    ok = mbar_wait(&st.q_full, seg & 1);
-                    ++seg;
+            for (int rb = 0; rb < blocks && ok; ++rb) {
+                ok = kvt::warp_wait(&st.q_full, seg & 1);
+                ++seg;
 #pragma unroll 1
-                    for (int t = w.t0; t < w.t1 && ok; ++t, ++n_t) {
-                        const int buf = n_t & 1;
-                        if (n_t >= 2) ok = mbar_wait(&st.s_empty[buf], ((n_t >> 1) - 1) & 1);
+                for (int i = 0; i < n && ok; ++i, ++n_t) {
+                    const int buf = n_t & 1;
+                    if (n_t >= 2) ok = kvt::warp_wait(&st.s_empty[buf], ((n_t >> 1) - 1) & 1);
 #pragma unroll 1
-                        for (int p = 0; p < pairs && ok; ++p) {
-                            ok = mbar_wait(&st.full[stage], round & 1);
-                            if (!ok) break;
-                            tc::fence_after();
-                            const uint64_t da = desc(aR + stage * stage_bytes, 16, 1024, kvt::SW128),
-                                           db = desc(aQ + 2 * p * NR * 128, 16, 1024, kvt::SW128);
+                    for (int p = 0; p < pairs && ok; ++p) {
+                        ok = kvt::warp_wait(&st.full[stage], round & 1);
+                        if (!ok) break;
+                        tc::fence_after();
+                        const uint64_t da = desc(aR + stage * stage_bytes, 16, 1024, kvt::SW128),
+                                       db = desc(aQ + 2 * p * NR * 128, 16, 1024, kvt::SW128);
+#pragma unroll
+                        for (int k = 0; k < BOX / 16; ++k)
+                            kvt::mma(tm + buf * NR, da + k * (32 >> 4), db + k * (32 >> 4), id, p + k > 0);
+                        if (boxes - 2 * p > 1) {
 #pragma unroll
                             for (int k = 0; k < BOX / 16; ++k)
-                                kvt::mma(tmem + buf * NR, da + k * (32 >> 4), db + k * (32 >> 4), id, p + k > 0);
-                            if (boxes - 2 * p > 1) {
-#pragma unroll
-                                for (int k = 0; k < BOX / 16; ++k)
-                                    kvt::mma(tmem + buf * NR, da + (BOX_BYTES >> 4) + k * (32 >> 4),
-                                             db + (NR * 128 >> 4) + k * (32 >> 4), id, true);
-                            }
-                            tc::commit(&st.empty[stage]);
-                            if (++stage == stages) stage = 0, ++round;
+                                kvt::mma(tm + buf * NR, da + (BOX_BYTES >> 4) + k * (32 >> 4),
+                                         db + (NR * 128 >> 4) + k * (32 >> 4), id, true);
                         }
-                        if (ok) tc::commit(&st.s_full[buf]);
+                        kvt::commit(&st.empty[stage]);
+                        if (++stage == stages) stage = 0, ++round;
                     }
-                    if (ok) tc::commit(&st.q_empty);  // the queries are read
+                    if (ok) kvt::commit(&st.s_full[buf]);
                 }
-            } while (ok && w.next());
-            if (!ok) {
-                set_error(a.dev_err, GDN_DEVERR_TIMEOUT);
-                tc::commit(&st.drain);  // MMAs in flight end before tensor memory is freed
-                mbar_wait(&st.drain, 0);
+                if (ok) kvt::commit(&st.q_empty);  // the queries are read
             }
+        } while (ok && w.next());
+        if (!ok) {
+            if (lane == 0) set_error(a.dev_err, GDN_DEVERR_TIMEOUT);
+            kvt::commit(&st.drain);  // MMAs in flight end before tensor memory is freed
+            mbar_wait(&st.drain, 0);
         }
         __syncwarp();
     } else if (warp < SM_WARPS && busy) {
