@@ -174,18 +174,6 @@ struct Half16<__half> {
     __device__ static __forceinline__ __half round(float x) { return __float2half_rn(x); }
 };
 
-// Row sums of N (up to 32) rows over a warp's threads: lane r holds row r's.
-template <int N>
-__device__ __forceinline__ float sum_rows(const float2* l, int lane) {
-    float x[N];
-#pragma unroll
-    for (int r = 0; r < N; ++r) x[r] = r & 1 ? l[r / 2].y : l[r / 2].x;
-    float y = reduce_scatter<N>(x, lane & (N - 1));
-#pragma unroll
-    for (int o = N; o < 32; o <<= 1) y += __shfl_xor_sync(FULL_MASK, y, o);
-    return y;
-}
-
 // Eight 16-bit values with those that are not finite replaced by zero.
 template <typename ST>
 __device__ __forceinline__ uint4 clear_odd(uint4 x) {
@@ -231,32 +219,45 @@ __device__ __noinline__ void add_odd(const KvArgs& a, int nodes, int b, int h, i
     }
 }
 
-// x * c + y on two values at a time
-__device__ __forceinline__ float2 fma2(float2 x, float2 c, float2 y) {
+// Two floats in one 64-bit register, for the packed instructions; the register is the variable, so that
+// operands that serve many of them are put together once.
+using Two = unsigned long long;
+__device__ __forceinline__ Two two(float x, float y) {
+    Two r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ float2 parts(Two x) {
     float2 r;
-    asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
-        "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
-        : "=f"(r.x), "=f"(r.y)
-        : "f"(x.x), "f"(x.y), "f"(c.x), "f"(c.y), "f"(y.x), "f"(y.y));
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+    return r;
+}
+__device__ __forceinline__ Two fma2(Two x, Two c, Two y) {
+    Two r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(x), "l"(c), "l"(y));
+    return r;
+}
+__device__ __forceinline__ Two add2(Two x, Two y) {
+    Two r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+    return r;
+}
+__device__ __forceinline__ Two mul2(Two x, Two y) {
+    Two r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
     return r;
 }
 
-__device__ __forceinline__ float2 add2(float2 x, float2 y) {
-    float2 r;
-    asm("{\n\t.reg .b64 a, b, c;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tadd.rn.f32x2 c, a, b;\n\t"
-        "mov.b64 {%0, %1}, c;\n\t}"
-        : "=f"(r.x), "=f"(r.y)
-        : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y));
-    return r;
-}
-
-__device__ __forceinline__ float2 mul2(float2 x, float2 y) {
-    float2 r;
-    asm("{\n\t.reg .b64 a, b, c;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmul.rn.f32x2 c, a, b;\n\t"
-        "mov.b64 {%0, %1}, c;\n\t}"
-        : "=f"(r.x), "=f"(r.y)
-        : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y));
-    return r;
+// Row sums of N (up to 32) rows over a warp's threads: lane r holds row r's.
+template <int N>
+__device__ __forceinline__ float sum_rows(const Two* l, int lane) {
+    float x[N];
+#pragma unroll
+    for (int r = 0; r < N; r += 2) x[r] = parts(l[r / 2]).x, x[r + 1] = parts(l[r / 2]).y;
+    float y = reduce_scatter<N>(x, lane & (N - 1));
+#pragma unroll
+    for (int o = N; o < 32; o <<= 1) y += __shfl_xor_sync(FULL_MASK, y, o);
+    return y;
 }
 
 // The largest of three (a NaN among them is dropped).
@@ -454,13 +455,13 @@ __global__ void __launch_bounds__(kvt::threads(NR), 1)
         const uint32_t lane_base = (uint32_t)(quad * 32) << 16;
         // (a scale of zero as the smallest normal number: -inf times it stays -inf)
         const float c2 = a.scale == 0.f ? 1.1754944e-38f : a.scale * LOG2E;
-        const float2 cc = make_float2(c2, c2);
+        const Two cc = two(c2, c2);
         const int64_t part_floats = kv_part_floats(NR, a.d);
         KvWalk<true, KT> w(a, split, st.scan);
         uint32_t n_t = 0, n_v = 0;  // tiles so far, v_ok rounds so far
         int checked = -1;
         bool pages_bad = false, failed = false, stop = false;  // stop: the whole group gives up
-        float2 l[NRH / 2];  // this key's share of the rows' sums
+        Two l[NRH / 2];  // this key's share of the rows' sums
         do {
             const int rows = min(NR, w.s.nodes * a.G - w.rb * NR), r_first = w.rb * NR, n = w.t1 - w.t0;
             // ---- row tables and queries of the group's rows
@@ -504,7 +505,7 @@ __global__ void __launch_bounds__(kvt::threads(NR), 1)
             }
             bool odd = false;  // a node's value is not finite
 #pragma unroll
-            for (int r = 0; r < NRH / 2; ++r) l[r] = make_float2(0.f, 0.f);
+            for (int r = 0; r < NRH / 2; ++r) l[r] = 0;
 
             for (int i = 0; i < n; ++i, ++n_t) {
                 const int t = w.t0 + i, buf = n_t & 1;
@@ -540,9 +541,9 @@ __global__ void __launch_bounds__(kvt::threads(NR), 1)
                     tc::tmem_ld<CH>(tm_s + r0, s);
 #pragma unroll
                     for (int r = 0; r < CH; r += 4) {
-                        const float4 m = *reinterpret_cast<const float4*>(&st.nref[g0 + r0 + r]);
-                        const float2 x = fma2(make_float2(s[r], s[r + 1]), cc, make_float2(m.x, m.y));
-                        const float2 y = fma2(make_float2(s[r + 2], s[r + 3]), cc, make_float2(m.z, m.w));
+                        const ulonglong2 m = *reinterpret_cast<const ulonglong2*>(&st.nref[g0 + r0 + r]);
+                        const float2 x = parts(fma2(two(s[r], s[r + 1]), cc, m.x));
+                        const float2 y = parts(fma2(two(s[r + 2], s[r + 3]), cc, m.y));
                         over = max3(max3(over, x.x, x.y), y.x, y.y);
                     }
                 }
@@ -579,8 +580,7 @@ __global__ void __launch_bounds__(kvt::threads(NR), 1)
                     if (i > 0) {  // the sums and the accumulator, once the last tile's product is in it
 #pragma unroll
                         for (int r = 0; r < NRH; r += 2) {
-                            const float2 f = *reinterpret_cast<const float2*>(&st.factor[g0 + r]);
-                            l[r / 2].x *= f.x, l[r / 2].y *= f.y;
+                            l[r / 2] = mul2(l[r / 2], *reinterpret_cast<const Two*>(&st.factor[g0 + r]));
                         }
                         const uint32_t p = n_t - 1;
                         failed = failed || !mbar_wait(&st.p_empty[p & pb], (p >> pb) & 1);
@@ -618,11 +618,11 @@ __global__ void __launch_bounds__(kvt::threads(NR), 1)
 #pragma unroll
                             for (int x = 0; x < 8; x += 4) {
                                 const int i2 = (r0 + r + x) / 2;
-                                const float4 m = *reinterpret_cast<const float4*>(&st.nref[g0 + r0 + r + x]);
-                                float2 y = fma2(make_float2(s[r + x], s[r + x + 1]), cc, make_float2(m.x, m.y));
-                                float2 z = fma2(make_float2(s[r + x + 2], s[r + x + 3]), cc, make_float2(m.z, m.w));
+                                const ulonglong2 m = *reinterpret_cast<const ulonglong2*>(&st.nref[g0 + r0 + r + x]);
+                                float2 y = parts(fma2(two(s[r + x], s[r + x + 1]), cc, m.x));
+                                float2 z = parts(fma2(two(s[r + x + 2], s[r + x + 3]), cc, m.y));
                                 y = make_float2(kv_ex2(y.x), kv_ex2(y.y)), z = make_float2(kv_ex2(z.x), kv_ex2(z.y));
-                                l[i2] = add2(l[i2], y), l[i2 + 1] = add2(l[i2 + 1], z);
+                                l[i2] = add2(l[i2], two(y.x, y.y)), l[i2 + 1] = add2(l[i2 + 1], two(z.x, z.y));
                                 u[i2] = H::pack(y.x, y.y), u[i2 + 1] = H::pack(z.x, z.y);
                             }
                         }

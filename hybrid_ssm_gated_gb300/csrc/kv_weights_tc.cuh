@@ -180,7 +180,7 @@ __global__ void __launch_bounds__(kvw::NT, 1)
         // ------------------------------------------------------------ weights
         const int g = warp >> 2, quad = warp & 3, key = quad * 32 + lane, wt = tid & 255;
         const uint32_t tm_s = tmem + ((uint32_t)(quad * 32) << 16) + g * NR;
-        const float2 scale = make_float2(a.scale, a.scale), log2e = make_float2(LOG2E, LOG2E);
+        const kvt::Two scale = kvt::two(a.scale, a.scale), log2e = kvt::two(LOG2E, LOG2E);
         KvWalk<false, KT> w(a, split, st.scan);
         uint32_t n_t = 0, seg = 0;
         int checked = -1;
@@ -249,19 +249,18 @@ __global__ void __launch_bounds__(kvw::NT, 1)
                     const int unseen = max(0, e - (w.s.len - w.s.nodes)) * a.G - rb * NR;
                     failed = failed || !mbar_wait(&st.s_full[g], (n_t >> 1) & 1);
                     tc::fence_after();
-                    float2 sum = make_float2(0.f, 0.f);
+                    kvt::Two sum = 0;
 #pragma unroll 1
                     for (int r = 0; r < NR; r += 16) {
                         float s[16];
                         tc::tmem_ld<16>(tm_s + r, s);
 #pragma unroll
                         for (int y = 0; y < 16; y += 4) {
-                            const float4 m = *reinterpret_cast<const float4*>(&st.nlse[r + y]);
+                            const ulonglong2 m = *reinterpret_cast<const ulonglong2*>(&st.nlse[r + y]);
                             // the exponent is formed before it is scaled to base 2: a weight near one keeps a
                             // small one
-                            float2 u = kvt::fma2(make_float2(s[y], s[y + 1]), scale, make_float2(m.x, m.y));
-                            float2 v = kvt::fma2(make_float2(s[y + 2], s[y + 3]), scale, make_float2(m.z, m.w));
-                            u = kvt::mul2(u, log2e), v = kvt::mul2(v, log2e);
+                            float2 u = kvt::parts(kvt::mul2(kvt::fma2(kvt::two(s[y], s[y + 1]), scale, m.x), log2e));
+                            float2 v = kvt::parts(kvt::mul2(kvt::fma2(kvt::two(s[y + 2], s[y + 3]), scale, m.y), log2e));
                             u = make_float2(kv_ex2(u.x), kv_ex2(u.y)), v = make_float2(kv_ex2(v.x), kv_ex2(v.y));
                             if (unseen > 0) {
                                 if (r + y < unseen) u.x = 0.f;
@@ -269,13 +268,13 @@ __global__ void __launch_bounds__(kvw::NT, 1)
                                 if (r + y + 2 < unseen) v.x = 0.f;
                                 if (r + y + 3 < unseen) v.y = 0.f;
                             }
-                            sum = kvt::add2(sum, kvt::add2(u, v));
+                            sum = kvt::add2(sum, kvt::add2(kvt::two(u.x, u.y), kvt::two(v.x, v.y)));
                         }
                     }
                     tc::fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&st.s_empty[g]);
-                    if (live && !failed) *x = fmaf(old, rb == 0 ? a.decay : 1.f, sum.x + sum.y);
+                    if (live && !failed) *x = fmaf(old, rb == 0 ? a.decay : 1.f, kvt::parts(sum).x + kvt::parts(sum).y);
                 }
             }
         } while (w.next());
