@@ -90,13 +90,14 @@ __global__ void __launch_bounds__(kvg::NT) kv_attn_kernel(const KvArgs a, const 
     kv_grid_launch();
     kv_empty_rows(a, nullptr, tid, NT);
     const KvSplit split = kv_locate<true, KT, NT>(a, scan, gridDim.x, LEAST);
-    if (!split.busy(blockIdx.x)) {
+    bool some;
+    KvWalk<true, KT> w(a, split, scan, some);
+    if (!some) {
         if (tid == 0) static_cast<KvBorder*>(a.border)[blockIdx.x].rows = 0;
         return;
     }
     int checked = -1;
     bool pages_ok = true;
-    KvWalk<true, KT> w(a, split, scan);
     do {
         const KvSeq& s = w.s;
         const int b = w.b, h = w.h, nt = w.nt, r0 = w.rb * RB;

@@ -3,13 +3,16 @@
 // persistent grid.
 //
 // Division. A sequence of a call is a row of units (key head, block of query
-// rows), each a run of key tiles; all units of all sequences in order make one
-// line of W tiles, and CTA c of G takes tiles [W c / G, W (c + 1) / G). So
-// every CTA streams the same number of tiles whatever the lengths, with no
-// host knowledge of them; a unit that spans several CTAs leaves one partial
-// result (unnormalised output, running maximum and sum) a CTA, joined
+// rows), each a run of key tiles behind a few cost tiles that stand for what a
+// unit costs beyond its tiles (start, sums, outputs); all units of all
+// sequences in order make one line of W, and CTA c of G takes [W c / G,
+// W (c + 1) / G) of it. So every CTA has the same work whatever the lengths,
+// with no host knowledge of them; a unit that spans several CTAs leaves one
+// partial result (unnormalised output, maximum and sum) a CTA, joined
 // afterwards by kv_join_kernel. A CTA holds at most two partials: that of the
-// unit it starts in and that of the unit it ends in.
+// unit it starts in and that of the unit it ends in. (Without the cost tiles
+// the CTAs that met five units of 16-node trees took 81 us, those that met two
+// 58 us.)
 #pragma once
 
 #include "../../include/kv.h"
@@ -102,18 +105,24 @@ template <bool ATTN>
 __device__ __forceinline__ int kv_row_blocks(const KvArgs& a, const KvSeq& s) {
     return ATTN ? (s.nodes * a.G + a.row_block - 1) / a.row_block : 1;
 }
+// Cost tiles of a unit, by kernel (128-key tiles: the tensor-core kernels).
 template <bool ATTN, int KT>
-__device__ __forceinline__ long long kv_seq_tiles(const KvArgs& a, const KvSeq& s) {
-    return (long long)kv_tiles<ATTN, KT>(s) * kv_row_blocks<ATTN>(a, s) * a.Hkv;
+__host__ __device__ constexpr int kv_extra() {
+    return KT == 128 ? (ATTN ? 2 : 1) : 0;
+}
+// The sequence's share of the line.
+template <bool ATTN, int KT>
+__device__ __forceinline__ long long kv_seq_cost(const KvArgs& a, const KvSeq& s) {
+    const int nt = kv_tiles<ATTN, KT>(s);
+    return nt ? (long long)(nt + kv_extra<ATTN, KT>()) * kv_row_blocks<ATTN>(a, s) * a.Hkv : 0;
 }
 
 __device__ __forceinline__ long long kv_div(long long a, long long b) {  // a, b >= 0; mostly both fit 32 bits
     return ((a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
 }
 
-// The line of W tiles cut into ranges of W / parts tiles, the first W % parts of them one longer. No
-// CTA gets less than `least` tiles, so that small calls are not cut into partials that cost more to
-// join than they save.
+// The line cut into ranges of W / parts, the first W % parts of them one longer. No CTA gets less than
+// `least`, so that small calls are not cut into partials that cost more to join than they save.
 struct KvSplit {
     long long W, q;
     int parts, r;
@@ -135,7 +144,7 @@ template <int NT>
 struct KvScan {
     KvSeq seq[NT];  // the batch's sequences, where there are at most NT
     long long warp_sum[NT / 32];
-    long long before;  // tiles of the sequences before the found one
+    long long before;  // where the found sequence's share of the line begins
     int b;
 };
 
@@ -150,7 +159,7 @@ __device__ __forceinline__ KvSplit kv_locate(const KvArgs& a, KvScan<NT>& sc, in
     for (int b = b0; b < b1; ++b) {
         const KvSeq s = kv_seq<ATTN>(a, b);
         if (run == 1) sc.seq[b] = s;
-        sum += kv_seq_tiles<ATTN, KT>(a, s);
+        sum += kv_seq_cost<ATTN, KT>(a, s);
     }
     long long inc = sum;
     if (a.B > 1) {
@@ -175,7 +184,7 @@ __device__ __forceinline__ KvSplit kv_locate(const KvArgs& a, KvScan<NT>& sc, in
         if (want >= before && want < before + sum) {
             int b = b0;
             for (; run > 1 && b < b1; ++b) {
-                const long long n = kv_seq_tiles<ATTN, KT>(a, kv_seq<ATTN>(a, b));
+                const long long n = kv_seq_cost<ATTN, KT>(a, kv_seq<ATTN>(a, b));
                 if (want < before + n) break;
                 before += n;
             }
@@ -190,23 +199,31 @@ __device__ __forceinline__ KvSplit kv_locate(const KvArgs& a, KvScan<NT>& sc, in
 // row block rb of sequence b) within the CTA's range. Every warp role of a kernel walks by itself.
 template <bool ATTN, int KT>
 struct KvWalk {
+    static constexpr int X = kv_extra<ATTN, KT>();
     const KvArgs& a;
-    const KvSeq* seq;   // the batch's sequences in shared memory, or NULL
-    long long at, end;  // next tile of the line, end of the range
+    const KvSeq* seq;  // the batch's sequences in shared memory, or NULL
+    long long u0, end;  // where the unit begins on the line, end of the range
     int b, unit, units, blocks, nt;
     KvSeq s;
     int h, rb, t0, t1;  // the segment: tiles t0 .. t1 - 1 of nt
-    bool later;         // it does not begin the CTA's range: its partial is the second one
+    bool later;         // it is not the CTA's first: its partial is the second one
 
-    // This CTA's range, which begins in sequence sc.b.
+    // This CTA's range, which begins in sequence sc.b. `some`: it has a tile.
     template <int NT>
-    __device__ __forceinline__ KvWalk(const KvArgs& a_, const KvSplit& split, const KvScan<NT>& sc)
-        : a(a_), seq(a_.B <= NT ? sc.seq : nullptr), at(split.start(blockIdx.x)), end(split.start(blockIdx.x + 1)),
-          b(sc.b), later(false) {
+    __device__ __forceinline__ KvWalk(const KvArgs& a_, const KvSplit& split, const KvScan<NT>& sc, bool& some)
+        : a(a_), seq(a_.B <= NT ? sc.seq : nullptr), later(false) {
+        some = split.busy(blockIdx.x);
+        t0 = t1 = nt = 0;
+        if (!some) return;
+        b = sc.b;
         load();
-        const long long off = at - sc.before;
-        unit = (int)kv_div(off, nt);
-        segment((int)(off - (long long)unit * nt));
+        const long long at = split.start(blockIdx.x), off = at - sc.before;
+        end = split.start(blockIdx.x + 1);
+        unit = (int)kv_div(off, nt + X);
+        const int p = (int)(off - (long long)unit * (nt + X));
+        u0 = at - p;
+        segment(max(0, p - X));
+        some = t1 > t0;  // not where the whole range is cost tiles
     }
     __device__ __forceinline__ void load() {
         s = seq ? seq[b] : kv_seq<ATTN>(a, b);
@@ -214,14 +231,14 @@ struct KvWalk {
     }
     __device__ __forceinline__ void segment(int tile) {
         h = unit / blocks, rb = unit - h * blocks;
-        t0 = tile, t1 = (int)min((long long)nt, tile + (end - at));
+        t0 = tile, t1 = (int)max(0ll, min((long long)nt, end - u0 - X));
     }
     __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == nt; }
-    __device__ __forceinline__ bool last() const { return at + (t1 - t0) >= end; }
+    __device__ __forceinline__ bool last() const { return end - (u0 + nt + X) <= X; }
     // The next segment; false at the end of the range.
     __device__ __forceinline__ bool next() {
-        at += t1 - t0, later = true;
-        if (at >= end) return false;
+        if (last()) return false;
+        u0 += nt + X, later = true;
         if (++unit == units) {
             unit = 0;
             do {
@@ -247,10 +264,10 @@ template <bool ATTN, int KT>
 __device__ __forceinline__ KvBorder kv_border(const KvArgs& a, const KvSplit& split, const KvWalk<ATTN, KT>& w) {
     KvBorder k{};
     if (w.t1 == w.nt) return k;
-    const long long u0 = w.at - w.t0;
+    const long long first = w.u0 + w.X;
     k.b = w.b, k.h = w.h, k.r0 = w.rb * a.row_block, k.rows = min(a.row_block, w.s.nodes * a.G - k.r0);
-    k.c0 = split.owner(u0), k.n = split.owner(u0 + w.nt - 1) - k.c0 + 1;
-    k.second = split.start(k.c0) < u0;
+    k.c0 = split.owner(first), k.n = split.owner(first + w.nt - 1) - k.c0 + 1;
+    k.second = split.start(k.c0) < w.u0;
     return k;
 }
 
@@ -293,7 +310,8 @@ __device__ __forceinline__ float kv_ex2(float x) {
     return r;
 }
 
-// Floats of one partial: row_block rows of d outputs, their maxima and their sums (16-byte blocks).
+// Floats of one partial: row_block rows of d outputs, their maxima and their sums (16-byte blocks). A sum
+// of -1 says that the CTA met a page outside the pool: the unit's rows are those of a refused sequence.
 __host__ __device__ inline int64_t kv_part_floats(int row_block, int d) { return ((int64_t)row_block * (d + 2) + 3) / 4 * 4; }
 
 __host__ __device__ inline int64_t kv_part_bytes(int64_t grid, int row_block, int d) {

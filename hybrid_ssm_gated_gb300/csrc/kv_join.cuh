@@ -16,6 +16,7 @@ namespace kvj {
 
 constexpr int NT = 256, WARPS = NT / 32;
 constexpr int SHARE = 4;  // blocks a border
+constexpr int AHEAD = 4;  // parts whose outputs a warp has in flight at once
 
 }  // namespace kvj
 
@@ -43,37 +44,57 @@ __global__ void __launch_bounds__(kvj::NT) kv_join_kernel(const __grid_constant_
         const int job = first + mine;
         const bool live = job < jobs;
         const int r = live ? job / cols : 0, e = live ? (job - r * cols) * 128 + lane * 4 : 0;
+        const auto outputs = [&](int j) {
+            const float* p = part(j) + (int64_t)r * a.d + e;
+            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (vec) {
+                if (e < a.d) x = *reinterpret_cast<const float4*>(p);
+            } else {
+                if (e < a.d) x.x = p[0];
+                if (e + 1 < a.d) x.y = p[1];
+                if (e + 2 < a.d) x.z = p[2];
+                if (e + 3 < a.d) x.w = p[3];
+            }
+            return x;
+        };
+        // the first parts' outputs are asked for before their maxima are known
+        float4 ahead[AHEAD];
+#pragma unroll
+        for (int y = 0; y < AHEAD; ++y)
+            if (me + y * team < n) ahead[y] = outputs(me + y * team);
         float m = -INFINITY, l = 0.f;
         for (int j = lane; j < n; j += 32) m = fmaxf(m, part(j)[RB * a.d + r]);
 #pragma unroll
         for (int x = 16; x; x >>= 1) m = fmaxf(m, __shfl_xor_sync(FULL_MASK, m, x));
         const float base = m == -INFINITY ? 0.f : m;
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        bool refused = false;
+        const auto add = [&](const float4& x, float w) {
+            o.x = fmaf(x.x, w, o.x), o.y = fmaf(x.y, w, o.y), o.z = fmaf(x.z, w, o.z), o.w = fmaf(x.w, w, o.w);
+        };
         for (int j0 = 0; j0 < n; j0 += 32) {
             float f = 0.f;
             if (j0 + lane < n) {
                 const float* p = part(j0 + lane);
+                const float sum = p[RB * a.d + RB + r];
                 f = kv_ex2(p[RB * a.d + r] - base);
-                l += p[RB * a.d + RB + r] * f;
+                l += sum * f;
+                refused = refused || sum == -1.f;
             }
             const int end = min(32, n - j0);
-#pragma unroll 4
-            for (int j = me; j < end; j += team) {
-                const float w = __shfl_sync(FULL_MASK, f, j);
-                const float* p = part(j0 + j) + (int64_t)r * a.d + e;
-                float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (vec) {
-                    if (e < a.d) x = *reinterpret_cast<const float4*>(p);
-                } else {
-                    if (e < a.d) x.x = p[0];
-                    if (e + 1 < a.d) x.y = p[1];
-                    if (e + 2 < a.d) x.z = p[2];
-                    if (e + 3 < a.d) x.w = p[3];
+            int j = me;
+            if (j0 == 0) {
+#pragma unroll
+                for (int y = 0; y < AHEAD; ++y, j += team) {
+                    const float w = __shfl_sync(FULL_MASK, f, j & 31);
+                    if (j < end) add(ahead[y], w);
                 }
-                o.x = fmaf(x.x, w, o.x), o.y = fmaf(x.y, w, o.y), o.z = fmaf(x.z, w, o.z), o.w = fmaf(x.w, w, o.w);
             }
+#pragma unroll 4
+            for (; j < end; j += team) add(outputs(j0 + j), __shfl_sync(FULL_MASK, f, j));
         }
         l = group_sum<32>(l);
+        if (__any_sync(FULL_MASK, refused)) l = 0.f;
         if (team > 1) {
             sums[warp][lane] = o;
             __syncthreads();

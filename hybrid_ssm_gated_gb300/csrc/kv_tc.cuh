@@ -53,7 +53,7 @@ constexpr int KT = 128;       // keys a tile
 // groups of softmax warps, and all warps, for a block of NR rows
 __host__ __device__ constexpr int groups(int NR) { return NR > 32 ? 4 : 2; }
 __host__ __device__ constexpr int threads(int NR) { return (4 * groups(NR) + 4) * 32; }
-constexpr int LEAST = 1;      // tiles a CTA at least
+constexpr int LEAST = 4;      // of the line a CTA at least: two tiles beside the two that a unit costs
 constexpr int BOX = 64;       // elements of d in one TMA box (128 bytes)
 constexpr int BOX_BYTES = KT * BOX * 2;
 constexpr float REF_NONE = -3.0e38f;  // reference of a row without a key yet
@@ -64,17 +64,26 @@ struct Maps {
     CUtensorMap k, v, kn, vn;
 };
 
+// What a segment's rows are, written by the K warp ahead of the softmax warps.
+template <int NR>
+struct __align__(16) Table {
+    uint32_t mask[2][NR];  // mask words of each row
+    int64_t row[NR];       // row of out and lse
+    int64_t q_at[NR];      // element offset of its query
+    int odd;               // a node's value is not finite
+    int bad;               // a page of the segment lies outside the pool
+};
+
 // Small shared-memory state of a CTA.
 template <int NR>
 struct __align__(16) State {
     float nref[NR];           // reference of each row, negated: -m
     float factor[NR];         // rescaling factor of a moved reference; at the end 1 / l
     float warp_max[4][NR];    // maxima by warp quadrant; at the end sums
-    uint32_t mask[2][NR];     // mask words of each row
-    int64_t row[NR];          // row of out and lse, -1 where the unit has none
     uint64_t full[MAX_STAGES], empty[MAX_STAGES];  // the K ring's stages, then the V ring's
-    uint64_t s_full[2], s_empty[2], p_full[2], p_empty[2], q_full, v_ok, drain[2];
-    int64_t q_at[NR];         // element offset of each row's query
+    uint64_t s_full[2], s_empty[2], p_full[2], p_empty[2], v_ok, drain[2];
+    Table<NR> table[2];       // of this segment and the next
+    uint64_t table_full[2], table_empty[2], seg_loaded[2];
     KvScan<threads(NR)> scan;
     int gave_up[4], v_stage;
     uint32_t tmem;
@@ -174,6 +183,17 @@ struct Half16<__half> {
     __device__ static __forceinline__ __half round(float x) { return __float2half_rn(x); }
 };
 
+// Whether one of eight 16-bit values is not finite.
+template <typename ST>
+__device__ __forceinline__ bool has_odd(const uint4& x) {
+    constexpr uint32_t e = Half16<ST>::exp_mask;
+    bool odd = false;
+    const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) odd = odd || (u[i] & e) == e || (u[i] >> 16 & e) == e;
+    return odd;
+}
+
 // Eight 16-bit values with those that are not finite replaced by zero.
 template <typename ST>
 __device__ __forceinline__ uint4 clear_odd(uint4 x) {
@@ -185,25 +205,6 @@ __device__ __forceinline__ uint4 clear_odd(uint4 x) {
         if ((u[i] >> 16 & e) == e) u[i] &= 0x0000ffffu;
     }
     return make_uint4(u[0], u[1], u[2], u[3]);
-}
-
-// Whether this thread's share of the nodes' values (all 128 threads of a group ask) is not all finite.
-template <typename ST>
-__device__ __forceinline__ bool odd_values(const KvArgs& a, int nodes, int b, int h, int gt) {
-    constexpr uint32_t m = Half16<ST>::exp_mask;
-    const ST* v = static_cast<const ST*>(a.vn.p) + (int64_t)b * a.vn.seq + (int64_t)h * a.vn.head;
-    bool odd = false;
-    const int per = (a.d + 63) / 64 * 8, n = nodes * per;
-#pragma unroll 4
-    for (int i = gt; i < n; i += 128) {
-        const int j = i / per, e = (i - j * per) * 8;
-        uint4 x = make_uint4(0, 0, 0, 0);
-        if (e < a.d) x = *reinterpret_cast<const uint4*>(v + (int64_t)j * a.vn.node + e);
-        const uint32_t u[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-        for (int y = 0; y < 4; ++y) odd = odd || (u[y] & m) == m || (u[y] >> 16 & m) == m;
-    }
-    return odd;
 }
 
 // The values that clear_odd took out, added to the rows' outputs where the row attends the node.
@@ -303,8 +304,9 @@ __global__ void __launch_bounds__(kvt::threads(NR), 1)
         if (lane < 2) {
             mbar_init(&st.s_full[lane], 1), mbar_init(&st.s_empty[lane], SM_WARPS);
             mbar_init(&st.p_full[lane], SM_WARPS), mbar_init(&st.p_empty[lane], 1);
+            mbar_init(&st.table_full[lane], 1), mbar_init(&st.table_empty[lane], SM_WARPS), mbar_init(&st.seg_loaded[lane], 1);
         }
-        if (lane == 2) mbar_init(&st.q_full, SM_WARPS), mbar_init(&st.v_ok, 1), mbar_init(&st.drain[0], 1), mbar_init(&st.drain[1], 1);
+        if (lane == 2) mbar_init(&st.v_ok, 1), mbar_init(&st.drain[0], 1), mbar_init(&st.drain[1], 1);
         if (lane < 4) st.gave_up[lane] = 0;
         fence_barrier_init();
     }
@@ -318,30 +320,50 @@ __global__ void __launch_bounds__(kvt::threads(NR), 1)
     const KvSplit split = kv_locate<true, KT, NT>(a, st.scan, gridDim.x, LEAST);
     tc::fence_after();
     const uint32_t tmem = st.tmem;
-    const bool busy = split.busy(blockIdx.x);
+    bool busy;
+    KvWalk<true, KT> w(a, split, st.scan, busy);
 
     if ((warp == K_WARP || warp == V_WARP) && busy) {
         // ------------------------------------------------------------ loads
         const bool keys = warp == K_WARP;
         const CUtensorMap *map = keys ? &maps.k : &maps.v, *map_new = keys ? &maps.kn : &maps.vn;
-        KvWalk<true, KT> w(a, split, st.scan);
         const int first = keys ? 0 : k_stages, end = keys ? k_stages : stages;
         int stage = first;
         uint32_t round = 0;
         bool ok = true;
         const int per_tile = KT / box_rows, step_pages = KT / a.page_size, step_places = KT - step_pages * a.page_size;
+        uint32_t seg = 0;
         do {
-            const int n = w.t1 - w.t0;
+            const int n = w.t1 - w.t0, side = seg & 1;
             const int32_t* table = a.page_table + (int64_t)w.s.slot * a.max_pages;
+            bool bad = false;
             // this lane's box of the next tile: its page (one tile ahead) and place
             const int e0 = w.t0 * KT + lane * box_rows;
             int pg = e0 / a.page_size, place = e0 - pg * a.page_size, e = e0;
             const auto look = [&]() { return lane < per_tile && e < w.s.len ? table[pg] : 0; };
             int page = look();
+            const auto rows_table = [&]() {  // for the softmax warps and the queries' loads
+                if (seg >= 2) ok = warp_wait(&st.table_empty[side], ((seg >> 1) - 1) & 1);
+                Table<NR>& tb = st.table[side];
+                const int r_first = w.rb * NR, rows = min(NR, w.s.nodes * a.G - r_first);
+#pragma unroll 1
+                for (int r = lane; r < NR; r += 32) {
+                    const int x = r_first + min(r, rows - 1), node = x / a.G, hq = w.h * a.G + x - node * a.G;
+                    const uint64_t m = a.mask[(int64_t)w.b * a.T + node];
+                    tb.mask[0][r] = (uint32_t)m, tb.mask[1][r] = (uint32_t)(m >> 32);
+                    tb.row[r] = ((int64_t)w.b * a.T + node) * a.Hq + hq;
+                    tb.q_at[r] = (int64_t)w.b * a.q.seq + (int64_t)node * a.q.node + (int64_t)hq * a.q.head;
+                }
+                if (lane == 0) tb.odd = 0, tb.bad = 0;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&st.table_full[side]);
+            };
+            if (keys && seg > 0) rows_table();
 #pragma unroll 1
             for (int i = 0; i < n && ok; ++i) {
                 const int t = w.t0 + i;
                 const bool tree = t == w.nt - 1;
+                bad = bad || (uint32_t)page >= (uint64_t)a.num_pages;
                 const int used = tree ? 0 : (min(KT, w.s.len - t * KT) + box_rows - 1) / box_rows;  // boxes with an entry
                 const int this_page = page, this_place = place;
                 e += KT, pg += step_pages, place += step_places;
@@ -366,7 +388,16 @@ __global__ void __launch_bounds__(kvt::threads(NR), 1)
                     }
                     if (++stage == end) stage = first, ++round;
                 }
+                if (keys && seg == 0 && i == 0) rows_table();  // (the first loads go ahead of it)
             }
+            if (keys) {
+                bad = __any_sync(FULL_MASK, bad);
+                if (lane == 0) {
+                    if (bad) st.table[side].bad = 1, set_error(a.dev_err, KV_DEVERR_PAGE);
+                    mbar_arrive(&st.seg_loaded[side]);
+                }
+            }
+            ++seg;
         } while (ok && w.next());
         if (!ok) {
             if (lane == 0) set_error(a.dev_err, GDN_DEVERR_TIMEOUT);
@@ -377,7 +408,6 @@ __global__ void __launch_bounds__(kvt::threads(NR), 1)
     } else if ((warp == S_WARP || warp == O_WARP) && busy) {
         // ------------------------------------------------------------ MMAs
         const bool outs = warp == O_WARP;
-        KvWalk<true, KT> w(a, split, st.scan);
         const uint32_t id = outs ? idesc(H::type, true, true, NR) : idesc(H::type, false, false, NR);
         const uint32_t aQ = smem_addr(sQ), aP = smem_addr(sP), aR = smem_addr(ring), tm = uniform(tmem);
         const int first = outs ? k_stages : 0, end = outs ? stages : k_stages;
@@ -389,7 +419,37 @@ __global__ void __launch_bounds__(kvt::threads(NR), 1)
             // the tile whose V has rows that the softmax threads clear: the cache's last one, if it is not
             // full, and the nodes'
             const int t0 = uniform(w.t0), short_t = uniform(w.s.len % KT ? w.nt - 2 : w.nt - 1), tree_t = uniform(w.nt - 1);
-            if (!outs) ok = warp_wait(&st.q_full, seg & 1);
+            if (!outs) {
+                // the queries, once the last segment's products have read theirs: a lane's eight loads all go out
+                // before the first is stored
+                const int side = seg & 1;
+                ok = warp_wait(&st.table_full[side], (seg >> 1) & 1);
+                if (n_t > 0) ok = ok && warp_wait(&st.s_full[(n_t - 1) & 1], ((n_t - 1) >> 1) & 1);
+                const Table<NR>& tb = st.table[side];
+                const int rows = min(NR, w.s.nodes * a.G - w.rb * NR), c = lane & 7;
+#pragma unroll 1
+                for (int x = 0; x < boxes && ok; ++x) {
+                    const bool in = x * BOX + c * 8 < a.d;
+#pragma unroll 1
+                    for (int r0 = lane >> 3; r0 < NR; r0 += 32) {
+                        uint4 v[8];
+#pragma unroll
+                        for (int y = 0; y < 8; ++y) {
+                            const int r = r0 + 4 * y;
+                            v[y] = make_uint4(0, 0, 0, 0);
+                            if (r < rows && in)
+                                v[y] = *reinterpret_cast<const uint4*>(static_cast<const ST*>(a.q.p) + tb.q_at[r] + x * BOX + c * 8);
+                        }
+#pragma unroll
+                        for (int y = 0; y < 8; ++y) {
+                            const int r = r0 + 4 * y;
+                            if (r < NR) *reinterpret_cast<uint4*>(sQ + x * NR * 128 + r * 128 + ((c ^ (r & 7)) << 4)) = v[y];
+                        }
+                    }
+                }
+                tc::fence_async_smem();
+                __syncwarp();
+            }
             ++seg;
 #pragma unroll 1
             for (int i = 0; i < n && ok; ++i, ++n_t) {
@@ -457,53 +517,15 @@ __global__ void __launch_bounds__(kvt::threads(NR), 1)
         const float c2 = a.scale == 0.f ? 1.1754944e-38f : a.scale * LOG2E;
         const Two cc = two(c2, c2);
         const int64_t part_floats = kv_part_floats(NR, a.d);
-        KvWalk<true, KT> w(a, split, st.scan);
-        uint32_t n_t = 0, n_v = 0;  // tiles so far, v_ok rounds so far
-        int checked = -1;
-        bool pages_bad = false, failed = false, stop = false;  // stop: the whole group gives up
+        uint32_t n_t = 0, n_v = 0, seg = 0;  // tiles, v_ok rounds and segments so far
+        bool failed = false, stop = false;   // stop: the whole group gives up
         Two l[NRH / 2];  // this key's share of the rows' sums
+        if (gt < NRH) st.nref[g0 + gt] = -REF_NONE;
+        group_sync(g);
         do {
-            const int rows = min(NR, w.s.nodes * a.G - w.rb * NR), r_first = w.rb * NR, n = w.t1 - w.t0;
-            // ---- row tables and queries of the group's rows
-            if (gt < NRH) {
-                const int r = g0 + gt, node = (r_first + r) / a.G, x = w.h * a.G + (r_first + r) - node * a.G;
-                const bool in = r < rows;
-                st.nref[r] = -REF_NONE;
-                st.row[r] = in ? ((int64_t)w.b * a.T + node) * a.Hq + x : -1;
-                st.q_at[r] = (int64_t)w.b * a.q.seq + (int64_t)node * a.q.node + (int64_t)x * a.q.head;
-                const uint64_t m = in ? a.mask[(int64_t)w.b * a.T + node] : 0;
-                st.mask[0][r] = (uint32_t)m, st.mask[1][r] = (uint32_t)(m >> 32);
-            }
-            group_sync(g);
-            {
-                // 16-byte pieces, eight of a row's box; a thread's loads all go out before the first is stored
-                constexpr int N = (NRH * 8 + 127) / 128;
-                for (int x = 0; x < boxes; ++x) {
-                    uint4 v[N];
-#pragma unroll
-                    for (int y = 0; y < N; ++y) {
-                        const int i = gt + y * 128, r = g0 + (i >> 3), e = x * BOX + (i & 7) * 8;
-                        v[y] = make_uint4(0, 0, 0, 0);
-                        if (i < NRH * 8 && r < rows && e < a.d)
-                            v[y] = *reinterpret_cast<const uint4*>(static_cast<const ST*>(a.q.p) + st.q_at[r] + e);
-                    }
-#pragma unroll
-                    for (int y = 0; y < N; ++y) {
-                        const int i = gt + y * 128, r = g0 + (i >> 3);
-                        if (i < NRH * 8)
-                            *reinterpret_cast<uint4*>(sQ + x * NR * 128 + r * 128 + (((i & 7) ^ (r & 7)) << 4)) = v[y];
-                    }
-                }
-            }
-            tc::fence_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&st.q_full);
-            if (checked != w.b) {
-                pages_bad = group_any(g, !kv_pages_ok(a, w.s, gt, 128));
-                if (pages_bad && tid == 0) set_error(a.dev_err, KV_DEVERR_PAGE);
-                checked = w.b;
-            }
-            bool odd = false;  // a node's value is not finite
+            const int rows = min(NR, w.s.nodes * a.G - w.rb * NR), n = w.t1 - w.t0, side = seg & 1;
+            Table<NR>& tb = st.table[side];
+            failed = failed || !mbar_wait(&st.table_full[side], (seg >> 1) & 1);
 #pragma unroll
             for (int r = 0; r < NRH / 2; ++r) l[r] = 0;
 
@@ -511,7 +533,6 @@ __global__ void __launch_bounds__(kvt::threads(NR), 1)
                 const int t = w.t0 + i, buf = n_t & 1;
                 const bool tree = t == w.nt - 1;
                 const int live = tree ? w.s.nodes : min(KT, w.s.len - t * KT);
-                if (tree) odd = group_any(g, odd_values<ST>(a, w.s.nodes, w.b, w.h, gt));
                 const uint32_t tm_s = tmem + lane_base + TM_S + buf * NR + g0;
                 const bool dead = key >= live;  // no key in this thread's row of the tile
                 failed = failed || !mbar_wait(&st.s_full[buf], (n_t >> 1) & 1);
@@ -522,8 +543,8 @@ __global__ void __launch_bounds__(kvt::threads(NR), 1)
                     for (int r = 0; r < NRH; r += 8) {
                         float x[8];
                         tc::tmem_ld<8>(tm_s + r, x);
-                        const uint4 m0 = *reinterpret_cast<const uint4*>(&st.mask[quad & 1][g0 + r]);
-                        const uint4 m1 = *reinterpret_cast<const uint4*>(&st.mask[quad & 1][g0 + r + 4]);
+                        const uint4 m0 = *reinterpret_cast<const uint4*>(&tb.mask[quad & 1][g0 + r]);
+                        const uint4 m1 = *reinterpret_cast<const uint4*>(&tb.mask[quad & 1][g0 + r + 4]);
                         const uint32_t m[8] = {m0.x, m0.y, m0.z, m0.w, m1.x, m1.y, m1.z, m1.w};
 #pragma unroll
                         for (int y = 0; y < 8; ++y)
@@ -648,10 +669,12 @@ __global__ void __launch_bounds__(kvt::threads(NR), 1)
                         uint4* row = reinterpret_cast<uint4*>(ring + stage * stage_bytes + (x & 1) * BOX_BYTES + key * 128);
 #pragma unroll 1
                         for (int y = 0; y < 8; ++y) {
-                            if (dead) row[y ^ (lane & 7)] = make_uint4(0, 0, 0, 0);  // (order against bank conflicts)
-                            else if (tree && odd) row[y] = clear_odd<ST>(row[y]);
+                            const int c = y ^ (lane & 7);  // (an order without bank conflicts)
+                            if (dead) row[c] = make_uint4(0, 0, 0, 0);
+                            else if (tree && has_odd<ST>(row[c])) row[c] = clear_odd<ST>(row[c]), tb.odd = 1;
                         }
                     }
+                    __threadfence_block();  // tb.odd, for every group once the product is done
                 }
                 tc::fence_async_smem();
                 tc::fence_before();
@@ -665,20 +688,24 @@ __global__ void __launch_bounds__(kvt::threads(NR), 1)
             group_sync(g);
             const bool whole = w.whole();
             float* part = a.part + ((int64_t)blockIdx.x * 2 + w.later) * part_floats;
+            failed = failed || !mbar_wait(&st.seg_loaded[side], (seg >> 1) & 1);
+            const bool bad = tb.bad;
             if (gt < NRH) {
                 const int r = g0 + gt;
-                const float sum = pages_bad ? 0.f : st.warp_max[0][r] + st.warp_max[1][r] + st.warp_max[2][r] + st.warp_max[3][r];
-                st.factor[r] = pages_bad ? 0.f : whole ? (sum == 0.f ? 0.f : 1.f / sum) : 1.f;
-                if (st.row[r] >= 0) {
+                const float sum = bad ? 0.f : st.warp_max[0][r] + st.warp_max[1][r] + st.warp_max[2][r] + st.warp_max[3][r];
+                st.factor[r] = bad ? 0.f : whole ? (sum == 0.f ? 0.f : 1.f / sum) : 1.f;
+                if (r < rows) {
                     if (!whole)
-                        part[NR * a.d + r] = -st.nref[r], part[NR * a.d + NR + r] = sum;
+                        part[NR * a.d + r] = -st.nref[r], part[NR * a.d + NR + r] = bad ? -1.f : sum;
                     else if (a.lse)
-                        a.lse[st.row[r]] = sum == 0.f ? -INFINITY : (log2f(sum) - st.nref[r]) * LN2;
+                        a.lse[tb.row[r]] = sum == 0.f ? -INFINITY : (log2f(sum) - st.nref[r]) * LN2;
                 }
+                st.nref[r] = -REF_NONE;  // for the next segment
             }
             group_sync(g);
             failed = failed || !mbar_wait(&st.p_empty[(n_t - 1) & pb], ((n_t - 1) >> pb) & 1);
             tc::fence_after();
+            const bool odd = w.t1 == w.nt && tb.odd;
 #pragma unroll 1
             for (int i = 0; i < pairs * (NRH / 8); ++i) {
                 const int hf = i / (NRH / 8), r0 = g0 + (i - hf * (NRH / 8)) * 8, e = hf * 128 + key;
@@ -686,23 +713,27 @@ __global__ void __launch_bounds__(kvt::threads(NR), 1)
                 __syncwarp();
                 tc::tmem_ld<8>(tmem + lane_base + TM_O + hf * NR + r0, o);
                 if (e >= a.d || r0 >= rows) continue;
-                if (odd) add_odd<ST>(a, w.s.nodes, w.b, w.h, e, &st.mask[0][r0], &st.mask[1][r0], o);
+                if (odd) add_odd<ST>(a, w.s.nodes, w.b, w.h, e, &tb.mask[0][r0], &tb.mask[1][r0], o);
                 const float4 f0 = *reinterpret_cast<const float4*>(&st.factor[r0]);
                 const float4 f1 = *reinterpret_cast<const float4*>(&st.factor[r0 + 4]);
                 const float f[8] = {f0.x, f0.y, f0.z, f0.w, f1.x, f1.y, f1.z, f1.w};
+                if (whole) {
+                    ST* out = static_cast<ST*>(a.out) + e;
 #pragma unroll
-                for (int x = 0; x < 8; ++x) {
-                    if (r0 + x >= rows) break;
-                    const float y = f[x] == 0.f ? 0.f : o[x] * f[x];
-                    if (whole)
-                        static_cast<ST*>(a.out)[st.row[r0 + x] * a.d + e] = H::round(y);
-                    else
-                        part[(r0 + x) * a.d + e] = y;
+                    for (int x = 0; x < 8; ++x)
+                        if (r0 + x < rows) out[tb.row[r0 + x] * a.d] = H::round(f[x] == 0.f ? 0.f : o[x] * f[x]);
+                } else {
+                    float* out = part + (int64_t)r0 * a.d + e;
+#pragma unroll
+                    for (int x = 0; x < 8; ++x)
+                        if (r0 + x < rows) out[x * a.d] = f[x] == 0.f ? 0.f : o[x];
                 }
             }
             tc::fence_before();
             if (tid == 0 && w.last()) static_cast<KvBorder*>(a.border)[blockIdx.x] = kv_border(a, split, w);
-            group_sync(g);  // the row tables are read
+            group_sync(g);  // the sums and factors are read
+            if (lane == 0) mbar_arrive(&st.table_empty[side]);
+            ++seg;
         } while (w.next());
         if (failed && lane == 0) set_error(a.dev_err, GDN_DEVERR_TIMEOUT);
     }

@@ -32,10 +32,11 @@ __global__ void __launch_bounds__(kvg::NT) kv_weights_kernel(const KvArgs a, con
         if (s.err && tid == 0) set_error(a.dev_err, s.err);
     }
     const KvSplit split = kv_locate<false, KT, NT>(a, scan, gridDim.x, 1);
-    if (!split.busy(blockIdx.x)) return;
+    bool some;
+    KvWalk<false, KT> w(a, split, scan, some);
+    if (!some) return;
     int checked = -1;
     bool ok = true;
-    KvWalk<false, KT> w(a, split, scan);
     do {
         const KvSeq& s = w.s;
         const int b = w.b, h = w.h;

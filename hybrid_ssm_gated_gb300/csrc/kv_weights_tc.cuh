@@ -40,6 +40,17 @@ struct __align__(16) State {
 // Barrier of the eight weight warps.
 __device__ __forceinline__ void all_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
+__device__ __forceinline__ bool any_of(bool x) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+        "barrier.cta.red.or.pred q, 1, 256, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"((uint32_t)x)
+        : "memory");
+    return r != 0;
+}
+
 template <int NR>
 __host__ __device__ constexpr int smem_bytes(int boxes, int stages) {
     return 1024 + boxes * NR * 128 + stages * (boxes > 1 ? 2 : 1) * BOX_BYTES + (int)sizeof(State<NR>);
@@ -80,11 +91,11 @@ __global__ void __launch_bounds__(kvw::NT, 1)
     const KvSplit split = kv_locate<false, KT, NT>(a, st.scan, gridDim.x, 1);
     tc::fence_after();
     const uint32_t tmem = st.tmem;
-    const bool busy = split.busy(blockIdx.x);
+    bool busy;
+    KvWalk<false, KT> w(a, split, st.scan, busy);
 
     if (warp == K_WARP && busy) {
         // ------------------------------------------------------------ loads
-        KvWalk<false, KT> w(a, split, st.scan);
         int stage = 0;
         uint32_t round = 0;
         bool ok = true;
@@ -130,7 +141,6 @@ __global__ void __launch_bounds__(kvw::NT, 1)
         }
     } else if (warp == S_WARP && busy) {
         // ------------------------------------------------------------ MMAs
-        KvWalk<false, KT> w(a, split, st.scan);
         const uint32_t id = kvt::idesc(H::type, false, false, NR);
         const uint32_t aQ = smem_addr(sQ), aR = smem_addr(ring), tm = kvt::uniform(tmem);
         int stage = 0;
@@ -181,22 +191,17 @@ __global__ void __launch_bounds__(kvw::NT, 1)
         const int g = warp >> 2, quad = warp & 3, key = quad * 32 + lane, wt = tid & 255;
         const uint32_t tm_s = tmem + ((uint32_t)(quad * 32) << 16) + g * NR;
         const kvt::Two scale = kvt::two(a.scale, a.scale), log2e = kvt::two(LOG2E, LOG2E);
-        KvWalk<false, KT> w(a, split, st.scan);
         uint32_t n_t = 0, seg = 0;
         int checked = -1;
         bool good = true, failed = false;
         do {
             const int32_t* table = a.page_table + (int64_t)w.s.slot * a.max_pages;
             const int rows_all = w.s.nodes * a.G, blocks = (rows_all + NR - 1) / NR;
-            if (checked != w.b) {  // every warp by itself: the path's nodes and the sequence's pages are in range
-                bool nodes_ok = true;
-                for (int j = lane; j < w.s.nodes; j += 32)
-                    nodes_ok = nodes_ok && (uint32_t)a.path[(int64_t)w.b * a.P + j] < (uint32_t)a.T;
-                nodes_ok = __all_sync(FULL_MASK, nodes_ok);
-                const bool pages_ok = __all_sync(FULL_MASK, kv_pages_ok(a, w.s, lane, 32));
-                good = nodes_ok && pages_ok;
-                if (!good && tid == 0)
-                    set_error(a.dev_err, (nodes_ok ? 0 : KV_DEVERR_NODES) | (pages_ok ? 0 : KV_DEVERR_PAGE));
+            if (checked != w.b) {  // the path's nodes and the sequence's pages are in range
+                int bad = kv_pages_ok(a, w.s, wt, 256) ? 0 : KV_DEVERR_PAGE;
+                if (wt < w.s.nodes && (uint32_t)a.path[(int64_t)w.b * a.P + wt] >= (uint32_t)a.T) bad |= KV_DEVERR_NODES;
+                if (bad) set_error(a.dev_err, bad);
+                good = !any_of(bad != 0);
                 checked = w.b;
             }
 #pragma unroll 1
