@@ -81,6 +81,10 @@ cudaError_t launch_kv_attn_tc(KvArgs& a, cudaStream_t stream) {
         !encode(maps.vn, a.dtype, a.vn.p, a.d, a.T, a.vn.node, a.Hkv, a.vn.head, a.B, a.vn.seq, a.T))
         return cudaErrorNotSupported;
     a.row_block = row_block_of((int64_t)a.T * a.G, boxes);
+    // queries: a block of rows is whole nodes' heads of one group
+    if (a.row_block % a.G == 0 &&
+        !encode(maps.q, a.dtype, a.q.p, a.d, a.Hq, a.q.head, a.T, a.q.node, a.B, a.q.seq, a.G, a.row_block / a.G))
+        return cudaErrorNotSupported;
     DeviceInfo di;
     int64_t grid = 0;
     cudaError_t e = wave(a, di, grid);

@@ -14,9 +14,9 @@ namespace gdn {
 
 namespace kvj {
 
-constexpr int NT = 256, WARPS = NT / 32;
-constexpr int SHARE = 4;  // blocks a border
-constexpr int AHEAD = 4;  // parts whose outputs a warp has in flight at once
+constexpr int NT = 128, WARPS = NT / 32;
+constexpr int SHARE = 8;  // blocks a border
+constexpr int AHEAD = 2;  // parts whose outputs are asked for before the maxima are known
 
 }  // namespace kvj
 
@@ -40,58 +40,54 @@ __global__ void __launch_bounds__(kvj::NT) kv_join_kernel(const __grid_constant_
     while (team < WARPS && team * 4 < n) team *= 2;
     const int teams = WARPS / team, mine = warp / team, me = warp - mine * team;
     const int rank = (i - c0) * SHARE + blockIdx.x % SHARE, ranks = (n - 1) * SHARE;
-    for (int first = rank * teams; first < jobs; first += ranks * teams) {
+    const auto outputs = [&](int j, int r, int e) {
+        const float* p = part(j) + (int64_t)r * a.d + e;
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (vec) {
+            if (e < a.d) x = *reinterpret_cast<const float4*>(p);
+        } else {
+            if (e < a.d) x.x = p[0];
+            if (e + 1 < a.d) x.y = p[1];
+            if (e + 2 < a.d) x.z = p[2];
+            if (e + 3 < a.d) x.w = p[3];
+        }
+        return x;
+    };
+    const int stride = ranks * teams;
+#pragma unroll 1
+    for (int first = rank * teams; first < jobs; first += stride) {
         const int job = first + mine;
         const bool live = job < jobs;
         const int r = live ? job / cols : 0, e = live ? (job - r * cols) * 128 + lane * 4 : 0;
-        const auto outputs = [&](int j) {
-            const float* p = part(j) + (int64_t)r * a.d + e;
-            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (vec) {
-                if (e < a.d) x = *reinterpret_cast<const float4*>(p);
-            } else {
-                if (e < a.d) x.x = p[0];
-                if (e + 1 < a.d) x.y = p[1];
-                if (e + 2 < a.d) x.z = p[2];
-                if (e + 3 < a.d) x.w = p[3];
-            }
-            return x;
-        };
-        // the first parts' outputs are asked for before their maxima are known
         float4 ahead[AHEAD];
 #pragma unroll
-        for (int y = 0; y < AHEAD; ++y)
-            if (me + y * team < n) ahead[y] = outputs(me + y * team);
+        for (int x = 0; x < AHEAD; ++x)
+            if (me + x * team < n) ahead[x] = outputs(me + x * team, r, e);
         float m = -INFINITY, l = 0.f;
+#pragma unroll 1
         for (int j = lane; j < n; j += 32) m = fmaxf(m, part(j)[RB * a.d + r]);
 #pragma unroll
         for (int x = 16; x; x >>= 1) m = fmaxf(m, __shfl_xor_sync(FULL_MASK, m, x));
         const float base = m == -INFINITY ? 0.f : m;
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
         bool refused = false;
-        const auto add = [&](const float4& x, float w) {
-            o.x = fmaf(x.x, w, o.x), o.y = fmaf(x.y, w, o.y), o.z = fmaf(x.z, w, o.z), o.w = fmaf(x.w, w, o.w);
-        };
+#pragma unroll 1
         for (int j0 = 0; j0 < n; j0 += 32) {
             float f = 0.f;
             if (j0 + lane < n) {
-                const float* p = part(j0 + lane);
-                const float sum = p[RB * a.d + RB + r];
-                f = kv_ex2(p[RB * a.d + r] - base);
+                const float* p = part(j0 + lane) + (int64_t)RB * a.d + r;
+                const float sum = p[RB];
+                f = kv_ex2(p[0] - base);
                 l += sum * f;
                 refused = refused || sum == -1.f;
             }
             const int end = min(32, n - j0);
-            int j = me;
-            if (j0 == 0) {
-#pragma unroll
-                for (int y = 0; y < AHEAD; ++y, j += team) {
-                    const float w = __shfl_sync(FULL_MASK, f, j & 31);
-                    if (j < end) add(ahead[y], w);
-                }
+#pragma unroll 2
+            for (int j = me, x = j0 == 0 ? 0 : AHEAD; j < end; j += team, ++x) {
+                const float w = __shfl_sync(FULL_MASK, f, j);
+                const float4 y = x == 0 ? ahead[0] : x == 1 ? ahead[1] : outputs(j0 + j, r, e);
+                o.x = fmaf(y.x, w, o.x), o.y = fmaf(y.y, w, o.y), o.z = fmaf(y.z, w, o.z), o.w = fmaf(y.w, w, o.w);
             }
-#pragma unroll 4
-            for (; j < end; j += team) add(outputs(j0 + j), __shfl_sync(FULL_MASK, f, j));
         }
         l = group_sum<32>(l);
         if (__any_sync(FULL_MASK, refused)) l = 0.f;
@@ -99,8 +95,8 @@ __global__ void __launch_bounds__(kvj::NT) kv_join_kernel(const __grid_constant_
             sums[warp][lane] = o;
             __syncthreads();
             for (int x = 1; x < team && me == 0; ++x) {
-                const float4 y = sums[warp + x][lane];
-                o.x += y.x, o.y += y.y, o.z += y.z, o.w += y.w;
+                const float4 z = sums[warp + x][lane];
+                o.x += z.x, o.y += z.y, o.z += z.z, o.w += z.w;
             }
             __syncthreads();
         }
@@ -108,10 +104,10 @@ __global__ void __launch_bounds__(kvj::NT) kv_join_kernel(const __grid_constant_
             const float inv = l == 0.f ? 0.f : 1.f / l;
             const int node = (r0 + r) / a.G, hq = h * a.G + (r0 + r) - node * a.G;
             const int64_t row = ((int64_t)b * a.T + node) * a.Hq + hq;
-            const float y[4] = {o.x, o.y, o.z, o.w};
+            const float z[4] = {o.x, o.y, o.z, o.w};
 #pragma unroll
             for (int x = 0; x < 4; ++x)
-                if (e + x < a.d) store_elem(a.out, row * a.d + e + x, a.dtype, l == 0.f ? 0.f : y[x] * inv);
+                if (e + x < a.d) store_elem(a.out, row * a.d + e + x, a.dtype, l == 0.f ? 0.f : z[x] * inv);
             if (e == 0 && a.lse) a.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * LN2;
         }
     }

@@ -26,13 +26,13 @@ inline Encode encoder() {
     return fn;
 }
 
-// 16-bit rows [n3][n2][n1][d] with strides s3, s2, s1 (elements), boxes of `rows` x 64 elements in the
-// 128-byte swizzle; past the ends zeros are read.
+// 16-bit rows [n3][n2][n1][d] with strides s3, s2, s1 (elements), boxes of `rows2` x `rows` x 64 elements in
+// the 128-byte swizzle; past the ends zeros are read.
 inline bool encode(CUtensorMap& m, int dtype, const void* p, int d, int64_t n1, int64_t s1, int64_t n2, int64_t s2, int64_t n3,
-            int64_t s3, int rows) {
+            int64_t s3, int rows, int rows2 = 1) {
     const cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)n1, (cuuint64_t)n2, (cuuint64_t)n3};
     const cuuint64_t strides[3] = {(cuuint64_t)s1 * 2, (cuuint64_t)s2 * 2, (cuuint64_t)s3 * 2};
-    const cuuint32_t box[4] = {kvt::BOX, (cuuint32_t)rows, 1, 1}, unit[4] = {1, 1, 1, 1};
+    const cuuint32_t box[4] = {kvt::BOX, (cuuint32_t)rows, (cuuint32_t)rows2, 1}, unit[4] = {1, 1, 1, 1};
     return encoder()(&m, dtype == GDN_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
                      const_cast<void*>(p), dims, strides, box, unit, CU_TENSOR_MAP_INTERLEAVE_NONE,
                      CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,

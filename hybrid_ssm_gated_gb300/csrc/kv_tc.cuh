@@ -53,7 +53,7 @@ constexpr int KT = 128;       // keys a tile
 // groups of softmax warps, and all warps, for a block of NR rows
 __host__ __device__ constexpr int groups(int NR) { return NR > 32 ? 4 : 2; }
 __host__ __device__ constexpr int threads(int NR) { return (4 * groups(NR) + 4) * 32; }
-constexpr int LEAST = 4;      // of the line a CTA at least: two tiles beside the two that a unit costs
+constexpr int LEAST = 2;      // of the line a CTA at least
 constexpr int BOX = 64;       // elements of d in one TMA box (128 bytes)
 constexpr int BOX_BYTES = KT * BOX * 2;
 constexpr float REF_NONE = -3.0e38f;  // reference of a row without a key yet
@@ -61,7 +61,7 @@ constexpr float REF_SLACK = 8.f;
 constexpr int MAX_STAGES = 14;
 
 struct Maps {
-    CUtensorMap k, v, kn, vn;
+    CUtensorMap k, v, kn, vn, q;
 };
 
 // What a segment's rows are, written by the K warp ahead of the softmax warps.
@@ -81,7 +81,7 @@ struct __align__(16) State {
     float factor[NR];         // rescaling factor of a moved reference; at the end 1 / l
     float warp_max[4][NR];    // maxima by warp quadrant; at the end sums
     uint64_t full[MAX_STAGES], empty[MAX_STAGES];  // the K ring's stages, then the V ring's
-    uint64_t s_full[2], s_empty[2], p_full[2], p_empty[2], v_ok, drain[2];
+    uint64_t s_full[2], s_empty[2], p_full[2], p_empty[2], q_full, v_ok, drain[2];
     Table<NR> table[2];       // of this segment and the next
     uint64_t table_full[2], table_empty[2], seg_loaded[2];
     KvScan<threads(NR)> scan;
@@ -296,8 +296,8 @@ __global__ void __launch_bounds__(kvt::threads(NR), 1)
 
     kv_grid_launch();
     if (warp == K_WARP) {
-        if (lane < 4) {
-            const CUtensorMap* m = lane == 0 ? &maps.k : lane == 1 ? &maps.v : lane == 2 ? &maps.kn : &maps.vn;
+        if (lane < 5) {
+            const CUtensorMap* m = lane == 0 ? &maps.k : lane == 1 ? &maps.v : lane == 2 ? &maps.kn : lane == 3 ? &maps.vn : &maps.q;
             asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory");
         }
         if (lane < stages) mbar_init(&st.full[lane], 1), mbar_init(&st.empty[lane], 1);
@@ -306,7 +306,7 @@ __global__ void __launch_bounds__(kvt::threads(NR), 1)
             mbar_init(&st.p_full[lane], SM_WARPS), mbar_init(&st.p_empty[lane], 1);
             mbar_init(&st.table_full[lane], 1), mbar_init(&st.table_empty[lane], SM_WARPS), mbar_init(&st.seg_loaded[lane], 1);
         }
-        if (lane == 2) mbar_init(&st.v_ok, 1), mbar_init(&st.drain[0], 1), mbar_init(&st.drain[1], 1);
+        if (lane == 2) mbar_init(&st.q_full, 1), mbar_init(&st.v_ok, 1), mbar_init(&st.drain[0], 1), mbar_init(&st.drain[1], 1);
         if (lane < 4) st.gave_up[lane] = 0;
         fence_barrier_init();
     }
@@ -420,35 +420,47 @@ __global__ void __launch_bounds__(kvt::threads(NR), 1)
             // full, and the nodes'
             const int t0 = uniform(w.t0), short_t = uniform(w.s.len % KT ? w.nt - 2 : w.nt - 1), tree_t = uniform(w.nt - 1);
             if (!outs) {
-                // the queries, once the last segment's products have read theirs: a lane's eight loads all go out
-                // before the first is stored
-                const int side = seg & 1;
-                ok = warp_wait(&st.table_full[side], (seg >> 1) & 1);
-                if (n_t > 0) ok = ok && warp_wait(&st.s_full[(n_t - 1) & 1], ((n_t - 1) >> 1) & 1);
-                const Table<NR>& tb = st.table[side];
-                const int rows = min(NR, w.s.nodes * a.G - w.rb * NR), c = lane & 7;
+                // the queries, once the last segment's products have read theirs: by TMA where the block holds
+                // whole nodes (nodes past the count may be there too: their columns are not looked at) ...
+                const int side = seg & 1, r_first = w.rb * NR;
+                if (n_t > 0) ok = warp_wait(&st.s_full[(n_t - 1) & 1], ((n_t - 1) >> 1) & 1);
+                if (NR % a.G == 0) {
+                    if (lane == 0 && ok) {
+                        mbar_arrive_expect_tx(&st.q_full, boxes * NR * 128);
 #pragma unroll 1
-                for (int x = 0; x < boxes && ok; ++x) {
-                    const bool in = x * BOX + c * 8 < a.d;
+                        for (int x = 0; x < boxes; ++x)
+                            tma_load(sQ + x * NR * 128, &maps.q, x * BOX, w.h * a.G, r_first / a.G, w.b, &st.q_full);
+                    }
+                    __syncwarp();
+                    ok = ok && warp_wait(&st.q_full, seg & 1);
+                } else {  // ... else by the lanes, eight loads of one out before the first is stored
+                    ok = ok && warp_wait(&st.table_full[side], (seg >> 1) & 1);
+                    const Table<NR>& tb = st.table[side];
+                    const int rows = min(NR, w.s.nodes * a.G - r_first), c = lane & 7;
 #pragma unroll 1
-                    for (int r0 = lane >> 3; r0 < NR; r0 += 32) {
-                        uint4 v[8];
+                    for (int x = 0; x < boxes && ok; ++x) {
+                        const bool in = x * BOX + c * 8 < a.d;
+#pragma unroll 1
+                        for (int r0 = lane >> 3; r0 < NR; r0 += 32) {
+                            uint4 v[8];
 #pragma unroll
-                        for (int y = 0; y < 8; ++y) {
-                            const int r = r0 + 4 * y;
-                            v[y] = make_uint4(0, 0, 0, 0);
-                            if (r < rows && in)
-                                v[y] = *reinterpret_cast<const uint4*>(static_cast<const ST*>(a.q.p) + tb.q_at[r] + x * BOX + c * 8);
-                        }
+                            for (int y = 0; y < 8; ++y) {
+                                const int r = r0 + 4 * y;
+                                v[y] = make_uint4(0, 0, 0, 0);
+                                if (r < rows && in)
+                                    v[y] = *reinterpret_cast<const uint4*>(static_cast<const ST*>(a.q.p) + tb.q_at[r] + x * BOX +
+                                                                           c * 8);
+                            }
 #pragma unroll
-                        for (int y = 0; y < 8; ++y) {
-                            const int r = r0 + 4 * y;
-                            if (r < NR) *reinterpret_cast<uint4*>(sQ + x * NR * 128 + r * 128 + ((c ^ (r & 7)) << 4)) = v[y];
+                            for (int y = 0; y < 8; ++y) {
+                                const int r = r0 + 4 * y;
+                                if (r < NR) *reinterpret_cast<uint4*>(sQ + x * NR * 128 + r * 128 + ((c ^ (r & 7)) << 4)) = v[y];
+                            }
                         }
                     }
+                    tc::fence_async_smem();
+                    __syncwarp();
                 }
-                tc::fence_async_smem();
-                __syncwarp();
             }
             ++seg;
 #pragma unroll 1
