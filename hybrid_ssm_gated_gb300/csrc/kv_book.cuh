@@ -88,52 +88,41 @@ __device__ __forceinline__ uint32_t kv_rank_key(float w, int stamp, int newest) 
 // Selection. A unit (sequence, key head) is the work of one CTA, or of a cluster of up to 8 that each
 // take a slice of the entries, so that one long sequence is not left to a handful of SMs. The entries'
 // order keys are formed once, into shared memory; three histogram passes of 11, 11 and 10 bits (summed
-// over the cluster's shared memories) find the budget-th largest key; then every thread counts and lists
-// a run of consecutive entries, placed by scans over threads and CTAs. Slices that do not fit shared
-// memory form their keys again at each pass.
-constexpr int KV_SEL_NT = 512, KV_SEL_BINS = 2048;
+// over the cluster's shared memories) find the budget-th largest key; then every warp counts, and in a
+// second walk lists, a run of entries, 128 at a time, so that the lists are written in lines
+// (a run of entries a thread wrote them four bytes a line, and took half of the kernel's time). Bound by
+// latency: the loads and barriers of a dozen steps. Slices that do not fit shared memory form their keys
+// again at each pass.
+constexpr int KV_SEL_NT = 512, KV_SEL_WARPS = KV_SEL_NT / 32, KV_SEL_BINS = 2048;
+
+// Entries of a slice, or of a warp's run: above the threshold and at it, below the budget and not.
+struct KvCounts {
+    unsigned above_low, at_low, above_high, at_high;
+};
+__device__ __forceinline__ KvCounts operator+(const KvCounts& x, const KvCounts& y) {
+    return {x.above_low + y.above_low, x.at_low + y.at_low, x.above_high + y.above_high, x.at_high + y.at_high};
+}
 
 struct __align__(16) KvSelect {
     unsigned hist[3][KV_SEL_BINS];
-    unsigned long long warp_sum[KV_SEL_NT / 32];
-    unsigned long long total[2];  // of this CTA: entries at the threshold; holes and fillers
+    unsigned warp_sum[KV_SEL_WARPS];
+    KvCounts counts[KV_SEL_WARPS], total;  // the CTA's warps', and all of them
     unsigned digit, need;
+    int bad;  // a page of the slice lies outside the pool
 };
 
-// Sum of x over the threads before this one; `all` is the sum over the block.
-__device__ __forceinline__ unsigned long long kv_block_before(KvSelect& st, unsigned long long x, unsigned long long& all) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    unsigned long long inc = x;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const unsigned long long y = __shfl_up_sync(FULL_MASK, inc, o);
-        if (lane >= o) inc += y;
-    }
-    __syncthreads();  // the last sums are read
-    if (lane == 31) st.warp_sum[warp] = inc;
-    __syncthreads();
-    unsigned long long before = inc - x;
-    all = 0;
-    for (int w = 0; w < KV_SEL_NT / 32; ++w) {
-        if (w < warp) before += st.warp_sum[w];
-        all += st.warp_sum[w];
-    }
-    return before;
-}
-
-// keys_cap: keys that the dynamic shared memory holds (one word in 32 is padding, so that threads that
-// walk runs of 32 entries meet different banks); vec: four entries' weights and stamps in one load each.
-__global__ void __launch_bounds__(KV_SEL_NT) kv_select_kernel(const __grid_constant__ KvArgs a, const int cap, const int keys_cap,
+// keys_cap: keys that the dynamic shared memory holds; vec: four entries' weights and stamps in one load.
+__global__ void __launch_bounds__(KV_SEL_NT, 4) kv_select_kernel(const __grid_constant__ KvArgs a, const int cap, const int keys_cap,
                                                               const int vec) {
     namespace cg = cooperative_groups;
-    constexpr int NT = KV_SEL_NT;
+    constexpr int NT = KV_SEL_NT, WARPS = KV_SEL_WARPS;
     extern __shared__ __align__(128) unsigned char smem[];
     KvSelect& st = *reinterpret_cast<KvSelect*>(smem);
     uint32_t* skey = reinterpret_cast<uint32_t*>(smem + sizeof(KvSelect));
     const cg::cluster_group cluster = cg::this_cluster();
     const int C = cluster.num_blocks(), rank = cluster.block_rank();
     const int unit = blockIdx.x / C, b = unit / a.Hkv, h = unit - b * a.Hkv;
-    const int tid = threadIdx.x;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     int32_t* list = a.moves + kv_moves_at(unit, cap);
     kv_grid_launch();
     const int slot = a.slots[b];
@@ -148,66 +137,122 @@ __global__ void __launch_bounds__(KV_SEL_NT) kv_select_kernel(const __grid_const
         if (rank == 0 && tid == 0) list[0] = -1;
         return;
     }
-    const KvSeq s{slot, len, 0, 0};
-    if (!__syncthreads_and(kv_pages_ok(a, s, tid, NT))) {
-        if (rank == 0 && tid == 0) list[0] = -1, set_error(a.dev_err, KV_DEVERR_PAGE);
-        return;
-    }
     const int32_t* table = a.page_table + (int64_t)slot * a.max_pages;
     const int newest = a.counts[slot] - a.recent;
     const int per = align_up((len + C - 1) / C, 4), e0 = min(len, rank * per), n = min(len, e0 + per) - e0;
-    const bool kept_here = per + (per >> 5) <= keys_cap;
-    const auto at = [](int i) { return i + (i >> 5); };
-    const auto place_of = [&](int e) {
-        const int pg = e / a.page_size;
-        return ((int64_t)table[pg] * a.Hkv + h) * a.page_size + (e - pg * a.page_size);
+    const bool kept_here = per <= keys_cap;
+    for (int i = tid; i < 3 * KV_SEL_BINS / 4; i += NT) reinterpret_cast<uint4*>(st.hist)[i] = make_uint4(0, 0, 0, 0);
+    if (tid == 0) st.bad = 0;
+    __syncthreads();
+
+    // ---- order keys; the slice's pages are looked at on the way
+    bool bad = false;
+    const auto place_of = [&](int e) {  // of entry e in weights and stamps, -1 on a page outside the pool
+        const int pg = e / a.page_size, page = table[pg];
+        if ((uint32_t)page >= (uint64_t)a.num_pages) {
+            bad = true;
+            return (int64_t)-1;
+        }
+        return ((int64_t)page * a.Hkv + h) * a.page_size + (e - pg * a.page_size);
     };
     const auto form = [&](int i) {
         const int64_t x = place_of(e0 + i);
-        return kv_rank_key(a.weights[x], a.stamps[x], newest);
+        return x < 0 ? 0u : kv_rank_key(a.weights[x], a.stamps[x], newest);
     };
-    const auto key_of = [&](int i) { return kept_here ? skey[at(i)] : form(i); };
-
-    for (int i = tid; i < 3 * KV_SEL_BINS; i += NT) (&st.hist[0][0])[i] = 0;
-    if (kept_here) {
-        if (vec) {
-#pragma unroll 2
-            for (int i = tid * 4; i < n; i += NT * 4) {
-                const int64_t x = place_of(e0 + i);
-                const float4 w = *reinterpret_cast<const float4*>(a.weights + x);
-                const int4 t = *reinterpret_cast<const int4*>(a.stamps + x);
-                uint32_t* k = skey + at(i);
-                k[0] = kv_rank_key(w.x, t.x, newest), k[1] = kv_rank_key(w.y, t.y, newest);
-                k[2] = kv_rank_key(w.z, t.z, newest), k[3] = kv_rank_key(w.w, t.w, newest);
+    if (!kept_here || !vec) {
+        for (int i = tid; i < n; i += NT) {
+            const uint32_t key = form(i);
+            if (kept_here) skey[i] = key;
+        }
+    } else {
+        constexpr int AHEAD = 2;  // loads of a thread that wait for nothing but their pages
+        for (int i0 = tid * 4; i0 < n; i0 += NT * 4 * AHEAD) {
+            int64_t x[AHEAD];
+            float4 w[AHEAD];
+            int4 t[AHEAD];
+#pragma unroll
+            for (int y = 0; y < AHEAD; ++y) {
+                const int i = i0 + y * NT * 4;
+                x[y] = i < n ? place_of(e0 + i) : -1;
             }
-        } else {
-            for (int i = tid; i < n; i += NT) skey[at(i)] = form(i);
+#pragma unroll
+            for (int y = 0; y < AHEAD; ++y) {
+                w[y] = make_float4(0.f, 0.f, 0.f, 0.f), t[y] = make_int4(0, 0, 0, 0);
+                if (x[y] >= 0) {
+                    w[y] = *reinterpret_cast<const float4*>(a.weights + x[y]);
+                    t[y] = *reinterpret_cast<const int4*>(a.stamps + x[y]);
+                }
+            }
+#pragma unroll
+            for (int y = 0; y < AHEAD; ++y)
+                if (x[y] >= 0)
+                    *reinterpret_cast<uint4*>(skey + i0 + y * NT * 4) =
+                        make_uint4(kv_rank_key(w[y].x, t[y].x, newest), kv_rank_key(w[y].y, t[y].y, newest),
+                                   kv_rank_key(w[y].z, t[y].z, newest), kv_rank_key(w[y].w, t[y].w, newest));
         }
     }
+    if (bad) st.bad = 1;
     __syncthreads();
 
+    // ---- the budget-th largest key
     uint32_t prefix = 0;
     unsigned need = a.budget;  // entries still to be taken among those that share the prefix
 #pragma unroll 1
     for (int pass = 0; pass < 3; ++pass) {
         const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
         const uint32_t dm = (1u << bits) - 1u;
-        for (int i = tid; i < n; i += NT) {
-            const uint32_t key = key_of(i);
+        const auto take = [&](uint32_t key) {
             if (pass == 0 || (key ^ prefix) >> (shift + bits) == 0) atomicAdd(&st.hist[pass][key >> shift & dm], 1u);
+        };
+        if (kept_here) {
+#pragma unroll 2
+            for (int i = tid * 4; i < n; i += NT * 4) {
+                const uint4 k = *reinterpret_cast<const uint4*>(skey + i);
+                take(k.x);
+                if (i + 1 < n) take(k.y);
+                if (i + 2 < n) take(k.z);
+                if (i + 3 < n) take(k.w);
+            }
+        } else {
+            for (int i = tid; i < n; i += NT) take(form(i));
         }
         if (C > 1) cluster.sync();
         else __syncthreads();
+        if (pass == 0) {  // a page outside the pool, in any slice: the sequence stays as it is
+            const int one = lane < C ? (C > 1 ? *cluster.map_shared_rank(&st.bad, lane) : st.bad) : 0;
+            if (__any_sync(FULL_MASK, one)) {
+                if (rank == 0 && tid == 0) list[0] = -1, set_error(a.dev_err, KV_DEVERR_PAGE);
+                if (C > 1) cluster.sync();
+                return;
+            }
+        }
         // thread t sums bins from the top: 4 (NT - 1 - t) ..
         const int bin = 4 * (NT - 1 - tid);
-        uint4 v = make_uint4(0, 0, 0, 0);
-        for (int c = 0; c < C; ++c) {
-            const uint4 x = *reinterpret_cast<const uint4*>(C > 1 ? cluster.map_shared_rank(&st.hist[pass][bin], c) : &st.hist[pass][bin]);
-            v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
+        uint4 v = *reinterpret_cast<const uint4*>(&st.hist[pass][bin]);
+        if (C > 1) {
+            uint4 x[8];
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+                x[c] = make_uint4(0, 0, 0, 0);
+                if (c < C && c != rank) x[c] = *reinterpret_cast<const uint4*>(cluster.map_shared_rank(&st.hist[pass][bin], c));
+            }
+#pragma unroll
+            for (int c = 0; c < 8; ++c) v.x += x[c].x, v.y += x[c].y, v.z += x[c].z, v.w += x[c].w;
         }
-        unsigned long long all;
-        unsigned above = (unsigned)kv_block_before(st, (unsigned long long)v.x + v.y + v.z + v.w, all);
-        if (above < need && need <= above + v.x + v.y + v.z + v.w) {
+        const unsigned mine = v.x + v.y + v.z + v.w;
+        unsigned inc = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const unsigned y = __shfl_up_sync(FULL_MASK, inc, o);
+            if (lane >= o) inc += y;
+        }
+        if (lane == 31) st.warp_sum[warp] = inc;
+        __syncthreads();
+        unsigned warps = lane < warp ? st.warp_sum[lane & (WARPS - 1)] : 0;  // (warp < 16 lanes)
+#pragma unroll
+        for (int o = 8; o; o >>= 1) warps += __shfl_xor_sync(FULL_MASK, warps, o);
+        unsigned above = __shfl_sync(FULL_MASK, warps, 0) + inc - mine;
+        if (above < need && need <= above + mine) {
             int d = bin + 3;
             unsigned in = v.w;
             if (need > above + in) above += in, --d, in = v.z;
@@ -219,48 +264,102 @@ __global__ void __launch_bounds__(KV_SEL_NT) kv_select_kernel(const __grid_const
         prefix |= st.digit << shift, need = st.need;
     }
 
-    // entries above the threshold are kept, and the first `need` of those at it
-    const int run = (n + NT - 1) / NT, i0 = min(n, tid * run), i1 = min(n, i0 + run);
-    unsigned long long eq = 0, all;
-    for (int i = i0; i < i1; ++i) eq += key_of(i) == prefix;
-    unsigned long long eq_before = kv_block_before(st, eq, all);
-    const auto before_cta = [&](int which, unsigned long long mine) {  // sum over the cluster's CTAs before this one
-        if (C == 1) return 0ull;
-        if (tid == 0) st.total[which] = mine;
-        cluster.sync();
-        unsigned long long x = 0;
-        for (int c = 0; c < rank; ++c) x += *cluster.map_shared_rank(&st.total[which], c);
-        return x;
-    };
-    eq_before += before_cta(0, all);
-    unsigned long long count = 0;  // holes in the low half, fillers in the high one
-    unsigned left = eq_before < need ? need - (unsigned)eq_before : 0;  // of those at the threshold, still to keep
-    const unsigned left0 = left;
-    const auto walk = [&](auto&& hole, auto&& fill) {
-        left = left0;
-        for (int i = i0; i < i1; ++i) {
-            const uint32_t key = key_of(i);
-            bool kept = key > prefix;
-            if (key == prefix && left > 0) kept = true, --left;
-            const int e = e0 + i;
-            if (e < a.budget) {
-                if (!kept) hole(e);
-            } else if (kept) {
-                fill(e);
-            }
+    // ---- entries above the threshold are kept, and the first `need` of those at it. A lane takes four
+    // entries of its warp's run at a time, its warp 128.
+    const int run = align_up((n + WARPS - 1) / WARPS, 128), i0 = min(n, warp * run), i1 = min(n, i0 + run);
+    const auto four = [&](int i, uint32_t (&k)[4]) {  // keys of entries i .. i + 3 of the slice (0 past its end)
+        if (kept_here) {
+            const uint4 x = i < i1 ? *reinterpret_cast<const uint4*>(skey + i) : make_uint4(0, 0, 0, 0);
+            k[0] = x.x, k[1] = x.y, k[2] = x.z, k[3] = x.w;
+        } else {
+#pragma unroll
+            for (int y = 0; y < 4; ++y) k[y] = i + y < i1 ? form(i + y) : 0;
         }
     };
-    walk([&](int) { ++count; }, [&](int) { count += 1ull << 32; });
-    unsigned long long before = kv_block_before(st, count, all);
-    before += before_cta(1, all);
-    int ih = (int)(before & 0xffffffffu), jf = (int)(before >> 32);
+    KvCounts here{};
+    for (int i = i0 + 4 * lane; i < i1; i += 128) {
+        uint32_t k[4];
+        four(i, k);
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+            const bool in = i + y < i1, low = e0 + i + y < a.budget;
+            here.above_low += in && low && k[y] > prefix, here.above_high += in && !low && k[y] > prefix;
+            here.at_low += in && low && k[y] == prefix, here.at_high += in && !low && k[y] == prefix;
+        }
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1)
+        here = here + KvCounts{__shfl_xor_sync(FULL_MASK, here.above_low, o), __shfl_xor_sync(FULL_MASK, here.at_low, o),
+                               __shfl_xor_sync(FULL_MASK, here.above_high, o), __shfl_xor_sync(FULL_MASK, here.at_high, o)};
+    if (lane == 0) st.counts[warp] = here;
+    __syncthreads();
+    KvCounts before{}, all{};  // in the CTA before this warp's run; in the whole line
+    for (int w = 0; w < WARPS; ++w) {
+        const KvCounts x = st.counts[w];
+        if (w < warp) before = before + x;
+        all = all + x;
+    }
+    if (C > 1) {
+        if (tid == 0) st.total = all;
+        cluster.sync();
+        all = KvCounts{};
+        for (int c = 0; c < C; ++c) {
+            const KvCounts x = *cluster.map_shared_rank(&st.total, c);
+            if (c < rank) before = before + x;
+            all = all + x;
+        }
+        cluster.sync();  // nobody leaves while its counts may be read
+    }
+    // Places on the lists. Entries at the threshold are kept in their order: those below the budget, which
+    // come first, while `need` lasts.
+    unsigned at_before = before.at_low + before.at_high;
+    const unsigned kept_low = min(need, all.at_low);  // of those at the threshold
+    unsigned hole = (unsigned)min(e0 + i0, a.budget) - before.above_low - min(need, before.at_low);
+    unsigned fill = before.above_high + min(need, at_before) - min(need, before.at_low);
     int32_t *holes = list + 4, *fills = holes + align_up(cap, 4);
-    walk([&](int e) { holes[ih++] = e; }, [&](int e) { fills[jf++] = e; });
-    if (rank == C - 1 && tid == NT - 1) list[0] = ih;  // all of them: the last thread's count ends the line
-    if (C > 1) cluster.sync();  // nobody leaves while its sums may be read
+    for (int base = i0; base < i1; base += 128) {
+        const int i = base + 4 * lane;
+        uint32_t k[4];
+        four(i, k);
+        // of the lane's entries: at the threshold; then holes and fillers
+        unsigned at = 0, mine = 0;
+#pragma unroll
+        for (int y = 0; y < 4; ++y) at += i + y < i1 && k[y] == prefix;
+        unsigned inc = at;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const unsigned x = __shfl_up_sync(FULL_MASK, inc, o);
+            if (lane >= o) inc += x;
+        }
+        unsigned at_here = at_before + inc - at;
+        bool hole_y[4], fill_y[4];
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+            const bool in = i + y < i1, low = e0 + i + y < a.budget, eq = in && k[y] == prefix;
+            const bool kept = (in && k[y] > prefix) || (eq && at_here < need);
+            at_here += eq;
+            hole_y[y] = in && low && !kept, fill_y[y] = kept && !low;
+            mine += (hole_y[y] ? 1u : 0u) + (fill_y[y] ? 0x10000u : 0u);
+        }
+        unsigned line = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const unsigned x = __shfl_up_sync(FULL_MASK, line, o);
+            if (lane >= o) line += x;
+        }
+        unsigned ih = hole + ((line - mine) & 0xffffu), jf = fill + ((line - mine) >> 16);
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+            if (hole_y[y]) holes[ih++] = e0 + i + y;
+            if (fill_y[y]) fills[jf++] = e0 + i + y;
+        }
+        const unsigned all_here = __shfl_sync(FULL_MASK, line, 31);
+        hole += all_here & 0xffffu, fill += all_here >> 16, at_before += __shfl_sync(FULL_MASK, inc, 31);
+    }
+    if (rank == 0 && tid == 0) list[0] = a.budget - (int)(all.above_low + kept_low);
 }
 
-// The moves of every unit. A warp takes 32 of them: a lane finds a move's rows, then all lanes copy the
+// The moves of every unit. A warp takes some of them: a lane finds a move's rows, then all lanes copy the
 // rows' 16-byte pieces, eight in flight each (a warp a row, one load after the other, took three times
 // as long). pieces: of a key and a value row together; magic: its reciprocal, 2^32 / pieces rounded up.
 constexpr int KV_MOVE_NT = 256, KV_MOVE_AHEAD = 8;
@@ -284,8 +383,10 @@ __global__ void __launch_bounds__(KV_MOVE_NT) kv_move_kernel(const __grid_consta
     const int32_t *holes = list + 4, *fills = holes + align_up(cap, 4);
     const int32_t* table = a.page_table + (int64_t)slot * a.max_pages;
     if (h == 0 && blockIdx.y == 0 && threadIdx.x == 0) a.lengths[slot] = a.budget;
-    for (int first = (blockIdx.y * (KV_MOVE_NT / 32) + warp) * 32; first < n; first += gridDim.y * KV_MOVE_NT) {
-        const int some = min(32, n - first);
+    // up to 32 moves a warp at a time, fewer where there are more warps than that
+    const int warps = gridDim.y * (KV_MOVE_NT / 32), chunk = min(32, (n + warps - 1) / warps);
+    for (int first = (blockIdx.y * (KV_MOVE_NT / 32) + warp) * chunk; first < n; first += warps * chunk) {
+        const int some = min(chunk, n - first);
         __syncwarp();
         if (lane < some) {
             const int to = holes[first + lane], from = fills[first + lane];

@@ -22,7 +22,7 @@ cudaError_t launch_kv_evict(const KvArgs& a, int cap, bool vec, cudaStream_t str
     // CTAs a unit: as many as keep every SM at one or two, with no less than 1024 entries each
     int C = 1;
     while (C < 8 && units * C * 2 <= 2 * di.sms && room / (C * 2) >= 1024) C *= 2;
-    const int64_t per = (room + C - 1) / C + 4, words = per + per / 32 + 1, most = 45 * 1024;
+    const int64_t words = ((room + C - 1) / C + 7) / 4 * 4, most = 45 * 1024;
     const int keys_cap = (int)(words < most ? words : most);
     const int smem = (int)sizeof(KvSelect) + keys_cap * 4;
     int bps = 0;
@@ -39,7 +39,7 @@ cudaError_t launch_kv_evict(const KvArgs& a, int cap, bool vec, cudaStream_t str
     if ((e = cudaLaunchKernelEx(&cfg, kv_select_kernel, a, cap, keys_cap, (int)vec4)) != cudaSuccess) return e;
 
     // enough CTAs that the rows of few units still spread over the device
-    const int64_t want = (1024 + units - 1) / units, rows = (cap + KV_MOVE_NT - 1) / KV_MOVE_NT;
+    const int64_t want = (1024 + units - 1) / units, rows = (cap + 31) / 32;  // four moves a warp at least
     const int esz = dtype_size(a.dtype), piece = vec ? 16 : 2, pieces = 2 * a.d * esz / piece;
     cudaLaunchConfig_t mv{};
     mv.gridDim = dim3((unsigned)units, (unsigned)(want < rows ? want : rows)), mv.blockDim = dim3(KV_MOVE_NT);
