@@ -105,10 +105,10 @@ template <bool ATTN>
 __device__ __forceinline__ int kv_row_blocks(const KvArgs& a, const KvSeq& s) {
     return ATTN ? (s.nodes * a.G + a.row_block - 1) / a.row_block : 1;
 }
-// Cost tiles of a unit, by kernel (128-key tiles: the tensor-core kernels).
+// Cost tiles of a unit.
 template <bool ATTN, int KT>
 __host__ __device__ constexpr int kv_extra() {
-    return KT == 128 ? (ATTN ? 2 : 1) : 0;
+    return ATTN ? 2 : 1;
 }
 // The sequence's share of the line.
 template <bool ATTN, int KT>
