@@ -58,6 +58,7 @@ constexpr int BOX = 64;       // elements of d in one TMA box (128 bytes)
 constexpr int BOX_BYTES = KT * BOX * 2;
 constexpr float REF_NONE = -3.0e38f;  // reference of a row without a key yet
 constexpr float REF_SLACK = 8.f;
+constexpr float FUSED_MOST = 16777216.f;  // references up to which exponents are formed in one rounding
 constexpr int MAX_STAGES = 14;
 
 struct Maps {
@@ -85,7 +86,7 @@ struct __align__(16) State {
     Table<NR> table[2];       // of this segment and the next
     uint64_t table_full[2], table_empty[2], seg_loaded[2];
     KvScan<threads(NR)> scan;
-    int gave_up[4], v_stage;
+    int gave_up[4], big[4], v_stage;
     uint32_t tmem;
 };
 
@@ -307,7 +308,7 @@ __global__ void __launch_bounds__(kvt::threads(NR), 1)
             mbar_init(&st.table_full[lane], 1), mbar_init(&st.table_empty[lane], SM_WARPS), mbar_init(&st.seg_loaded[lane], 1);
         }
         if (lane == 2) mbar_init(&st.q_full, 1), mbar_init(&st.v_ok, 1), mbar_init(&st.drain[0], 1), mbar_init(&st.drain[1], 1);
-        if (lane < 4) st.gave_up[lane] = 0;
+        if (lane < 4) st.gave_up[lane] = 0, st.big[lane] = 0;
         fence_barrier_init();
     }
     if (warp == O_WARP) {
@@ -527,7 +528,7 @@ __global__ void __launch_bounds__(kvt::threads(NR), 1)
         const uint32_t lane_base = (uint32_t)(quad * 32) << 16;
         // (a scale of zero as the smallest normal number: -inf times it stays -inf)
         const float c2 = a.scale == 0.f ? 1.1754944e-38f : a.scale * LOG2E;
-        const Two cc = two(c2, c2);
+        const Two cc = two(c2, c2), one = two(1.f, 1.f);
         const int64_t part_floats = kv_part_floats(NR, a.d);
         uint32_t n_t = 0, n_v = 0, seg = 0;  // tiles, v_ok rounds and segments so far
         bool failed = false, stop = false;   // stop: the whole group gives up
@@ -540,6 +541,7 @@ __global__ void __launch_bounds__(kvt::threads(NR), 1)
             failed = failed || !mbar_wait(&st.table_full[side], (seg >> 1) & 1);
 #pragma unroll
             for (int r = 0; r < NRH / 2; ++r) l[r] = 0;
+            bool big = false;
 
             for (int i = 0; i < n; ++i, ++n_t) {
                 const int t = w.t0 + i, buf = n_t & 1;
@@ -564,10 +566,26 @@ __global__ void __launch_bounds__(kvt::threads(NR), 1)
                         tc::tmem_st<8>(tm_s + r, x);
                     }
                 }
+                // Exponents c s - m are fused, one rounding: exact enough while a product's own rounding is under
+                // one. Where a reference is larger, the segment goes on with scores that are scaled first, so
+                // that the largest exponent is zero still.
+                bool again = false;
+                const auto scale_tile = [&]() {
+#pragma unroll 1
+                    for (int r = 0; r < NRH; r += 8) {
+                        float x[8];
+                        tc::tmem_ld<8>(tm_s + r, x);
+#pragma unroll
+                        for (int y = 0; y < 8; ++y) x[y] *= c2;
+                        tc::tmem_st<8>(tm_s + r, x);
+                    }
+                };
+                if (big) scale_tile();
                 // sixteen scores at a time: 32 beside the 32 sums do not fit the registers of 20 warps, and are
                 // read from tensor memory a second time below
                 constexpr int CH = NRH < 16 ? NRH : 16;
                 float s[CH];
+                const Two cf0 = big ? one : cc;
                 float over = -INFINITY;  // the largest exponent against the references
 #pragma unroll
                 for (int r0 = 0; r0 < NRH; r0 += CH) {
@@ -575,8 +593,8 @@ __global__ void __launch_bounds__(kvt::threads(NR), 1)
 #pragma unroll
                     for (int r = 0; r < CH; r += 4) {
                         const ulonglong2 m = *reinterpret_cast<const ulonglong2*>(&st.nref[g0 + r0 + r]);
-                        const float2 x = parts(fma2(two(s[r], s[r + 1]), cc, m.x));
-                        const float2 y = parts(fma2(two(s[r + 2], s[r + 3]), cc, m.y));
+                        const float2 x = parts(fma2(two(s[r], s[r + 1]), cf0, m.x));
+                        const float2 y = parts(fma2(two(s[r + 2], s[r + 3]), cf0, m.y));
                         over = max3(max3(over, x.x, x.y), y.x, y.y);
                     }
                 }
@@ -595,7 +613,7 @@ __global__ void __launch_bounds__(kvt::threads(NR), 1)
                         tc::tmem_ld<8>(tm_s + r, x);
 #pragma unroll
                         for (int y = 0; y < 8; ++y) {
-                            x[y] = warp_max(dead ? -INFINITY : x[y] * c2);
+                            x[y] = warp_max(dead ? -INFINITY : big ? x[y] : x[y] * c2);
                             if (lane == y) st.warp_max[quad][g0 + r + y] = x[y];
                         }
                     }
@@ -605,11 +623,12 @@ __global__ void __launch_bounds__(kvt::threads(NR), 1)
                         const float old = -st.nref[r];
                         float m = fmaxf(fmaxf(st.warp_max[0][r], st.warp_max[1][r]),
                                         fmaxf(st.warp_max[2][r], st.warp_max[3][r]));
-                        // an ulp up: the weights' exponents come from one fused rounding, the maximum from two
-                        m = fmaxf(fmaf(fabsf(m), 1.1920929e-7f, m), old);
+                        m = fmaxf(m, old);
+                        if (fabsf(m) > FUSED_MOST && m > REF_NONE) st.big[g] = 1;
                         st.factor[r] = kv_ex2(old - m), st.nref[r] = -m;
                     }
                     group_sync(g);
+                    if (!big && st.big[g]) big = true, again = true, scale_tile();
                     if (i > 0) {  // the sums and the accumulator, once the last tile's product is in it
 #pragma unroll
                         for (int r = 0; r < NRH; r += 2) {
@@ -636,10 +655,11 @@ __global__ void __launch_bounds__(kvt::threads(NR), 1)
                 // weights: FP32 sums, rounded once to the cache's type for the product with the values
                 const int pbuf = n_t & pb;
                 unsigned char* dst = sP + pbuf * p_bytes<NR>() + g * (NRH / 8) * (KT * 16) + key * 16;
+                const Two cf = big ? one : cc;
                 uint32_t u[NRH / 2];
 #pragma unroll
                 for (int r0 = 0; r0 < NRH; r0 += CH) {
-                    if (NRH > CH) tc::tmem_ld<CH>(tm_s + r0, s);
+                    if (NRH > CH || again) tc::tmem_ld<CH>(tm_s + r0, s);
                     if (r0 + CH >= NRH) {  // the scores are read
                         tc::fence_before();
                         __syncwarp();
@@ -652,8 +672,8 @@ __global__ void __launch_bounds__(kvt::threads(NR), 1)
                             for (int x = 0; x < 8; x += 4) {
                                 const int i2 = (r0 + r + x) / 2;
                                 const ulonglong2 m = *reinterpret_cast<const ulonglong2*>(&st.nref[g0 + r0 + r + x]);
-                                float2 y = parts(fma2(two(s[r + x], s[r + x + 1]), cc, m.x));
-                                float2 z = parts(fma2(two(s[r + x + 2], s[r + x + 3]), cc, m.y));
+                                float2 y = parts(fma2(two(s[r + x], s[r + x + 1]), cf, m.x));
+                                float2 z = parts(fma2(two(s[r + x + 2], s[r + x + 3]), cf, m.y));
                                 y = make_float2(kv_ex2(y.x), kv_ex2(y.y)), z = make_float2(kv_ex2(z.x), kv_ex2(z.y));
                                 l[i2] = add2(l[i2], two(y.x, y.y)), l[i2 + 1] = add2(l[i2 + 1], two(z.x, z.y));
                                 u[i2] = H::pack(y.x, y.y), u[i2 + 1] = H::pack(z.x, z.y);
@@ -713,6 +733,7 @@ __global__ void __launch_bounds__(kvt::threads(NR), 1)
                         a.lse[tb.row[r]] = sum == 0.f ? -INFINITY : (log2f(sum) - st.nref[r]) * LN2;
                 }
                 st.nref[r] = -REF_NONE;  // for the next segment
+                st.big[g] = 0;
             }
             group_sync(g);
             failed = failed || !mbar_wait(&st.p_empty[(n_t - 1) & pb], ((n_t - 1) >> pb) & 1);

@@ -7,6 +7,8 @@ import math
 import numpy as np
 import torch
 
+from tests.gpu_util import canaries_intact, guarded
+
 TORCH = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}
 UNIT = {"f32": 2.0 ** -24, "bf16": 2.0 ** -8, "f16": 2.0 ** -11}  # largest relative rounding error
 
@@ -219,15 +221,16 @@ class Case:
                                      self.stamps)
 
     def attend(self, stream=None, with_nodes=True, with_lse=True):
-        out = torch.full(self.q.shape, 7.0, dtype=self.q.dtype, device="cuda")
-        lse = torch.full(self.q.shape[:3], 7.0, device="cuda") if with_lse else None
-        ws = self.kv.kv_tree_workspace(self.cache, self.q)
-        ws.view(torch.float32).fill_(float("nan"))
+        guards = []  # poisoned bytes around everything the call writes
+        out = guarded(self.q.shape, self.q.dtype, guards).fill_(7.0)
+        lse = guarded(self.q.shape[:3], torch.float32, guards).fill_(7.0) if with_lse else None
+        ws = guarded((self.kv.kv_tree_workspace(self.cache, self.q).numel(),), torch.uint8, guards).fill_(0xFF)
         torch.cuda.synchronize()
         self.kv.kv_tree_attention(self.cache, self.d_slots, self.q, self.kn, self.vn, self.d_mask, out, self.err, ws,
                                   num_nodes=self.d_nodes if with_nodes else None, lse=lse, scale=self.scale,
                                   stream=stream)
         torch.cuda.synchronize()
+        assert canaries_intact(guards)
         return out, lse
 
     def reference(self):

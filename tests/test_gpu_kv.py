@@ -162,6 +162,52 @@ def test_long_sequences_over_many_blocks(dtype):
     assert torch.equal(a, b) and torch.equal(za, zb)  # one order of additions
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_one_unit_over_the_whole_grid(dtype):
+    """A single key head of one long sequence: more partial results than a warp has lanes."""
+    Case(19, dtype, [21003], T=2, Hq=2, Hkv=1, d=64, page=64).check_attention()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_scores_beyond_the_rounding_of_one(dtype):
+    """Scores near 1e9, whose own rounding is dozens: the largest still takes the row."""
+    c = Case(24, dtype, [300], T=2, Hq=2, Hkv=1, d=64, page=16)
+    c.q[:], c.kn[:] = 0, 0
+    c.q[..., 0] = 30000.0
+    c.k[torch.from_numpy(c.table[c.slots[0], :19]).long()] = 0
+    for e in range(300):  # entry 271 leads by far
+        c.k[int(c.table[c.slots[0], e // 16]), :, e % 16, 0] = 30000.0 if e == 271 else 20000.0 - e
+    c.scale = 1.0
+    c.sync()
+    out, lse = c.attend()
+    want = host(c.v[int(c.table[c.slots[0], 271 // 16]), 0, 271 % 16])
+    assert (np.abs(host(out) - want) <= 2 * ref.UNIT[dtype] * np.abs(want) + 1e-6).all()
+    assert np.isfinite(host(lse)).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_calls_in_a_graph(dtype):
+    """Every call can be captured (none synchronises or allocates) and replayed on new contents."""
+    c = Case(25, dtype, [60, 200], T=3, Hq=4, Hkv=2, d=64, page=16, room=3)
+    plain, lse = c.attend()
+    out, lse = torch.empty_like(plain), torch.empty_like(lse)
+    ws, ev = kv.kv_tree_workspace(c.cache, c.q), kv.kv_evict_workspace(c.cache, 2, 100)
+    path = torch.tensor([[0, 1], [0, 2]], dtype=torch.int32, device="cuda")
+    n = torch.tensor([2, 1], dtype=torch.int32, device="cuda")
+    want = c.pools()
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.graph(graph, stream=side):
+        kv.kv_tree_attention(c.cache, c.d_slots, c.q, c.kn, c.vn, c.d_mask, out, c.err, ws, lse=lse, scale=c.scale)
+        kv.kv_commit(c.cache, c.d_slots, c.kn, c.vn, path, n, c.err)
+        kv.kv_accumulate(c.cache, c.d_slots, c.q, lse, path, n, c.err, scale=c.scale)
+        kv.kv_evict(c.cache, c.d_slots, 100, 20, c.err, ev)
+    c.assert_pools(want)  # capturing ran nothing
+    graph.replay()
+    torch.cuda.synchronize()
+    assert int(c.err.item()) == 0 and torch.equal(out, plain)
+    assert c.d_lengths[c.d_slots.long()].tolist() == [62, 100]
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_optional_outputs_and_counts(dtype):
     c = Case(15, dtype, [90, 4], T=3, Hq=4, Hkv=2, d=64, page=16)
@@ -335,6 +381,16 @@ def test_commit_then_accumulate_is_the_attention_given(dtype):
         assert abs(total - 2 * npath[b]) < 1e-4 * 2 * npath[b]
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_accumulate_many_sequences(dtype):
+    r = np.random.default_rng(5)
+    lens = [int(x) for x in r.integers(2, 12, 700)]
+    c = Case(34, dtype, lens, T=2, Hq=2, Hkv=1, d=32, page=8, pad=tuple(range(3, 700, 10)))
+    path, npath = _paths(c, 2, [int(x) for x in r.integers(0, 3, 700)])
+    _accumulate(c, path, npath, 0.5, torch.full((700, 2, 2), 2.0, device="cuda"))
+    assert int(c.err.item()) == 0
+
+
 def test_accumulate_refusals():
     c = Case(33, "bf16", [20, 2, 30, 40], T=4, Hq=2, Hkv=2, d=64, page=16)
     path = np.tile(np.arange(4, dtype=np.int32), (4, 1))
@@ -433,3 +489,45 @@ def test_evict_refusals():
     assert int(c.err.item()) == kv.DEVERR_PAGE | kv.DEVERR_LENGTH | gdn.DEVERR_SLOT
     c.assert_pools(want)
     assert np.array_equal(c.d_lengths.cpu().numpy(), c.lengths)
+
+
+def test_evict_offsets_past_32_bits():
+    """Pages more than 2^31 elements into the pools of keys and values."""
+    page, H, d = 64, 2, 128
+    num = (1 << 31) // (page * H * d) + 6
+    c = Case(45, "bf16", [page * 3], T=1, Hq=2, Hkv=H, d=d, page=page)
+    _scramble(c)
+    want = c.pools()
+    lengths = c.lengths.copy()
+    ref.evict(want, c.table, lengths, c.counts, c.slots, 100, 10)
+    used, far = c.table[c.slots[0], :3].copy(), [num - 2, 1, num - 1]
+    k = torch.empty(num, H, page, d, dtype=torch.bfloat16, device="cuda")
+    v = torch.empty_like(k)
+    w = torch.zeros(num, H, page, device="cuda")
+    s = torch.zeros(num, H, page, dtype=torch.int32, device="cuda")
+    for i, f in enumerate(far):
+        u = int(used[i])
+        k[f], v[f], w[f], s[f] = c.k[u], c.v[u], c.weights[u], c.stamps[u]
+        c.table[c.slots[0], i] = f
+    c.k, c.v, c.weights, c.stamps = k, v, w, s
+    c.sync()
+    kv.kv_evict(c.cache, c.d_slots, 100, 10, c.err, kv.kv_evict_workspace(c.cache, 1, 100))
+    assert int(c.err.item()) == 0
+    for i, f in enumerate(far):
+        u = int(used[i])
+        assert np.array_equal(host(k[f]), want["k"][u]) and np.array_equal(host(v[f]), want["v"][u])
+        assert np.array_equal(w[f].cpu().numpy(), want["weights"][u]) and np.array_equal(s[f].cpu().numpy(), want["stamps"][u])
+
+
+# ---------------------------------------------------------------- together
+
+
+def test_speculative_decoding_gives_the_tokens_of_plain_decoding():
+    """The example: verified trees of a hybrid model against one token at a time, and with a budget."""
+    from examples import hybrid_tree_verify as ex
+
+    plain, said, rounds, tree = ex.run(batch=3, steps=40)
+    assert int(tree.err.item()) == 0 and plain == said and rounds < 40
+    _, _, _, tree = ex.run(batch=2, steps=60, budget=32, recent=8)
+    assert int(tree.err.item()) == 0
+    assert tree.cache.lengths.tolist() == [32, 32] and min(tree.cache.counts.tolist()) >= 60
