@@ -528,7 +528,6 @@ __global__ void __launch_bounds__(kvt::threads(NR), 1)
         const uint32_t lane_base = (uint32_t)(quad * 32) << 16;
         // (a scale of zero as the smallest normal number: -inf times it stays -inf)
         const float c2 = a.scale == 0.f ? 1.1754944e-38f : a.scale * LOG2E;
-        const Two cc = two(c2, c2), one = two(1.f, 1.f);
         const int64_t part_floats = kv_part_floats(NR, a.d);
         uint32_t n_t = 0, n_v = 0, seg = 0;  // tiles, v_ok rounds and segments so far
         bool failed = false, stop = false;   // stop: the whole group gives up
@@ -585,17 +584,17 @@ __global__ void __launch_bounds__(kvt::threads(NR), 1)
                 // read from tensor memory a second time below
                 constexpr int CH = NRH < 16 ? NRH : 16;
                 float s[CH];
-                const Two cf0 = big ? one : cc;
+                const float cf = big ? 1.f : c2;
                 float over = -INFINITY;  // the largest exponent against the references
 #pragma unroll
                 for (int r0 = 0; r0 < NRH; r0 += CH) {
                     tc::tmem_ld<CH>(tm_s + r0, s);
 #pragma unroll
                     for (int r = 0; r < CH; r += 4) {
-                        const ulonglong2 m = *reinterpret_cast<const ulonglong2*>(&st.nref[g0 + r0 + r]);
-                        const float2 x = parts(fma2(two(s[r], s[r + 1]), cf0, m.x));
-                        const float2 y = parts(fma2(two(s[r + 2], s[r + 3]), cf0, m.y));
-                        over = max3(max3(over, x.x, x.y), y.x, y.y);
+                        // (one at a time: pairs cost two moves each out of the registers that tensor memory fills)
+                        const float4 m = *reinterpret_cast<const float4*>(&st.nref[g0 + r0 + r]);
+                        over = max3(max3(over, fmaf(s[r], cf, m.x), fmaf(s[r + 1], cf, m.y)), fmaf(s[r + 2], cf, m.z),
+                                    fmaf(s[r + 3], cf, m.w));
                     }
                 }
                 if (dead) over = -INFINITY;
@@ -655,7 +654,7 @@ __global__ void __launch_bounds__(kvt::threads(NR), 1)
                 // weights: FP32 sums, rounded once to the cache's type for the product with the values
                 const int pbuf = n_t & pb;
                 unsigned char* dst = sP + pbuf * p_bytes<NR>() + g * (NRH / 8) * (KT * 16) + key * 16;
-                const Two cf = big ? one : cc;
+                const float ce = big ? 1.f : c2;
                 uint32_t u[NRH / 2];
 #pragma unroll
                 for (int r0 = 0; r0 < NRH; r0 += CH) {
@@ -671,12 +670,11 @@ __global__ void __launch_bounds__(kvt::threads(NR), 1)
 #pragma unroll
                             for (int x = 0; x < 8; x += 4) {
                                 const int i2 = (r0 + r + x) / 2;
-                                const ulonglong2 m = *reinterpret_cast<const ulonglong2*>(&st.nref[g0 + r0 + r + x]);
-                                float2 y = parts(fma2(two(s[r + x], s[r + x + 1]), cf, m.x));
-                                float2 z = parts(fma2(two(s[r + x + 2], s[r + x + 3]), cf, m.y));
-                                y = make_float2(kv_ex2(y.x), kv_ex2(y.y)), z = make_float2(kv_ex2(z.x), kv_ex2(z.y));
-                                l[i2] = add2(l[i2], two(y.x, y.y)), l[i2 + 1] = add2(l[i2 + 1], two(z.x, z.y));
-                                u[i2] = H::pack(y.x, y.y), u[i2 + 1] = H::pack(z.x, z.y);
+                                const float4 m = *reinterpret_cast<const float4*>(&st.nref[g0 + r0 + r + x]);
+                                const float p0 = kv_ex2(fmaf(s[r + x], ce, m.x)), p1 = kv_ex2(fmaf(s[r + x + 1], ce, m.y));
+                                const float p2 = kv_ex2(fmaf(s[r + x + 2], ce, m.z)), p3 = kv_ex2(fmaf(s[r + x + 3], ce, m.w));
+                                l[i2] = add2(l[i2], two(p0, p1)), l[i2 + 1] = add2(l[i2 + 1], two(p2, p3));
+                                u[i2] = H::pack(p0, p1), u[i2 + 1] = H::pack(p2, p3);
                             }
                         }
                     } else {

@@ -190,7 +190,7 @@ __global__ void __launch_bounds__(kvw::NT, 1)
         // ------------------------------------------------------------ weights
         const int g = warp >> 2, quad = warp & 3, key = quad * 32 + lane, wt = tid & 255;
         const uint32_t tm_s = tmem + ((uint32_t)(quad * 32) << 16) + g * NR;
-        const kvt::Two scale = kvt::two(a.scale, a.scale), log2e = kvt::two(LOG2E, LOG2E);
+        const kvt::Two log2e = kvt::two(LOG2E, LOG2E);
         uint32_t n_t = 0, seg = 0;
         int checked = -1;
         bool good = true, failed = false;
@@ -261,11 +261,13 @@ __global__ void __launch_bounds__(kvw::NT, 1)
                         tc::tmem_ld<16>(tm_s + r, s);
 #pragma unroll
                         for (int y = 0; y < 16; y += 4) {
-                            const ulonglong2 m = *reinterpret_cast<const ulonglong2*>(&st.nlse[r + y]);
+                            const float4 m = *reinterpret_cast<const float4*>(&st.nlse[r + y]);
                             // the exponent is formed before it is scaled to base 2: a weight near one keeps a
                             // small one
-                            float2 u = kvt::parts(kvt::mul2(kvt::fma2(kvt::two(s[y], s[y + 1]), scale, m.x), log2e));
-                            float2 v = kvt::parts(kvt::mul2(kvt::fma2(kvt::two(s[y + 2], s[y + 3]), scale, m.y), log2e));
+                            const float x0 = fmaf(s[y], a.scale, m.x), x1 = fmaf(s[y + 1], a.scale, m.y);
+                            const float x2 = fmaf(s[y + 2], a.scale, m.z), x3 = fmaf(s[y + 3], a.scale, m.w);
+                            float2 u = kvt::parts(kvt::mul2(kvt::two(x0, x1), log2e));
+                            float2 v = kvt::parts(kvt::mul2(kvt::two(x2, x3), log2e));
                             u = make_float2(kv_ex2(u.x), kv_ex2(u.y)), v = make_float2(kv_ex2(v.x), kv_ex2(v.y));
                             if (unseen > 0) {
                                 if (r + y < unseen) u.x = 0.f;
