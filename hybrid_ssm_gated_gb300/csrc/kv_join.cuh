@@ -1,11 +1,13 @@
 // kv_join.cuh -- joins the partial results of units whose key tiles span CTAs:
 // with m = max m_c, out = sum_c 2^{m_c - m} O_c / sum_c 2^{m_c - m} l_c.
 //
-// Bound by latency: a few hundred KB at most, read once. So a job is one row's
-// 128 outputs (16 bytes a lane), the parts of a unit with many are split over
-// the warps of a block, and the loads of a lane do not depend on one another.
-// (With one warp a row and the factors formed at every load it took 55 us of
-// a 63 us call: 32 rows of d = 256 in 7 parts.)
+// Bound by latency: a few megabytes at most, read once, in three dependent loads
+// (the border's record; maxima, sums and the first outputs; further outputs). So
+// a job is one row's 128 outputs (16 bytes a lane), many small blocks share a
+// border, and the code is short: it is fetched once a call. 4 us behind a short
+// call, 6 behind 152 CTAs with 64 rows each. (A warp a row with a factor formed
+// at every load took 55 us for 32 rows in 7 parts; four jobs a warp in straight
+// code 10 us.)
 #pragma once
 
 #include "kv_common.cuh"

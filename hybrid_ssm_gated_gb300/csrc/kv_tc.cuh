@@ -19,18 +19,20 @@
 // moves; otherwise a tile costs one barrier, which carries the vote.
 //
 // Kernel shape: persistent, one CTA per SM:
-//   softmax    NG groups of four warps (two up to 32 rows, four above: 16 or 32
-//              rows a thread keep scores and sums in registers); group g owns
-//              NR / NG query rows (columns of S^T and O^T), thread key
+//   softmax    NG groups of four warps (two up to 32 rows, four above); group g
+//              owns NR / NG query rows (columns of S^T and O^T), thread key
 //              (warp % 4) * 32 + lane = its tensor-memory lane;
-//   loads      a warp for K and one for V: tiles by TMA, each into a ring of
-//              stages of 128 keys x 128 elements (64 where d <= 64), 128-byte
-//              swizzle, boxes of as many keys as a page and the tile share. A
-//              warp needs about 80 cycles a box: with pages of 16 entries one
-//              warp for both took 4400 cycles a tile, where HBM takes 2800;
-//   MMAs       a thread for S^T and one for O^T: the issue of a tile's eight
-//              products takes several hundred cycles. S^T runs up to two tiles
-//              ahead, so that the tensor cores work while weights form.
+//   K, V       a warp each: tiles by TMA into a ring of stages of 128 keys x 128
+//              elements (64 where d <= 64), 128-byte swizzle, boxes of as many
+//              keys as a page and the tile share. A warp needs about 80 cycles a
+//              box: with pages of 16 entries one warp for both took 4400 cycles
+//              a tile, where HBM takes 2800. The K warp also writes the tables
+//              of a segment's rows ahead of the softmax warps, and looks at the
+//              pages that it loads;
+//   S^T, O^T   a warp each, one elected thread of which issues the products from
+//              uniform registers. The S^T warp loads a segment's queries beside
+//              the last one's end and runs up to two tiles ahead, so that the
+//              tensor cores work while weights form.
 // Each ring has one producer and one consumer, both in tile order: a barrier's
 // phase is never more than one ahead of its waiter. (In one ring for both, K
 // could reach a stage two rounds ahead of V, and a parity wait passes then.)
@@ -38,6 +40,20 @@
 // product transposed (MN-major); P^T is written by its threads, 16 bytes for
 // eight rows, in the unswizzled MN-major layout, which a warp fills without
 // bank conflicts. The drafted nodes are the unit's last tile.
+//
+// Bound and measurement (GB300, whole calls with the join). Up to 64 rows a key
+// head: HBM. A decode step of 64 sequences of up to 8192 tokens (32 / 8 heads,
+// d = 128, bf16, 1.32 GB) takes 204 us, 6.5 TB/s or 0.97 of the measured copy
+// bandwidth; 16-node trees over 32 x 4096 tokens (0.33 GB) 72 us, 0.69, of which
+// some 20 us are start, the units' ends and the join. At 128 rows the softmax
+// warps' chain bounds a tile (2800 cycles; the products take 1200): a 64-node
+// tree over 131072 tokens (0.54 GB, 137 GFLOP) 179 us, 770 TFLOP/s. Short calls
+// are latency: 10 us of steps (lengths, first tiles, maxima, outputs) and the
+// join's 4.
+// Measured and not taken: exponents before the vote instead of after it (the 64-
+// node tree 208 -> 248 us); a look at the next tile beside this one's exponents
+// with three buffers of S^T (179 -> 185, the 16-node trees 72 -> 76); two weight
+// buffers at 128 rows, which leave K a ring of one stage (179 -> 211).
 #pragma once
 
 #include <cuda.h>

@@ -6,7 +6,10 @@
 // key adds 2^{(scale s - lse) log2 e} over its NR columns and updates the one
 // weight it owns: no maximum, no sum across threads, no atomics.
 //
-// Bound: the keys' bytes (d x 2 a key and head, and 8 for the weight). Shape:
+// Bound: the keys' bytes (d x 2 a key and head, and 8 for the weight). Paths of up
+// to 4 nodes over 64 sequences of up to 8192 entries (32 / 8 heads, d = 128,
+// fp16, 0.66 GB): 115 us, 5.8 TB/s or 0.86 of the measured copy bandwidth (FP32
+// pipe: 1040 us). Shape:
 // persistent, one CTA per SM; one warp loads K tiles by TMA into a ring that
 // fills shared memory, one thread issues the MMAs, two groups of four warps
 // take tiles in turn, each with a buffer of S^T in tensor memory, so that one

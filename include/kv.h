@@ -50,6 +50,7 @@ extern "C" {
  * entries past a sequence's length are not read. A page may belong to several
  * sequences as long as no call writes it.
  *
+ * max_pages * page_size is at most 2^31 - 65536, d at most KV_MAX_D.
  * dtype      GDN_F32, GDN_BF16 or GDN_F16, of k and v.
  * lengths    [num_slots] int32, entries of each slot's sequence.
  * counts     [num_slots] int32, tokens ever committed to the slot (evicted
@@ -103,6 +104,12 @@ typedef struct kv_rows {
  * lse        [B][T][Hq] fp32, or NULL.
  * workspace  kv_tree_attention_workspace() bytes, 16-byte aligned; of one
  *            call at a time. Its contents need no initialisation.
+ * 16-bit caches whose pages hold a multiple of 8 entries, with d a multiple of
+ * 8 and bases and strides of 16 bytes, run on the tensor cores; everything
+ * else, fp32 caches among it, on the FP32 pipe. How a sequence's keys are
+ * split over the device, and so the order of its sums, depends on the sizes
+ * of the call and the other sequences' lengths; the same call gives the same
+ * bits.
  */
 int kv_tree_attention(const kv_cache* cache, int32_t B, int32_t T, int32_t Hq,
                       const int32_t* slots, const kv_rows* q, const kv_rows* k_new,
