@@ -66,6 +66,8 @@ int check_call(const char* fn, const int32_t* slots, const int32_t* dev_err) {
 int check_heads(const char* fn, const kv_cache* c, int32_t Hq, float scale) {
     if (Hq < 1 || Hq % c->Hkv != 0)
         return fail(GDN_ERR_SHAPE, "%s: Hq=%d is not a positive multiple of Hkv=%d", fn, Hq, c->Hkv);
+    // rows of a unit, KV_MAX_NODES x Hq / Hkv at most, are counted in 32 bits
+    if (Hq > 1 << 24) return fail(GDN_ERR_SHAPE, "%s: Hq=%d is more than 2^24", fn, Hq);
     if (!isfinite(scale)) return fail(GDN_ERR_SHAPE, "%s: scale is not finite", fn);
     return GDN_OK;
 }

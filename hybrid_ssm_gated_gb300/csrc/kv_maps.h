@@ -27,11 +27,14 @@ inline Encode encoder() {
 }
 
 // 16-bit rows [n3][n2][n1][d] with strides s3, s2, s1 (elements), boxes of `rows2` x `rows` x 64 elements in
-// the 128-byte swizzle; past the ends zeros are read.
+// the 128-byte swizzle; past the ends zeros are read. Rows that share memory (a stride of zero) or run
+// backwards are not described by a map: false, as where the driver refuses one.
 inline bool encode(CUtensorMap& m, int dtype, const void* p, int d, int64_t n1, int64_t s1, int64_t n2, int64_t s2, int64_t n3,
             int64_t s3, int rows, int rows2 = 1) {
     const cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)n1, (cuuint64_t)n2, (cuuint64_t)n3};
-    const cuuint64_t strides[3] = {(cuuint64_t)s1 * 2, (cuuint64_t)s2 * 2, (cuuint64_t)s3 * 2};
+    if ((n1 > 1 && s1 < 1) || (n2 > 1 && s2 < 1) || (n3 > 1 && s3 < 1)) return false;
+    const auto bytes = [&](int64_t n, int64_t st) { return (cuuint64_t)(n > 1 ? st : d) * 2; };  // of one: any
+    const cuuint64_t strides[3] = {bytes(n1, s1), bytes(n2, s2), bytes(n3, s3)};
     const cuuint32_t box[4] = {kvt::BOX, (cuuint32_t)rows, (cuuint32_t)rows2, 1}, unit[4] = {1, 1, 1, 1};
     return encoder()(&m, dtype == GDN_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
                      const_cast<void*>(p), dims, strides, box, unit, CU_TENSOR_MAP_INTERLEAVE_NONE,

@@ -96,7 +96,7 @@ typedef struct kv_rows {
  * cache the weights are rounded once to the cache's dtype before they meet
  * the values. The cache is not written.
  * slots      [B] int32.
- * q          [B][T][Hq][d];  k_new, v_new  [B][T][Hkv][d].
+ * q          [B][T][Hq][d];  k_new, v_new  [B][T][Hkv][d]; Hq at most 2^24.
  * mask       [B][T] 64-bit words. Bits >= num_nodes[b] are not looked at.
  * num_nodes  [B] int32, drafted nodes of each sequence (<= T; out and lse of
  *            the others are 0 and -inf); NULL: T for all.

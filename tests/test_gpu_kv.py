@@ -44,6 +44,28 @@ def test_tree_sizes(dtype, T, G):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("T", [1, 3])
+@pytest.mark.parametrize("G", [16, 71, 128, 160])
+@pytest.mark.parametrize("d", [64, 256])
+def test_many_heads_a_group(dtype, T, G, d):
+    """More query heads a key head than a block of rows takes, and numbers that no block divides by."""
+    Case(26, dtype, [70, 300], T=T, Hq=G, Hkv=1, d=d, page=16, nodes=[T, max(1, T - 1)]).check_attention()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("dims", [(0,), (2,), (0, 1, 2)], ids=str)
+def test_rows_shared_by_strides_of_zero(dtype, dims):
+    """Drafted keys, values and queries that sequences, heads or all have in common, without a copy."""
+    c = Case(27, dtype, [100, 20], T=3, Hq=4, Hkv=2, d=64, page=16)
+    for name in ("q", "kn", "vn"):
+        x = getattr(c, name)
+        for i in dims:
+            x = x.narrow(i, 0, 1)
+        setattr(c, name, x.expand_as(getattr(c, name)))
+    c.check_attention()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("d", [8, 40, 80, 96, 120, 192, 200])
 def test_head_sizes(dtype, d):
     Case(3, dtype, [133, 40], T=4, Hq=6, Hkv=3, d=d, page=16).check_attention()
@@ -349,6 +371,15 @@ def test_accumulate(dtype, d, page, kind, G):
     lse[1, path[1, 0], 0] = float("-inf")
     _accumulate(c, path, npath, 0.75, lse)
     assert int(c.err.item()) == 0
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("G", [16, 71, 160])
+@pytest.mark.parametrize("d", [64, 256])
+def test_accumulate_many_heads_a_group(dtype, G, d):
+    c = Case(35, dtype, [200, 41], T=3, Hq=G, Hkv=1, d=d, page=16)
+    path, npath = _paths(c, 2, [2, 1])
+    _accumulate(c, path, npath, 1.0, torch.full((2, 3, G), 5.0, device="cuda"))
 
 
 @pytest.mark.parametrize("dtype", DTYPES)

@@ -90,6 +90,7 @@ def test_attention_refusals(lib):
                                  None) == NULL
     assert _attend(lib, T=0) == WINDOW and _attend(lib, T=65) == WINDOW
     assert _attend(lib, Hq=3) == SHAPE and _attend(lib, Hq=0) == SHAPE and _attend(lib, B=-1) == SHAPE
+    assert _attend(lib, Hq=(1 << 24) + 2) == SHAPE
     assert _attend(lib, scale=float("nan")) == SHAPE and _attend(lib, scale=float("inf")) == SHAPE
     for name in ("slots", "mask", "out", "ws", "err"):
         assert _attend(lib, **{name: None}) == NULL, name
