@@ -32,7 +32,7 @@ constexpr int K_WARP = SM_WARPS, S_WARP = SM_WARPS + 1;
 
 template <int NR>
 struct __align__(16) State {
-    float nlse[NR];    // -lse of each row; -inf where the block has none (its weights are 0)
+    float nlse[NR];    // -lse of each row; -inf where the block has none, or its lse is -inf (its weights are 0)
     int64_t q_at[NR];  // element offset of each row's query
     uint64_t full[kvt::MAX_STAGES], empty[kvt::MAX_STAGES];
     uint64_t s_full[2], s_empty[2], q_full, q_empty, drain;
@@ -257,34 +257,46 @@ __global__ void __launch_bounds__(kvw::NT, 1)
                     const int unseen = max(0, e - (w.s.len - w.s.nodes)) * a.G - rb * NR;
                     failed = failed || !mbar_wait(&st.s_full[g], (n_t >> 1) & 1);
                     tc::fence_after();
-                    kvt::Two sum = 0;
+                    // Columns that add nothing (past the block's rows, or of a row without a log-sum-exp) do so by
+                    // their exponent of -inf. That is 0 for every finite score; a score that is not (0 x inf for
+                    // the zero queries of a column without a row) makes it NaN, and the sum with it. So a sum that
+                    // is NaN is formed again with those columns selected away, and no other needs the selection.
+                    kvt::Two sum;
+                    float total;
+                    bool select = false;
+                    while (true) {
+                        sum = 0;
 #pragma unroll 1
-                    for (int r = 0; r < NR; r += 16) {
-                        float s[16];
-                        tc::tmem_ld<16>(tm_s + r, s);
+                        for (int r = 0; r < NR; r += 16) {
+                            float s[16];
+                            tc::tmem_ld<16>(tm_s + r, s);
 #pragma unroll
-                        for (int y = 0; y < 16; y += 4) {
-                            const float4 m = *reinterpret_cast<const float4*>(&st.nlse[r + y]);
-                            // the exponent is formed before it is scaled to base 2: a weight near one keeps a
-                            // small one
-                            const float x0 = fmaf(s[y], a.scale, m.x), x1 = fmaf(s[y + 1], a.scale, m.y);
-                            const float x2 = fmaf(s[y + 2], a.scale, m.z), x3 = fmaf(s[y + 3], a.scale, m.w);
-                            float2 u = kvt::parts(kvt::mul2(kvt::two(x0, x1), log2e));
-                            float2 v = kvt::parts(kvt::mul2(kvt::two(x2, x3), log2e));
-                            u = make_float2(kv_ex2(u.x), kv_ex2(u.y)), v = make_float2(kv_ex2(v.x), kv_ex2(v.y));
-                            if (unseen > 0) {
-                                if (r + y < unseen) u.x = 0.f;
-                                if (r + y + 1 < unseen) u.y = 0.f;
-                                if (r + y + 2 < unseen) v.x = 0.f;
-                                if (r + y + 3 < unseen) v.y = 0.f;
+                            for (int y = 0; y < 16; y += 4) {
+                                const float4 m = *reinterpret_cast<const float4*>(&st.nlse[r + y]);
+                                // the exponent is formed before it is scaled to base 2: a weight near one keeps a
+                                // small one
+                                const float x0 = fmaf(s[y], a.scale, m.x), x1 = fmaf(s[y + 1], a.scale, m.y);
+                                const float x2 = fmaf(s[y + 2], a.scale, m.z), x3 = fmaf(s[y + 3], a.scale, m.w);
+                                float2 u = kvt::parts(kvt::mul2(kvt::two(x0, x1), log2e));
+                                float2 v = kvt::parts(kvt::mul2(kvt::two(x2, x3), log2e));
+                                u = make_float2(kv_ex2(u.x), kv_ex2(u.y)), v = make_float2(kv_ex2(v.x), kv_ex2(v.y));
+                                if (unseen > 0 || select) {
+                                    if (r + y < unseen || m.x == -INFINITY) u.x = 0.f;
+                                    if (r + y + 1 < unseen || m.y == -INFINITY) u.y = 0.f;
+                                    if (r + y + 2 < unseen || m.z == -INFINITY) v.x = 0.f;
+                                    if (r + y + 3 < unseen || m.w == -INFINITY) v.y = 0.f;
+                                }
+                                sum = kvt::add2(sum, kvt::add2(kvt::two(u.x, u.y), kvt::two(v.x, v.y)));
                             }
-                            sum = kvt::add2(sum, kvt::add2(kvt::two(u.x, u.y), kvt::two(v.x, v.y)));
                         }
+                        total = kvt::parts(sum).x + kvt::parts(sum).y;
+                        if (select || !__any_sync(FULL_MASK, live && total != total)) break;
+                        select = true;
                     }
                     tc::fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&st.s_empty[g]);
-                    if (live && !failed) *x = fmaf(old, rb == 0 ? a.decay : 1.f, kvt::parts(sum).x + kvt::parts(sum).y);
+                    if (live && !failed) *x = fmaf(old, rb == 0 ? a.decay : 1.f, total);
                 }
             }
         } while (w.next());
