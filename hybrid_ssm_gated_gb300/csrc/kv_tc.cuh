@@ -10,6 +10,14 @@
 // whatever the number of rows, and its share of the row sums stays in
 // registers until the unit ends.
 //
+// The sum over tiles. The tensor cores keep O^T in FP32 but cut each product
+// off at about 2^-25 of what the accumulator holds, always towards zero: over
+// 131072 entries the outputs came out 0.12% (equal weights) to 0.39% (one leader)
+// too small, and in proportion over more. So O^T is a sum over FOLD tiles (2048
+// entries, 2^-14 at most), and is then added to a second one in tensor memory,
+// by the softmax threads, which round to nearest. (FOLD 16 and 32 take the same
+// time: nothing where HBM bounds, 2% of the 64-node tree below.)
+//
 // The reference. m is not the running maximum but one that lags: as long as
 // no score of a tile exceeds m by more than REF_SLACK (in powers of two), the
 // tile's weights are formed against the old m, which is exact (numerator and
@@ -47,7 +55,7 @@
 // bandwidth; 16-node trees over 32 x 4096 tokens (0.33 GB) 72 us, 0.69, of which
 // some 20 us are start, the units' ends and the join. At 128 rows the softmax
 // warps' chain bounds a tile (2800 cycles; the products take 1200): a 64-node
-// tree over 131072 tokens (0.54 GB, 137 GFLOP) 179 us, 770 TFLOP/s. Short calls
+// tree over 131072 tokens (0.54 GB, 137 GFLOP) 184 us, 745 TFLOP/s. Short calls
 // are latency: 10 us of steps (lengths, first tiles, maxima, outputs) and the
 // join's 4.
 // Measured and not taken: exponents before the vote instead of after it (the 64-
@@ -75,6 +83,7 @@ constexpr int BOX_BYTES = KT * BOX * 2;
 constexpr float REF_NONE = -3.0e38f;  // reference of a row without a key yet
 constexpr float REF_SLACK = 8.f;
 constexpr float FUSED_MOST = 16777216.f;  // references up to which exponents are formed in one rounding
+constexpr int FOLD = 16;  // tiles of one sum in tensor memory
 constexpr int MAX_STAGES = 14;
 
 struct Maps {
@@ -308,8 +317,9 @@ __global__ void __launch_bounds__(kvt::threads(NR), 1)
     const int stages = k_stages + v_stages, pb = p_bufs - 1;  // tile n's weights: buffer n & pb, its use n >> pb
     State<NR>& st = *reinterpret_cast<State<NR>*>(ring + stages * stage_bytes);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    constexpr uint32_t TM_S = 0, TM_O = 2 * NR;  // tensor memory: two buffers of S^T, then O^T by halves of d
-    constexpr uint32_t TM_COLS = NR * 4;
+    constexpr uint32_t TM_S = 0, TM_O = 2 * NR;  // tensor memory: two buffers of S^T, then O^T by halves of d,
+    const uint32_t TM_F = TM_O + pairs * NR;     // then the sum of its folds, alike
+    const uint32_t TM_COLS = NR * (pairs > 1 ? 8 : 4);
 
     kv_grid_launch();
     if (warp == K_WARP) {
@@ -513,7 +523,7 @@ __global__ void __launch_bounds__(kvt::threads(NR), 1)
                         const uint64_t db = desc(aP + buf * p_bytes<NR>(), 128, KT * 16, SW_NONE);
 #pragma unroll
                         for (int k = 0; k < KT / 16; ++k)
-                            mma(tm + TM_O + p * NR, da + k * (2048 >> 4), db + k * (256 >> 4), id, i + k > 0);
+                            mma(tm + TM_O + p * NR, da + k * (2048 >> 4), db + k * (256 >> 4), id, i % FOLD + k > 0);
                     } else {
                         const uint64_t da = desc(in, 16, 1024, SW128), db = desc(aQ + 2 * p * NR * 128, 16, 1024, SW128);
 #pragma unroll
@@ -652,8 +662,9 @@ __global__ void __launch_bounds__(kvt::threads(NR), 1)
                         const uint32_t p = n_t - 1;
                         failed = failed || !mbar_wait(&st.p_empty[p & pb], (p >> pb) & 1);
                         tc::fence_after();
+                        const int blocks = i > FOLD ? 2 * pairs : pairs;  // O^T's, and its folds'
 #pragma unroll 1
-                        for (int hf = 0; hf < pairs; ++hf)
+                        for (int hf = 0; hf < blocks; ++hf)
 #pragma unroll 1
                             for (int r = 0; r < NRH; r += 8) {
                                 float o[8];
@@ -704,6 +715,26 @@ __global__ void __launch_bounds__(kvt::threads(NR), 1)
 #pragma unroll
                 for (int r = 0; r < NRH / 2; r += 4)
                     *reinterpret_cast<uint4*>(dst + (r / 4) * (KT * 16)) = make_uint4(u[r], u[r + 1], u[r + 2], u[r + 3]);
+                if (i > 0 && i % FOLD == 0) {  // O^T into its folds; this tile's product begins a new one
+                    const uint32_t p = n_t - 1;
+                    failed = failed || !mbar_wait(&st.p_empty[p & pb], (p >> pb) & 1);
+                    tc::fence_after();
+#pragma unroll 1
+                    for (int hf = 0; hf < pairs; ++hf)
+#pragma unroll 1
+                        for (int r = 0; r < NRH; r += 8) {
+                            float o[8], f[8];
+                            const uint32_t at = tmem + lane_base + hf * NR + g0 + r;
+                            __syncwarp();
+                            tc::tmem_ld<8>(at + TM_O, o);
+                            if (i > FOLD) {
+                                tc::tmem_ld<8>(at + TM_F, f);
+#pragma unroll
+                                for (int y = 0; y < 8; ++y) o[y] += f[y];
+                            }
+                            tc::tmem_st<8>(at + TM_F, o);
+                        }
+                }
                 if (live < KT) {
                     // Rows of V past the last key become zero (0 x NaN would reach the sums), and so do a
                     // node's values that are not finite: the epilogue adds them to the rows that attend it.
@@ -759,6 +790,12 @@ __global__ void __launch_bounds__(kvt::threads(NR), 1)
                 float o[8];
                 __syncwarp();
                 tc::tmem_ld<8>(tmem + lane_base + TM_O + hf * NR + r0, o);
+                if (n > FOLD) {
+                    float f[8];
+                    tc::tmem_ld<8>(tmem + lane_base + TM_F + hf * NR + r0, f);
+#pragma unroll
+                    for (int x = 0; x < 8; ++x) o[x] += f[x];
+                }
                 if (e >= a.d || r0 >= rows) continue;
                 if (odd) add_odd<ST>(a, w.s.nodes, w.b, w.h, e, &tb.mask[0][r0], &tb.mask[1][r0], o);
                 const float4 f0 = *reinterpret_cast<const float4*>(&st.factor[r0]);

@@ -1,5 +1,5 @@
-"""GPU parity of the cache operators of include/kv.h where their inputs or sizes are extreme: infinite keys
-and rows without a log-sum-exp in the accumulation. References in 64 bits, as tests/test_gpu_kv.py.
+"""GPU parity of the cache operators of include/kv.h where their inputs or sizes are extreme: long sums, infinite
+keys, rows without a log-sum-exp. References in 64 bits, as tests/test_gpu_kv.py.
 """
 import numpy as np
 import pytest
@@ -21,6 +21,91 @@ def _lib():
 
 
 dev = lambda a: torch.from_numpy(np.ascontiguousarray(a)).cuda()
+
+
+# ---------------------------------------------------------------- attention
+
+
+def _one_text(dtype, T, gap, n=131072, page=128, d=64):
+    """Attention over n entries of which the first leads the others, all alike, by `gap`: outputs, log-sum-exps
+    and what both should be. Enough sequences (of one text, so that the pool is two pages) that a block of the
+    device takes a whole one."""
+    B = 2 * torch.cuda.get_device_properties(0).multi_processor_count
+    dt = ref.TORCH[dtype]
+    k, v = torch.zeros(2, 1, page, d, dtype=dt, device="cuda"), torch.zeros(2, 1, page, d, dtype=dt, device="cuda")
+    k[0, 0, 0, 0] = gap
+    gap = float(k[0, 0, 0, 0])  # as the cache holds it
+    tail = torch.linspace(0.5, 2.0, d, device="cuda").to(dt)
+    v[:] = tail
+    v[0, 0, 0] = 1.0
+    table = torch.ones(1, n // page, dtype=torch.int32, device="cuda")
+    table[0, 0] = 0
+    cache = kv.KVCache(k, v, table, torch.full((1,), n, dtype=torch.int32, device="cuda"))
+    q = torch.zeros(B, T, 1, d, dtype=dt, device="cuda")
+    q[..., 0] = 1.0
+    new = torch.zeros(B, T, 1, d, dtype=dt, device="cuda")
+    out, lse = torch.empty_like(q), torch.empty(B, T, 1, device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    kv.kv_tree_attention(cache, torch.zeros(B, dtype=torch.int32, device="cuda"), q, new, new,
+                         torch.zeros(B, T, dtype=torch.int64, device="cuda"), out, err, kv.kv_tree_workspace(cache, q),
+                         lse=lse, scale=1.0)
+    assert int(err.item()) == 0
+    rest = (n - 1) * np.exp(-gap)
+    return host(out), host(lse), (1.0 + rest * host(tail)) / (1.0 + rest), gap + np.log1p(rest), gap
+
+
+def _check_one_text(dtype, out, lse, want, z, gap, n=131072, d=64):
+    """Beside the bound of any row, the sums': of 2048 entries at most in tensor memory, which cuts off at 2^-24
+    at worst; on the FP32 pipe of 64, and of the tiles."""
+    mag, smag = np.broadcast_to(want, out.shape), np.full(lse.shape, gap)
+    sums = (64 + n / 64) * 2.0 ** -24 if dtype == "f32" else 2048 * 2.0 ** -24
+    off = np.abs(out - want)
+    assert (off <= ref.out_bound(mag, smag, d, dtype) + sums * mag).all(), f"outputs off by {off.max():.3e}"
+    assert (np.abs(lse - z) <= ref.lse_bound(np.full(lse.shape, z), smag, d)).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("T", [1, 40])
+@pytest.mark.parametrize("gap", [0.0, 2.0, 4.0, 8.0])
+def test_sums_over_long_caches(dtype, T, gap):
+    """Outputs do not shrink with the number of like entries that are summed."""
+    _check_one_text(dtype, *_one_text(dtype, T, gap))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("d", [64, 128, 192, 256])
+@pytest.mark.parametrize("T,G", [(1, 1), (5, 5), (50, 2)])
+@pytest.mark.parametrize("moves", [0, 1])
+def test_whole_sequences_of_many_tiles(dtype, d, T, G, moves):
+    """A block of the device takes a sequence whole, 43 tiles of 128 entries, for every size of a block of rows
+    and of a head; moves: the maximum rises again and again on the way."""
+    n, page, B = 5500, 128, 2 * torch.cuda.get_device_properties(0).multi_processor_count
+    dt, g = ref.TORCH[dtype], torch.Generator(device="cuda").manual_seed(60)
+    rnd = lambda *s: torch.randn(*s, generator=g, device="cuda")
+    pages = -(-n // page)
+    k, v = rnd(pages, 1, page, d), rnd(pages, 1, page, d)
+    if moves:
+        k *= 1.0 + 3.0 * (torch.arange(pages, device="cuda") // 5 / (pages // 5)).view(-1, 1, 1, 1)
+    k, v = k.to(dt), v.to(dt)
+    order = torch.randperm(pages, generator=g, device="cuda").int().view(1, pages)
+    cache = kv.KVCache(k, v, order, torch.full((1,), n, dtype=torch.int32, device="cuda"))
+    q, kn, vn = rnd(1, T, G, d).to(dt), rnd(1, T, 1, d).to(dt), rnd(1, T, 1, d).to(dt)
+    mask = torch.ones(1, T, dtype=torch.int64, device="cuda").expand(B, T).contiguous()  # every node sees the first
+    out, lse = torch.empty(B, T, G, d, dtype=dt, device="cuda"), torch.empty(B, T, G, device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    many = lambda x: x.expand(B, -1, -1, -1).contiguous()
+    kv.kv_tree_attention(cache, torch.zeros(B, dtype=torch.int32, device="cuda"), many(q), many(kn), many(vn), mask, out,
+                         err, kv.kv_tree_workspace(cache, out), lse=lse)
+    assert int(err.item()) == 0
+    at = order[0].long()
+    keys = torch.cat([k[at, 0].reshape(-1, d)[:n], kn[0, :1, 0]]).double()
+    vals = torch.cat([v[at, 0].reshape(-1, d)[:n], vn[0, :1, 0]]).double()
+    s = q[0].double() @ keys.T / d ** 0.5
+    p = s.softmax(-1)
+    want, mag, z = host(p @ vals), host(p @ vals.abs()), host(s.logsumexp(-1))
+    smag = host((q[0].double().abs() @ keys.abs().T).amax(-1) / d ** 0.5)
+    assert (np.abs(host(out) - want) <= ref.out_bound(mag, smag, d, dtype)).all()
+    assert (np.abs(host(lse) - z) <= ref.lse_bound(z, smag, d)).all()
 
 
 # ---------------------------------------------------------------- accumulation
