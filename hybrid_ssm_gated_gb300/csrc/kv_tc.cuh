@@ -19,12 +19,21 @@
 // time: nothing where HBM bounds, 2% of the 64-node tree below.)
 //
 // The reference. m is not the running maximum but one that lags: as long as
-// no score of a tile exceeds m by more than REF_SLACK (in powers of two), the
-// tile's weights are formed against the old m, which is exact (numerator and
-// denominator carry the same factor) and stays far inside the range of fp16
-// (2^8). So the cross-thread maximum, and the rescaling of the accumulator in
-// tensor memory, happen on a unit's first tile and where the maximum really
-// moves; otherwise a tile costs one barrier, which carries the vote.
+// no score of a tile exceeds the maximum that m was formed from by more than
+// REF_SLACK (in powers of two), the tile's weights are formed against the old
+// m, which is exact (numerator and denominator carry the same factor). So the
+// cross-thread maximum, and the rescaling of the accumulator in tensor memory,
+// happen on a unit's first tile and where the maximum really moves; otherwise a
+// tile costs one barrier, which carries the vote.
+//
+// Weights in fp16. Their range ends at 2^16 above and at steps of 2^-24 below.
+// Weights against the maximum itself would use eight powers of two above 1 and
+// lose, in the product with V but not in the sum, what lies under 2^-25: 131071
+// entries of 2^-25.2 below a leader are 0.3% of its row. So m lies seven powers
+// of two under the maximum (Half16::lift): the largest weight is 2^7 to 2^15,
+// and what is rounded to nothing lies under 2^-32 of the maximum: 2^20 such
+// entries together are under half an fp16 unit of rounding. bf16 has FP32's
+// range and no lift.
 //
 // Kernel shape: persistent, one CTA per SM:
 //   softmax    NG groups of four warps (two up to 32 rows, four above); group g
@@ -81,7 +90,7 @@ constexpr int LEAST = 2;      // of the line a CTA at least
 constexpr int BOX = 64;       // elements of d in one TMA box (128 bytes)
 constexpr int BOX_BYTES = KT * BOX * 2;
 constexpr float REF_NONE = -3.0e38f;  // reference of a row without a key yet
-constexpr float REF_SLACK = 8.f;
+constexpr float REF_SLACK = 8.f;      // how far scores may rise above a reference's own maximum
 constexpr float FUSED_MOST = 16777216.f;  // references up to which exponents are formed in one rounding
 constexpr int FOLD = 16;  // tiles of one sum in tensor memory
 constexpr int MAX_STAGES = 14;
@@ -103,7 +112,7 @@ struct __align__(16) Table {
 // Small shared-memory state of a CTA.
 template <int NR>
 struct __align__(16) State {
-    float nref[NR];           // reference of each row, negated: -m
+    float nref[NR];           // reference of each row, negated: -m (m: its maximum, less Half16::lift)
     float factor[NR];         // rescaling factor of a moved reference; at the end 1 / l
     float warp_max[4][NR];    // maxima by warp quadrant; at the end sums
     uint64_t full[MAX_STAGES], empty[MAX_STAGES];  // the K ring's stages, then the V ring's
@@ -199,12 +208,14 @@ struct Half16;
 template <>
 struct Half16<__nv_bfloat16> {
     static constexpr uint32_t type = 1, exp_mask = 0x7f80u;
+    static constexpr float lift = 0.f;  // log2 of the weight of a score at the reference's maximum
     __device__ static __forceinline__ uint32_t pack(float lo, float hi) { return pack_bf16x2(lo, hi); }
     __device__ static __forceinline__ __nv_bfloat16 round(float x) { return __float2bfloat16_rn(x); }
 };
 template <>
 struct Half16<__half> {
     static constexpr uint32_t type = 0, exp_mask = 0x7c00u;
+    static constexpr float lift = 7.f;
     __device__ static __forceinline__ uint32_t pack(float lo, float hi) { return pack_f16x2(lo, hi); }
     __device__ static __forceinline__ __half round(float x) { return __float2half_rn(x); }
 };
@@ -625,7 +636,7 @@ __global__ void __launch_bounds__(kvt::threads(NR), 1)
                 }
                 if (dead) over = -INFINITY;
                 if (failed) st.gave_up[g] = 1;
-                if (group_any(g, failed || over > REF_SLACK)) {
+                if (group_any(g, failed || over > REF_SLACK + H::lift)) {
                     if (st.gave_up[g]) {
                         stop = true;
                         break;
@@ -648,7 +659,7 @@ __global__ void __launch_bounds__(kvt::threads(NR), 1)
                         const float old = -st.nref[r];
                         float m = fmaxf(fmaxf(st.warp_max[0][r], st.warp_max[1][r]),
                                         fmaxf(st.warp_max[2][r], st.warp_max[3][r]));
-                        m = fmaxf(m, old);
+                        m = fmaxf(m - H::lift, old);
                         if (fabsf(m) > FUSED_MOST && m > REF_NONE) st.big[g] = 1;
                         st.factor[r] = kv_ex2(old - m), st.nref[r] = -m;
                     }

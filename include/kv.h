@@ -92,9 +92,10 @@ typedef struct kv_rows {
  * over all cache entries and the nodes j with bit j of mask[b][i] set (a tree:
  * its ancestors and itself; any mask is taken, one that leaves nothing too: a
  * row without a key gives out = 0, lse = -inf). T = 1 is the decode step of a
- * single token. Scores, softmax statistics and sums are FP32; with a 16-bit
- * cache the weights are rounded once to the cache's dtype before they meet
- * the values. The cache is not written.
+ * single token. Scores, softmax statistics and sums are FP32; on the tensor
+ * cores (below) the weights are rounded once to the cache's dtype before they
+ * meet the values, in fp16 to no finer than 2^-31 of the row's largest. The
+ * cache is not written.
  * slots      [B] int32.
  * q          [B][T][Hq][d];  k_new, v_new  [B][T][Hkv][d]; Hq at most 2^24.
  * mask       [B][T] 64-bit words. Bits >= num_nodes[b] are not looked at.

@@ -1,5 +1,5 @@
-"""GPU parity of the cache operators of include/kv.h where their inputs or sizes are extreme: long sums, infinite
-keys, rows without a log-sum-exp. References in 64 bits, as tests/test_gpu_kv.py.
+"""GPU parity of the cache operators of include/kv.h where their inputs or sizes are extreme: long sums, weights
+far below a leader's, infinite keys, rows without a log-sum-exp. References in 64 bits, as tests/test_gpu_kv.py.
 """
 import numpy as np
 import pytest
@@ -69,6 +69,15 @@ def _check_one_text(dtype, out, lse, want, z, gap, n=131072, d=64):
 @pytest.mark.parametrize("gap", [0.0, 2.0, 4.0, 8.0])
 def test_sums_over_long_caches(dtype, T, gap):
     """Outputs do not shrink with the number of like entries that are summed."""
+    _check_one_text(dtype, *_one_text(dtype, T, gap))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("T", [1, 40])
+@pytest.mark.parametrize("gap", [12.0, 14.0, 16.0, 16.96875, 17.46875, 18.0])
+def test_many_entries_far_below_one(dtype, T, gap):
+    """One entry leads 131071 others, each of which weighs 2^-17 to 2^-26 of it: too little for fp16 beside a
+    weight of one, and together up to half of the row."""
     _check_one_text(dtype, *_one_text(dtype, T, gap))
 
 
