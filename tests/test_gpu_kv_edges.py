@@ -64,7 +64,7 @@ def _check_one_text(dtype, out, lse, want, z, gap, n=131072, d=64):
     assert (np.abs(lse - z) <= ref.lse_bound(np.full(lse.shape, z), smag, d)).all()
 
 
-@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("T", [1, 40])
 @pytest.mark.parametrize("gap", [0.0, 2.0, 4.0, 8.0])
 def test_sums_over_long_caches(dtype, T, gap):
@@ -72,7 +72,7 @@ def test_sums_over_long_caches(dtype, T, gap):
     _check_one_text(dtype, *_one_text(dtype, T, gap))
 
 
-@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("T", [1, 40])
 @pytest.mark.parametrize("gap", [12.0, 14.0, 16.0, 16.96875, 17.46875, 18.0])
 def test_many_entries_far_below_one(dtype, T, gap):
