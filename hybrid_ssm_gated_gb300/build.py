@@ -5,6 +5,9 @@ linked into hybrid_ssm_gated_gb300/lib/libgdn.so against the shared CUDA
 runtime. Rebuilds only when a source or header is newer than the library.
 build(debug=True) builds the bounds-checking variant (GDN_DEBUG_BOUNDS: every
 global copy and store checked against its array) into lib/debug/libgdn.so.
+build(stall=True) builds a variant for the tests of bounded waits into
+lib/stall/libgdn.so: in the kernels of STALL one CTA waits for an arrival that
+never comes, with a short limit (GDN_TEST_STALL).
 """
 from __future__ import annotations
 
@@ -25,6 +28,9 @@ NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2"
                      "-I", INCLUDE]
 
 
+STALL = ["kv_inst_tc.cu"]
+
+
 def nvcc() -> str:
     path = shutil.which("nvcc") or "/usr/local/cuda/bin/nvcc"
     if not os.path.exists(path):
@@ -41,9 +47,9 @@ def _deps() -> list[str]:
         [os.path.join(INCLUDE, "gdn.h"), os.path.join(INCLUDE, "kv.h"), __file__]
 
 
-def _paths(debug: bool) -> tuple[str, str]:
-    """(library, object directory) of the normal or the bounds-checking build."""
-    d = os.path.join(LIBDIR, "debug") if debug else LIBDIR
+def _paths(variant: str = "") -> tuple[str, str]:
+    """(library, object directory) of the normal build, or of the variant of that name."""
+    d = os.path.join(LIBDIR, variant)
     return os.path.join(d, "libgdn.so"), os.path.join(d, "obj")
 
 
@@ -62,9 +68,10 @@ def _compile(src: str, extra: list[str], objdir: str) -> str:
     return obj
 
 
-def build(force: bool = False, verbose_ptxas: bool = False, debug: bool = False) -> str:
-    """Compile and link libgdn.so (debug: the bounds-checking build); returns its path."""
-    lib, objdir = _paths(debug)
+def build(force: bool = False, verbose_ptxas: bool = False, debug: bool = False, stall: bool = False) -> str:
+    """Compile and link libgdn.so (debug: the bounds-checking build; stall: the one whose waits run out);
+    returns its path."""
+    lib, objdir = _paths("debug" if debug else "stall" if stall else "")
     os.makedirs(objdir, exist_ok=True)
     newest = max(os.path.getmtime(d) for d in _deps())
     if not force and os.path.exists(lib) and os.path.getmtime(lib) >= newest:
@@ -74,7 +81,9 @@ def build(force: bool = False, verbose_ptxas: bool = False, debug: bool = False)
         os.makedirs(objdir, exist_ok=True)
     extra = (["-Xptxas", "-v"] if verbose_ptxas else []) + (["-DGDN_DEBUG_BOUNDS"] if debug else [])
     with ThreadPoolExecutor(max_workers=min(16, os.cpu_count() or 1)) as ex:
-        objs = list(ex.map(lambda s: _compile(s, extra, objdir), sources()))
+        special = lambda s: stall and os.path.basename(s) in STALL  # the rest are the normal build's objects
+        objs = list(ex.map(lambda s: _compile(s, extra + (["-DGDN_TEST_STALL"] if special(s) else []),
+                                              objdir if special(s) or not stall else _paths()[1]), sources()))
     cmd = [nvcc()] + ARCH + ["-shared", "-cudart", "shared", "-o", lib + ".tmp"] + objs
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:

@@ -120,8 +120,13 @@ struct __align__(16) State {
     Table<NR> table[2];       // of this segment and the next
     uint64_t table_full[2], table_empty[2], seg_loaded[2];
     KvScan<threads(NR)> scan;
+    KvSplit split;            // (for refuse_range alone: nothing of it stays in registers)
     int gave_up[4], big[4], v_stage;
+    int stopped;  // a wait ran out
     uint32_t tmem;
+#ifdef GDN_TEST_STALL
+    uint64_t never;
+#endif
 };
 
 template <int NR>
@@ -305,6 +310,32 @@ __device__ __forceinline__ float max3(float x, float y, float z) {
     return r;
 }
 
+// What a CTA leaves whose waits ran out, by the whole block: the rows of its range as those of a refused
+// sequence. Units that it shares with other CTAs get partials that say so, and the join a record as ever (the
+// workspace is not initialised: what it held would be taken for one).
+template <int NR>
+__device__ __noinline__ void refuse_range(const KvArgs& a, const State<NR>& st) {
+    const KvSplit split = st.split;
+    bool some;
+    KvWalk<true, KT> w(a, split, st.scan, some);
+    if (!some) return;
+    do {
+        const int r0 = w.rb * NR, rows = min(NR, w.s.nodes * a.G - r0);
+        if (w.whole()) {
+            for (int i = threadIdx.x; i < rows * a.d; i += threads(NR)) {
+                const int r = i / a.d, node = (r0 + r) / a.G, hq = w.h * a.G + (r0 + r) - node * a.G;
+                const int64_t row = ((int64_t)w.b * a.T + node) * a.Hq + hq;
+                store_elem(a.out, row * a.d + (i - r * a.d), a.dtype, 0.f);
+                if (a.lse && i == r * a.d) a.lse[row] = -INFINITY;
+            }
+        } else {
+            float* part = a.part + ((int64_t)blockIdx.x * 2 + w.later) * kv_part_floats(NR, a.d) + NR * a.d;
+            for (int r = threadIdx.x; r < rows; r += threads(NR)) part[r] = REF_NONE, part[NR + r] = -1.f;
+        }
+        if (threadIdx.x == 0 && w.last()) static_cast<KvBorder*>(a.border)[blockIdx.x] = kv_border(a, split, w);
+    } while (w.next());
+}
+
 }  // namespace kvt
 
 // boxes: 64-element boxes of d; k_stages, v_stages: of the rings; p_bufs: weight buffers (1 or 2: one where
@@ -346,6 +377,10 @@ __global__ void __launch_bounds__(kvt::threads(NR), 1)
         }
         if (lane == 2) mbar_init(&st.q_full, 1), mbar_init(&st.v_ok, 1), mbar_init(&st.drain[0], 1), mbar_init(&st.drain[1], 1);
         if (lane < 4) st.gave_up[lane] = 0, st.big[lane] = 0;
+        if (lane == 0) st.stopped = 0;
+#ifdef GDN_TEST_STALL
+        if (lane == 0) mbar_init(&st.never, 1);
+#endif
         fence_barrier_init();
     }
     if (warp == O_WARP) {
@@ -360,6 +395,7 @@ __global__ void __launch_bounds__(kvt::threads(NR), 1)
     const uint32_t tmem = st.tmem;
     bool busy;
     KvWalk<true, KT> w(a, split, st.scan, busy);
+    if (tid == 0) st.split = split;
 
     if ((warp == K_WARP || warp == V_WARP) && busy) {
         // ------------------------------------------------------------ loads
@@ -438,7 +474,7 @@ __global__ void __launch_bounds__(kvt::threads(NR), 1)
             ++seg;
         } while (ok && w.next());
         if (!ok) {
-            if (lane == 0) set_error(a.dev_err, GDN_DEVERR_TIMEOUT);
+            if (lane == 0) st.stopped = 1, set_error(a.dev_err, GDN_DEVERR_TIMEOUT);
             // copies in flight land long before this
             const uint64_t t0 = global_timer_ns();
             while (global_timer_ns() - t0 < 2000000) __nanosleep(1000);
@@ -554,7 +590,7 @@ __global__ void __launch_bounds__(kvt::threads(NR), 1)
             }
         } while (ok && w.next());
         if (!ok) {
-            if (lane == 0) set_error(a.dev_err, GDN_DEVERR_TIMEOUT);
+            if (lane == 0) st.stopped = 1, set_error(a.dev_err, GDN_DEVERR_TIMEOUT);
             commit(&st.drain[outs]);  // MMAs in flight end before tensor memory is freed
             mbar_wait(&st.drain[outs], 0);
         }
@@ -586,6 +622,9 @@ __global__ void __launch_bounds__(kvt::threads(NR), 1)
                 const uint32_t tm_s = tmem + lane_base + TM_S + buf * NR + g0;
                 const bool dead = key >= live;  // no key in this thread's row of the tile
                 failed = failed || !mbar_wait(&st.s_full[buf], (n_t >> 1) & 1);
+#ifdef GDN_TEST_STALL
+                if (blockIdx.x == gridDim.x / 2 && g == 0 && n_t == 1) failed = failed || !mbar_wait(&st.never, 0);
+#endif
                 tc::fence_after();
                 if (tree) {  // scores that a row does not see, made such that the scaled ones are -inf
                     const float never = c2 > 0.f ? -INFINITY : INFINITY;
@@ -826,11 +865,13 @@ __global__ void __launch_bounds__(kvt::threads(NR), 1)
             }
             tc::fence_before();
             if (tid == 0 && w.last()) static_cast<KvBorder*>(a.border)[blockIdx.x] = kv_border(a, split, w);
+            if (failed) st.gave_up[g] = 1;
             group_sync(g);  // the sums and factors are read
+            stop = st.gave_up[g];
             if (lane == 0) mbar_arrive(&st.table_empty[side]);
             ++seg;
-        } while (w.next());
-        if (failed && lane == 0) set_error(a.dev_err, GDN_DEVERR_TIMEOUT);
+        } while (!stop && w.next());
+        if (stop && lane == 0) st.stopped = 1, set_error(a.dev_err, GDN_DEVERR_TIMEOUT);
     }
     if (warp == S_WARP) kv_empty_rows(a, a.B <= NT ? st.scan.seq : nullptr, lane, 32);
     if (!busy && tid == 0) static_cast<KvBorder*>(a.border)[blockIdx.x].rows = 0;
@@ -839,6 +880,7 @@ __global__ void __launch_bounds__(kvt::threads(NR), 1)
     tc::fence_after();
     if (warp == O_WARP)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(TM_COLS) : "memory");
+    if (st.stopped) refuse_range<NR>(a, st);
 }
 
 }  // namespace gdn

@@ -1,0 +1,33 @@
+"""Calls of the cache's operators on which tests/test_gpu_kv_waits.py compares the normal library with the build
+whose waits run out. Run as a program (python -m tests.kv_stalled CALL NAME FILE, the library named by
+GDN_LIBRARY), it leaves a call's results in a file."""
+import sys
+
+import numpy as np
+import torch
+
+from hybrid_ssm_gated_gb300 import kv
+from tests.gpu_util import canaries_intact, guarded
+from tests.kv_ref import Case, host
+
+LONG = [5000, 20, 1700, 0, 2900, 300]
+# of attention: lengths, nodes, query heads (of 8 key heads), head size
+ATTENTION = {"shared units, 16 rows": (LONG, 5, 16, 64), "shared units, 128 rows": (LONG, 20, 48, 64)}
+
+
+def attention(name: str) -> dict:
+    lens, T, Hq, d = ATTENTION[name]
+    c = Case(70, "bf16", lens, T=T, Hq=Hq, Hkv=8, d=d, page=64)
+    guards = []
+    out = guarded(c.q.shape, c.q.dtype, guards).fill_(7.0)
+    lse = guarded(c.q.shape[:3], torch.float32, guards).fill_(7.0)
+    ws = guarded((kv.kv_tree_workspace(c.cache, c.q).numel(),), torch.uint8, guards).fill_(1)
+    kv.kv_tree_attention(c.cache, c.d_slots, c.q, c.kn, c.vn, c.d_mask, out, c.err, ws, num_nodes=c.d_nodes, lse=lse)
+    assert canaries_intact(guards)
+    return {"out": host(out), "lse": host(lse), "err": int(c.err.item())}
+
+
+CALLS = {"attention": attention}
+
+if __name__ == "__main__":
+    np.savez(sys.argv[3], **CALLS[sys.argv[1]](sys.argv[2]))
