@@ -790,7 +790,7 @@ __global__ void __launch_bounds__(kvt::threads(NR), 1)
                     // node's values that are not finite: the epilogue adds them to the rows that attend it.
                     failed = failed || !mbar_wait(&st.v_ok, n_v & 1);
                     ++n_v;
-                    for (int x = g; x < boxes; x += NG) {
+                    for (int x = g; x < boxes && !failed; x += NG) {  // (v_stage is not there if the wait ran out)
                         int stage = st.v_stage + (x >> 1);
                         if (stage >= stages) stage -= v_stages;
                         uint4* row = reinterpret_cast<uint4*>(ring + stage * stage_bytes + (x & 1) * BOX_BYTES + key * 128);

@@ -10,9 +10,10 @@ from hybrid_ssm_gated_gb300 import kv
 from tests.gpu_util import canaries_intact, guarded
 from tests.kv_ref import Case, host
 
-LONG = [5000, 20, 1700, 0, 2900, 300]
+LONG, SHORT = [5000, 20, 1700, 0, 2900, 300], [130 + 17 * i % 171 for i in range(40)]
 # of attention: lengths, nodes, query heads (of 8 key heads), head size
-ATTENTION = {"shared units, 16 rows": (LONG, 5, 16, 64), "shared units, 128 rows": (LONG, 20, 48, 64)}
+ATTENTION = {"shared units, 16 rows": (LONG, 5, 16, 64), "whole units": (SHORT, 5, 16, 128),
+             "shared units, 128 rows": (LONG, 20, 48, 64), "whole units, 64 rows, two halves": (SHORT, 5, 64, 256)}
 
 
 def attention(name: str) -> dict:
