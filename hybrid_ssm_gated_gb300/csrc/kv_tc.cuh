@@ -189,6 +189,16 @@ __device__ __forceinline__ void tma_load(void* dst, const CUtensorMap* map, int 
         : "memory");
 }
 
+// Waits for a load warp's own copies: the last ones into the stages of its ring, of which `stage` would be
+// the next to fill, for the time `round`.
+__device__ __forceinline__ void landed(uint64_t* full, int first, int end, int stage, uint32_t round) {
+#pragma unroll 1
+    for (int s = first; s < end; ++s) {
+        const uint32_t n = s < stage ? round + 1 : round;
+        if (n > 0) mbar_wait(&full[s], (n - 1) & 1);
+    }
+}
+
 // Barrier of one softmax group (128 threads), and the same with a vote.
 __device__ __forceinline__ void group_sync(int g) { asm volatile("bar.sync %0, 128;" ::"r"(1 + g) : "memory"); }
 __device__ __forceinline__ bool group_any(int g, bool x) {
@@ -473,12 +483,8 @@ __global__ void __launch_bounds__(kvt::threads(NR), 1)
             }
             ++seg;
         } while (ok && w.next());
-        if (!ok) {
-            if (lane == 0) st.stopped = 1, set_error(a.dev_err, GDN_DEVERR_TIMEOUT);
-            // copies in flight land long before this
-            const uint64_t t0 = global_timer_ns();
-            while (global_timer_ns() - t0 < 2000000) __nanosleep(1000);
-        }
+        if (!ok && lane == 0) st.stopped = 1, set_error(a.dev_err, GDN_DEVERR_TIMEOUT);
+        landed(st.full, first, end, stage, round);
     } else if ((warp == S_WARP || warp == O_WARP) && busy) {
         // ------------------------------------------------------------ MMAs
         const bool outs = warp == O_WARP;
@@ -486,7 +492,7 @@ __global__ void __launch_bounds__(kvt::threads(NR), 1)
         const uint32_t aQ = smem_addr(sQ), aP = smem_addr(sP), aR = smem_addr(ring), tm = uniform(tmem);
         const int first = outs ? k_stages : 0, end = outs ? stages : k_stages;
         int stage = first;
-        uint32_t round = 0, n_t = 0, seg = 0;
+        uint32_t round = 0, n_t = 0, seg = 0, asked = 0;  // asked: copies of queries
         bool ok = true;
         do {
             const int n = uniform(w.t1 - w.t0);
@@ -506,6 +512,7 @@ __global__ void __launch_bounds__(kvt::threads(NR), 1)
                             tma_load(sQ + x * NR * 128, &maps.q, x * BOX, w.h * a.G, r_first / a.G, w.b, &st.q_full);
                     }
                     __syncwarp();
+                    asked += ok;
                     ok = ok && warp_wait(&st.q_full, seg & 1);
                 } else {  // ... else by the lanes, eight loads of one out before the first is stored
                     ok = ok && warp_wait(&st.table_full[side], (seg >> 1) & 1);
@@ -589,11 +596,12 @@ __global__ void __launch_bounds__(kvt::threads(NR), 1)
                 if (ok) commit(outs ? &st.p_empty[buf] : &st.s_full[buf]);
             }
         } while (ok && w.next());
-        if (!ok) {
-            if (lane == 0) st.stopped = 1, set_error(a.dev_err, GDN_DEVERR_TIMEOUT);
-            commit(&st.drain[outs]);  // MMAs in flight end before tensor memory is freed
-            mbar_wait(&st.drain[outs], 0);
-        }
+        // products and copies in flight end before tensor memory is freed and the CTA leaves, also where it is the
+        // softmax warps that gave up (else nobody waits here for long: they have waited for these)
+        if (!ok && lane == 0) st.stopped = 1, set_error(a.dev_err, GDN_DEVERR_TIMEOUT);
+        if (asked) mbar_wait(&st.q_full, (asked - 1) & 1);
+        commit(&st.drain[outs]);
+        mbar_wait(&st.drain[outs], 0);
         __syncwarp();
     } else if (warp < SM_WARPS && busy) {
         // ------------------------------------------------------------ softmax

@@ -137,11 +137,8 @@ __global__ void __launch_bounds__(kvw::NT, 1)
                 }
             }
         } while (ok && w.next());
-        if (!ok) {
-            if (lane == 0) set_error(a.dev_err, GDN_DEVERR_TIMEOUT);
-            const uint64_t t0 = global_timer_ns();  // copies in flight land long before this
-            while (global_timer_ns() - t0 < 2000000) __nanosleep(1000);
-        }
+        if (!ok && lane == 0) set_error(a.dev_err, GDN_DEVERR_TIMEOUT);
+        kvt::landed(st.full, 0, stages, stage, round);
     } else if (warp == S_WARP && busy) {
         // ------------------------------------------------------------ MMAs
         const uint32_t id = kvt::idesc(H::type, false, false, NR);
@@ -183,11 +180,9 @@ __global__ void __launch_bounds__(kvw::NT, 1)
                 if (ok) kvt::commit(&st.q_empty);  // the queries are read
             }
         } while (ok && w.next());
-        if (!ok) {
-            if (lane == 0) set_error(a.dev_err, GDN_DEVERR_TIMEOUT);
-            kvt::commit(&st.drain);  // MMAs in flight end before tensor memory is freed
-            mbar_wait(&st.drain, 0);
-        }
+        if (!ok && lane == 0) set_error(a.dev_err, GDN_DEVERR_TIMEOUT);
+        kvt::commit(&st.drain);  // products in flight end before tensor memory is freed, whoever gave up
+        mbar_wait(&st.drain, 0);
         __syncwarp();
     } else if (warp < SM_WARPS && busy) {
         // ------------------------------------------------------------ weights
