@@ -38,6 +38,9 @@ struct __align__(16) State {
     uint64_t s_full[2], s_empty[2], q_full, q_empty, drain;
     KvScan<NT> scan;
     uint32_t tmem;
+#ifdef GDN_TEST_STALL
+    uint64_t never;
+#endif
 };
 
 // Barrier of the eight weight warps.
@@ -82,6 +85,9 @@ __global__ void __launch_bounds__(kvw::NT, 1)
         if (lane < stages) mbar_init(&st.full[lane], 1), mbar_init(&st.empty[lane], 1);
         if (lane < 2) mbar_init(&st.s_full[lane], 1), mbar_init(&st.s_empty[lane], 4);
         if (lane == 2) mbar_init(&st.q_full, SM_WARPS), mbar_init(&st.q_empty, 1), mbar_init(&st.drain, 1);
+#ifdef GDN_TEST_STALL
+        if (lane == 3) mbar_init(&st.never, 1);
+#endif
         fence_barrier_init();
     }
     if (warp == S_WARP) {
@@ -191,6 +197,9 @@ __global__ void __launch_bounds__(kvw::NT, 1)
         const kvt::Two log2e = kvt::two(LOG2E, LOG2E);
         uint32_t n_t = 0, seg = 0;
         int checked = -1;
+        // A warp whose wait ran out takes part in the barriers and in nothing else: it neither frees a buffer
+        // nor hands over queries, so that the other roles' waits run out too and no weight is formed from a
+        // product that nobody waited for.
         bool good = true, failed = false;
         do {
             const int32_t* table = a.page_table + (int64_t)w.s.slot * a.max_pages;
@@ -205,7 +214,7 @@ __global__ void __launch_bounds__(kvw::NT, 1)
 #pragma unroll 1
             for (int rb = 0; rb < blocks; ++rb, ++seg) {
                 // ---- row tables and queries, once the last block's are read
-                if (seg > 0) failed = failed || !mbar_wait(&st.q_empty, (seg - 1) & 1);
+                if (seg > 0) failed = failed || !kvt::warp_wait(&st.q_empty, (seg - 1) & 1);
                 all_sync();  // nobody reads the last block's table any more
                 const int rows = min(NR, rows_all - rb * NR);
                 if (wt < NR) {
@@ -217,7 +226,7 @@ __global__ void __launch_bounds__(kvw::NT, 1)
                 }
                 all_sync();
                 constexpr int N = (NR * 8 + 255) / 256;
-                for (int x = 0; x < boxes; ++x) {
+                for (int x = 0; x < boxes && !failed; ++x) {
                     uint4 v[N];
 #pragma unroll
                     for (int y = 0; y < N; ++y) {
@@ -235,7 +244,7 @@ __global__ void __launch_bounds__(kvw::NT, 1)
                 }
                 tc::fence_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&st.q_full);
+                if (lane == 0 && !failed) mbar_arrive(&st.q_full);
                 // ---- this group's tiles
 #pragma unroll 1
                 for (int t = w.t0; t < w.t1; ++t, ++n_t) {
@@ -250,7 +259,11 @@ __global__ void __launch_bounds__(kvw::NT, 1)
                     }
                     // rows of nodes before entry e's own do not see it
                     const int unseen = max(0, e - (w.s.len - w.s.nodes)) * a.G - rb * NR;
-                    failed = failed || !mbar_wait(&st.s_full[g], (n_t >> 1) & 1);
+                    failed = failed || !kvt::warp_wait(&st.s_full[g], (n_t >> 1) & 1);
+#ifdef GDN_TEST_STALL
+                    if (blockIdx.x == gridDim.x / 2 && g == 0 && n_t == 2) failed = failed || !kvt::warp_wait(&st.never, 0);
+#endif
+                    if (failed) continue;
                     tc::fence_after();
                     // Columns that add nothing (past the block's rows, or of a row without a log-sum-exp) do so by
                     // their exponent of -inf. That is 0 for every finite score; a score that is not (0 x inf for
@@ -291,7 +304,7 @@ __global__ void __launch_bounds__(kvw::NT, 1)
                     tc::fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&st.s_empty[g]);
-                    if (live && !failed) *x = fmaf(old, rb == 0 ? a.decay : 1.f, total);
+                    if (live) *x = fmaf(old, rb == 0 ? a.decay : 1.f, total);
                 }
             }
         } while (w.next());

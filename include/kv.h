@@ -17,8 +17,10 @@
  * gdn_last_error_string(); problems only visible on the device set bits in
  * *dev_err. A sequence whose slot is negative is padding: nothing of it is
  * read or written and its outputs are zero (lse: -inf). A sequence with an
- * error bit is treated the same way. Slots within a call that writes must be
- * distinct (not checked).
+ * error bit is treated the same way, but for GDN_DEVERR_TIMEOUT, after which
+ * some key heads of a sequence may be refused and others not, and weights
+ * that kv_accumulate was to update may be as they were. Slots within a call
+ * that writes must be distinct (not checked).
  */
 #ifndef GDN_KV_H
 #define GDN_KV_H

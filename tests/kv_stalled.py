@@ -28,7 +28,25 @@ def attention(name: str) -> dict:
     return {"out": host(out), "lse": host(lse), "err": int(c.err.item())}
 
 
-CALLS = {"attention": attention}
+# of accumulation: nodes of the paths, query heads (of 8 key heads), head size
+ACCUMULATION = {"one block of rows": (3, 16, 128), "two blocks of rows": (40, 48, 64), "four boxes": (3, 32, 256)}
+
+
+def accumulation(name: str) -> dict:
+    P, Hq, d = ACCUMULATION[name]
+    c = Case(71, "bf16", [5000, 60, 1700, 41, 2900, 300], T=P, Hq=Hq, Hkv=8, d=d, page=64)
+    guards = []
+    c.weights = guarded(c.weights.shape, torch.float32, guards).copy_(c.weights)
+    c.sync()
+    before = host(c.weights)
+    path = torch.arange(P, dtype=torch.int32, device="cuda").repeat(6, 1)
+    n = torch.tensor([P, P, P - 1, P, 1, P], dtype=torch.int32, device="cuda")
+    kv.kv_accumulate(c.cache, c.d_slots, c.q, torch.full((6, P, Hq), 3.0, device="cuda"), path, n, c.err, decay=0.5)
+    assert canaries_intact(guards)
+    return {"before": before, "weights": host(c.weights), "err": int(c.err.item())}
+
+
+CALLS = {"attention": attention, "accumulation": accumulation}
 
 if __name__ == "__main__":
     np.savez(sys.argv[3], **CALLS[sys.argv[1]](sys.argv[2]))

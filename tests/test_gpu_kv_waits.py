@@ -42,3 +42,17 @@ def test_attention_that_gives_up(name, tmp_path):
     refused = (heads(got["out"]) == 0).all(1) & np.isneginf(heads(got["lse"])).all(1)
     assert (same | refused).all(), f"{(~(same | refused)).sum()} units are neither right nor refused"
     assert 1 <= refused.sum() <= 8
+
+
+@pytest.mark.parametrize("name", kv_stalled.ACCUMULATION)
+def test_accumulation_that_gives_up(name, tmp_path):
+    """A weight is as it was, or the right one to the bit; of paths in two blocks of rows, or has gathered the
+    first."""
+    want, got = _both("accumulation", name, tmp_path)
+    assert want["err"] == 0 and got["err"] == gdn.DEVERR_TIMEOUT
+    before, w, new = got["before"], got["weights"], want["weights"]
+    right = (w == new) | (w == before)
+    if name == "two blocks of rows":
+        right |= (w >= 0.5 * before) & (w <= new)
+    assert np.array_equal(before, want["before"]) and right.all(), f"{(~right).sum()} weights are wrong"
+    assert 64 <= ((w != new) & (new != before)).sum() <= 8 * 128 * 8
