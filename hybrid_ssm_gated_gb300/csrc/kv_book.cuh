@@ -11,9 +11,10 @@ namespace gdn {
 // One CTA a sequence: the whole path is checked first, and its entries' places are left in shared memory;
 // then every thread copies 16-byte pieces (2-byte ones where the rows allow no more) that do not depend
 // on one another, four in flight (a warp a row, one after the other, took 9 us for six tokens of eight
-// heads; bound by latency, three loads deep).
+// heads; bound by latency, three loads deep). Index: 32 bits, or 64 where a call's pieces need them (tens of
+// thousands of key heads).
 constexpr int KV_COMMIT_NT = 256, KV_COMMIT_AHEAD = 4;
-template <typename Piece>
+template <typename Piece, typename Index>
 __global__ void __launch_bounds__(KV_COMMIT_NT) kv_commit_kernel(const __grid_constant__ KvArgs a) {
     constexpr int NT = KV_COMMIT_NT;
     __shared__ int s_node[KV_MAX_NODES], s_page[KV_MAX_NODES], s_place[KV_MAX_NODES];
@@ -38,18 +39,19 @@ __global__ void __launch_bounds__(KV_COMMIT_NT) kv_commit_kernel(const __grid_co
     if (err) set_error(a.dev_err, err);
     if (__syncthreads_or(err)) return;  // the lengths were read by every thread: they may change now
     const int esz = dtype_size(a.dtype), per = a.d * esz / (int)sizeof(Piece);
-    const int rows = n * a.Hkv, total = 2 * rows * per;
-    for (int i0 = tid; i0 < total; i0 += NT * KV_COMMIT_AHEAD) {
+    const Index rows = (Index)n * a.Hkv, total = 2 * rows * per;
+    for (Index i0 = tid; i0 < total; i0 += NT * KV_COMMIT_AHEAD) {
         Piece x[KV_COMMIT_AHEAD];
         Piece* to[KV_COMMIT_AHEAD];
 #pragma unroll
         for (int y = 0; y < KV_COMMIT_AHEAD; ++y) {
-            const int i = i0 + y * NT;
+            const Index i = i0 + y * NT;
             to[y] = nullptr;
             if (i < total) {
-                const int q = i / per, p = i - q * per;
+                const Index q = i / per;
                 const bool val = q >= rows;
-                const int r = val ? q - rows : q, j = r / a.Hkv, h = r - j * a.Hkv;
+                const Index r = val ? q - rows : q;
+                const int p = (int)(i - q * per), j = (int)(r / a.Hkv), h = (int)(r - (Index)j * a.Hkv);
                 const KvPages& c = val ? a.v : a.k;
                 const KvRows& from = val ? a.vn : a.kn;
                 to[y] = reinterpret_cast<Piece*>(static_cast<char*>(const_cast<void*>(c.p)) +
@@ -64,8 +66,8 @@ __global__ void __launch_bounds__(KV_COMMIT_NT) kv_commit_kernel(const __grid_co
             if (to[y]) *to[y] = x[y];
     }
     if (a.weights)
-        for (int i = tid; i < rows; i += NT) {
-            const int j = i / a.Hkv, h = i - j * a.Hkv;
+        for (Index i = tid; i < rows; i += NT) {
+            const int j = (int)(i / a.Hkv), h = (int)(i - (Index)j * a.Hkv);
             const int64_t w = ((int64_t)s_page[j] * a.Hkv + h) * a.page_size + s_place[j];
             a.weights[w] = 0.f, a.stamps[w] = count + j;
         }

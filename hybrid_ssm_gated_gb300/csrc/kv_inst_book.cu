@@ -6,10 +6,12 @@
 namespace gdn {
 
 cudaError_t launch_kv_commit(const KvArgs& a, bool vec, cudaStream_t stream) {
-    if (vec)
-        kv_commit_kernel<uint4><<<(unsigned)a.B, KV_COMMIT_NT, 0, stream>>>(a);
-    else
-        kv_commit_kernel<uint16_t><<<(unsigned)a.B, KV_COMMIT_NT, 0, stream>>>(a);
+    // the longest path's pieces, and what a thread's index passes them by
+    const int64_t pieces = 2ll * a.P * a.Hkv * (a.d * dtype_size(a.dtype) / (vec ? 16 : 2));
+    const bool wide = pieces > 0x7fffffff - KV_COMMIT_NT * KV_COMMIT_AHEAD;
+    auto kern = vec ? (wide ? kv_commit_kernel<uint4, int64_t> : kv_commit_kernel<uint4, int>)
+                    : (wide ? kv_commit_kernel<uint16_t, int64_t> : kv_commit_kernel<uint16_t, int>);
+    kern<<<(unsigned)a.B, KV_COMMIT_NT, 0, stream>>>(a);
     return cudaGetLastError();
 }
 

@@ -1,5 +1,6 @@
 """GPU parity of the cache operators of include/kv.h where their inputs or sizes are extreme: long sums, weights
-far below a leader's, infinite keys, rows without a log-sum-exp. References in 64 bits, as tests/test_gpu_kv.py.
+far below a leader's, paths of more than 2^31 pieces, infinite keys, rows without a log-sum-exp. References in
+64 bits, as tests/test_gpu_kv.py.
 """
 import numpy as np
 import pytest
@@ -115,6 +116,30 @@ def test_whole_sequences_of_many_tiles(dtype, d, T, G, moves):
     smag = host((q[0].double().abs() @ keys.abs().T).amax(-1) / d ** 0.5)
     assert (np.abs(host(out) - want) <= ref.out_bound(mag, smag, d, dtype)).all()
     assert (np.abs(host(lse) - z) <= ref.lse_bound(z, smag, d)).all()
+
+
+# ---------------------------------------------------------------- commit
+
+
+@pytest.mark.parametrize("n", [1, 64])
+def test_commit_of_more_pieces_than_32_bits(n):
+    """32768 key heads of fp32 rows off the 16-byte grid: 2^31 pieces of two bytes, or a call that could have them."""
+    H, T, d = 32768, 64, 256
+    k, v = (torch.full((1, H, T, d + 1), float("nan"), device="cuda")[..., 1:] for _ in range(2))
+    zeros = lambda *s: torch.zeros(*s, dtype=torch.int32, device="cuda")
+    w = torch.full((1, H, T), 5.0, device="cuda")
+    cache = kv.KVCache(k, v, zeros(1, 1), zeros(1), zeros(1) + 7, w, zeros(1, H, T))
+    g = torch.Generator(device="cuda").manual_seed(80)
+    kn, vn = (torch.randn(1, T, 1, d, generator=g, device="cuda").expand(1, T, H, d) for _ in range(2))
+    path = torch.randperm(T, generator=g, device="cuda").int().view(1, T)
+    err = zeros(1)
+    kv.kv_commit(cache, zeros(1), kn, vn, path, zeros(1) + n, err)
+    assert int(err.item()) == 0 and cache.lengths.tolist() == [n] and cache.counts.tolist() == [7 + n]
+    at = path[0, :n].long()
+    for pool, new in ((k, kn), (v, vn)):
+        assert (pool[0, :, :n] == new[0, at, 0]).all() and pool[0, :, n:].isnan().all()
+    assert (w[0, :, :n] == 0).all() and (w[0, :, n:] == 5).all()
+    assert (cache.stamps[0, :, :n] == torch.arange(7, 7 + n, device="cuda")).all()
 
 
 # ---------------------------------------------------------------- accumulation
