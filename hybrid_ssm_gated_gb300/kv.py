@@ -89,6 +89,9 @@ class KVCache:
         if weights is not None and (weights.dtype != torch.float32 or weights.shape != k.shape[:3]
                                     or stamps.shape != k.shape[:3]):
             raise ValueError("kv: weights (float32) and stamps must be [num_pages, Hkv, page_size]")
+        if any(t is not None and t.get_device() != k.get_device()
+               for t in (v, page_table, lengths, counts, weights, stamps)):
+            raise ValueError("kv: a cache's tensors lie on one device")
         self.k, self.v, self.page_table, self.lengths, self.counts = k, v, page_table, lengths, counts
         self.weights, self.stamps = weights, stamps
         self.dtype, self.Hkv, self.d, self.device = k.dtype, Hkv, d, k.get_device()
@@ -118,21 +121,36 @@ class KVCache:
 
 def _rows(t: torch.Tensor, cache: KVCache, shape, name: str) -> kv_rows:
     strides = t.stride()
-    if t.dtype is not cache.dtype or t.shape != shape or not t.is_cuda or strides[3] != 1:
-        raise ValueError(f"kv: {name} must be a CUDA tensor {list(shape)} of the cache's dtype with unit stride in d")
+    if t.dtype is not cache.dtype or t.shape != shape or t.get_device() != cache.device or strides[3] != 1:
+        raise ValueError(f"kv: {name} must be a tensor {list(shape)} of the cache's dtype on the cache's device, with "
+                         "unit stride in d")
     return kv_rows(t.data_ptr(), strides[0], strides[1], strides[2])
 
 
-def _ints(t, shape, name: str, dtype=torch.int32) -> int | None:
+def _ints(t, cache: KVCache, shape, name: str, dtype=torch.int32) -> int | None:
     if t is None:
         return None
-    if t.dtype is not dtype or t.shape != shape or not t.is_cuda or not t.is_contiguous():
-        raise ValueError(f"kv: {name} must be a contiguous CUDA tensor of {dtype} and shape {list(shape)}")
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != cache.device or not t.is_contiguous():
+        raise ValueError(f"kv: {name} must be a contiguous tensor of {dtype} and shape {list(shape)} on the cache's device")
+    return t.data_ptr()
+
+
+def _whole(t: torch.Tensor, cache: KVCache, name: str) -> int:
+    if t.get_device() != cache.device or not t.is_contiguous():
+        raise ValueError(f"kv: {name} must be a contiguous tensor on the cache's device")
     return t.data_ptr()
 
 
 def _stream(stream, device: int) -> int:
     return torch._C._cuda_getCurrentRawStream(device) if stream is None else _given_stream(stream)
+
+
+def _on_device(cache: KVCache, fn, *args):
+    """A call of the library, which takes the current device, on the cache's."""
+    if torch._C._cuda_getDevice() == cache.device:
+        return fn(*args)
+    with torch.cuda.device(cache.device):
+        return fn(*args)
 
 
 def tree_masks(parents) -> torch.Tensor:
@@ -150,21 +168,22 @@ def tree_masks(parents) -> torch.Tensor:
     return torch.tensor(out, dtype=torch.int64)
 
 
-def _workspace(nbytes: int) -> torch.Tensor:
+def _workspace(cache: KVCache, fn, *args) -> torch.Tensor:
+    nbytes = _on_device(cache, fn, cache._ref, *args)
     if nbytes < 0:
         _check(int(nbytes))
-    return torch.empty(max(16, nbytes), dtype=torch.uint8, device="cuda")
+    return torch.empty(max(16, nbytes), dtype=torch.uint8, device=cache.k.device)
 
 
 def kv_tree_workspace(cache: KVCache, q) -> torch.Tensor:
     """Workspace for kv_tree_attention calls with queries of q's shape [B, T, Hq, d] (or a smaller batch)."""
     B, T, Hq = q.shape[:3]
-    return _workspace(lib().kv_tree_attention_workspace(cache._ref, B, T, Hq))
+    return _workspace(cache, lib().kv_tree_attention_workspace, B, T, Hq)
 
 
 def kv_evict_workspace(cache: KVCache, B: int, budget: int) -> torch.Tensor:
     """Workspace for kv_evict calls of up to B sequences with this budget."""
-    return _workspace(lib().kv_evict_workspace(cache._ref, int(B), int(budget)))
+    return _workspace(cache, lib().kv_evict_workspace, int(B), int(budget))
 
 
 def kv_tree_attention(cache: KVCache, slots, q, k_new, v_new, mask, out, dev_err, workspace, num_nodes=None, lse=None,
@@ -177,11 +196,11 @@ def kv_tree_attention(cache: KVCache, slots, q, k_new, v_new, mask, out, dev_err
     rq, rk, rv = _rows(q, cache, q.shape, "q"), _rows(k_new, cache, new, "k_new"), _rows(v_new, cache, new, "v_new")
     if d != cache.d or out.shape != q.shape or out.dtype is not cache.dtype:
         raise ValueError("kv: q and out must be [B, T, Hq, d] of the cache's dtype and d")
-    _check(lib().kv_tree_attention(cache._ref, B, T, Hq, _ints(slots, (B,), "slots"), rq, rk, rv,
-                                   _ints(mask, (B, T), "mask", torch.int64), _ints(num_nodes, (B,), "num_nodes"),
-                                   1.0 / math.sqrt(d) if scale is None else scale, _ptr(out),
-                                   _ints(lse, (B, T, Hq), "lse", torch.float32), _ptr(workspace), workspace.numel(),
-                                   _ptr(dev_err), _stream(stream, cache.device)))
+    _check(_on_device(cache, lib().kv_tree_attention, cache._ref, B, T, Hq, _ints(slots, cache, (B,), "slots"), rq, rk, rv,
+                      _ints(mask, cache, (B, T), "mask", torch.int64), _ints(num_nodes, cache, (B,), "num_nodes"),
+                      1.0 / math.sqrt(d) if scale is None else scale, _whole(out, cache, "out"),
+                      _ints(lse, cache, (B, T, Hq), "lse", torch.float32), _whole(workspace, cache, "workspace"),
+                      workspace.numel(), _whole(dev_err, cache, "dev_err"), _stream(stream, cache.device)))
 
 
 def kv_commit(cache: KVCache, slots, k_new, v_new, path, n_path, dev_err, stream=None) -> None:
@@ -190,9 +209,10 @@ def kv_commit(cache: KVCache, slots, k_new, v_new, path, n_path, dev_err, stream
     B, T = k_new.shape[:2]
     P = path.shape[1]
     new = (B, T, cache.Hkv, cache.d)
-    _check(lib().kv_commit(cache._ref, B, T, P, _ints(slots, (B,), "slots"), _rows(k_new, cache, new, "k_new"),
-                           _rows(v_new, cache, new, "v_new"), _ints(path, (B, P), "path"),
-                           _ints(n_path, (B,), "n_path"), _ptr(dev_err), _stream(stream, cache.device)))
+    _check(_on_device(cache, lib().kv_commit, cache._ref, B, T, P, _ints(slots, cache, (B,), "slots"),
+                      _rows(k_new, cache, new, "k_new"), _rows(v_new, cache, new, "v_new"),
+                      _ints(path, cache, (B, P), "path"), _ints(n_path, cache, (B,), "n_path"),
+                      _whole(dev_err, cache, "dev_err"), _stream(stream, cache.device)))
 
 
 def kv_accumulate(cache: KVCache, slots, q, lse, path, n_path, dev_err, decay=1.0, scale=None, stream=None) -> None:
@@ -202,15 +222,17 @@ def kv_accumulate(cache: KVCache, slots, q, lse, path, n_path, dev_err, decay=1.
     P = path.shape[1]
     if d != cache.d:
         raise ValueError("kv: q must have the cache's d")
-    _check(lib().kv_accumulate(cache._ref, B, T, P, Hq, _ints(slots, (B,), "slots"), _rows(q, cache, q.shape, "q"),
-                               _ints(lse, (B, T, Hq), "lse", torch.float32), _ints(path, (B, P), "path"),
-                               _ints(n_path, (B,), "n_path"), 1.0 / math.sqrt(d) if scale is None else scale, decay,
-                               _ptr(dev_err), _stream(stream, cache.device)))
+    _check(_on_device(cache, lib().kv_accumulate, cache._ref, B, T, P, Hq, _ints(slots, cache, (B,), "slots"),
+                      _rows(q, cache, q.shape, "q"), _ints(lse, cache, (B, T, Hq), "lse", torch.float32),
+                      _ints(path, cache, (B, P), "path"), _ints(n_path, cache, (B,), "n_path"),
+                      1.0 / math.sqrt(d) if scale is None else scale, decay, _whole(dev_err, cache, "dev_err"),
+                      _stream(stream, cache.device)))
 
 
 def kv_evict(cache: KVCache, slots, budget: int, recent: int, dev_err, workspace, stream=None) -> None:
     """Keep `budget` entries of each longer sequence, per key head: the `recent` newest tokens, then the
     largest weights. workspace from kv_evict_workspace."""
     B = slots.shape[0]
-    _check(lib().kv_evict(cache._ref, B, _ints(slots, (B,), "slots"), budget, recent, _ptr(workspace),
-                          workspace.numel(), _ptr(dev_err), _stream(stream, cache.device)))
+    _check(_on_device(cache, lib().kv_evict, cache._ref, B, _ints(slots, cache, (B,), "slots"), budget, recent,
+                      _whole(workspace, cache, "workspace"), workspace.numel(), _whole(dev_err, cache, "dev_err"),
+                      _stream(stream, cache.device)))
