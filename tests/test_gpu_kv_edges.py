@@ -189,3 +189,58 @@ def test_accumulate_rows_without_a_log_sum_exp(dtype, poison):
     got = c.weights.cpu().numpy().astype(np.float64)
     assert int(c.err.item()) == 0
     assert (np.abs(got - want) <= tol).all()
+
+
+# ---------------------------------------------------------------- eviction
+
+
+@pytest.mark.parametrize("weights", ["random", "few"])
+@pytest.mark.parametrize("H,lens,page", [(3, [20001], 16),            # clusters of eight
+                                         (50, [9003, 4200], 16),      # of two (a hundred units)
+                                         (25, [9003, 8800], 20),      # of four
+                                         (40, [9003, 70], 6),         # of two, entries one by one
+                                         (80, [50001, 300], 16),      # one block a unit, more keys than it holds
+                                         (80, [46081, 46080], 5),     # and entries one by one
+                                         (2, [400003], 16)],          # clusters of eight, more than their blocks hold
+                         ids=str)
+def test_evict_in_slices_of_every_kind(H, lens, page, weights):
+    """The selection by one block to eight a unit, with its keys in shared memory and formed again and again, to
+    the bit; few: ties over all slices, the threshold among them."""
+    r = np.random.default_rng(90)
+    d, B, need = 2, len(lens), [-(-n // page) for n in lens]
+    num = sum(need) + 1
+    order = r.permutation(num).astype(np.int32)
+    table = np.full((B, max(need) + 1), -5, np.int32)
+    table[0, :need[0]] = order[:need[0]]
+    if B > 1:
+        table[1, :need[1]] = order[need[0]:sum(need)]
+    k, v = (r.normal(size=(num, H, page, d)).astype(np.float16) for _ in range(2))
+    w = r.exponential(size=(num, H, page)) if weights == "random" else r.integers(0, 3, size=(num, H, page))
+    w = w.astype(np.float32)
+    s = r.integers(0, max(lens), size=(num, H, page)).astype(np.int32)
+    counts = np.array(lens, np.int32) + 3
+    budget, recent = max(lens) * 2 // 5, max(lens) // 50
+    dk, dv, dw, ds = dev(k), dev(v), dev(w), dev(s)
+    cache = kv.KVCache(dk, dv, dev(table), dev(np.array(lens, np.int32)), dev(counts), dw, ds)
+    for b, L in enumerate(lens):
+        if L <= budget:
+            continue
+        e = np.arange(L)
+        pg, at = table[b, e // page], e % page
+        for h in range(H):
+            x, st = w[pg, h, at], s[pg, h, at]
+            best = np.lexsort((e, -x, st < counts[b] - recent))[:budget]  # kept by age first, then weight, then place
+            kept = np.zeros(L, bool)
+            kept[best] = True
+            holes, fill = np.flatnonzero(~kept[:budget]), budget + np.flatnonzero(kept[budget:])
+            # (among those kept by age the lowest entry goes first, whatever its weight; they are fewer than the budget)
+            assert len(holes) == len(fill) > 0 and (st >= counts[b] - recent).sum() < budget
+            for a in (k, v, w, s):
+                a[pg[holes], h, at[holes]] = a[pg[fill], h, at[fill]]
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    ws = kv.kv_evict_workspace(cache, B, budget)
+    ws.view(torch.int32).fill_(-12345)
+    kv.kv_evict(cache, torch.arange(B, dtype=torch.int32, device="cuda"), budget, recent, err, ws)
+    assert int(err.item()) == 0 and cache.lengths.tolist() == [min(n, budget) for n in lens]
+    for got, want in ((dk, k), (dv, v), (dw, w), (ds, s)):
+        assert np.array_equal(got.cpu().numpy(), want)
