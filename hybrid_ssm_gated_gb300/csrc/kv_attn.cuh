@@ -21,9 +21,11 @@
 //   RB = 4: two threads a key, each half of d x four rows; for the outputs the
 //   threads split the keys too and are summed when the unit ends.
 // Bound by shared-memory loads at 16 rows, by latency at 4. fp32, 32 / 8 heads,
-// d = 128, 8 sequences of up to 4096 tokens (0.17 GB): a decode step 60 us (2.8
-// TB/s), 16-node trees 450 us (11.6 TFLOP/s). (With synchronous loads of tiles by
-// 256 threads: 188 and 640 us.)
+// d = 128, 8 sequences of 1301 to 4096 tokens, 21297 in all (0.17 GB): a decode
+// step 56 us (3.1 TB/s), 16-node trees 484 us (11.5 TFLOP/s). (With synchronous
+// loads of tiles by 256 threads: 188 and 640 us.) 16-bit rows are unpacked by the
+// threads that load them, with nothing in flight beside: the same decode step of
+// bf16 with d = 124 takes 354 us, with d = 128 on the tensor cores 21.
 #pragma once
 
 #include "kv_common.cuh"

@@ -8,8 +8,9 @@ namespace gdn {
 
 namespace {
 
-// Query rows a unit: the smallest block that holds them all, up to 128 (64 where the outputs of two
-// halves of d share tensor memory with the scores).
+// Query rows a unit: the smallest block that holds them all, up to 128 (64 where d has two halves: at 128
+// their outputs, the folds of these and the scores are more than tensor memory's 512 columns, and shared memory
+// would leave the rings one tile each).
 int row_block_of(int64_t rows, int boxes) {
     const int most = boxes > 2 ? 64 : 128;
     int nr = 16;

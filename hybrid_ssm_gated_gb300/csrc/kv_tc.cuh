@@ -60,13 +60,15 @@
 //
 // Bound and measurement (GB300, whole calls with the join). Up to 64 rows a key
 // head: HBM. A decode step of 64 sequences of up to 8192 tokens (32 / 8 heads,
-// d = 128, bf16, 1.32 GB) takes 204 us, 6.5 TB/s or 0.97 of the measured copy
+// d = 128, bf16, 1.32 GB) takes 205 us, 6.5 TB/s or 0.97 of the measured copy
 // bandwidth; 16-node trees over 32 x 4096 tokens (0.33 GB) 72 us, 0.69, of which
-// some 20 us are start, the units' ends and the join. At 128 rows the softmax
-// warps' chain bounds a tile (2800 cycles; the products take 1200): a 64-node
-// tree over 131072 tokens (0.54 GB, 137 GFLOP) 184 us, 745 TFLOP/s. Short calls
-// are latency: 10 us of steps (lengths, first tiles, maxima, outputs) and the
-// join's 4.
+// some 20 us are start, the units' ends and the join. Above 128 rows a key head
+// each block of 128 is a unit that reads all keys: a 64-node tree over 131072
+// tokens (256 rows, 0.54 GB, 137 GFLOP) takes 184 us, 745 TFLOP/s, and reads
+// 1.08 GB from HBM (161 us of it; the softmax warps' chain, 2800 cycles a tile
+// where HBM takes 2900 and the products 1200, is close behind). Short calls are
+// latency: 10 us of steps (lengths, first tiles, maxima, outputs) and the join's
+// 4.
 // Measured and not taken: exponents before the vote instead of after it (the 64-
 // node tree 208 -> 248 us); a look at the next tile beside this one's exponents
 // with three buffers of S^T (179 -> 185, the 16-node trees 72 -> 76); two weight

@@ -109,7 +109,8 @@ typedef struct kv_rows {
  *            call at a time. Its contents need no initialisation.
  * 16-bit caches whose pages hold a multiple of 8 entries, with d a multiple of
  * 8 and bases and strides of 16 bytes, run on the tensor cores; everything
- * else, fp32 caches among it, on the FP32 pipe. How a sequence's keys are
+ * else, fp32 caches among it, on the FP32 pipe (a 16-bit decode step takes
+ * some fifteen times as long there). How a sequence's keys are
  * split over the device, and so the order of its sums, depends on the sizes
  * of the call and the other sequences' lengths; the same call gives the same
  * bits.
