@@ -107,6 +107,45 @@ cudaError_t attention_workspace(gdn::KvArgs& a, int64_t& bytes) {
     return e;
 }
 
+// The same for prompts.
+cudaError_t prompt_workspace(gdn::KvArgs& a, int64_t& bytes) { return gdn::kv_prompt_workspace(a, bytes); }
+
+// What the places of a call's units on its line are counted in: rows in 31 bits, keys in 62.
+int check_prompt(const char* fn, const kv_cache* c, int32_t B, int32_t total, int32_t Hq) {
+    if (total < 0) return fail(GDN_ERR_SHAPE, "%s: total=%d", fn, total);
+    const double G = Hq / c->Hkv, room = (double)c->max_pages * c->page_size + 1024, blocks = total * G / 64 + B;
+    if (total * G > 0x7fff0000 || blocks * (G * room + total * G + 1024) * c->Hkv > 4e18)
+        return fail(GDN_ERR_SHAPE, "%s: total=%d rows of %d query heads are too many", fn, total, Hq);
+    return GDN_OK;
+}
+
+int check_rotary(const char* fn, const kv_rotary* r, int32_t d, bool positions) {
+    if (!r) return fail(GDN_ERR_NULL, "%s: rotary is NULL", fn);
+    if (r->rot < 0 || r->rot > d || r->rot % 2 != 0)
+        return fail(GDN_ERR_SHAPE, "%s: rot=%d is not an even number in [0, d=%d]", fn, r->rot, d);
+    if (r->axes < 1 || r->axes > KV_MAX_AXES) return fail(GDN_ERR_SHAPE, "%s: axes=%d not in [1, %d]", fn, r->axes, KV_MAX_AXES);
+    if (r->rot > 0 && (!r->turns || !positions)) return fail(GDN_ERR_NULL, "%s: turns or positions is NULL", fn);
+    if (r->q_norm_head < 0 || r->k_norm_head < 0) return fail(GDN_ERR_SHAPE, "%s: negative strides of the norms' weights", fn);
+    if (!(r->eps >= 0.f) || !isfinite(r->eps) || !isfinite(r->offset))
+        return fail(GDN_ERR_SHAPE, "%s: eps must be a finite number from 0 on, offset finite", fn);
+    if (!aligned_to(r->q_norm, 4) || !aligned_to(r->k_norm, 4) || !aligned_to(r->turns, 8) || !aligned_to(r->axis, 4))
+        return fail(GDN_ERR_ALIGN, "%s: a norm's weights, turns or axis misaligned", fn);
+    return GDN_OK;
+}
+
+gdn::KvTurn turn_of(const kv_rows* in, const kv_rows* out, const float* norm, int64_t head) {
+    gdn::KvTurn t{};
+    if (!in) return t;
+    t.in = in->p, t.in_seq = in->seq, t.in_node = in->node, t.in_head = in->head, t.norm = norm, t.norm_head = head;
+    if (out) t.out = const_cast<void*>(out->p), t.out_seq = out->seq, t.out_node = out->node, t.out_head = out->head;
+    return t;
+}
+void rotary_of(gdn::KvRotateArgs& a, const kv_rotary* r) {
+    a.turns = r->turns, a.axis = r->axis, a.eps = r->eps, a.offset = r->offset;
+    a.rot = r->rot, a.axes = r->axes, a.interleaved = r->interleaved != 0;
+}
+bool vec_norm(const float* p, int64_t head) { return aligned_to(p, 16) && head % 4 == 0; }
+
 bool vec_pages(const gdn::KvPages& c, int d, int esz) { return vec_rows(c.p, c.page, c.head, c.token, d, esz); }
 bool vec_rows(const gdn::KvRows& r, int d, int esz) { return vec_rows(r.p, r.seq, r.node, r.head, d, esz); }
 
@@ -254,6 +293,167 @@ int kv_evict(const kv_cache* cache, int32_t B, const int32_t* slots, int32_t bud
     return launched(gdn::launch_kv_evict(a, cap, vec, static_cast<cudaStream_t>(stream)), fn);
 } catch (...) {
     return caught("kv_evict");
+}
+
+int kv_norm_rotate(const kv_rotary* rotary, int32_t dtype, int32_t B, int32_t T, int32_t Hq, int32_t Hkv, int32_t d,
+                   const int32_t* positions, const kv_rows* q, const kv_rows* q_out, const kv_rows* k,
+                   const kv_rows* k_out, void* stream) try {
+    const char* fn = "kv_norm_rotate";
+    if (dtype != GDN_F32 && dtype != GDN_BF16 && dtype != GDN_F16) return fail(GDN_ERR_DTYPE, "%s: unsupported dtype %d", fn, dtype);
+    if (d < 1 || d > KV_MAX_D) return fail(GDN_ERR_SHAPE, "%s: d=%d not in [1, %d]", fn, d, KV_MAX_D);
+    if (B < 0 || T < 0 || (int64_t)B * T > 0x7fffff00) return fail(GDN_ERR_SHAPE, "%s: B=%d, T=%d", fn, B, T);
+    if ((q && Hq < 1) || (k && Hkv < 1) || Hq > 1 << 24 || Hkv > 1 << 24)
+        return fail(GDN_ERR_SHAPE, "%s: Hq=%d, Hkv=%d", fn, Hq, Hkv);
+    if ((!q && !k) || !q != !q_out || !k != !k_out) return fail(GDN_ERR_NULL, "%s: q, k and their outputs come in pairs", fn);
+    int rc = check_rotary(fn, rotary, d, positions != nullptr || (int64_t)B * T == 0);
+    if (rc || (int64_t)B * T == 0) return rc;
+    for (const kv_rows* r : {q, q_out, k, k_out})
+        if (r && (rc = check_rows(fn, "q, k or an output", r, dtype))) return rc;
+    if (!aligned_to(positions, 4)) return fail(GDN_ERR_ALIGN, "%s: positions misaligned", fn);
+    gdn::KvRotateArgs a{};
+    rotary_of(a, rotary);
+    a.q = turn_of(q, q_out, rotary->q_norm, rotary->q_norm_head);
+    a.k = turn_of(k, k_out, rotary->k_norm, rotary->k_norm_head);
+    a.positions = positions, a.tokens = B * T, a.T = T, a.Hq = Hq, a.Hkv = Hkv, a.d = d, a.dtype = dtype;
+    const int esz = gdn::dtype_size(dtype);
+    bool vec = true;
+    for (const kv_rows* r : {q, q_out, k, k_out})
+        if (r) vec = vec && vec_rows(r->p, r->seq, r->node, r->head, d, esz);
+    vec = vec && (!q || vec_norm(rotary->q_norm, rotary->q_norm_head)) && (!k || vec_norm(rotary->k_norm, rotary->k_norm_head));
+    return launched(gdn::launch_kv_rotate(a, nullptr, vec, static_cast<cudaStream_t>(stream)), fn);
+} catch (...) {
+    return caught("kv_norm_rotate");
+}
+
+int kv_append(const kv_cache* cache, int32_t B, int32_t total, int32_t Hq, const int32_t* slots, const int32_t* cu_seqlens,
+              const kv_rows* k, const kv_rows* v, const kv_rotary* rotary, const int32_t* positions, const kv_rows* q,
+              const kv_rows* q_out, int32_t* dev_err, void* stream) try {
+    const char* fn = "kv_append";
+    int rc = check_cache(fn, cache, B);
+    if (rc) return rc;
+    if (total < 0 || total > 0x7fffff00) return fail(GDN_ERR_SHAPE, "%s: total=%d", fn, total);
+    if (!q != !q_out || (q && !rotary)) return fail(GDN_ERR_NULL, "%s: q, q_out and rotary come together", fn);
+    if (q && (Hq < 1 || Hq > 1 << 24)) return fail(GDN_ERR_SHAPE, "%s: Hq=%d", fn, Hq);
+    if (rotary && (rc = check_rotary(fn, rotary, cache->d, true))) return rc;
+    if (B == 0) return GDN_OK;
+    if ((rc = check_call(fn, slots, dev_err))) return rc;
+    if (!cu_seqlens) return fail(GDN_ERR_NULL, "%s: cu_seqlens is NULL", fn);
+    if (!aligned_to(cu_seqlens, 4) || !aligned_to(positions, 4)) return fail(GDN_ERR_ALIGN, "%s: cu_seqlens or positions misaligned", fn);
+    if ((rc = check_rows(fn, "k", k, cache->dtype)) || (rc = check_rows(fn, "v", v, cache->dtype))) return rc;
+    for (const kv_rows* r : {q, q_out})
+        if (r && (rc = check_rows(fn, "q or q_out", r, cache->dtype))) return rc;
+    if (cache->stamps && !cache->counts) return fail(GDN_ERR_NULL, "%s: a cache with stamps needs counts", fn);
+    gdn::KvArgs c = args_of(cache, B, slots, dev_err);
+    c.cu = cu_seqlens, c.total = total;
+    gdn::KvRotateArgs a{};
+    if (rotary) rotary_of(a, rotary);
+    else a.axes = 1;
+    const kv_rows kp = {cache->k, 0, 0, cache->k_head}, vp = {cache->v, 0, 0, cache->v_head};  // (places: on the device)
+    a.q = turn_of(q, q_out, rotary ? rotary->q_norm : nullptr, rotary ? rotary->q_norm_head : 0);
+    a.k = turn_of(k, &kp, rotary ? rotary->k_norm : nullptr, rotary ? rotary->k_norm_head : 0);
+    a.v = turn_of(v, &vp, nullptr, 0);
+    a.positions = positions, a.tokens = total, a.T = 1, a.Hq = Hq, a.Hkv = cache->Hkv, a.d = cache->d, a.dtype = cache->dtype;
+    const int esz = gdn::dtype_size(cache->dtype);
+    bool vec = vec_pages(c.k, a.d, esz) && vec_pages(c.v, a.d, esz);
+    for (const kv_rows* r : {q, q_out, k, v})
+        if (r) vec = vec && vec_rows(r->p, 0, r->node, r->head, a.d, esz);
+    if (rotary) vec = vec && (!q || vec_norm(rotary->q_norm, rotary->q_norm_head)) && vec_norm(rotary->k_norm, rotary->k_norm_head);
+    return launched(gdn::launch_kv_rotate(a, &c, vec, static_cast<cudaStream_t>(stream)), fn);
+} catch (...) {
+    return caught("kv_append");
+}
+
+int64_t kv_prompt_attention_workspace(const kv_cache* cache, int32_t B, int32_t total, int32_t Hq) try {
+    const char* fn = "kv_prompt_attention_workspace";
+    int rc = check_cache(fn, cache, 0);
+    if (rc) return rc;
+    if (B < 0) return fail(GDN_ERR_SHAPE, "%s: B=%d", fn, B);
+    if ((rc = check_heads(fn, cache, Hq, 1.f)) || (rc = check_prompt(fn, cache, B, total, Hq))) return rc;
+    gdn::KvArgs a = args_of(cache, B, nullptr, nullptr);
+    a.total = total, a.Hq = Hq, a.G = Hq / cache->Hkv;
+    int64_t bytes = 0;
+    const cudaError_t e = prompt_workspace(a, bytes);
+    if (e != cudaSuccess) return launched(e, fn);
+    return bytes;
+} catch (...) {
+    return caught("kv_prompt_attention_workspace");
+}
+
+int kv_prompt_attention(const kv_cache* cache, int32_t B, int32_t total, int32_t Hq, const int32_t* slots,
+                        const int32_t* cu_seqlens, const kv_rows* q, float scale, void* out, float* lse, void* workspace,
+                        int64_t workspace_bytes, int32_t* dev_err, void* stream) try {
+    const char* fn = "kv_prompt_attention";
+    int rc = check_cache(fn, cache, B);
+    if (rc) return rc;
+    if ((rc = check_heads(fn, cache, Hq, scale)) || (rc = check_prompt(fn, cache, B, total, Hq))) return rc;
+    if (B == 0) return GDN_OK;
+    if ((rc = check_call(fn, slots, dev_err))) return rc;
+    if (!cu_seqlens || !out || !workspace) return fail(GDN_ERR_NULL, "%s: cu_seqlens, out or workspace is NULL", fn);
+    if ((rc = check_rows(fn, "q", q, cache->dtype))) return rc;
+    if (!aligned_to(cu_seqlens, 4) || !aligned_to(lse, 4) || !aligned_to(workspace, 16) ||
+        !aligned_to(out, gdn::dtype_size(cache->dtype)))
+        return fail(GDN_ERR_ALIGN, "%s: cu_seqlens, out, lse or workspace misaligned", fn);
+    gdn::KvArgs a = args_of(cache, B, slots, dev_err);
+    a.cu = cu_seqlens, a.total = total, a.Hq = Hq, a.G = Hq / cache->Hkv;
+    a.q = rows_of(q), a.scale = scale, a.out = out, a.lse = lse, a.part = static_cast<float*>(workspace);
+    int64_t need = 0;
+    cudaError_t e = prompt_workspace(a, need);
+    if (e != cudaSuccess) return launched(e, fn);
+    if (workspace_bytes < need)
+        return fail(GDN_ERR_SHAPE, "%s: workspace of %lld bytes, %lld needed", fn, (long long)workspace_bytes,
+                    (long long)need);
+    const int esz = gdn::dtype_size(cache->dtype);
+    const bool vec = vec_pages(a.k, a.d, esz) && vec_pages(a.v, a.d, esz) && vec_rows(a.q.p, 0, a.q.node, a.q.head, a.d, esz);
+    e = gdn::launch_kv_prompt(a, vec, static_cast<cudaStream_t>(stream));
+    return launched(e, fn);
+} catch (...) {
+    return caught("kv_prompt_attention");
+}
+
+int kv_fork(const kv_cache* cache, int32_t n, const int32_t* src, const int32_t* dst, const int32_t* new_pages,
+            int32_t* dev_err, void* stream) try {
+    const char* fn = "kv_fork";
+    int rc = check_cache(fn, cache, n);
+    if (rc) return rc;
+    if (n == 0) return GDN_OK;
+    if ((rc = check_call(fn, src, dev_err))) return rc;
+    if (!dst || !new_pages) return fail(GDN_ERR_NULL, "%s: dst or new_pages is NULL", fn);
+    if (!aligned_to(dst, 4) || !aligned_to(new_pages, 4)) return fail(GDN_ERR_ALIGN, "%s: dst or new_pages misaligned", fn);
+    const gdn::KvArgs a = args_of(cache, n, src, dev_err);
+    const int esz = gdn::dtype_size(cache->dtype);
+    return launched(gdn::launch_kv_fork(a, src, dst, new_pages, vec_pages(a.k, a.d, esz) && vec_pages(a.v, a.d, esz),
+                                        static_cast<cudaStream_t>(stream)), fn);
+} catch (...) {
+    return caught("kv_fork");
+}
+
+int64_t kv_compact_workspace(const kv_cache* cache) try {
+    const int rc = check_cache("kv_compact_workspace", cache, 0);
+    if (rc) return rc;
+    return gdn::kv_plan_ints(cache->num_pages) * 4;
+} catch (...) {
+    return caught("kv_compact_workspace");
+}
+
+int kv_compact(const kv_cache* cache, int32_t* used, void* workspace, int64_t workspace_bytes, int32_t* dev_err,
+               void* stream) try {
+    const char* fn = "kv_compact";
+    const int rc = check_cache(fn, cache, 1);
+    if (rc) return rc;
+    if (!used || !workspace || !dev_err) return fail(GDN_ERR_NULL, "%s: used, workspace or dev_err is NULL", fn);
+    if (!aligned_to(used, 4) || !aligned_to(workspace, 16) || !aligned_to(dev_err, 4))
+        return fail(GDN_ERR_ALIGN, "%s: used, workspace or dev_err misaligned", fn);
+    const int64_t need = gdn::kv_plan_ints(cache->num_pages) * 4;
+    if (workspace_bytes < need)
+        return fail(GDN_ERR_SHAPE, "%s: workspace of %lld bytes, %lld needed", fn, (long long)workspace_bytes,
+                    (long long)need);
+    const gdn::KvArgs a = args_of(cache, 1, nullptr, dev_err);
+    const int esz = gdn::dtype_size(cache->dtype);
+    return launched(gdn::launch_kv_compact(a, static_cast<int32_t*>(workspace), used,
+                                           vec_pages(a.k, a.d, esz) && vec_pages(a.v, a.d, esz),
+                                           static_cast<cudaStream_t>(stream)), fn);
+} catch (...) {
+    return caught("kv_compact");
 }
 
 }  // extern "C"

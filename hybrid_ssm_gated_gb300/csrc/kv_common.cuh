@@ -60,6 +60,9 @@ struct KvArgs {
     // eviction
     int budget, recent;
     int32_t* moves;
+    // prompts
+    const int32_t* cu;  // row offsets of the packed sequences
+    int total;
 };
 
 // Entry e of a sequence with page-table row `row`: its page and place.
@@ -334,6 +337,43 @@ __host__ __device__ inline int kv_moves_cap(int max_pages, int page_size, int bu
     const int room = max_pages * page_size;
     const int over = room > budget ? room - budget : 0;
     return over < budget ? over : budget;
+}
+
+// Norm, rotation and append.
+struct KvTurn {  // one side's rows
+    const void* in;
+    void* out;
+    int64_t in_seq, in_node, in_head, out_seq, out_node, out_head;
+    const float* norm;
+    int64_t norm_head;
+};
+
+struct KvRotateArgs {
+    KvTurn q, k, v;  // (in NULL: none; v: values, copied; of an append the keys and values go to the cache)
+    const uint64_t* turns;
+    const int32_t* axis;
+    const int32_t* positions;
+    float eps, offset;
+    int rot, axes, interleaved;
+    int tokens;  // B T, or the rows of an append
+    int T, Hq, Hkv, d, dtype;
+    int per_block;  // tokens of a block
+};
+
+// Compaction's workspace: held pages, a bit each; where each page above the border goes; the pages that move, in order.
+struct KvPlan {
+    uint32_t* bits;
+    int32_t *to, *hole, *mover, *head;  // head: pages that move (-1: refused), pages held
+    int words;
+};
+__host__ __device__ inline int64_t kv_plan_words(int64_t num_pages) { return (num_pages + 31) / 32; }
+__host__ __device__ inline int64_t kv_plan_ints(int64_t num_pages) { return 8 + kv_plan_words(num_pages) + 3 * num_pages; }
+__host__ __device__ inline KvPlan kv_plan(int32_t* ws, int64_t num_pages) {
+    KvPlan p;
+    p.words = (int)kv_plan_words(num_pages);
+    p.head = ws, p.bits = reinterpret_cast<uint32_t*>(ws + 8);
+    p.to = ws + 8 + p.words, p.hole = p.to + num_pages, p.mover = p.hole + num_pages;
+    return p;
 }
 
 }  // namespace gdn

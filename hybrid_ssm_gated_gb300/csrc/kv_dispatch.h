@@ -23,6 +23,18 @@ cudaError_t launch_kv_weights_tc(const KvArgs& a, cudaStream_t stream);
 // Joins the partials of an attention kernel of `grid` CTAs, on the same stream.
 cudaError_t launch_kv_join(const KvArgs& a, int grid, cudaStream_t stream);
 
+// Attention of packed prompts: on the FP32 pipe, on the tensor cores (as above), the join of either, workspaces.
+cudaError_t launch_kv_prompt(KvArgs& a, bool vec, cudaStream_t stream);
+cudaError_t kv_prompt_workspace(KvArgs& a, int64_t& bytes);
+cudaError_t launch_kp_join(const KvArgs& a, int grid, cudaStream_t stream);
+
+// Norm and rotation of rows; with `cache`, keys and values go to its pages. vec: rows 16 bytes at a time.
+cudaError_t launch_kv_rotate(KvRotateArgs& r, const KvArgs* cache, bool vec, cudaStream_t stream);
+
+cudaError_t launch_kv_fork(const KvArgs& a, const int32_t* src, const int32_t* dst, const int32_t* new_pages, bool vec,
+                           cudaStream_t stream);
+cudaError_t launch_kv_compact(const KvArgs& a, int32_t* ws, int32_t* used, bool vec, cudaStream_t stream);
+
 cudaError_t launch_kv_commit(const KvArgs& a, bool vec, cudaStream_t stream);
 cudaError_t launch_kv_evict(const KvArgs& a, int cap, bool vec, cudaStream_t stream);
 

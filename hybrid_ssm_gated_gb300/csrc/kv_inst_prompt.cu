@@ -1,0 +1,62 @@
+// Instantiations and launches of the prompt attention on the FP32 pipe, and of its join.
+#include "gdn_launch.cuh"
+#include "kv_dispatch.h"
+#include "kv_prompt_fp32.cuh"
+
+namespace gdn {
+
+namespace {
+
+using Kernel = void (*)(const KvArgs, const int);
+
+template <int NC>
+Kernel of_dtype(int dtype) {
+    return dtype == GDN_F32 ? kv_prompt_kernel<float, NC>
+                            : dtype == GDN_BF16 ? kv_prompt_kernel<__nv_bfloat16, NC> : kv_prompt_kernel<__half, NC>;
+}
+Kernel choose(const KvArgs& a) {
+    return a.d <= 64 ? of_dtype<1>(a.dtype) : a.d <= 128 ? of_dtype<2>(a.dtype) : of_dtype<4>(a.dtype);
+}
+
+cudaError_t wave(const KvArgs& a, int64_t& grid) {
+    DeviceInfo di;
+    cudaError_t e = device_info(di);
+    if (e != cudaSuccess) return e;
+    int bps = 0;
+    if ((e = prepare_kernel(choose(a), kpg::NT, kpg::layout(a.d).bytes, bps)) != cudaSuccess) return e;
+    grid = (int64_t)di.sms * bps;
+    return cudaSuccess;
+}
+
+}  // namespace
+
+cudaError_t launch_kp_join(const KvArgs& a, int grid, cudaStream_t stream) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(grid * kpj::SHARE)), cfg.blockDim = dim3(kpj::NT), cfg.stream = stream;
+    cudaLaunchAttribute pdl{};
+    pdl.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    pdl.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &pdl, cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kp_join_kernel, a);
+}
+
+cudaError_t kv_prompt_workspace(KvArgs& a, int64_t& bytes) {
+    int64_t grid = 0;
+    a.row_block = kpg::RB;
+    const cudaError_t e = wave(a, grid);
+    bytes = kp_part_bytes(grid, a.row_block, a.d) + grid * (int64_t)sizeof(KpBorder);
+    return e;
+}
+
+cudaError_t launch_kv_prompt(KvArgs& a, bool vec, cudaStream_t stream) {
+    int64_t grid = 0;
+    a.row_block = kpg::RB;
+    cudaError_t e = wave(a, grid);
+    if (e != cudaSuccess) return e;
+    a.border = reinterpret_cast<char*>(a.part) + kp_part_bytes(grid, a.row_block, a.d);
+    choose(a)<<<(unsigned)grid, kpg::NT, kpg::layout(a.d).bytes, stream>>>(a, vec);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    return launch_kp_join(a, (int)grid, stream);
+}
+
+}  // namespace gdn

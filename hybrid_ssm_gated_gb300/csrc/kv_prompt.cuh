@@ -1,0 +1,342 @@
+// kv_prompt.cuh -- what the prompt attention kernels share: the division of packed
+// causal prompts over a persistent grid, rows that no unit computes, and the join
+// of units that several CTAs computed.
+//
+// Units. The rows of a sequence and key head are its tokens' heads of the group,
+// token by token (row = token * G + head). A unit is a block of RB of them; its keys
+// end behind its last token, so that blocks grow along a prompt.
+//
+// Division. All units in order (sequence, key head, block) make a line, a unit as
+// long as its keys and a few more (KP_EXTRA) that stand for what it costs beyond its
+// tiles, and CTA c of `parts` takes [W c / parts, W (c + 1) / parts) of it: every CTA
+// has the same work, whatever the lengths, and neighbours read the same keys. In
+// units of a G-th key the length of block i is G (prefix + extra) + RB (i + 1), so
+// its place on the line is a quadratic in i: a CTA finds its range without a walk. A
+// unit that a border cuts is cut between tiles, and leaves one partial result a CTA
+// (unnormalised outputs, maximum and sum), joined by kp_join_kernel.
+#pragma once
+
+#include "kv_common.cuh"
+
+namespace gdn {
+
+struct KpSeq {
+    int slot;   // -1: padding, or refused with an error bit
+    int first;  // its first row
+    int n, len;  // rows, entries
+    int err;
+    bool owned;  // the offsets are in order: its rows are its own
+};
+
+__device__ __forceinline__ KpSeq kp_seq(const KvArgs& a, int b) {
+    KpSeq s{-1, 0, 0, 0, 0, true};
+    const int first = a.cu[b], end = a.cu[b + 1], slot = a.slots[b];
+    if (first < 0 || end < first || end > a.total) {
+        s.err = GDN_DEVERR_SEQLEN, s.owned = false;
+        return s;
+    }
+    s.first = first, s.n = end - first;
+    if (slot < 0) return s;
+    if (slot >= a.num_slots) {
+        s.err = GDN_DEVERR_SLOT;
+        return s;
+    }
+    const int len = a.lengths[slot];
+    if (len < s.n || (int64_t)len > (int64_t)a.max_pages * a.page_size) {
+        s.err = KV_DEVERR_LENGTH;
+        return s;
+    }
+    s.slot = slot, s.len = len;
+    return s;
+}
+
+constexpr int KP_EXTRA = 256;  // keys that a unit's start and end cost as much as
+constexpr int KP_LEAST = 512;  // keys of a CTA's range at least
+
+// Blocks of a sequence, and the length of the line before block i of a key head.
+template <int RB>
+__device__ __forceinline__ int kp_blocks(const KvArgs& a, const KpSeq& s) {
+    return s.slot < 0 ? 0 : (int)(((long long)s.n * a.G + RB - 1) / RB);
+}
+template <int RB>
+__device__ __forceinline__ long long kp_before(const KvArgs& a, const KpSeq& s, long long i) {
+    return i * ((long long)a.G * (s.len - s.n + KP_EXTRA)) + RB * (i * (i + 1) / 2);
+}
+template <int RB>
+__device__ __forceinline__ long long kp_seq_cost(const KvArgs& a, const KpSeq& s) {
+    return kp_before<RB>(a, s, kp_blocks<RB>(a, s)) * a.Hkv;
+}
+
+// What the scan over sequences leaves in shared memory: the CTA's range.
+struct KpMark {
+    long long off;  // from the beginning of sequence b's share of the line
+    int b;          // a.B: the end of the line
+};
+template <int NT>
+struct KpScan {
+    KpSeq seq[NT];  // the batch's sequences, where there are at most NT
+    long long warp_sum[NT / 32];
+    KpMark mark[2];  // beginning and end of the range
+    long long q;     // ranges: length, and how many are one longer
+    int r, parts;
+};
+
+// By the whole block of NT threads: the division, and this CTA's range.
+template <int RB, int NT>
+__device__ __forceinline__ void kp_locate(const KvArgs& a, KpScan<NT>& sc) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int run = a.B <= NT ? 1 : (a.B + NT - 1) / NT;
+    const int b0 = (int)min((long long)a.B, (long long)tid * run), b1 = min(a.B, b0 + run);
+    long long sum = 0;
+    for (int b = b0; b < b1; ++b) {
+        const KpSeq s = kp_seq(a, b);
+        if (run == 1) sc.seq[b] = s;
+        sum += kp_seq_cost<RB>(a, s);
+    }
+    long long inc = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(FULL_MASK, inc, o);
+        if (lane >= o) inc += y;
+    }
+    if (lane == 31) sc.warp_sum[warp] = inc;
+    if (tid < 2) sc.mark[tid].b = a.B, sc.mark[tid].off = 0;
+    __syncthreads();
+    long long before = inc - sum, total = 0;
+    for (int w = 0; w < NT / 32; ++w) {
+        if (w < warp) before += sc.warp_sum[w];
+        total += sc.warp_sum[w];
+    }
+    const long long most = total / ((long long)KP_LEAST * a.G);
+    const int parts = (int)(most < 1 ? 1 : most < gridDim.x ? most : gridDim.x);
+    const long long q = total / parts;
+    const int r = (int)(total - q * parts), c = blockIdx.x;
+    if (tid == 0) sc.q = q, sc.r = r, sc.parts = parts;
+    for (int side = 0; side < 2; ++side) {
+        const int x = c + side;
+        if (x > parts) break;
+        const long long want = q * x + min(x, r);
+        if (want >= before && want < before + sum) {
+            long long at = before;
+            int b = b0;
+            for (; b < b1 - 1; ++b) {
+                const long long n = kp_seq_cost<RB>(a, run == 1 ? sc.seq[b] : kp_seq(a, b));
+                if (want < at + n) break;
+                at += n;
+            }
+            sc.mark[side].b = b, sc.mark[side].off = want - at;
+        }
+    }
+    __syncthreads();
+}
+
+// A place between tiles: in sequence b, key head h, block i, ahead of tile t.
+struct KpPlace {
+    int b, h, i, t;
+};
+
+// A walk along a CTA's segments: runs of tiles of one unit.
+template <int RB, int KT>
+struct KpWalk {
+    const KvArgs& a;
+    const KpSeq* seq;  // the batch's sequences in shared memory, or NULL
+    KpPlace end;
+    int b, h, i, blocks;
+    KpSeq s;
+    int nt, t0, t1;  // the unit's tiles, and the segment's
+
+    __device__ __forceinline__ int tiles(const KpSeq& x, int blk) const {
+        const long long rows = min((long long)x.n * a.G, (long long)(blk + 1) * RB);
+        return (x.len - x.n + (int)((rows - 1) / a.G) + KT) / KT;  // keys 0 .. prefix + last token
+    }
+    __device__ __forceinline__ KpSeq get(int x) const { return seq ? seq[x] : kp_seq(a, x); }
+    // The place that a point of the line is cut at.
+    __device__ __forceinline__ KpPlace place(const KpMark& m) const {
+        KpPlace p{m.b, 0, 0, 0};
+        if (m.b >= a.B) return p;
+        const KpSeq x = get(m.b);
+        const int nb = kp_blocks<RB>(a, x);
+        const long long one = kp_before<RB>(a, x, nb);
+        p.h = (int)(m.off / one);
+        const long long off = m.off - one * p.h;
+        int lo = 0, hi = nb;  // the block that holds `off`
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (kp_before<RB>(a, x, mid) <= off) lo = mid;
+            else hi = mid;
+        }
+        p.i = lo;
+        p.t = tile_at(off - kp_before<RB>(a, x, lo), tiles(x, lo));
+        return p;
+    }
+    // Tile that a point `off` of a unit is cut ahead of.
+    __device__ __forceinline__ int tile_at(long long off, int n) const {
+        const long long t = (off - (long long)KP_EXTRA * a.G) / ((long long)KT * a.G);
+        return (int)(t < 0 ? 0 : t < n ? t : n - 1);  // (the last tile's CTA is the one that ends the unit)
+    }
+    __device__ __forceinline__ bool before_end() const {
+        return b < end.b || (b == end.b && (h < end.h || (h == end.h && i <= end.i)));
+    }
+    __device__ __forceinline__ void load() {
+        s = get(b);
+        blocks = kp_blocks<RB>(a, s);
+    }
+    // The segment of the current unit from tile t on; false if the range ends ahead of it.
+    __device__ __forceinline__ bool segment(int t) {
+        if (!before_end() || b >= a.B) return false;
+        nt = tiles(s, i), t0 = t;
+        t1 = b == end.b && h == end.h && i == end.i ? min(end.t, nt) : nt;
+        return true;
+    }
+    template <int NT>
+    __device__ __forceinline__ KpWalk(const KvArgs& a_, const KpScan<NT>& sc, bool& some)
+        : a(a_), seq(a_.B <= NT ? sc.seq : nullptr) {
+        t0 = t1 = nt = 0;
+        some = false;
+        if ((int)blockIdx.x >= sc.parts) return;
+        const KpPlace from = place(sc.mark[0]);
+        end = place(sc.mark[1]);
+        b = from.b, h = from.h, i = from.i;
+        if (b >= a.B) return;
+        load();
+        some = segment(from.t);
+        if (some && t0 >= t1) some = next();
+    }
+    __device__ __forceinline__ bool step() {  // to the next unit
+        if (++i == blocks) {
+            i = 0;
+            if (++h == a.Hkv) {
+                h = 0;
+                do {
+                    if (++b >= a.B) return false;
+                    load();
+                } while (blocks == 0);
+            }
+        }
+        return true;
+    }
+    // The next segment with a tile; false at the end of the range.
+    __device__ __forceinline__ bool next() {
+        do {
+            if (!step() || !segment(0)) return false;
+        } while (t0 >= t1);
+        return true;
+    }
+    __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == nt; }
+    // Which of the CTA's two partials the segment's is: only its first segment begins inside a unit.
+    __device__ __forceinline__ int later() const { return t0 == 0; }
+    __device__ __forceinline__ int r0() const { return i * RB; }
+    __device__ __forceinline__ int rows() const {
+        const long long left = (long long)s.n * a.G - (long long)i * RB;
+        return (int)(left < RB ? left : RB);
+    }
+};
+
+// A unit cut by the end of the CTA's range in which it begins: what the join needs, one record a CTA.
+struct KpBorder {
+    int first, h, r0, rows, n;  // the sequence's first row, and CTAs of the unit: this one and n - 1 behind it (0: none)
+    int pad[3];
+};
+
+// Writes this CTA's record: of the segment `w`, if the unit begins in it and goes on past the range (which is then at
+// its end, sc.mark[1] inside the unit), else that there is none. By one thread.
+template <int RB, int KT, int NT>
+__device__ __forceinline__ void kp_border(const KvArgs& a, const KpScan<NT>& sc, const KpWalk<RB, KT>& w) {
+    KpBorder k{};
+    k.first = w.s.first, k.h = w.h, k.r0 = w.r0(), k.rows = w.rows(), k.n = 1;
+    const long long u0 = kp_before<RB>(a, w.s, w.blocks) * w.h + kp_before<RB>(a, w.s, w.i);  // in its sequence's share
+    const long long size = kp_before<RB>(a, w.s, w.i + 1) - kp_before<RB>(a, w.s, w.i), at = sc.mark[1].off - u0;
+    const auto start = [&](int x) { return sc.q * x + min(x, sc.r); };
+    const int c = blockIdx.x;
+    // a range is longer than two tiles: each CTA whose range begins inside the unit has one of its tiles
+    for (int x = c + 1; x < sc.parts; ++x) {
+        ++k.n;
+        if (at + start(x + 1) - start(c + 1) >= size) break;
+    }
+    static_cast<KpBorder*>(a.border)[blockIdx.x] = k;
+}
+__device__ __forceinline__ void kp_no_border(const KvArgs& a) { static_cast<KpBorder*>(a.border)[blockIdx.x].n = 0; }
+
+// Rows of sequences that no unit computes (padding, refused), by `n` threads of each CTA, of which this is
+// thread `i`. Error bits of refused sequences are set here, once a call.
+__device__ __forceinline__ void kp_empty_rows(const KvArgs& a, const KpSeq* seq, int i, int n) {
+    const int64_t row_bytes = (int64_t)a.Hq * a.d * dtype_size(a.dtype);
+    const bool vec = (reinterpret_cast<uintptr_t>(a.out) & 15) == 0 && row_bytes % 16 == 0;
+    for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
+        const KpSeq s = seq ? seq[b] : kp_seq(a, b);
+        if (s.err && i == 0) set_error(a.dev_err, s.err);
+        if (s.slot >= 0 || !s.owned) continue;
+        char* o = static_cast<char*>(a.out) + s.first * row_bytes;
+        const int64_t bytes = s.n * row_bytes;
+        if (vec)
+            for (int64_t x = (int64_t)i * 16; x < bytes; x += (int64_t)n * 16)
+                *reinterpret_cast<uint4*>(o + x) = make_uint4(0, 0, 0, 0);
+        else
+            for (int64_t x = (int64_t)i * 2; x < bytes; x += (int64_t)n * 2) *reinterpret_cast<uint16_t*>(o + x) = 0;
+        if (a.lse)
+            for (int64_t r = (int64_t)s.first * a.Hq + i; r < ((int64_t)s.first + s.n) * a.Hq; r += n) a.lse[r] = -INFINITY;
+    }
+}
+
+// Partials: column e of the outputs of RB rows, then the rows' maxima and sums. A sum of -1 says that the CTA
+// met a page outside the pool (or gave up): the unit's rows are those of a refused sequence.
+__host__ __device__ inline int64_t kp_part_floats(int row_block, int d) { return (int64_t)row_block * (d + 2); }
+__host__ __device__ inline int64_t kp_part_bytes(int64_t grid, int row_block, int d) {
+    return grid * 2 * kp_part_floats(row_block, d) * 4;
+}
+
+namespace kpj {
+constexpr int NT = 128, WARPS = NT / 32, SHARE = 16;  // blocks a border
+}
+
+// Blocks SHARE c .. SHARE c + SHARE - 1 join the unit of CTA c's record. A job is 32 rows (a lane each) by eight
+// outputs.
+__global__ void __launch_bounds__(kpj::NT) kp_join_kernel(const __grid_constant__ KvArgs a) {
+    using namespace kpj;
+    const int c = blockIdx.x / SHARE, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    kv_grid_wait();
+    const KpBorder k = static_cast<const KpBorder*>(a.border)[c];
+    if (k.n == 0) return;
+    const int RB = a.row_block, cols = (a.d + 7) / 8, jobs = (k.rows + 31) / 32 * cols;
+    const int64_t size = kp_part_floats(RB, a.d);
+    const auto part = [&](int j) { return a.part + ((int64_t)(c + j) * 2 + (j == 0)) * size; };
+    const bool vec = a.d % 8 == 0 && reinterpret_cast<uintptr_t>(a.out) % 16 == 0;
+    for (int x = (blockIdx.x % SHARE) * WARPS + warp; x < jobs; x += SHARE * WARPS) {
+        const int g = x / cols, e0 = (x - g * cols) * 8, r = g * 32 + lane;
+        if (r >= k.rows) continue;
+        float m = -INFINITY;
+        bool refused = false;
+        for (int j = 0; j < k.n; ++j) {
+            const float* p = part(j) + (int64_t)RB * a.d + r;
+            m = fmaxf(m, p[0]), refused = refused || p[RB] == -1.f;
+        }
+        const float base = m == -INFINITY ? 0.f : m;
+        float o[8] = {}, l = 0.f;
+        for (int j = 0; j < k.n; ++j) {
+            const float* p = part(j) + r;
+            const float f = kv_ex2(p[(int64_t)RB * a.d] - base);
+            l = fmaf(p[(int64_t)RB * a.d + RB], f, l);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (e0 + e < a.d) o[e] = fmaf(p[(int64_t)(e0 + e) * RB], f, o[e]);
+        }
+        if (refused) l = 0.f;
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        const int row = k.r0 + r, tok = row / a.G;
+        const int64_t to = ((int64_t)k.first + tok) * a.Hq + k.h * a.G + (row - tok * a.G);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o[e] = l == 0.f ? 0.f : o[e] * inv;
+        if (vec && a.dtype != GDN_F32) {
+            uint4 w;
+            if (a.dtype == GDN_BF16) w = Store<__nv_bfloat16>::pack(o);
+            else w = Store<__half>::pack(o);
+            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + to * a.d + e0) = w;
+        } else {
+            for (int e = 0; e < 8; ++e)
+                if (e0 + e < a.d) store_elem(a.out, to * a.d + e0 + e, a.dtype, o[e]);
+        }
+        if (e0 == 0 && a.lse) a.lse[to] = l == 0.f ? -INFINITY : (m + log2f(l)) * LN2;
+    }
+}
+
+}  // namespace gdn

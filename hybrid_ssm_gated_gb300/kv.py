@@ -16,7 +16,7 @@ from .gdn import DTYPE_CODE, _check, _ptr
 from .gdn import _stream as _given_stream
 
 DEVERR_LENGTH, DEVERR_PAGE, DEVERR_NODES = 64, 128, 256
-MAX_NODES, MAX_D = 64, 256
+MAX_NODES, MAX_D, MAX_AXES = 64, 256, 4
 
 
 class kv_cache(C.Structure):
@@ -32,8 +32,14 @@ class kv_rows(C.Structure):
     _fields_ = [("p", C.c_void_p), ("seq", C.c_int64), ("node", C.c_int64), ("head", C.c_int64)]
 
 
+class kv_rotary(C.Structure):
+    _fields_ = [("q_norm", C.c_void_p), ("k_norm", C.c_void_p), ("q_norm_head", C.c_int64), ("k_norm_head", C.c_int64),
+                ("eps", C.c_float), ("offset", C.c_float), ("turns", C.c_void_p), ("axis", C.c_void_p),
+                ("rot", C.c_int32), ("axes", C.c_int32), ("interleaved", C.c_int32)]
+
+
 _P, _I, _F, _L = C.c_void_p, C.c_int32, C.c_float, C.c_int64
-_CACHE, _ROWS = C.POINTER(kv_cache), C.POINTER(kv_rows)
+_CACHE, _ROWS, _ROTARY = C.POINTER(kv_cache), C.POINTER(kv_rows), C.POINTER(kv_rotary)
 _SIGS = {
     "kv_tree_attention": ([_CACHE, _I, _I, _I, _P, _ROWS, _ROWS, _ROWS, _P, _P, _F, _P, _P, _P, _L, _P, _P], C.c_int),
     "kv_tree_attention_workspace": ([_CACHE, _I, _I, _I], _L),
@@ -41,6 +47,13 @@ _SIGS = {
     "kv_accumulate": ([_CACHE, _I, _I, _I, _I, _P, _ROWS, _P, _P, _P, _F, _F, _P, _P], C.c_int),
     "kv_evict": ([_CACHE, _I, _P, _I, _I, _P, _L, _P, _P], C.c_int),
     "kv_evict_workspace": ([_CACHE, _I, _I], _L),
+    "kv_norm_rotate": ([_ROTARY, _I, _I, _I, _I, _I, _I, _P, _ROWS, _ROWS, _ROWS, _ROWS, _P], C.c_int),
+    "kv_append": ([_CACHE, _I, _I, _I, _P, _P, _ROWS, _ROWS, _ROTARY, _P, _ROWS, _ROWS, _P, _P], C.c_int),
+    "kv_prompt_attention": ([_CACHE, _I, _I, _I, _P, _P, _ROWS, _F, _P, _P, _P, _L, _P, _P], C.c_int),
+    "kv_prompt_attention_workspace": ([_CACHE, _I, _I, _I], _L),
+    "kv_fork": ([_CACHE, _I, _P, _P, _P, _P, _P], C.c_int),
+    "kv_compact": ([_CACHE, _P, _P, _L, _P, _P], C.c_int),
+    "kv_compact_workspace": ([_CACHE], _L),
 }
 _lib = None
 
@@ -234,5 +247,160 @@ def kv_evict(cache: KVCache, slots, budget: int, recent: int, dev_err, workspace
     largest weights. workspace from kv_evict_workspace."""
     B = slots.shape[0]
     _check(_on_device(cache, lib().kv_evict, cache._ref, B, _ints(slots, cache, (B,), "slots"), budget, recent,
+                      _whole(workspace, cache, "workspace"), workspace.numel(), _whole(dev_err, cache, "dev_err"),
+                      _stream(stream, cache.device)))
+
+
+class Rotary:
+    """Norms of queries and keys and the position rotation of an attention layer (kv_rotary in include/kv.h).
+
+    inv_freq: radians a position of each turned pair (rot / 2 numbers, taken in 64 bits), or None for no
+    rotation; axis: which of the `axes` positions each pair follows (None: the first); interleaved: pairs
+    are neighbours, else elements i and i + rot / 2. q_norm, k_norm: None, or FP32 weights [d], or [heads, d]
+    of each head, to which `offset` is added (1 for weights stored about zero).
+    """
+
+    def __init__(self, inv_freq=None, axis=None, axes: int = 1, interleaved: bool = False, q_norm=None, k_norm=None,
+                 eps: float = 1e-6, offset: float = 0.0, device="cuda"):
+        freq = [] if inv_freq is None else torch.as_tensor(inv_freq, dtype=torch.float64, device="cpu").tolist()
+        if not all(math.isfinite(f) for f in freq):
+            raise ValueError("kv: inv_freq must be finite")
+        if axis is not None and (len(axis) != len(freq) or any(not 0 <= int(x) < axes for x in axis)):
+            raise ValueError("kv: axis must name one of the axes for every frequency")
+        if not 1 <= axes <= MAX_AXES:
+            raise ValueError(f"kv: axes must be 1 to {MAX_AXES}")
+        for name, t in (("q_norm", q_norm), ("k_norm", k_norm)):
+            if t is not None and (t.dtype != torch.float32 or t.dim() not in (1, 2) or not t.is_cuda or t.stride(-1) != 1):
+                raise ValueError(f"kv: {name} must be a float32 CUDA tensor [d] or [heads, d] with unit stride in d")
+        norms = [t for t in (q_norm, k_norm) if t is not None]
+        if norms:
+            device = norms[0].device
+        turns = [round(f / (2 * math.pi) * 2.0 ** 64) % (1 << 64) for f in freq]
+        self.turns = torch.tensor([t - (1 << 64) if t >> 63 else t for t in turns], dtype=torch.int64, device=device)
+        self.axis = None if axis is None else torch.tensor([int(x) for x in axis], dtype=torch.int32, device=device)
+        self.q_norm, self.k_norm, self.rot, self.axes = q_norm, k_norm, 2 * len(freq), int(axes)
+        self.device = self.turns.get_device()
+        if any(t.get_device() != self.device for t in norms):
+            raise ValueError("kv: the norms' weights lie on one device")
+        head = lambda t: t.stride(0) if t is not None and t.dim() == 2 else 0
+        at = lambda t: None if t is None else t.data_ptr()
+        self._c = kv_rotary(at(q_norm), at(k_norm), head(q_norm), head(k_norm), eps, offset,
+                            self.turns.data_ptr() if freq else None, at(self.axis), self.rot, self.axes, int(interleaved))
+        self._ref = C.byref(self._c)
+
+    def check(self, norm, heads: int, d: int) -> None:
+        """That a side's weights are those of rows [heads, d]."""
+        if norm is not None and (norm.shape[-1] != d or (norm.dim() == 2 and norm.shape[0] != heads)):
+            raise ValueError(f"kv: a norm's weights must be [{d}] or [{heads}, {d}]")
+
+
+def _turned(x, out, name: str, like):
+    """kv_rows of a side of kv_norm_rotate [B, T, heads, d] and of its output; None for neither."""
+    if x is None and out is None:
+        return None, None
+    if x is None or out is None or x.dim() != 4 or x.shape != out.shape or x.shape[:2] != like.shape[:2] or \
+            x.shape[3] != like.shape[3] or any(t.dtype is not like.dtype or t.get_device() != like.get_device()
+                                               or t.stride(3) != 1 for t in (x, out)):
+        raise ValueError(f"kv: {name} and {name}_out must be tensors [B, T, heads, d] of one dtype and device, with unit "
+                         "stride in d")
+    return tuple(kv_rows(t.data_ptr(), *t.stride()[:3]) for t in (x, out))
+
+
+def kv_norm_rotate(rotary: Rotary, positions, q=None, k=None, q_out=None, k_out=None, stream=None) -> None:
+    """Norm and rotation of drafted tokens: q [B, T, Hq, d], k [B, T, Hkv, d] into q_out, k_out (which may be q
+    and k); positions [axes, B, T] int32 ([B, T] with one axis; None where nothing is turned)."""
+    like = q if q is not None else k
+    if like is None or like.dim() != 4 or like.dtype not in DTYPE_CODE or like.get_device() != rotary.device:
+        raise ValueError("kv: q or k must be a tensor [B, T, heads, d] on the rotary's device")
+    B, T, _, d = like.shape
+    Hq, Hkv = (0 if t is None else t.shape[2] for t in (q, k))
+    rq, ro = _turned(q, q_out, "q", like)
+    rk, rp = _turned(k, k_out, "k", like)
+    if q is not None:
+        rotary.check(rotary.q_norm, Hq, d)
+    if k is not None:
+        rotary.check(rotary.k_norm, Hkv, d)
+    shape = (B, T) if positions is not None and positions.dim() == 2 and rotary.axes == 1 else (rotary.axes, B, T)
+    pos = _ints(positions, rotary, shape, "positions")
+    _check(_on_device(rotary, lib().kv_norm_rotate, rotary._ref, DTYPE_CODE[like.dtype], B, T, Hq, Hkv, d, pos, rq, ro,
+                      rk, rp, _stream(stream, rotary.device)))
+
+
+def _packed(t, cache: KVCache, heads: int, total: int, name: str) -> kv_rows:
+    if t.dim() != 3 or t.shape != (total, heads, cache.d) or t.dtype is not cache.dtype or \
+            t.get_device() != cache.device or t.stride(2) != 1:
+        raise ValueError(f"kv: {name} must be a tensor [{total}, {heads}, {cache.d}] of the cache's dtype on the cache's "
+                         "device, with unit stride in d")
+    return kv_rows(t.data_ptr(), 0, t.stride(0), t.stride(1))
+
+
+def kv_append(cache: KVCache, slots, cu_seqlens, k, v, dev_err, rotary: Rotary | None = None, positions=None, q=None,
+              q_out=None, stream=None) -> None:
+    """The prompts' keys and values into the cache: k, v [total, Hkv, d], sequence b's rows cu_seqlens[b] on
+    (cu_seqlens [B + 1] int32, on the device). With `rotary`, keys are normed and turned on the way, and q
+    [total, Hq, d] into q_out (which may be q); positions [axes, total] int32 ([total] with one axis), None:
+    the sequence's count and on."""
+    B, total = slots.shape[0], k.shape[0]
+    rk, rv = _packed(k, cache, cache.Hkv, total, "k"), _packed(v, cache, cache.Hkv, total, "v")
+    rq = ro = None
+    Hq = 0
+    if (q is None) != (q_out is None) or (q is not None and rotary is None):
+        raise ValueError("kv: q, q_out and rotary come together")
+    if q is not None:
+        Hq = q.shape[1]
+        rq, ro = _packed(q, cache, Hq, total, "q"), _packed(q_out, cache, Hq, total, "q_out")
+        rotary.check(rotary.q_norm, Hq, cache.d)
+    if rotary is not None:
+        if rotary.device != cache.device:
+            raise ValueError("kv: the rotary must lie on the cache's device")
+        rotary.check(rotary.k_norm, cache.Hkv, cache.d)
+    axes = 1 if rotary is None else rotary.axes
+    shape = (total,) if positions is not None and positions.dim() == 1 and axes == 1 else (axes, total)
+    _check(_on_device(cache, lib().kv_append, cache._ref, B, total, Hq, _ints(slots, cache, (B,), "slots"),
+                      _ints(cu_seqlens, cache, (B + 1,), "cu_seqlens"), rk, rv, None if rotary is None else rotary._ref,
+                      _ints(positions, cache, shape, "positions"), rq, ro, _whole(dev_err, cache, "dev_err"),
+                      _stream(stream, cache.device)))
+
+
+def kv_prompt_workspace(cache: KVCache, B: int, q) -> torch.Tensor:
+    """Workspace for kv_prompt_attention calls of up to B sequences with queries of q's shape [total, Hq, d] (or
+    fewer rows)."""
+    return _workspace(cache, lib().kv_prompt_attention_workspace, int(B), q.shape[0], q.shape[1])
+
+
+def kv_prompt_attention(cache: KVCache, slots, cu_seqlens, q, out, dev_err, workspace, lse=None, scale=None,
+                        stream=None) -> None:
+    """Causal attention of packed prompts over the cache, after kv_append of the same rows: q [total, Hq, d]; out
+    [total, Hq, d]; lse None or [total, Hq] fp32; workspace from kv_prompt_workspace."""
+    total, Hq = q.shape[:2]
+    B = slots.shape[0]
+    rq = _packed(q, cache, Hq, total, "q")
+    if out.shape != q.shape or out.dtype is not cache.dtype:
+        raise ValueError("kv: out must be [total, Hq, d] of the cache's dtype")
+    _check(_on_device(cache, lib().kv_prompt_attention, cache._ref, B, total, Hq, _ints(slots, cache, (B,), "slots"),
+                      _ints(cu_seqlens, cache, (B + 1,), "cu_seqlens"), rq,
+                      1.0 / math.sqrt(cache.d) if scale is None else scale, _whole(out, cache, "out"),
+                      _ints(lse, cache, (total, Hq), "lse", torch.float32), _whole(workspace, cache, "workspace"),
+                      workspace.numel(), _whole(dev_err, cache, "dev_err"), _stream(stream, cache.device)))
+
+
+def kv_fork(cache: KVCache, src, dst, new_pages, dev_err, stream=None) -> None:
+    """Sequences dst become copies of sequences src ([n] int32 slots): page j is shared where new_pages[i][j]
+    ([n, max_pages] int32) is negative, else copied to that page."""
+    n = src.shape[0]
+    _check(_on_device(cache, lib().kv_fork, cache._ref, n, _ints(src, cache, (n,), "src"), _ints(dst, cache, (n,), "dst"),
+                      _ints(new_pages, cache, (n, cache.page_table.shape[1]), "new_pages"),
+                      _whole(dev_err, cache, "dev_err"), _stream(stream, cache.device)))
+
+
+def kv_compact_workspace(cache: KVCache) -> torch.Tensor:
+    """Workspace for kv_compact calls."""
+    return _workspace(cache, lib().kv_compact_workspace)
+
+
+def kv_compact(cache: KVCache, used, dev_err, workspace, stream=None) -> None:
+    """Moves the pages that sequences hold to the front of the pool; used [1] int32 takes their number (the pages
+    from there on are free)."""
+    _check(_on_device(cache, lib().kv_compact, cache._ref, _ints(used, cache, (1,), "used"),
                       _whole(workspace, cache, "workspace"), workspace.numel(), _whole(dev_err, cache, "dev_err"),
                       _stream(stream, cache.device)))

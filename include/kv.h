@@ -170,6 +170,139 @@ int kv_evict(const kv_cache* cache, int32_t B, const int32_t* slots, int32_t bud
 
 int64_t kv_evict_workspace(const kv_cache* cache, int32_t B, int32_t budget);
 
+/*
+ * ---------------------------------------------------------------- prompts
+ *
+ * A prompt's way through an attention layer: kv_append turns its queries and
+ * keys, and puts keys and values into the cache; kv_prompt_attention attends.
+ * The prompts of a call are packed as in gdn_prefill: sequence b owns rows
+ * cu_seqlens[b] .. cu_seqlens[b+1]-1 of [total][heads][d] activations, whose
+ * kv_rows take `node` as the stride of a row (`seq` is not looked at).
+ * cu_seqlens [B + 1] int32 (device), 0 <= cu_seqlens[b] <= cu_seqlens[b+1] <=
+ * total. Rows of no sequence are neither read nor written.
+ */
+
+/*
+ * The norm of each head's row and the position rotation. With x a row of d
+ * elements:
+ *     y = x / sqrt(mean(x^2) + eps) * (weight + offset)     (no weight: y = x)
+ * and pair i < rot / 2 of its first `rot` elements is turned by the angle
+ * a = 2 pi turns[i] / 2^64 * position[axis[i]]:
+ *     z_1 = y_1 cos a - y_2 sin a,  z_2 = y_1 sin a + y_2 cos a
+ * Pairs are elements i and i + rot / 2, or 2i and 2i + 1 (interleaved). FP32
+ * arithmetic, one rounding at the end; angles are formed in whole numbers
+ * modulo a turn, so that far positions lose nothing.
+ * q_norm, k_norm       FP32 weights of queries and keys, head h's at p + h *
+ *                      head stride (0: one row for all heads), d of them;
+ *                      NULL: that side is not normed.
+ * turns    [rot / 2] 64-bit fractions of a turn a position.
+ * axis     [rot / 2] int32, which of the `axes` positions a pair follows
+ *          (text: one axis; images and video: time, height, width); NULL: 0.
+ *          A value outside [0, axes) counts as 0.
+ * rot      even, 0 (no rotation) to d.  axes 1 to KV_MAX_AXES.
+ */
+#define KV_MAX_AXES 4
+typedef struct kv_rotary {
+    const float* q_norm;
+    const float* k_norm;
+    int64_t q_norm_head, k_norm_head;
+    float eps, offset;
+    const uint64_t* turns;
+    const int32_t* axis;
+    int32_t rot, axes, interleaved;
+} kv_rotary;
+
+/*
+ * kv_norm_rotate -- norm and rotation of drafted tokens' queries and keys (a
+ * decode step's single ones too), ahead of kv_tree_attention.
+ * q, q_out   [B][T][Hq][d], k, k_out [B][T][Hkv][d], of `dtype`; q or k may be
+ *            NULL with its output. An output may be its input (the same rows),
+ *            else they must not overlap.
+ * positions  [axes][B][T] int32; NULL where rot is 0.
+ */
+int kv_norm_rotate(const kv_rotary* rotary, int32_t dtype, int32_t B, int32_t T, int32_t Hq, int32_t Hkv, int32_t d,
+                   const int32_t* positions, const kv_rows* q, const kv_rows* q_out, const kv_rows* k,
+                   const kv_rows* k_out, void* stream);
+
+/*
+ * kv_append -- the prompts' keys and values into the cache: entry lengths + j
+ * of a sequence takes key and value of its row j, its weight becomes 0 and its
+ * stamp counts + j (where the cache has them); then lengths and counts grow by
+ * the sequence's rows. With `rotary` keys are normed and turned on the way, and
+ * so are the rows of q into q_out (both NULL: keys and values alone; without
+ * rotary they must be).
+ * positions  [axes][total] int32; NULL: counts + j on every axis.
+ * The pages of the new entries must be in the page table; a sequence that
+ * lacks one (KV_DEVERR_PAGE) keeps its length and count, and what its other
+ * new entries' places held is lost. q_out rows of padding and of sequences
+ * refused for their slot or length are zero. Offsets that decrease or pass
+ * `total` anywhere (GDN_DEVERR_SEQLEN) refuse the whole call.
+ */
+int kv_append(const kv_cache* cache, int32_t B, int32_t total, int32_t Hq, const int32_t* slots,
+              const int32_t* cu_seqlens, const kv_rows* k, const kv_rows* v, const kv_rotary* rotary,
+              const int32_t* positions, const kv_rows* q, const kv_rows* q_out, int32_t* dev_err, void* stream);
+
+/*
+ * kv_prompt_attention -- causal attention of packed prompts over the cache,
+ * after kv_append of the same rows: with n the sequence's rows and len its
+ * length (its last n entries are the rows' own), row j and query head h attend
+ * the entries e <= len - n + j of key head h / (Hq / Hkv):
+ *     out = sum_e e^(scale q.k_e - lse) v_e,  lse = ln sum_e e^(scale q.k_e)
+ * Entries from before the prompt (an earlier chunk, a shared prefix) are
+ * attended like the others. Arithmetic as in kv_tree_attention.
+ * q          [total][Hq][d].  out [total][Hq][d] of the cache's dtype,
+ *            contiguous.  lse [total][Hq] fp32, or NULL.
+ * workspace  kv_prompt_attention_workspace() bytes, 16-byte aligned; of one
+ *            call at a time. Its contents need no initialisation.
+ * A sequence shorter than its rows sets KV_DEVERR_LENGTH; offsets that
+ * decrease or pass `total` set GDN_DEVERR_SEQLEN, and the sequence is skipped
+ * (its rows are not written). Rows whose entries lie in a page outside the
+ * pool are zero, as those of the rows of their block.
+ * The tensor cores run what they run in kv_tree_attention.
+ */
+int kv_prompt_attention(const kv_cache* cache, int32_t B, int32_t total, int32_t Hq, const int32_t* slots,
+                        const int32_t* cu_seqlens, const kv_rows* q, float scale, void* out, float* lse,
+                        void* workspace, int64_t workspace_bytes, int32_t* dev_err, void* stream);
+
+int64_t kv_prompt_attention_workspace(const kv_cache* cache, int32_t B, int32_t total, int32_t Hq);
+
+/*
+ * ---------------------------------------------------------------- shared pages
+ *
+ * kv_fork -- sequences dst[i] become copies of sequences src[i]: for every page
+ * j that the source holds, dst's table takes the source's page (shared) where
+ * new_pages[i][j] is negative, else that page, into which the entries (keys,
+ * values, weights, stamps; up to the source's length) are copied. Lengths and
+ * counts are copied; dst's table past the last page stays as it is. Sequences
+ * that will grow need their last page, unless it is full, for themselves, and
+ * those whose weights will be accumulated or evicted all of them.
+ * src, dst   [n] int32 slots; either negative: nothing is done. Destinations
+ *            are distinct and no call's sources (not checked, but for src[i]
+ *            == dst[i], which sets GDN_DEVERR_SLOT); new pages are distinct
+ *            and held by no sequence (not checked).
+ * new_pages  [n][max_pages] int32.
+ * A fork with an error bit leaves dst as it was.
+ */
+int kv_fork(const kv_cache* cache, int32_t n, const int32_t* src, const int32_t* dst, const int32_t* new_pages,
+            int32_t* dev_err, void* stream);
+
+/*
+ * kv_compact -- moves the pages that sequences hold to the front of the pool.
+ * A page is held if the table names it within some slot's length (an ended
+ * sequence is freed by a length of 0). With U pages held, the j-th lowest page
+ * below U that is not held takes the contents (keys, values, weights, stamps)
+ * of the j-th lowest held one at or above it, and every table entry within a
+ * length follows: afterwards pages U and up are free.
+ * used       [1] int32: U, or -1 where a length or a page within one is out of
+ *            range (KV_DEVERR_LENGTH, KV_DEVERR_PAGE) and nothing is done.
+ * workspace  kv_compact_workspace() bytes, 16-byte aligned; of one call at a
+ *            time. Its contents need no initialisation.
+ */
+int kv_compact(const kv_cache* cache, int32_t* used, void* workspace, int64_t workspace_bytes, int32_t* dev_err,
+               void* stream);
+
+int64_t kv_compact_workspace(const kv_cache* cache);
+
 #ifdef __cplusplus
 }
 #endif
