@@ -108,7 +108,14 @@ cudaError_t attention_workspace(gdn::KvArgs& a, int64_t& bytes) {
 }
 
 // The same for prompts.
-cudaError_t prompt_workspace(gdn::KvArgs& a, int64_t& bytes) { return gdn::kv_prompt_workspace(a, bytes); }
+cudaError_t prompt_workspace(gdn::KvArgs& a, int64_t& bytes) {
+    cudaError_t e = gdn::kv_prompt_workspace(a, bytes);
+    if (e != cudaSuccess || !gdn::kv_prompt_tc_fits(a)) return e;
+    int64_t more = 0;
+    e = gdn::kv_prompt_tc_workspace(a, more);
+    if (more > bytes) bytes = more;
+    return e;
+}
 
 // What the places of a call's units on its line are counted in: rows in 31 bits, keys in 62.
 int check_prompt(const char* fn, const kv_cache* c, int32_t B, int32_t total, int32_t Hq) {
@@ -404,7 +411,8 @@ int kv_prompt_attention(const kv_cache* cache, int32_t B, int32_t total, int32_t
                     (long long)need);
     const int esz = gdn::dtype_size(cache->dtype);
     const bool vec = vec_pages(a.k, a.d, esz) && vec_pages(a.v, a.d, esz) && vec_rows(a.q.p, 0, a.q.node, a.q.head, a.d, esz);
-    e = gdn::launch_kv_prompt(a, vec, static_cast<cudaStream_t>(stream));
+    e = vec && gdn::kv_prompt_tc_fits(a) ? gdn::launch_kv_prompt_tc(a, static_cast<cudaStream_t>(stream)) : cudaErrorNotSupported;
+    if (e == cudaErrorNotSupported) e = gdn::launch_kv_prompt(a, vec, static_cast<cudaStream_t>(stream));
     return launched(e, fn);
 } catch (...) {
     return caught("kv_prompt_attention");

@@ -63,6 +63,7 @@ struct KvArgs {
     // prompts
     const int32_t* cu;  // row offsets of the packed sequences
     int total;
+    int tile_rows, tile_places, part_rows;  // rows of a tile of a unit, places for them, places of a unit
 };
 
 // Entry e of a sequence with page-table row `row`: its page and place.

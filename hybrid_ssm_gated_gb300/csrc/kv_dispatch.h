@@ -26,6 +26,9 @@ cudaError_t launch_kv_join(const KvArgs& a, int grid, cudaStream_t stream);
 // Attention of packed prompts: on the FP32 pipe, on the tensor cores (as above), the join of either, workspaces.
 cudaError_t launch_kv_prompt(KvArgs& a, bool vec, cudaStream_t stream);
 cudaError_t kv_prompt_workspace(KvArgs& a, int64_t& bytes);
+bool kv_prompt_tc_fits(const KvArgs& a);
+cudaError_t launch_kv_prompt_tc(KvArgs& a, cudaStream_t stream);
+cudaError_t kv_prompt_tc_workspace(KvArgs& a, int64_t& bytes);
 cudaError_t launch_kp_join(const KvArgs& a, int grid, cudaStream_t stream);
 
 // Norm and rotation of rows; with `cache`, keys and values go to its pages. vec: rows 16 bytes at a time.

@@ -2,6 +2,7 @@
 #include "gdn_launch.cuh"
 #include "kv_dispatch.h"
 #include "kv_prompt_fp32.cuh"
+#include "kv_prompt_join.cuh"
 
 namespace gdn {
 
@@ -42,18 +43,17 @@ cudaError_t launch_kp_join(const KvArgs& a, int grid, cudaStream_t stream) {
 
 cudaError_t kv_prompt_workspace(KvArgs& a, int64_t& bytes) {
     int64_t grid = 0;
-    a.row_block = kpg::RB;
     const cudaError_t e = wave(a, grid);
-    bytes = kp_part_bytes(grid, a.row_block, a.d) + grid * (int64_t)sizeof(KpBorder);
+    bytes = kp_part_bytes(grid, kpg::RB, a.d) + grid * (int64_t)sizeof(KpBorder);
     return e;
 }
 
 cudaError_t launch_kv_prompt(KvArgs& a, bool vec, cudaStream_t stream) {
     int64_t grid = 0;
-    a.row_block = kpg::RB;
+    a.row_block = a.tile_rows = a.tile_places = a.part_rows = kpg::RB;
     cudaError_t e = wave(a, grid);
     if (e != cudaSuccess) return e;
-    a.border = reinterpret_cast<char*>(a.part) + kp_part_bytes(grid, a.row_block, a.d);
+    a.border = reinterpret_cast<char*>(a.part) + kp_part_bytes(grid, kpg::RB, a.d);
     choose(a)<<<(unsigned)grid, kpg::NT, kpg::layout(a.d).bytes, stream>>>(a, vec);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     return launch_kp_join(a, (int)grid, stream);

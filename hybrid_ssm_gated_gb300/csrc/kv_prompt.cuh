@@ -1,10 +1,9 @@
 // kv_prompt.cuh -- what the prompt attention kernels share: the division of packed
-// causal prompts over a persistent grid, rows that no unit computes, and the join
-// of units that several CTAs computed.
+// causal prompts over a persistent grid, and rows that no unit computes.
 //
 // Units. The rows of a sequence and key head are its tokens' heads of the group,
-// token by token (row = token * G + head). A unit is a block of RB of them; its keys
-// end behind its last token, so that blocks grow along a prompt.
+// token by token (row = token * G + head). A unit is a block of RB of them (the call's
+// row_block); its keys end behind its last token, so that blocks grow along a prompt.
 //
 // Division. All units in order (sequence, key head, block) make a line, a unit as
 // long as its keys and a few more (KP_EXTRA) that stand for what it costs beyond its
@@ -13,7 +12,7 @@
 // units of a G-th key the length of block i is G (prefix + extra) + RB (i + 1), so
 // its place on the line is a quadratic in i: a CTA finds its range without a walk. A
 // unit that a border cuts is cut between tiles, and leaves one partial result a CTA
-// (unnormalised outputs, maximum and sum), joined by kp_join_kernel.
+// (unnormalised outputs, maximum and sum), joined by kp_join_kernel (kv_prompt_join.cuh).
 #pragma once
 
 #include "kv_common.cuh"
@@ -54,17 +53,14 @@ constexpr int KP_EXTRA = 256;  // keys that a unit's start and end cost as much 
 constexpr int KP_LEAST = 512;  // keys of a CTA's range at least
 
 // Blocks of a sequence, and the length of the line before block i of a key head.
-template <int RB>
 __device__ __forceinline__ int kp_blocks(const KvArgs& a, const KpSeq& s) {
-    return s.slot < 0 ? 0 : (int)(((long long)s.n * a.G + RB - 1) / RB);
+    return s.slot < 0 ? 0 : (int)((uint32_t)(s.n * a.G + a.row_block - 1) / (uint32_t)a.row_block);
 }
-template <int RB>
 __device__ __forceinline__ long long kp_before(const KvArgs& a, const KpSeq& s, long long i) {
-    return i * ((long long)a.G * (s.len - s.n + KP_EXTRA)) + RB * (i * (i + 1) / 2);
+    return i * ((long long)a.G * (s.len - s.n + KP_EXTRA)) + a.row_block * (i * (i + 1) / 2);
 }
-template <int RB>
 __device__ __forceinline__ long long kp_seq_cost(const KvArgs& a, const KpSeq& s) {
-    return kp_before<RB>(a, s, kp_blocks<RB>(a, s)) * a.Hkv;
+    return kp_before(a, s, kp_blocks(a, s)) * a.Hkv;
 }
 
 // What the scan over sequences leaves in shared memory: the CTA's range.
@@ -72,9 +68,10 @@ struct KpMark {
     long long off;  // from the beginning of sequence b's share of the line
     int b;          // a.B: the end of the line
 };
-template <int NT>
+template <int NT, int KEEP>
 struct KpScan {
-    KpSeq seq[NT];  // the batch's sequences, where there are at most NT
+    static constexpr int keep = KEEP;
+    KpSeq seq[KEEP];  // the batch's sequences, where there are at most KEEP (which is at most NT)
     long long warp_sum[NT / 32];
     KpMark mark[2];  // beginning and end of the range
     long long q;     // ranges: length, and how many are one longer
@@ -82,16 +79,16 @@ struct KpScan {
 };
 
 // By the whole block of NT threads: the division, and this CTA's range.
-template <int RB, int NT>
-__device__ __forceinline__ void kp_locate(const KvArgs& a, KpScan<NT>& sc) {
+template <int NT, int KEEP>
+__device__ __forceinline__ void kp_locate(const KvArgs& a, KpScan<NT, KEEP>& sc) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int run = a.B <= NT ? 1 : (a.B + NT - 1) / NT;
     const int b0 = (int)min((long long)a.B, (long long)tid * run), b1 = min(a.B, b0 + run);
     long long sum = 0;
     for (int b = b0; b < b1; ++b) {
         const KpSeq s = kp_seq(a, b);
-        if (run == 1) sc.seq[b] = s;
-        sum += kp_seq_cost<RB>(a, s);
+        if (a.B <= KEEP) sc.seq[b] = s;
+        sum += kp_seq_cost(a, s);
     }
     long long inc = sum;
 #pragma unroll
@@ -120,7 +117,7 @@ __device__ __forceinline__ void kp_locate(const KvArgs& a, KpScan<NT>& sc) {
             long long at = before;
             int b = b0;
             for (; b < b1 - 1; ++b) {
-                const long long n = kp_seq_cost<RB>(a, run == 1 ? sc.seq[b] : kp_seq(a, b));
+                const long long n = kp_seq_cost(a, a.B <= KEEP ? sc.seq[b] : kp_seq(a, b));
                 if (want < at + n) break;
                 at += n;
             }
@@ -136,7 +133,7 @@ struct KpPlace {
 };
 
 // A walk along a CTA's segments: runs of tiles of one unit.
-template <int RB, int KT>
+template <int KT>
 struct KpWalk {
     const KvArgs& a;
     const KpSeq* seq;  // the batch's sequences in shared memory, or NULL
@@ -146,8 +143,8 @@ struct KpWalk {
     int nt, t0, t1;  // the unit's tiles, and the segment's
 
     __device__ __forceinline__ int tiles(const KpSeq& x, int blk) const {
-        const long long rows = min((long long)x.n * a.G, (long long)(blk + 1) * RB);
-        return (x.len - x.n + (int)((rows - 1) / a.G) + KT) / KT;  // keys 0 .. prefix + last token
+        const int rows = (int)min((long long)x.n * a.G, (long long)(blk + 1) * a.row_block);
+        return (x.len - x.n + (rows - 1) / a.G + KT) / KT;  // keys 0 .. prefix + last token
     }
     __device__ __forceinline__ KpSeq get(int x) const { return seq ? seq[x] : kp_seq(a, x); }
     // The place that a point of the line is cut at.
@@ -155,18 +152,18 @@ struct KpWalk {
         KpPlace p{m.b, 0, 0, 0};
         if (m.b >= a.B) return p;
         const KpSeq x = get(m.b);
-        const int nb = kp_blocks<RB>(a, x);
-        const long long one = kp_before<RB>(a, x, nb);
+        const int nb = kp_blocks(a, x);
+        const long long one = kp_before(a, x, nb);
         p.h = (int)(m.off / one);
         const long long off = m.off - one * p.h;
         int lo = 0, hi = nb;  // the block that holds `off`
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
-            if (kp_before<RB>(a, x, mid) <= off) lo = mid;
+            if (kp_before(a, x, mid) <= off) lo = mid;
             else hi = mid;
         }
         p.i = lo;
-        p.t = tile_at(off - kp_before<RB>(a, x, lo), tiles(x, lo));
+        p.t = tile_at(off - kp_before(a, x, lo), tiles(x, lo));
         return p;
     }
     // Tile that a point `off` of a unit is cut ahead of.
@@ -179,7 +176,7 @@ struct KpWalk {
     }
     __device__ __forceinline__ void load() {
         s = get(b);
-        blocks = kp_blocks<RB>(a, s);
+        blocks = kp_blocks(a, s);
     }
     // The segment of the current unit from tile t on; false if the range ends ahead of it.
     __device__ __forceinline__ bool segment(int t) {
@@ -188,9 +185,9 @@ struct KpWalk {
         t1 = b == end.b && h == end.h && i == end.i ? min(end.t, nt) : nt;
         return true;
     }
-    template <int NT>
-    __device__ __forceinline__ KpWalk(const KvArgs& a_, const KpScan<NT>& sc, bool& some)
-        : a(a_), seq(a_.B <= NT ? sc.seq : nullptr) {
+    template <int NT, int KEEP>
+    __device__ __forceinline__ KpWalk(const KvArgs& a_, const KpScan<NT, KEEP>& sc, bool& some)
+        : a(a_), seq(a_.B <= KEEP ? sc.seq : nullptr) {
         t0 = t1 = nt = 0;
         some = false;
         if ((int)blockIdx.x >= sc.parts) return;
@@ -225,11 +222,8 @@ struct KpWalk {
     __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == nt; }
     // Which of the CTA's two partials the segment's is: only its first segment begins inside a unit.
     __device__ __forceinline__ int later() const { return t0 == 0; }
-    __device__ __forceinline__ int r0() const { return i * RB; }
-    __device__ __forceinline__ int rows() const {
-        const long long left = (long long)s.n * a.G - (long long)i * RB;
-        return (int)(left < RB ? left : RB);
-    }
+    __device__ __forceinline__ int r0() const { return i * a.row_block; }
+    __device__ __forceinline__ int rows() const { return min(a.row_block, s.n * a.G - r0()); }
 };
 
 // A unit cut by the end of the CTA's range in which it begins: what the join needs, one record a CTA.
@@ -240,12 +234,12 @@ struct KpBorder {
 
 // Writes this CTA's record: of the segment `w`, if the unit begins in it and goes on past the range (which is then at
 // its end, sc.mark[1] inside the unit), else that there is none. By one thread.
-template <int RB, int KT, int NT>
-__device__ __forceinline__ void kp_border(const KvArgs& a, const KpScan<NT>& sc, const KpWalk<RB, KT>& w) {
+template <int KT, int NT, int KEEP>
+__device__ __forceinline__ void kp_border(const KvArgs& a, const KpScan<NT, KEEP>& sc, const KpWalk<KT>& w) {
     KpBorder k{};
     k.first = w.s.first, k.h = w.h, k.r0 = w.r0(), k.rows = w.rows(), k.n = 1;
-    const long long u0 = kp_before<RB>(a, w.s, w.blocks) * w.h + kp_before<RB>(a, w.s, w.i);  // in its sequence's share
-    const long long size = kp_before<RB>(a, w.s, w.i + 1) - kp_before<RB>(a, w.s, w.i), at = sc.mark[1].off - u0;
+    const long long u0 = kp_before(a, w.s, w.blocks) * w.h + kp_before(a, w.s, w.i);  // in its sequence's share
+    const long long size = kp_before(a, w.s, w.i + 1) - kp_before(a, w.s, w.i), at = sc.mark[1].off - u0;
     const auto start = [&](int x) { return sc.q * x + min(x, sc.r); };
     const int c = blockIdx.x;
     // a range is longer than two tiles: each CTA whose range begins inside the unit has one of its tiles
@@ -278,65 +272,12 @@ __device__ __forceinline__ void kp_empty_rows(const KvArgs& a, const KpSeq* seq,
     }
 }
 
-// Partials: column e of the outputs of RB rows, then the rows' maxima and sums. A sum of -1 says that the CTA
+// Partials: column e of the outputs of a unit's places, then the rows' maxima and sums. A unit's rows lie in tiles of
+// tile_rows, each in the first of tile_places places. A sum of -1 says that the CTA
 // met a page outside the pool (or gave up): the unit's rows are those of a refused sequence.
-__host__ __device__ inline int64_t kp_part_floats(int row_block, int d) { return (int64_t)row_block * (d + 2); }
-__host__ __device__ inline int64_t kp_part_bytes(int64_t grid, int row_block, int d) {
-    return grid * 2 * kp_part_floats(row_block, d) * 4;
-}
-
-namespace kpj {
-constexpr int NT = 128, WARPS = NT / 32, SHARE = 16;  // blocks a border
-}
-
-// Blocks SHARE c .. SHARE c + SHARE - 1 join the unit of CTA c's record. A job is 32 rows (a lane each) by eight
-// outputs.
-__global__ void __launch_bounds__(kpj::NT) kp_join_kernel(const __grid_constant__ KvArgs a) {
-    using namespace kpj;
-    const int c = blockIdx.x / SHARE, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    kv_grid_wait();
-    const KpBorder k = static_cast<const KpBorder*>(a.border)[c];
-    if (k.n == 0) return;
-    const int RB = a.row_block, cols = (a.d + 7) / 8, jobs = (k.rows + 31) / 32 * cols;
-    const int64_t size = kp_part_floats(RB, a.d);
-    const auto part = [&](int j) { return a.part + ((int64_t)(c + j) * 2 + (j == 0)) * size; };
-    const bool vec = a.d % 8 == 0 && reinterpret_cast<uintptr_t>(a.out) % 16 == 0;
-    for (int x = (blockIdx.x % SHARE) * WARPS + warp; x < jobs; x += SHARE * WARPS) {
-        const int g = x / cols, e0 = (x - g * cols) * 8, r = g * 32 + lane;
-        if (r >= k.rows) continue;
-        float m = -INFINITY;
-        bool refused = false;
-        for (int j = 0; j < k.n; ++j) {
-            const float* p = part(j) + (int64_t)RB * a.d + r;
-            m = fmaxf(m, p[0]), refused = refused || p[RB] == -1.f;
-        }
-        const float base = m == -INFINITY ? 0.f : m;
-        float o[8] = {}, l = 0.f;
-        for (int j = 0; j < k.n; ++j) {
-            const float* p = part(j) + r;
-            const float f = kv_ex2(p[(int64_t)RB * a.d] - base);
-            l = fmaf(p[(int64_t)RB * a.d + RB], f, l);
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                if (e0 + e < a.d) o[e] = fmaf(p[(int64_t)(e0 + e) * RB], f, o[e]);
-        }
-        if (refused) l = 0.f;
-        const float inv = l == 0.f ? 0.f : 1.f / l;
-        const int row = k.r0 + r, tok = row / a.G;
-        const int64_t to = ((int64_t)k.first + tok) * a.Hq + k.h * a.G + (row - tok * a.G);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) o[e] = l == 0.f ? 0.f : o[e] * inv;
-        if (vec && a.dtype != GDN_F32) {
-            uint4 w;
-            if (a.dtype == GDN_BF16) w = Store<__nv_bfloat16>::pack(o);
-            else w = Store<__half>::pack(o);
-            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + to * a.d + e0) = w;
-        } else {
-            for (int e = 0; e < 8; ++e)
-                if (e0 + e < a.d) store_elem(a.out, to * a.d + e0 + e, a.dtype, o[e]);
-        }
-        if (e0 == 0 && a.lse) a.lse[to] = l == 0.f ? -INFINITY : (m + log2f(l)) * LN2;
-    }
+__host__ __device__ inline int64_t kp_part_floats(int places, int d) { return (int64_t)places * (d + 2); }
+__host__ __device__ inline int64_t kp_part_bytes(int64_t grid, int places, int d) {
+    return grid * 2 * kp_part_floats(places, d) * 4;
 }
 
 }  // namespace gdn

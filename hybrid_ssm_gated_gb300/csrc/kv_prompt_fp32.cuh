@@ -40,7 +40,7 @@ __host__ __device__ inline Layout layout(int d) {
     L.off_at = L.off_p + RB * (KT + 4) * 4;
     L.off_q_at = L.off_at + 2 * 2 * KT * 8;
     L.off_scan = L.off_q_at + RB * 8;
-    L.off_bad = L.off_scan + (int)sizeof(KpScan<NT>);
+    L.off_bad = L.off_scan + (int)sizeof(KpScan<NT, NT>);
     L.bytes = L.off_bad + 16;
     return L;
 }
@@ -59,15 +59,15 @@ __global__ void __launch_bounds__(kpg::NT) kv_prompt_kernel(const __grid_constan
     float* sP = reinterpret_cast<float*>(smem + L.off_p);
     int64_t(*s_at)[2][KT] = reinterpret_cast<int64_t(*)[2][KT]>(smem + L.off_at);  // [buffer][k, v]: rows of a tile
     int64_t* s_q = reinterpret_cast<int64_t*>(smem + L.off_q_at);
-    KpScan<NT>& sc = *reinterpret_cast<KpScan<NT>*>(smem + L.off_scan);
+    KpScan<NT, NT>& sc = *reinterpret_cast<KpScan<NT, NT>*>(smem + L.off_scan);
     int& s_bad = *reinterpret_cast<int*>(smem + L.off_bad);  // a page of the segment lies outside the pool
     constexpr int PP = KT + 4;
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4, pitch = L.pitch, d4 = L.dp / 4;
     const float c2 = a.scale * LOG2E;
     kv_grid_launch();
-    kp_locate<RB, NT>(a, sc);
+    kp_locate(a, sc);
     bool busy;
-    KpWalk<RB, KT> w(a, sc, busy);
+    KpWalk<KT> w(a, sc, busy);
     kp_empty_rows(a, a.B <= NT ? sc.seq : nullptr, tid, NT);
     if (tid == 0) kp_no_border(a);
     if (!busy) return;

@@ -1,0 +1,586 @@
+// kv_prompt_tc.cuh -- causal attention of packed prompts over the paged cache on the
+// tcgen05 tensor cores (16-bit caches whose pages hold a multiple of 8 entries and
+// whose rows the TMA engine can address; up to 128 query heads a key head).
+//
+// Mathematics. One pass over tiles of 128 keys for tiles of 128 query rows: S = Q K^T
+// (128 x 128), P = 2^{c S - m} with a reference m a row, O += P V (128 x d). A thread
+// owns a row: its 128 scores of a tile come from tensor memory into its registers, and
+// maximum, sum and weights need no other thread. The weights go back to tensor memory,
+// over the scores, as the A operand of the second product.
+//
+// The reference lags behind the row's maximum, and weights in fp16 are lifted by seven
+// powers of two, as in kv_tc.cuh. O is a sum over FOLD tiles in tensor memory (whose
+// FP32 sums are cut off towards zero), which the softmax threads then add, rounding to
+// nearest, to a sum in the CTA's partial in the workspace: tensor memory is full.
+//
+// Kernel shape: persistent, one CTA a SM;
+//   QT = 2 (d up to 128): a unit is two tiles of query rows, which share each tile of
+//     keys and values; while one tile's weights form, the tensor cores work for the
+//     other one. Tensor memory: two S (P over them), two O.
+//   QT = 1 (d above 128, and calls with few units): one tile, two buffers of S in turn.
+//   softmax    four warps a tile of rows, thread = row = tensor-memory lane;
+//   K, V       a warp each: tiles by TMA into a ring of stages of 128 keys x 128
+//              elements, boxes of as many keys as a page and the tile share;
+//   S, O       a warp each, one elected thread of which issues the products; the S
+//              warp loads a unit's queries (whole tokens: a tile of rows holds as many
+//              as have their G heads in it).
+// A tile of which some row sees a part ("mixed") has its values looked through by the
+// softmax threads: rows of V past the sequence's end become zero, and so does what is
+// not finite (0 x NaN would reach rows that do not see it); the epilogue adds the
+// latter to the rows that do.
+#pragma once
+
+#include "kv_prompt.cuh"
+#include "kv_tc.cuh"
+
+namespace gdn {
+
+namespace kpt {
+
+using kvt::BOX;
+using kvt::BOX_BYTES;
+using kvt::KT;
+constexpr int TILE = 128;  // rows of a tile
+constexpr int KEEP = 32;   // sequences that the scan keeps
+constexpr int MAX_STAGES = 12;
+constexpr int FOLD = 32;   // tiles of one sum in tensor memory
+__host__ __device__ constexpr int threads(int QT) { return (4 * QT + 4) * 32; }
+
+struct Maps {
+    CUtensorMap k, v, q;
+};
+
+template <int QT>
+struct __align__(16) State {
+    uint64_t full[MAX_STAGES], empty[MAX_STAGES];  // the K ring's stages, then the V ring's
+    uint64_t s_full[2], o_done[2], p_full[2][2], q_full, v_ok, v_clean, drain[2];
+    uint64_t seg_open[2], seg_loaded[2], seg_free[2];
+    KpScan<threads(QT), KEEP> scan;
+    int bad[2], odd[2];  // of this segment and the next: a page outside the pool; a value that is not finite
+    int v_stage, stopped;
+    uint32_t tmem;
+#ifdef GDN_TEST_STALL
+    uint64_t never;
+#endif
+};
+
+__host__ __device__ constexpr int stage_bytes(int boxes) { return (boxes > 1 ? 2 : 1) * BOX_BYTES; }
+template <int QT>
+__host__ __device__ constexpr int smem_bytes(int boxes, int stages) {
+    return 1024 + QT * boxes * TILE * 128 + stages * stage_bytes(boxes) + (int)sizeof(State<QT>);
+}
+
+// The product with the A operand in tensor memory (issued as kvt::mma).
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, bool accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(id), "r"((uint32_t)accumulate)
+        : "memory");
+}
+
+// Sixteen words to consecutive columns of this thread's lane; in tensor memory once st_wait returns.
+__device__ __forceinline__ void st16(uint32_t taddr, const uint32_t* v) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(v[0]),
+        "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]),
+        "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// The values of a row's mixed tiles that are not finite, added to outputs e0 .. e0 + 31 where the row sees the entry.
+template <typename ST>
+__device__ __noinline__ void add_odd(const KvArgs& a, const int32_t* table, int h, int from, int last, int e0, float* o) {
+    for (int e = from; e <= last; ++e) {
+        const int pg = e / a.page_size, page = table[pg];
+        if ((uint32_t)page >= (uint64_t)a.num_pages) continue;
+        const int64_t at = kv_at(a.v, page, h, e - pg * a.page_size);
+        for (int x = 0; x < 32 && e0 + x < a.d; ++x) {
+            const float v = load_elem(a.v.p, at + e0 + x, Store<ST>::code);
+            if (!isfinite(v)) o[x] += v;
+        }
+    }
+}
+
+// What a CTA leaves whose waits ran out, by the whole block: the rows of its range as those of a refused sequence.
+template <int QT>
+__device__ __noinline__ void refuse_range(const KvArgs& a, const State<QT>& st) {
+    constexpr int NT = threads(QT), PLACES = QT * TILE;
+    bool some;
+    KpWalk<KT> w(a, st.scan, some);
+    if (!some) return;
+    do {
+        const int r0 = w.r0(), rows = w.rows();
+        if (w.whole()) {
+            for (int64_t i = threadIdx.x; i < (int64_t)rows * a.d; i += NT) {
+                const int r = (int)(i / a.d), x = r0 + r, tok = x / a.G;
+                const int64_t row = (int64_t)(w.s.first + tok) * a.Hq + w.h * a.G + (x - tok * a.G);
+                store_elem(a.out, row * a.d + (i - (int64_t)r * a.d), a.dtype, 0.f);
+                if (a.lse && i == (int64_t)r * a.d) a.lse[row] = -INFINITY;
+            }
+        } else {
+            float* part = a.part + ((int64_t)blockIdx.x * 2 + w.later()) * kp_part_floats(PLACES, a.d) + (int64_t)PLACES * a.d;
+            for (int r = threadIdx.x; r < PLACES; r += NT) part[r] = -INFINITY, part[PLACES + r] = -1.f;
+            if (threadIdx.x == 0 && w.t0 == 0) kp_border(a, st.scan, w);
+        }
+    } while (w.next());
+}
+
+}  // namespace kpt
+
+// boxes: 64-element boxes of d; k_stages, v_stages: of the rings; box_rows: keys of one TMA box.
+template <typename ST, int QT>
+__global__ void __launch_bounds__(kpt::threads(QT), 1)
+    kv_prompt_tc_kernel(const __grid_constant__ KvArgs a, const __grid_constant__ kpt::Maps maps, const int boxes,
+                        const int k_stages, const int v_stages, const int box_rows) {
+    using namespace kpt;
+    using kvt::desc, kvt::idesc, kvt::SW128, kvt::uniform, kvt::warp_wait, kvt::tma_load, kvt::commit;
+    using kvt::Two, kvt::two, kvt::fma2, kvt::add2, kvt::parts, kvt::max3;
+    using H = kvt::Half16<ST>;
+    constexpr int NT = threads(QT), SM_WARPS = 4 * QT, PLACES = QT * TILE;
+    constexpr int K_WARP = SM_WARPS, V_WARP = SM_WARPS + 1, S_WARP = SM_WARPS + 2, O_WARP = SM_WARPS + 3;
+    constexpr uint32_t TM_S = 0, TM_O = 256, TM_COLS = 512;
+    extern __shared__ unsigned char smem_raw[];
+    unsigned char* smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
+    const int pairs = (boxes + 1) >> 1, one_stage = stage_bytes(boxes), stages = k_stages + v_stages;
+    unsigned char* sQ = smem;
+    unsigned char* ring = smem + QT * boxes * TILE * 128;
+    State<QT>& st = *reinterpret_cast<State<QT>*>(ring + stages * one_stage);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int per = a.tile_rows;  // rows of a tile: whole tokens
+
+    kv_grid_launch();
+    if (warp == K_WARP) {
+        if (lane < 3) {
+            const CUtensorMap* m = lane == 0 ? &maps.k : lane == 1 ? &maps.v : &maps.q;
+            asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory");
+        }
+        if (lane < stages) mbar_init(&st.full[lane], 1), mbar_init(&st.empty[lane], 1);
+        if (lane < 2) {
+            mbar_init(&st.s_full[lane], 1), mbar_init(&st.o_done[lane], 1);
+            mbar_init(&st.p_full[lane][0], 4), mbar_init(&st.p_full[lane][1], 4), mbar_init(&st.drain[lane], 1);
+            mbar_init(&st.seg_open[lane], 1), mbar_init(&st.seg_loaded[lane], 1), mbar_init(&st.seg_free[lane], SM_WARPS);
+            st.bad[lane] = st.odd[lane] = 0;
+        }
+        if (lane == 2) mbar_init(&st.q_full, 1), mbar_init(&st.v_ok, 1), mbar_init(&st.v_clean, SM_WARPS), st.stopped = 0;
+#ifdef GDN_TEST_STALL
+        if (lane == 0) mbar_init(&st.never, 1);
+#endif
+        fence_barrier_init();
+    }
+    if (warp == O_WARP) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&st.tmem)),
+                     "r"(TM_COLS)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    if (tid == 0) kp_no_border(a);
+    tc::fence_before();
+    kp_locate(a, st.scan);
+    tc::fence_after();
+    const uint32_t tmem = st.tmem;
+    bool busy;
+    KpWalk<KT> w(a, st.scan, busy);
+    // the first tile of the unit that some row sees a part of only
+    const auto first_mixed = [&]() { return (w.s.len - w.s.n + w.r0() / a.G + 1) / KT; };
+
+    if ((warp == K_WARP || warp == V_WARP) && busy) {
+        // ------------------------------------------------------------ loads
+        const bool keys = warp == K_WARP;
+        const CUtensorMap* map = keys ? &maps.k : &maps.v;
+        const int first = keys ? 0 : k_stages, end = keys ? k_stages : stages;
+        int stage = first;
+        uint32_t round = 0, seg = 0;
+        bool ok = true;
+        const int per_tile = KT / box_rows, step_pages = KT / a.page_size, step_places = KT - step_pages * a.page_size;
+        do {
+            const int side = seg & 1;
+            const int32_t* table = a.page_table + (int64_t)w.s.slot * a.max_pages;
+            bool bad = false;
+            // this lane's box of the next tile: its page (one tile ahead) and place
+            int e = w.t0 * KT + lane * box_rows, pg = e / a.page_size, place = e - pg * a.page_size;
+            const auto look = [&]() { return lane < per_tile && e < w.s.len ? table[pg] : 0; };
+            int page = look();
+            if (keys) {
+                if (seg >= 2) {
+                    ok = warp_wait(&st.seg_free[side], ((seg >> 1) - 1) & 1);
+                    if (lane == 0) st.bad[side] = st.odd[side] = 0;
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&st.seg_open[side]);
+            }
+#pragma unroll 1
+            for (int t = w.t0; t < w.t1 && ok; ++t) {
+                bad = bad || (uint32_t)page >= (uint64_t)a.num_pages;
+                const int used = (min(KT, w.s.len - t * KT) + box_rows - 1) / box_rows;  // boxes with an entry
+                const int this_page = page, this_place = place;
+                e += KT, pg += step_pages, place += step_places;
+                if (place >= a.page_size) place -= a.page_size, ++pg;
+                page = look();
+#pragma unroll 1
+                for (int p = 0; p < pairs; ++p) {
+                    ok = warp_wait(&st.empty[stage], (round & 1) ^ 1);
+                    if (!ok) break;
+                    const int nb = min(2, boxes - 2 * p);
+                    uint64_t* full = &st.full[stage];
+                    unsigned char* dst = ring + stage * one_stage;
+                    if (lane == 0) mbar_arrive_expect_tx(full, used * box_rows * 128 * nb);
+                    __syncwarp();
+                    if (lane < used) {
+                        tma_load(dst + lane * box_rows * 128, map, 2 * p * BOX, this_place, w.h, this_page, full);
+                        if (nb > 1)
+                            tma_load(dst + BOX_BYTES + lane * box_rows * 128, map, (2 * p + 1) * BOX, this_place, w.h,
+                                     this_page, full);
+                    }
+                    if (++stage == end) stage = first, ++round;
+                }
+            }
+            if (keys) {
+                bad = __any_sync(FULL_MASK, bad);
+                if (lane == 0) {
+                    if (bad) st.bad[side] = 1, set_error(a.dev_err, KV_DEVERR_PAGE);
+                    mbar_arrive(&st.seg_loaded[side]);
+                }
+            }
+            ++seg;
+        } while (ok && w.next());
+        if (!ok && lane == 0) st.stopped = 1, set_error(a.dev_err, GDN_DEVERR_TIMEOUT);
+        kvt::landed(st.full, first, end, stage, round);
+    } else if (warp == S_WARP && busy) {
+        // ------------------------------------------------------------ S = Q K^T
+        const uint32_t id = idesc(H::type, false, false, KT), aQ = smem_addr(sQ), aR = smem_addr(ring), tm = uniform(tmem);
+        const int tokens = per / a.G;  // of a tile
+        int stage = 0;
+        uint32_t round = 0, n_t = 0, asked = 0;
+        bool ok = true;
+        do {
+            const int n = uniform(w.t1 - w.t0);
+            if (n_t > 0)  // the last segment's products have read their queries
+                ok = QT == 2 ? warp_wait(&st.s_full[1], (n_t - 1) & 1) : warp_wait(&st.s_full[(n_t - 1) & 1], ((n_t - 1) >> 1) & 1);
+            if (ok) {
+                if (lane == 0) mbar_arrive_expect_tx(&st.q_full, QT * boxes * per * 128);
+                __syncwarp();
+                if (lane < QT * boxes) {
+                    const int j = lane / boxes, x = lane - j * boxes;
+                    tma_load(sQ + (j * boxes + x) * TILE * 128, &maps.q, x * BOX, w.h * a.G, w.s.first + w.r0() / a.G + j * tokens, 0,
+                             &st.q_full);
+                }
+                __syncwarp();
+                ok = warp_wait(&st.q_full, asked & 1);
+                ++asked;
+            }
+#pragma unroll 1
+            for (int i = 0; i < n && ok; ++i, ++n_t) {
+                const int buf = QT == 2 ? 0 : n_t & 1;
+                if (QT == 1 && n_t >= 2) ok = warp_wait(&st.o_done[buf], ((n_t >> 1) - 1) & 1);
+#pragma unroll 1
+                for (int p = 0; p < pairs && ok; ++p) {
+                    ok = warp_wait(&st.full[stage], round & 1);
+                    if (!ok) break;
+                    tc::fence_after();
+                    const uint64_t db = desc(aR + stage * one_stage, 16, 1024, SW128);
+                    const int nb = min(2, boxes - 2 * p);
+#pragma unroll 1
+                    for (int j = 0; j < QT; ++j) {
+                        if (QT == 2 && n_t > 0) {
+                            ok = warp_wait(&st.o_done[j], (n_t - 1) & 1);
+                            if (!ok) break;
+                            tc::fence_after();
+                        }
+                        const uint32_t to = tm + TM_S + (QT == 2 ? j : buf) * KT;
+                        const uint64_t da = desc(aQ + (j * boxes + 2 * p) * TILE * 128, 16, 1024, SW128);
+#pragma unroll 1
+                        for (int x = 0; x < nb; ++x) {
+                            const int steps = min(BOX / 16, (a.d - (2 * p + x) * BOX + 15) / 16);
+                            const uint64_t da_x = da + x * (TILE * 128 >> 4), db_x = db + x * (BOX_BYTES >> 4);
+                            if (steps == BOX / 16) {
+#pragma unroll
+                                for (int k = 0; k < BOX / 16; ++k)
+                                    kvt::mma(to, da_x + k * (32 >> 4), db_x + k * (32 >> 4), id, p + x + k > 0);
+                            } else {
+#pragma unroll 1
+                                for (int k = 0; k < steps; ++k)
+                                    kvt::mma(to, da_x + k * (32 >> 4), db_x + k * (32 >> 4), id, p + x + k > 0);
+                            }
+                        }
+                        if (QT == 2) commit(&st.s_full[j]);
+                    }
+                    if (!ok) break;
+                    commit(&st.empty[stage]);
+                    if (++stage == k_stages) stage = 0, ++round;
+                }
+                if (QT == 1 && ok) commit(&st.s_full[buf]);
+            }
+        } while (ok && w.next());
+        if (!ok && lane == 0) st.stopped = 1, set_error(a.dev_err, GDN_DEVERR_TIMEOUT);
+        if (asked) mbar_wait(&st.q_full, (asked - 1) & 1);
+        commit(&st.drain[0]);
+        mbar_wait(&st.drain[0], 0);
+        __syncwarp();
+    } else if (warp == O_WARP && busy) {
+        // ------------------------------------------------------------ O += P V
+        const uint32_t aR = smem_addr(ring), tm = uniform(tmem);
+        int stage = k_stages;
+        uint32_t round = 0, n_t = 0, n_v = 0;
+        bool ok = true;
+        do {
+            const int n = uniform(w.t1 - w.t0), t0 = uniform(w.t0), mixed = uniform(first_mixed());
+#pragma unroll 1
+            for (int i = 0; i < n && ok; ++i, ++n_t) {
+                int s2 = stage;
+                uint32_t r2 = round;
+#pragma unroll 1
+                for (int p = 0; p < pairs && ok; ++p) {
+                    ok = warp_wait(&st.full[s2], r2 & 1);
+                    if (++s2 == stages) s2 = k_stages, ++r2;
+                }
+                if (ok && t0 + i >= mixed) {  // the softmax threads look the values through
+                    if (lane == 0) st.v_stage = stage, mbar_arrive(&st.v_ok);
+                    __syncwarp();
+                    ok = warp_wait(&st.v_clean, n_v & 1);
+                    ++n_v;
+                }
+#pragma unroll 1
+                for (int j = 0; j < QT && ok; ++j) {
+                    const int buf = QT == 2 ? j : n_t & 1;
+                    const uint32_t use = QT == 2 ? n_t : n_t >> 1;
+#pragma unroll 1
+                    for (int half = 0; half < 2; ++half) {
+                        ok = warp_wait(&st.p_full[buf][half], use & 1);
+                        if (!ok) break;
+                        tc::fence_after();
+                        int sp = stage;
+#pragma unroll 1
+                        for (int p = 0; p < pairs; ++p) {
+                            const int nb = min(2, boxes - 2 * p), N = min(128, (a.d - p * 128 + 15) / 16 * 16);
+                            const uint32_t id = idesc(H::type, false, true, N);
+                            const uint32_t to = tm + TM_O + (QT == 2 ? j : p) * 128, from = tm + TM_S + buf * KT + half * 32;
+                            const uint64_t db = desc(aR + sp * one_stage, nb > 1 ? BOX_BYTES : 0, 1024, SW128) + half * 4 * (2048 >> 4);
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) mma_ts(to, from + k * 8, db + k * (2048 >> 4), id, i % FOLD + half + k > 0);
+                            if (++sp == stages) sp = k_stages;
+                        }
+                    }
+                    if (ok) commit(&st.o_done[buf]);
+                }
+                for (int p = 0; p < pairs && ok; ++p) {
+                    commit(&st.empty[stage]);
+                    if (++stage == stages) stage = k_stages, ++round;
+                }
+            }
+        } while (ok && w.next());
+        if (!ok && lane == 0) st.stopped = 1, set_error(a.dev_err, GDN_DEVERR_TIMEOUT);
+        commit(&st.drain[1]);
+        mbar_wait(&st.drain[1], 0);
+        __syncwarp();
+    } else if (warp < SM_WARPS && busy) {
+        // ------------------------------------------------------------ softmax
+        const int g = warp >> 2, quad = warp & 3, r = quad * 32 + lane;
+        const uint32_t lane_base = tmem + ((uint32_t)(quad * 32) << 16);
+        const uint32_t tm_o = lane_base + TM_O + g * 128;
+        const bool flip = a.scale < 0.f;
+        // (a scale of zero as the smallest normal number: -inf times it stays -inf)
+        const float c2 = a.scale == 0.f ? 1.1754944e-38f : fabsf(a.scale) * LOG2E;
+        const bool vec = reinterpret_cast<uintptr_t>(a.out) % 16 == 0;
+        uint32_t n_t = 0, n_v = 0, seg = 0;
+        bool ok = true;
+        const auto done = [&](uint32_t x) {  // tile x's product with V
+            const bool y = QT == 2 ? warp_wait(&st.o_done[g], x & 1) : warp_wait(&st.o_done[x & 1], (x >> 1) & 1);
+            tc::fence_after();
+            return y;
+        };
+        do {
+            const int n = w.t1 - w.t0, side = seg & 1, prefix = w.s.len - w.s.n, rows = w.rows(), r0 = w.r0();
+            const int mine = g * per + r;  // row of the unit
+            const bool live = r < per && mine < rows;
+            const int x = r0 + (live ? mine : r < per ? rows - 1 : min(g * per, rows - 1)), tok = x / a.G, last = prefix + tok;
+            const int mixed = first_mixed();
+            float* part = a.part + ((int64_t)blockIdx.x * 2 + w.later()) * kp_part_floats(PLACES, a.d) + g * TILE + r;
+            float m = -INFINITY, nref = 0.f, l = 0.f, folded = -INFINITY;  // reference (unscaled), lift - c m, sum; m of the fold
+            ok = ok && warp_wait(&st.seg_open[side], (seg >> 1) & 1);
+#pragma unroll 1
+            for (int i = 0; i < n && ok; ++i, ++n_t) {
+                const int t = w.t0 + i, buf = QT == 2 ? g : n_t & 1;
+                const uint32_t tm_s = lane_base + TM_S + buf * KT;
+                ok = warp_wait(&st.s_full[buf], (QT == 2 ? n_t : n_t >> 1) & 1);
+#ifdef GDN_TEST_STALL
+                if (blockIdx.x == gridDim.x / 2 && warp == 0 && n_t == 1) ok = ok && warp_wait(&st.never, 0);
+#endif
+                if (!ok) break;
+                tc::fence_after();
+                float s[KT];
+                tc::tmem_ld<64>(tm_s, s);
+                tc::tmem_ld<64>(tm_s + 64, s + 64);
+                if (flip) {
+#pragma unroll
+                    for (int y = 0; y < KT; ++y) s[y] = -s[y];
+                }
+                const int lim = last - t * KT;
+                if (__any_sync(FULL_MASK, lim < KT - 1)) {
+#pragma unroll
+                    for (int y = 0; y < KT; ++y)
+                        if (y > lim) s[y] = -INFINITY;
+                }
+                float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int y = 0; y < KT; y += 8)
+#pragma unroll
+                    for (int z = 0; z < 4; ++z) top[z] = max3(top[z], s[y + 2 * z], s[y + 2 * z + 1]);
+                const float mx = max3(max3(top[0], top[1], top[2]), top[3], top[3]);
+                if (i > 0 && i % FOLD == 0) {  // the sum in tensor memory joins the folds; this tile's product begins a new one
+                    ok = ok && done(n_t - 1);
+                    const float f = folded == -INFINITY ? 1.f : kv_ex2((folded - m) * c2);
+#pragma unroll 1
+                    for (int e = 0; e < a.d; e += 8) {
+                        float o[8];
+                        tc::tmem_ld<8>(tm_o + e, o);
+#pragma unroll
+                        for (int y = 0; y < 8; ++y) {
+                            float* at = part + (int64_t)(e + y) * PLACES;
+                            *at = i > FOLD ? fmaf(*at, f, o[y]) : o[y];
+                        }
+                    }
+                    folded = m;
+                    tc::fence_before();
+                }
+                // a new reference where the maximum has left the old one behind (not for places without a row: what they
+                // hold is anything)
+                const bool need = live && mx > m && (m == -INFINITY || fmaf(mx, c2, nref) > kvt::REF_SLACK + H::lift);
+                if (__any_sync(FULL_MASK, need)) {
+                    float f = 1.f;
+                    if (need) {
+                        f = m == -INFINITY ? 1.f : kv_ex2((m - mx) * c2);
+                        m = mx, nref = fmaf(-m, c2, H::lift), l *= f;
+                    }
+                    if (i % FOLD != 0) {
+                        ok = ok && done(n_t - 1);
+#pragma unroll 1
+                        for (int e = 0; e < a.d; e += 8) {
+                            float o[8];
+                            tc::tmem_ld<8>(tm_o + e, o);
+#pragma unroll
+                            for (int y = 0; y < 8; ++y) o[y] *= f;
+                            tc::tmem_st<8>(tm_o + e, o);
+                        }
+                    }
+                }
+                // Exponents c s - m are fused, one rounding: exact enough while a product's own rounding is under one.
+                float from = nref;
+                if (__any_sync(FULL_MASK, fabsf(nref) > kvt::FUSED_MOST && m > -INFINITY)) {
+                    const float base = m == -INFINITY ? 0.f : m;
+#pragma unroll
+                    for (int y = 0; y < KT; ++y) s[y] -= base;
+                    from = H::lift;
+                }
+                // weights: FP32 sums, rounded once to the cache's type for the product with the values
+                const Two cc = two(c2, c2), nn = two(from, from);
+                Two sum[2] = {0, 0};
+#pragma unroll
+                for (int h = 0; h < 4; ++h) {
+                    uint32_t u[16];
+#pragma unroll
+                    for (int y = 0; y < 32; y += 2) {
+                        const float2 z = parts(fma2(two(s[h * 32 + y], s[h * 32 + y + 1]), cc, nn));
+                        const float p0 = kv_ex2(z.x), p1 = kv_ex2(z.y);
+                        sum[y / 2 & 1] = add2(sum[y / 2 & 1], two(p0, p1));
+                        u[y / 2] = H::pack(p0, p1);
+                    }
+                    st16(tm_s + h * 16, u);
+                    if (h & 1) {
+                        if (h == 3 && t >= mixed) {
+                            // this thread's row of V, a key: the boxes are shared out over the groups
+                            ok = ok && warp_wait(&st.v_ok, n_v & 1);
+                            ++n_v;
+                            const bool dead = t * KT + r >= w.s.len;
+                            for (int b = g; b < boxes && ok; b += QT) {
+                                int stage = st.v_stage + (b >> 1);
+                                if (stage >= stages) stage -= v_stages;
+                                uint4* row = reinterpret_cast<uint4*>(ring + stage * one_stage + (b & 1) * BOX_BYTES + r * 128);
+#pragma unroll
+                                for (int y = 0; y < 8; ++y) {
+                                    const int c = y ^ (lane & 7);  // (an order without bank conflicts)
+                                    if (dead) row[c] = make_uint4(0, 0, 0, 0);
+                                    else if (kvt::has_odd<ST>(row[c])) row[c] = kvt::clear_odd<ST>(row[c]), st.odd[side] = 1;
+                                }
+                            }
+                            __threadfence_block();
+                            tc::fence_async_smem();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(&st.v_clean);
+                        }
+                        st_wait();
+                        tc::fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&st.p_full[buf][h >> 1]);
+                    }
+                }
+                const float2 all = parts(add2(sum[0], sum[1]));
+                l += all.x + all.y;
+            }
+            if (!ok) break;
+            // ------------------------------------------------------------ outputs
+            ok = done(n_t - 1) && warp_wait(&st.seg_loaded[side], (seg >> 1) & 1);
+            if (!ok) break;
+            const bool bad = st.bad[side], odd = st.odd[side], whole = w.whole(), fold = n > FOLD;
+            const int32_t* table = a.page_table + (int64_t)w.s.slot * a.max_pages;
+            const float back = folded == -INFINITY ? 1.f : kv_ex2((folded - m) * c2);
+            const float inv = bad || l == 0.f ? 0.f : 1.f / l;
+            const int64_t to = (int64_t)(w.s.first + tok) * a.Hq + w.h * a.G + (x - tok * a.G);
+#pragma unroll 1
+            for (int e = 0; e < a.d; e += 32) {
+                float o[32];
+                __syncwarp();
+                tc::tmem_ld<32>(tm_o + e, o);
+                const int cols = min(32, a.d - e);
+                if (fold) {
+#pragma unroll
+                    for (int y = 0; y < 32; ++y)
+                        if (y < cols) o[y] = fmaf(part[(int64_t)(e + y) * PLACES], back, o[y]);
+                }
+                if (!live) continue;
+                if (odd && !bad) add_odd<ST>(a, table, w.h, max(mixed, w.t0) * KT, min(last, w.t1 * KT - 1), e, o);
+                if (!whole) {
+#pragma unroll
+                    for (int y = 0; y < 32; ++y)
+                        if (y < cols) part[(int64_t)(e + y) * PLACES] = bad ? 0.f : o[y];
+                    continue;
+                }
+                ST* out = static_cast<ST*>(a.out) + to * a.d + e;
+#pragma unroll
+                for (int y = 0; y < 32; y += 8) {
+                    if (y >= cols) break;
+                    float z[8];
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) z[q] = inv == 0.f ? 0.f : o[y + q] * inv;
+                    if (vec) *reinterpret_cast<uint4*>(out + y) = Store<ST>::pack(z);
+                    else
+                        for (int q = 0; q < 8; ++q) out[y + q] = H::round(z[q]);
+                }
+            }
+            tc::fence_before();
+            if (live) {
+                if (!whole) {
+                    float* stat = part + (int64_t)PLACES * a.d;
+                    stat[0] = m == -INFINITY ? -INFINITY : -nref, stat[PLACES] = bad ? -1.f : l;
+                } else if (a.lse) {
+                    a.lse[to] = bad || l == 0.f ? -INFINITY : (log2f(l) - nref) * LN2;
+                }
+            }
+            if (tid == 0 && w.t0 == 0 && !whole) kp_border(a, st.scan, w);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&st.seg_free[side]);
+            ++seg;
+        } while (w.next());
+        if (!ok && lane == 0) st.stopped = 1, set_error(a.dev_err, GDN_DEVERR_TIMEOUT);
+    }
+    if (warp == S_WARP) kp_empty_rows(a, a.B <= KEEP ? st.scan.seq : nullptr, lane, 32);
+    tc::fence_before();
+    __syncthreads();
+    tc::fence_after();
+    if (warp == O_WARP)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(TM_COLS) : "memory");
+    if (st.stopped) refuse_range<QT>(a, st);
+}
+
+}  // namespace gdn

@@ -78,43 +78,69 @@ def test_few_rows_over_a_long_cache(dtype, d, G):
     Prompt(7, dtype, [(3, 20000), (40, 7000)], Hq=G, Hkv=1, d=d, page=64).check()
 
 
+def check_sampled(c, step, more=()):
+    """Every step-th row and `more` against the definition in 64 bits, formed on the device."""
+    out, lse = c.attend()
+    assert int(c.err.item()) == 0
+    k, v, q, G = c.k.double(), c.v.double(), c.q.double(), c.Hq // c.Hkv
+    rows = np.unique(np.concatenate([np.arange(0, c.total, step), c.cu[1:] - 1, c.cu[:-1], more])).astype(int)
+    for b, (n, p) in enumerate(c.prompts):
+        if n == 0 or c.slots[b] < 0:
+            continue
+        pages = torch.from_numpy(c.table[c.slots[b], :-(-(n + p) // c.page)]).long().cuda()
+        kc, vc = (x[pages].transpose(0, 1).reshape(c.Hkv, -1, c.d)[:, :n + p] for x in (k, v))
+        for r in rows[(rows >= c.cu[b]) & (rows < c.cu[b + 1])]:
+            L = p + int(r) - int(c.cu[b]) + 1
+            qr = q[r].view(c.Hkv, G, c.d)
+            s = qr @ kc[:, :L].transpose(1, 2) * c.scale
+            w = torch.softmax(s, -1)
+            want, mag = (w @ vc[:, :L]).cpu().numpy(), (w @ vc[:, :L].abs()).cpu().numpy()
+            smag = ((qr.abs() @ kc[:, :L].abs().transpose(1, 2)).amax(-1) * abs(c.scale)).cpu().numpy()
+            assert (np.abs(host(out[r]).reshape(want.shape) - want) <= ref.out_bound(mag, smag, c.d, c.dtype)).all(), r
+            z = torch.logsumexp(s, -1).cpu().numpy()
+            assert (np.abs(host(lse[r]).reshape(z.shape) - z) <= ref.lse_bound(z, smag, c.d)).all(), r
+    return out, lse
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
 @pytest.mark.parametrize("d", [64, 128, 256])
 def test_long_prompts(dtype, d):
     """Several units a key head, cut by the ranges of the grid; every 37th row is compared."""
-    c = Prompt(8, dtype, [(2100, 0), (1500, 3000)], Hq=4, Hkv=2, d=d, page=64)
-    out, lse = c.attend()
-    assert int(c.err.item()) == 0
-    k, v, q = c.k.double(), c.v.double(), c.q.double()
-    rows = np.unique(np.concatenate([np.arange(0, c.total, 37), [0, 2099, 2100, c.total - 1]]))
-    for b, (n, p) in enumerate(c.prompts):
-        pages = torch.from_numpy(c.table[c.slots[b], :-(-(n + p) // c.page)]).long().cuda()
-        kc, vc = (x[pages].transpose(0, 1).reshape(2, -1, d)[:, :n + p] for x in (k, v))
-        for r in rows[(rows >= c.cu[b]) & (rows < c.cu[b + 1])]:
-            L = p + int(r) - int(c.cu[b]) + 1
-            for x in range(4):
-                s = kc[x // 2, :L] @ q[r, x] * c.scale
-                w = torch.softmax(s, 0)
-                want, mag = (w @ vc[x // 2, :L]).cpu().numpy(), (w @ vc[x // 2, :L].abs()).cpu().numpy()
-                smag = float((kc[x // 2, :L].abs() @ q[r, x].abs()).max()) * c.scale
-                assert (np.abs(host(out[r, x]) - want) <= ref.out_bound(mag, np.array(smag), d, dtype)).all(), (r, x)
-                z = float(torch.logsumexp(s, 0))
-                assert abs(float(lse[r, x]) - z) <= ref.lse_bound(np.array(z), smag, d), (r, x)
+    check_sampled(Prompt(8, dtype, [(2100, 0), (1500, 3000)], Hq=4, Hkv=2, d=d, page=64), 37)
+
+
+# (rows, entries before them), query and key heads: units for every SM, so that each holds two tiles of rows
+MANY_UNITS = [([(2500, 0)], 16, 2), ([(300, 20), (0, 5), (411, 900), (63, 0)], 64, 8), ([(1, 0), (900, 130)], 40, 8),
+              ([(700, 5000)], 24, 24), ([(640, 0), (33, 1)], 96, 8), ([(1290, 77)], 71 * 2, 2), ([(130, 10000)], 128 * 2, 2)]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("d", [64, 80, 128])
+@pytest.mark.parametrize("prompts,Hq,Hkv", MANY_UNITS, ids=str)
+def test_many_units(dtype, d, prompts, Hq, Hkv):
+    total = sum(n for n, _ in prompts)
+    assert total // (2 * (128 // (Hq // Hkv))) * Hkv >= 120 or d > 128
+    check_sampled(Prompt(27, dtype, prompts, Hq=Hq, Hkv=Hkv, d=d, page=16), max(1, total // 60))
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
 @pytest.mark.parametrize("d", [64, 128, 256])
 @pytest.mark.parametrize("leader", [False, True])
-def test_sums_of_a_long_cache_do_not_shrink(dtype, d, leader):
+@pytest.mark.parametrize("heads", [1, 160])
+def test_sums_of_a_long_cache_do_not_shrink(dtype, d, leader, heads):
     """Every value is 1 and so is every output: equal weights, or one entry that holds most of the weight. A sum of
     weights that lost more than half a unit of rounding of the cache's type would not come out as 1."""
-    n, p = 140, 60000
-    c = Prompt(9, dtype, [(n, p)], Hq=1, Hkv=1, d=d, page=64)
+    n, p = (140, 60000) if heads == 1 else (260, 20000)
+    c = Prompt(9, dtype, [(0, p + n)], Hq=heads, Hkv=1, d=d, page=64) if heads == 1 else \
+        Prompt(9, dtype, [(0, p + n)], Hq=heads, Hkv=heads, d=d, page=64)
+    c.cu, c.total = np.array([0, n], np.int32), n
+    c.q = torch.empty(n, heads, d, dtype=c.k.dtype, device="cuda")
+    c.sync()
     c.k.zero_()
     c.v.fill_(1.0)
     c.q.fill_(1.0)
     if leader:
-        c.k[int(c.table[c.slots[0], 0]), 0, 0] = 10.0 / math.sqrt(d)
+        c.k[int(c.table[c.slots[0], 0]), :, 0] = 10.0 / math.sqrt(d)
     out, _ = c.attend()
     assert int(c.err.item()) == 0
     assert (out.float() - 1.0).abs().max().item() <= UNIT[dtype]
@@ -123,14 +149,16 @@ def test_sums_of_a_long_cache_do_not_shrink(dtype, d, leader):
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("d", [64, 256])
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
-def test_values_that_are_not_finite_reach_only_rows_that_see_them(dtype, d, bad):
-    c = Prompt(10, dtype, [(90, 45), (20, 0)], Hq=4, Hkv=2, d=d, page=16)
+@pytest.mark.parametrize("heads", [(4, 2), (80 * 8, 80)], ids=str)
+def test_values_that_are_not_finite_reach_only_rows_that_see_them(dtype, d, bad, heads):
+    Hq, Hkv = heads
+    c = Prompt(10, dtype, [(90, 45), (20, 0)], Hq=Hq, Hkv=Hkv, d=d, page=16)
     slot, e = c.slots[0], 45 + 50  # the entry of row 50
     c.v[int(c.table[slot, e // 16]), 1, e % 16, 3] = bad
-    want = Prompt(10, dtype, [(90, 45), (20, 0)], Hq=4, Hkv=2, d=d, page=16)
+    want = Prompt(10, dtype, [(90, 45), (20, 0)], Hq=Hq, Hkv=Hkv, d=d, page=16)
     got, base = c.attend()[0], want.attend()[0]
     hit = torch.zeros_like(got, dtype=torch.bool)
-    hit[50:90, 2:, 3] = True
+    hit[50:90, Hq // Hkv:2 * (Hq // Hkv), 3] = True
     assert torch.equal(got[~hit], base[~hit])
     assert not got[hit].isfinite().any() and (math.isnan(bad) or (got[hit] == bad).all())
 
@@ -206,9 +234,11 @@ def test_refused_sequences(dtype, what, bit):
 
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("page", [-7, 10 ** 6])
-def test_a_page_outside_the_pool(dtype, page):
-    """The second sequence's third page: blocks that reach it are refused, the others and other sequences are right."""
-    c = Prompt(17, dtype, [(40, 3), (300, 20), (70, 9)], Hq=4, Hkv=2, d=64, page=16)
+@pytest.mark.parametrize("heads", [(4, 2), (25 * 8, 25)], ids=str)
+def test_a_page_outside_the_pool(dtype, page, heads):
+    """A page in the middle of the second sequence: blocks that reach it are refused, the others and other sequences
+    are right."""
+    c = Prompt(17, dtype, [(40, 3), (300, 20), (70, 9)], Hq=heads[0], Hkv=heads[1], d=64, page=16)
     want, wl = c.attend()
     c.table[c.slots[1], 14] = page
     c.sync()
@@ -216,8 +246,8 @@ def test_a_page_outside_the_pool(dtype, page):
     assert int(c.err.item()) == kv.DEVERR_PAGE
     own = np.r_[0:40, 340:410]
     assert torch.equal(out[own], want[own]) and torch.equal(lse[own], wl[own])
-    same = (out == want).flatten(1).all(1) & (lse == wl).all(1)
-    zero = (out == 0).flatten(1).all(1) & torch.isneginf(lse).all(1)
+    same = (out == want).all(2) & (lse == wl)
+    zero = (out == 0).all(2) & torch.isneginf(lse)
     assert (same | zero)[40:340].all() and zero[40 + 14 * 16 - 20:340].all()
 
 
