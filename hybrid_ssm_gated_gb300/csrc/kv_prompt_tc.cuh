@@ -21,9 +21,19 @@
 //   softmax    four warps a tile of rows, thread = row = tensor-memory lane;
 //   K, V       a warp each: tiles by TMA into a ring of stages of 128 keys x 128
 //              elements, boxes of as many keys as a page and the tile share;
-//   S, O       a warp each, one elected thread of which issues the products; the S
-//              warp loads a unit's queries (whole tokens: a tile of rows holds as many
-//              as have their G heads in it).
+//              the V warp loads a unit's queries too, once the last one's products have
+//              read theirs (whole tokens: a tile of rows holds as many as have their G
+//              heads in it);
+//   products   a warp a tile of rows, an elected thread of which issues all of its
+//              products in order: with QT = 2 a tile's S is issued right behind the last
+//              product that reads the P it is written over, and waits for nobody. (A
+//              commit holds a thread up for 120 to 210 cycles, one right behind another
+//              for 12: a thread for both tiles took 4100 cycles a tile of keys where the
+//              products take 2048.)
+// A tile's chain is S, softmax, O, S ...: what bounds the kernel is its latency. So the
+// weights' first half is formed against the last tile's reference while the maximum is
+// still looked for (it is formed again where that moved the reference), and is given to
+// the tensor cores while the second half is formed.
 // A tile of which some row sees a part ("mixed") has its values looked through by the
 // softmax threads: rows of V past the sequence's end become zero, and so does what is
 // not finite (0 x NaN would reach rows that do not see it); the epilogue adds the
@@ -53,7 +63,7 @@ struct Maps {
 template <int QT>
 struct __align__(16) State {
     uint64_t full[MAX_STAGES], empty[MAX_STAGES];  // the K ring's stages, then the V ring's
-    uint64_t s_full[2], o_done[2], p_full[2][2], q_full, v_ok, v_clean, drain[2];
+    uint64_t s_full[2], o_done[2], p_full[2][2], q_full, q_free, v_ok, v_clean, drain[2], turn[2];
     uint64_t seg_open[2], seg_loaded[2], seg_free[2];
     KpScan<threads(QT), KEEP> scan;
     int bad[2], odd[2];  // of this segment and the next: a page outside the pool; a value that is not finite
@@ -70,12 +80,33 @@ __host__ __device__ constexpr int smem_bytes(int boxes, int stages) {
     return 1024 + QT * boxes * TILE * 128 + stages * stage_bytes(boxes) + (int)sizeof(State<QT>);
 }
 
-// The product with the A operand in tensor memory (issued as kvt::mma).
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, bool accumulate) {
+// Operand descriptors of the 128-byte swizzle, 1024 bytes between groups of eight rows: the upper word is the same for
+// all, the lower one holds address and leading offset.
+constexpr uint32_t DESC_HI = (1024 >> 4) | 1u << 14 | kvt::SW128 << 29;
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo) { return (saddr & 0x3FFFF) >> 4 | (lbo >> 4) << 16; }
+
+// One thread of a converged warp.
+__device__ __forceinline__ bool elected() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\tselp.u32 %0, 1, 0, e;\n\t}" : "=r"(r));
+    return r != 0;
+}
+
+// A product, by one thread; A in shared memory, or in tensor memory.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t id, bool accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p, e;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(id), "r"((uint32_t)accumulate)
+        "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "mov.b64 x, {%1, %5};\n\tmov.b64 y, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(id), "r"((uint32_t)accumulate), "n"(DESC_HI)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t id, bool accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 y;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "mov.b64 y, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(id), "r"((uint32_t)accumulate), "n"(DESC_HI)
         : "memory");
 }
 
@@ -89,18 +120,39 @@ __device__ __forceinline__ void st16(uint32_t taddr, const uint32_t* v) {
 }
 __device__ __forceinline__ void st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// The values of a row's mixed tiles that are not finite, added to outputs e0 .. e0 + 31 where the row sees the entry.
+// The values of a row's mixed tiles that are not finite, added to its outputs where the row sees the entry (entries
+// `from` to `last`): output e is out[e * step], of type `dtype`.
 template <typename ST>
-__device__ __noinline__ void add_odd(const KvArgs& a, const int32_t* table, int h, int from, int last, int e0, float* o) {
+__device__ __noinline__ void add_odd(const KvArgs& a, const int32_t* table, int h, int from, int last, void* out, int64_t step,
+                                     int dtype) {
     for (int e = from; e <= last; ++e) {
         const int pg = e / a.page_size, page = table[pg];
         if ((uint32_t)page >= (uint64_t)a.num_pages) continue;
         const int64_t at = kv_at(a.v, page, h, e - pg * a.page_size);
-        for (int x = 0; x < 32 && e0 + x < a.d; ++x) {
-            const float v = load_elem(a.v.p, at + e0 + x, Store<ST>::code);
-            if (!isfinite(v)) o[x] += v;
+        for (int x = 0; x < a.d; ++x) {
+            const float v = load_elem(a.v.p, at + x, Store<ST>::code);
+            if (!isfinite(v)) store_elem(out, x * step, dtype, load_elem(out, x * step, dtype) + v);
         }
     }
+}
+
+// Four pieces of each of four lanes (a lane's piece i its row's) turned, so that piece k of a lane is of row k and all
+// lie next to one another.
+__device__ __forceinline__ void turn4(uint4 (&x)[4], int lane) {
+#pragma unroll
+    for (int b = 1; b < 4; b <<= 1)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (i & b) continue;
+            const bool up = lane & b;
+            uint4& lo = x[i];
+            uint4& hi = x[i | b];
+            uint4 y = up ? lo : hi;
+            y.x = __shfl_xor_sync(FULL_MASK, y.x, b), y.y = __shfl_xor_sync(FULL_MASK, y.y, b);
+            y.z = __shfl_xor_sync(FULL_MASK, y.z, b), y.w = __shfl_xor_sync(FULL_MASK, y.w, b);
+            if (up) lo = y;
+            else hi = y;
+        }
 }
 
 // What a CTA leaves whose waits ran out, by the whole block: the rows of its range as those of a refused sequence.
@@ -135,11 +187,11 @@ __global__ void __launch_bounds__(kpt::threads(QT), 1)
     kv_prompt_tc_kernel(const __grid_constant__ KvArgs a, const __grid_constant__ kpt::Maps maps, const int boxes,
                         const int k_stages, const int v_stages, const int box_rows) {
     using namespace kpt;
-    using kvt::desc, kvt::idesc, kvt::SW128, kvt::uniform, kvt::warp_wait, kvt::tma_load, kvt::commit;
+    using kvt::idesc, kvt::warp_wait, kvt::tma_load;
     using kvt::Two, kvt::two, kvt::fma2, kvt::add2, kvt::parts, kvt::max3;
     using H = kvt::Half16<ST>;
     constexpr int NT = threads(QT), SM_WARPS = 4 * QT, PLACES = QT * TILE;
-    constexpr int K_WARP = SM_WARPS, V_WARP = SM_WARPS + 1, S_WARP = SM_WARPS + 2, O_WARP = SM_WARPS + 3;
+    constexpr int K_WARP = SM_WARPS, V_WARP = SM_WARPS + 1, M_WARP = SM_WARPS + 2;
     constexpr uint32_t TM_S = 0, TM_O = 256, TM_COLS = 512;
     extern __shared__ unsigned char smem_raw[];
     unsigned char* smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
@@ -156,20 +208,24 @@ __global__ void __launch_bounds__(kpt::threads(QT), 1)
             const CUtensorMap* m = lane == 0 ? &maps.k : lane == 1 ? &maps.v : &maps.q;
             asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory");
         }
-        if (lane < stages) mbar_init(&st.full[lane], 1), mbar_init(&st.empty[lane], 1);
+        if (lane < stages) mbar_init(&st.full[lane], 1), mbar_init(&st.empty[lane], QT);
         if (lane < 2) {
             mbar_init(&st.s_full[lane], 1), mbar_init(&st.o_done[lane], 1);
-            mbar_init(&st.p_full[lane][0], 4), mbar_init(&st.p_full[lane][1], 4), mbar_init(&st.drain[lane], 1);
+            mbar_init(&st.p_full[lane][0], 4), mbar_init(&st.p_full[lane][1], 4);
             mbar_init(&st.seg_open[lane], 1), mbar_init(&st.seg_loaded[lane], 1), mbar_init(&st.seg_free[lane], SM_WARPS);
             st.bad[lane] = st.odd[lane] = 0;
         }
-        if (lane == 2) mbar_init(&st.q_full, 1), mbar_init(&st.v_ok, 1), mbar_init(&st.v_clean, SM_WARPS), st.stopped = 0;
+        if (lane == 2) {
+            mbar_init(&st.q_full, 1), mbar_init(&st.q_free, QT), mbar_init(&st.v_ok, 1), mbar_init(&st.v_clean, SM_WARPS);
+            mbar_init(&st.drain[0], 1), mbar_init(&st.drain[1], 1), st.stopped = 0;
+            mbar_init(&st.turn[0], 1), mbar_init(&st.turn[1], 1);
+        }
 #ifdef GDN_TEST_STALL
         if (lane == 0) mbar_init(&st.never, 1);
 #endif
         fence_barrier_init();
     }
-    if (warp == O_WARP) {
+    if (warp == M_WARP) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&st.tmem)),
                      "r"(TM_COLS)
                      : "memory");
@@ -185,13 +241,17 @@ __global__ void __launch_bounds__(kpt::threads(QT), 1)
     // the first tile of the unit that some row sees a part of only
     const auto first_mixed = [&]() { return (w.s.len - w.s.n + w.r0() / a.G + 1) / KT; };
 
+    // (of two tiles' kernel) registers to the threads that hold a row of scores: 256 x 208 + 128 x 88 of the launch's
+    // 384 x 168
+    if (warp >= SM_WARPS) {
+    if constexpr (QT == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if ((warp == K_WARP || warp == V_WARP) && busy) {
         // ------------------------------------------------------------ loads
         const bool keys = warp == K_WARP;
         const CUtensorMap* map = keys ? &maps.k : &maps.v;
         const int first = keys ? 0 : k_stages, end = keys ? k_stages : stages;
         int stage = first;
-        uint32_t round = 0, seg = 0;
+        uint32_t round = 0, seg = 0, asked = 0;
         bool ok = true;
         const int per_tile = KT / box_rows, step_pages = KT / a.page_size, step_places = KT - step_pages * a.page_size;
         do {
@@ -202,6 +262,20 @@ __global__ void __launch_bounds__(kpt::threads(QT), 1)
             int e = w.t0 * KT + lane * box_rows, pg = e / a.page_size, place = e - pg * a.page_size;
             const auto look = [&]() { return lane < per_tile && e < w.s.len ? table[pg] : 0; };
             int page = look();
+            if (!keys) {  // the unit's queries
+                if (seg > 0) ok = warp_wait(&st.q_free, (seg - 1) & 1);
+                if (ok) {
+                    if (lane == 0) mbar_arrive_expect_tx(&st.q_full, QT * boxes * per * 128);
+                    __syncwarp();
+                    if (lane < QT * boxes) {
+                        const int j = lane / boxes, x = lane - j * boxes;
+                        tma_load(sQ + (j * boxes + x) * TILE * 128, &maps.q, x * BOX, w.h * a.G,
+                                 w.s.first + w.r0() / a.G + j * (per / a.G), 0, &st.q_full);
+                    }
+                    __syncwarp();
+                    ++asked;
+                }
+            }
             if (keys) {
                 if (seg >= 2) {
                     ok = warp_wait(&st.seg_free[side], ((seg >> 1) - 1) & 1);
@@ -247,134 +321,140 @@ __global__ void __launch_bounds__(kpt::threads(QT), 1)
         } while (ok && w.next());
         if (!ok && lane == 0) st.stopped = 1, set_error(a.dev_err, GDN_DEVERR_TIMEOUT);
         kvt::landed(st.full, first, end, stage, round);
-    } else if (warp == S_WARP && busy) {
-        // ------------------------------------------------------------ S = Q K^T
-        const uint32_t id = idesc(H::type, false, false, KT), aQ = smem_addr(sQ), aR = smem_addr(ring), tm = uniform(tmem);
-        const int tokens = per / a.G;  // of a tile
-        int stage = 0;
-        uint32_t round = 0, n_t = 0, asked = 0;
-        bool ok = true;
-        do {
-            const int n = uniform(w.t1 - w.t0);
-            if (n_t > 0)  // the last segment's products have read their queries
-                ok = QT == 2 ? warp_wait(&st.s_full[1], (n_t - 1) & 1) : warp_wait(&st.s_full[(n_t - 1) & 1], ((n_t - 1) >> 1) & 1);
-            if (ok) {
-                if (lane == 0) mbar_arrive_expect_tx(&st.q_full, QT * boxes * per * 128);
-                __syncwarp();
-                if (lane < QT * boxes) {
-                    const int j = lane / boxes, x = lane - j * boxes;
-                    tma_load(sQ + (j * boxes + x) * TILE * 128, &maps.q, x * BOX, w.h * a.G, w.s.first + w.r0() / a.G + j * tokens, 0,
-                             &st.q_full);
-                }
-                __syncwarp();
-                ok = warp_wait(&st.q_full, asked & 1);
-                ++asked;
-            }
-#pragma unroll 1
-            for (int i = 0; i < n && ok; ++i, ++n_t) {
-                const int buf = QT == 2 ? 0 : n_t & 1;
-                if (QT == 1 && n_t >= 2) ok = warp_wait(&st.o_done[buf], ((n_t >> 1) - 1) & 1);
-#pragma unroll 1
-                for (int p = 0; p < pairs && ok; ++p) {
-                    ok = warp_wait(&st.full[stage], round & 1);
-                    if (!ok) break;
-                    tc::fence_after();
-                    const uint64_t db = desc(aR + stage * one_stage, 16, 1024, SW128);
-                    const int nb = min(2, boxes - 2 * p);
-#pragma unroll 1
-                    for (int j = 0; j < QT; ++j) {
-                        if (QT == 2 && n_t > 0) {
-                            ok = warp_wait(&st.o_done[j], (n_t - 1) & 1);
-                            if (!ok) break;
-                            tc::fence_after();
-                        }
-                        const uint32_t to = tm + TM_S + (QT == 2 ? j : buf) * KT;
-                        const uint64_t da = desc(aQ + (j * boxes + 2 * p) * TILE * 128, 16, 1024, SW128);
-#pragma unroll 1
-                        for (int x = 0; x < nb; ++x) {
-                            const int steps = min(BOX / 16, (a.d - (2 * p + x) * BOX + 15) / 16);
-                            const uint64_t da_x = da + x * (TILE * 128 >> 4), db_x = db + x * (BOX_BYTES >> 4);
-                            if (steps == BOX / 16) {
-#pragma unroll
-                                for (int k = 0; k < BOX / 16; ++k)
-                                    kvt::mma(to, da_x + k * (32 >> 4), db_x + k * (32 >> 4), id, p + x + k > 0);
-                            } else {
-#pragma unroll 1
-                                for (int k = 0; k < steps; ++k)
-                                    kvt::mma(to, da_x + k * (32 >> 4), db_x + k * (32 >> 4), id, p + x + k > 0);
-                            }
-                        }
-                        if (QT == 2) commit(&st.s_full[j]);
-                    }
-                    if (!ok) break;
-                    commit(&st.empty[stage]);
-                    if (++stage == k_stages) stage = 0, ++round;
-                }
-                if (QT == 1 && ok) commit(&st.s_full[buf]);
-            }
-        } while (ok && w.next());
-        if (!ok && lane == 0) st.stopped = 1, set_error(a.dev_err, GDN_DEVERR_TIMEOUT);
         if (asked) mbar_wait(&st.q_full, (asked - 1) & 1);
-        commit(&st.drain[0]);
-        mbar_wait(&st.drain[0], 0);
-        __syncwarp();
-    } else if (warp == O_WARP && busy) {
-        // ------------------------------------------------------------ O += P V
-        const uint32_t aR = smem_addr(ring), tm = uniform(tmem);
-        int stage = k_stages;
-        uint32_t round = 0, n_t = 0, n_v = 0;
-        bool ok = true;
-        do {
-            const int n = uniform(w.t1 - w.t0), t0 = uniform(w.t0), mixed = uniform(first_mixed());
-#pragma unroll 1
-            for (int i = 0; i < n && ok; ++i, ++n_t) {
-                int s2 = stage;
-                uint32_t r2 = round;
-#pragma unroll 1
+    } else if (warp >= M_WARP && warp < M_WARP + QT && busy) {
+        // ------------------------------------------------------------ products
+        // (one thread, and one that the compiler knows to be alone: elsewhere a product took 107 cycles to issue, for
+        // operands that might differ from thread to thread)
+        if (elected()) {
+            const int j = warp - M_WARP;
+            const uint32_t id_s = idesc(H::type, false, false, KT), aQ = smem_addr(sQ) + j * boxes * TILE * 128, aR = smem_addr(ring);
+            int ks = 0, vs = k_stages;  // the rings' next stages
+            uint32_t k_round = 0, v_round = 0, n_t = 0, n_v = 0, seg = 0;
+            bool ok = true;
+            // The two tiles take turns at the tensor cores, so that one's weights form while the other's products run (left
+            // alone they fall into step and wait for both).
+            uint32_t turns = 0;
+            const auto my_turn = [&]() {
+                if (QT == 2 && (j == 1 || turns > 0)) ok = ok && mbar_wait(&st.turn[j], (j == 1 ? turns : turns - 1) & 1);
+                ++turns;
+            };
+            const auto pass = [&]() {
+                if (QT == 2) mbar_arrive(&st.turn[j ^ 1]);
+            };
+            const auto k_there = [&]() {
+                int sk = ks;
+                uint32_t rk = k_round;
                 for (int p = 0; p < pairs && ok; ++p) {
-                    ok = warp_wait(&st.full[s2], r2 & 1);
-                    if (++s2 == stages) s2 = k_stages, ++r2;
+                    ok = mbar_wait(&st.full[sk], rk & 1);
+                    if (++sk == k_stages) sk = 0, ++rk;
                 }
-                if (ok && t0 + i >= mixed) {  // the softmax threads look the values through
-                    if (lane == 0) st.v_stage = stage, mbar_arrive(&st.v_ok);
-                    __syncwarp();
-                    ok = warp_wait(&st.v_clean, n_v & 1);
-                    ++n_v;
+                tc::fence_after();
+            };
+            const auto scores = [&](int buf) {  // S into buffer `buf`, from the K stages at ks, which are there
+                const uint32_t to = tmem + TM_S + buf * KT;
+                int sk = ks;
+#pragma unroll 1
+                for (int p = 0; p < pairs; ++p) {
+                    const int nb = min(2, boxes - 2 * p);
+                    const uint32_t db = desc_lo(aR + sk * one_stage, 16), da = desc_lo(aQ + 2 * p * TILE * 128, 16);
+#pragma unroll 1
+                    for (int x = 0; x < nb; ++x) {
+                        const int steps = min(BOX / 16, (a.d - (2 * p + x) * BOX + 15) / 16);
+                        const uint32_t da_x = da + x * (TILE * 128 >> 4), db_x = db + x * (BOX_BYTES >> 4);
+                        if (steps == BOX / 16) {
+#pragma unroll
+                            for (int k = 0; k < BOX / 16; ++k)
+                                mma_ss(to, da_x + k * (32 >> 4), db_x + k * (32 >> 4), id_s, p + x + k > 0);
+                        } else {
+#pragma unroll 1
+                            for (int k = 0; k < steps; ++k)
+                                mma_ss(to, da_x + k * (32 >> 4), db_x + k * (32 >> 4), id_s, p + x + k > 0);
+                        }
+                    }
+                    if (++sk == k_stages) sk = 0;
+                }
+                pass();  // (ahead of the commits, which hold this thread up)
+                tc::commit(&st.s_full[buf]);
+                for (int p = 0; p < pairs; ++p) {
+                    tc::commit(&st.empty[ks]);
+                    if (++ks == k_stages) ks = 0, ++k_round;
+                }
+            };
+            do {
+                const int n = w.t1 - w.t0, t0 = w.t0, mixed = first_mixed();
+                ok = ok && mbar_wait(&st.q_full, seg & 1);
+                if (ok) k_there();
+                my_turn();
+                if (ok) {
+                    scores(QT == 2 ? j : n_t & 1);
+                    if (n == 1) tc::commit(&st.q_free);
                 }
 #pragma unroll 1
-                for (int j = 0; j < QT && ok; ++j) {
+                for (int i = 0; i < n && ok; ++i, ++n_t) {
+                    const bool more = i + 1 < n;
                     const int buf = QT == 2 ? j : n_t & 1;
                     const uint32_t use = QT == 2 ? n_t : n_t >> 1;
+                    if (more) k_there();
+                    if (QT == 1 && more && ok) {
+                        scores((n_t + 1) & 1);
+                        if (i + 2 == n) tc::commit(&st.q_free);
+                    }
+                    int sp = vs;
+                    uint32_t rp = v_round;
+                    for (int p = 0; p < pairs && ok; ++p) {
+                        ok = mbar_wait(&st.full[sp], rp & 1);
+                        if (++sp == stages) sp = k_stages, ++rp;
+                    }
+                    if (ok && t0 + i >= mixed) {  // the softmax threads look the values through
+                        if (j == 0) st.v_stage = vs, mbar_arrive(&st.v_ok);
+                        ok = mbar_wait(&st.v_clean, n_v & 1);
+                        ++n_v;
+                    }
+                    my_turn();
 #pragma unroll 1
-                    for (int half = 0; half < 2; ++half) {
-                        ok = warp_wait(&st.p_full[buf][half], use & 1);
+                    for (int half = 0; half < 2 && ok; ++half) {
+                        ok = mbar_wait(&st.p_full[buf][half], use & 1);
                         if (!ok) break;
                         tc::fence_after();
-                        int sp = stage;
+                        sp = vs;
 #pragma unroll 1
                         for (int p = 0; p < pairs; ++p) {
                             const int nb = min(2, boxes - 2 * p), N = min(128, (a.d - p * 128 + 15) / 16 * 16);
-                            const uint32_t id = idesc(H::type, false, true, N);
-                            const uint32_t to = tm + TM_O + (QT == 2 ? j : p) * 128, from = tm + TM_S + buf * KT + half * 32;
-                            const uint64_t db = desc(aR + sp * one_stage, nb > 1 ? BOX_BYTES : 0, 1024, SW128) + half * 4 * (2048 >> 4);
+                            const uint32_t id = idesc(H::type, false, true, N), to = tmem + TM_O + (QT == 2 ? j : p) * 128;
+                            const uint32_t from = tmem + TM_S + buf * KT + half * 32;
+                            const uint32_t db = desc_lo(aR + sp * one_stage + half * 4 * 2048, nb > 1 ? BOX_BYTES : 0);
 #pragma unroll
                             for (int k = 0; k < 4; ++k) mma_ts(to, from + k * 8, db + k * (2048 >> 4), id, i % FOLD + half + k > 0);
                             if (++sp == stages) sp = k_stages;
                         }
                     }
-                    if (ok) commit(&st.o_done[buf]);
+                    if (!ok) break;
+                    if (QT == 2 && more) {
+                        scores(j);
+                        if (i + 2 == n) tc::commit(&st.q_free);
+                    } else {
+                        pass();
+                        tc::commit(&st.o_done[buf]);
+                    }
+                    for (int p = 0; p < pairs; ++p) {
+                        tc::commit(&st.empty[vs]);
+                        if (++vs == stages) vs = k_stages, ++v_round;
+                    }
                 }
-                for (int p = 0; p < pairs && ok; ++p) {
-                    commit(&st.empty[stage]);
-                    if (++stage == stages) stage = k_stages, ++round;
-                }
-            }
-        } while (ok && w.next());
-        if (!ok && lane == 0) st.stopped = 1, set_error(a.dev_err, GDN_DEVERR_TIMEOUT);
-        commit(&st.drain[1]);
-        mbar_wait(&st.drain[1], 0);
+                ++seg;
+            } while (ok && w.next());
+            // products in flight end before tensor memory is freed and the CTA leaves, whoever gave up
+            if (!ok) st.stopped = 1, set_error(a.dev_err, GDN_DEVERR_TIMEOUT);
+            tc::commit(&st.drain[j]);
+            mbar_wait(&st.drain[j], 0);
+        }
         __syncwarp();
-    } else if (warp < SM_WARPS && busy) {
+    }
+    if (warp == V_WARP) kp_empty_rows(a, a.B <= KEEP ? st.scan.seq : nullptr, lane, 32);
+    } else {
+    if constexpr (QT == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    if (busy) {
         // ------------------------------------------------------------ softmax
         const int g = warp >> 2, quad = warp & 3, r = quad * 32 + lane;
         const uint32_t lane_base = tmem + ((uint32_t)(quad * 32) << 16);
@@ -385,8 +465,12 @@ __global__ void __launch_bounds__(kpt::threads(QT), 1)
         const bool vec = reinterpret_cast<uintptr_t>(a.out) % 16 == 0;
         uint32_t n_t = 0, n_v = 0, seg = 0;
         bool ok = true;
-        const auto done = [&](uint32_t x) {  // tile x's product with V
-            const bool y = QT == 2 ? warp_wait(&st.o_done[g], x & 1) : warp_wait(&st.o_done[x & 1], (x >> 1) & 1);
+        // Tile x's product with V is done. (Of two tiles of rows: the next S, which is there, lay behind it, and
+        // only a segment's last product has a barrier of its own.)
+        const auto done = [&](uint32_t x, bool end) {
+            bool y = true;
+            if (QT == 1) y = warp_wait(&st.o_done[x & 1], (x >> 1) & 1);
+            else if (end) y = warp_wait(&st.o_done[g], seg & 1);
             tc::fence_after();
             return y;
         };
@@ -398,6 +482,7 @@ __global__ void __launch_bounds__(kpt::threads(QT), 1)
             const int mixed = first_mixed();
             float* part = a.part + ((int64_t)blockIdx.x * 2 + w.later()) * kp_part_floats(PLACES, a.d) + g * TILE + r;
             float m = -INFINITY, nref = 0.f, l = 0.f, folded = -INFINITY;  // reference (unscaled), lift - c m, sum; m of the fold
+            bool big = false;
             ok = ok && warp_wait(&st.seg_open[side], (seg >> 1) & 1);
 #pragma unroll 1
             for (int i = 0; i < n && ok; ++i, ++n_t) {
@@ -416,68 +501,38 @@ __global__ void __launch_bounds__(kpt::threads(QT), 1)
 #pragma unroll
                     for (int y = 0; y < KT; ++y) s[y] = -s[y];
                 }
-                const int lim = last - t * KT;
-                if (__any_sync(FULL_MASK, lim < KT - 1)) {
+                if (t >= mixed) {
+                    const int lim = last - t * KT;
 #pragma unroll
                     for (int y = 0; y < KT; ++y)
                         if (y > lim) s[y] = -INFINITY;
                 }
-                float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                for (int y = 0; y < KT; y += 8)
-#pragma unroll
-                    for (int z = 0; z < 4; ++z) top[z] = max3(top[z], s[y + 2 * z], s[y + 2 * z + 1]);
-                const float mx = max3(max3(top[0], top[1], top[2]), top[3], top[3]);
                 if (i > 0 && i % FOLD == 0) {  // the sum in tensor memory joins the folds; this tile's product begins a new one
-                    ok = ok && done(n_t - 1);
+                    ok = done(n_t - 1, false);
                     const float f = folded == -INFINITY ? 1.f : kv_ex2((folded - m) * c2);
 #pragma unroll 1
                     for (int e = 0; e < a.d; e += 8) {
-                        float o[8];
+                        float o[8], old[8];
+#pragma unroll
+                        for (int y = 0; y < 8; ++y) old[y] = i > FOLD ? part[(e + y) * PLACES] : 0.f;
                         tc::tmem_ld<8>(tm_o + e, o);
 #pragma unroll
-                        for (int y = 0; y < 8; ++y) {
-                            float* at = part + (int64_t)(e + y) * PLACES;
-                            *at = i > FOLD ? fmaf(*at, f, o[y]) : o[y];
-                        }
+                        for (int y = 0; y < 8; ++y) part[(e + y) * PLACES] = fmaf(old[y], f, o[y]);
                     }
                     folded = m;
-                    tc::fence_before();
-                }
-                // a new reference where the maximum has left the old one behind (not for places without a row: what they
-                // hold is anything)
-                const bool need = live && mx > m && (m == -INFINITY || fmaf(mx, c2, nref) > kvt::REF_SLACK + H::lift);
-                if (__any_sync(FULL_MASK, need)) {
-                    float f = 1.f;
-                    if (need) {
-                        f = m == -INFINITY ? 1.f : kv_ex2((m - mx) * c2);
-                        m = mx, nref = fmaf(-m, c2, H::lift), l *= f;
-                    }
-                    if (i % FOLD != 0) {
-                        ok = ok && done(n_t - 1);
-#pragma unroll 1
-                        for (int e = 0; e < a.d; e += 8) {
-                            float o[8];
-                            tc::tmem_ld<8>(tm_o + e, o);
-#pragma unroll
-                            for (int y = 0; y < 8; ++y) o[y] *= f;
-                            tc::tmem_st<8>(tm_o + e, o);
-                        }
-                    }
                 }
                 // Exponents c s - m are fused, one rounding: exact enough while a product's own rounding is under one.
-                float from = nref;
-                if (__any_sync(FULL_MASK, fabsf(nref) > kvt::FUSED_MOST && m > -INFINITY)) {
+                // Where a reference is larger, the rest of the segment takes it off the scores first.
+                if (big) {
                     const float base = m == -INFINITY ? 0.f : m;
 #pragma unroll
                     for (int y = 0; y < KT; ++y) s[y] -= base;
-                    from = H::lift;
                 }
                 // weights: FP32 sums, rounded once to the cache's type for the product with the values
-                const Two cc = two(c2, c2), nn = two(from, from);
-                Two sum[2] = {0, 0};
-#pragma unroll
-                for (int h = 0; h < 4; ++h) {
+                Two sum[2];
+                const auto weights = [&](int h) {  // of 32 keys
+                    const float from = big ? H::lift : nref;
+                    const Two cc = two(c2, c2), nn = two(from, from);
                     uint32_t u[16];
 #pragma unroll
                     for (int y = 0; y < 32; y += 2) {
@@ -487,75 +542,131 @@ __global__ void __launch_bounds__(kpt::threads(QT), 1)
                         u[y / 2] = H::pack(p0, p1);
                     }
                     st16(tm_s + h * 16, u);
-                    if (h & 1) {
-                        if (h == 3 && t >= mixed) {
-                            // this thread's row of V, a key: the boxes are shared out over the groups
-                            ok = ok && warp_wait(&st.v_ok, n_v & 1);
-                            ++n_v;
-                            const bool dead = t * KT + r >= w.s.len;
-                            for (int b = g; b < boxes && ok; b += QT) {
-                                int stage = st.v_stage + (b >> 1);
-                                if (stage >= stages) stage -= v_stages;
-                                uint4* row = reinterpret_cast<uint4*>(ring + stage * one_stage + (b & 1) * BOX_BYTES + r * 128);
+                };
+                sum[0] = sum[1] = 0;
+                weights(0), weights(1);
+                float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                                for (int y = 0; y < 8; ++y) {
-                                    const int c = y ^ (lane & 7);  // (an order without bank conflicts)
-                                    if (dead) row[c] = make_uint4(0, 0, 0, 0);
-                                    else if (kvt::has_odd<ST>(row[c])) row[c] = kvt::clear_odd<ST>(row[c]), st.odd[side] = 1;
-                                }
-                            }
-                            __threadfence_block();
-                            tc::fence_async_smem();
-                            __syncwarp();
-                            if (lane == 0) mbar_arrive(&st.v_clean);
+                for (int y = 0; y < KT; y += 8)
+#pragma unroll
+                    for (int z = 0; z < 4; ++z) top[z] = max3(top[z], s[y + 2 * z], s[y + 2 * z + 1]);
+                const float mx = max3(max3(top[0], top[1], top[2]), top[3], top[3]);
+                // a new reference where the maximum has left the old one behind (not for places without a row: what they
+                // hold is anything)
+                const bool need = live && mx > (big ? 0.f : m) &&
+                                  (m == -INFINITY || fmaf(mx, c2, big ? H::lift : nref) > kvt::REF_SLACK + H::lift);
+                if (__any_sync(FULL_MASK, need)) {
+                    float f = 1.f;
+                    if (need) {
+                        const float to = big && m != -INFINITY ? m + mx : mx;
+                        f = m == -INFINITY ? 1.f : kv_ex2((big ? -mx : m - mx) * c2);
+                        m = to, nref = fmaf(-m, c2, H::lift), l *= f;
+                        if (big) {
+#pragma unroll
+                            for (int y = 0; y < KT; ++y) s[y] -= mx;
                         }
-                        st_wait();
-                        tc::fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&st.p_full[buf][h >> 1]);
                     }
+                    if (!big && __any_sync(FULL_MASK, fabsf(nref) > kvt::FUSED_MOST && m > -INFINITY)) {
+                        big = true;
+                        const float base = m == -INFINITY ? 0.f : m;
+#pragma unroll
+                        for (int y = 0; y < KT; ++y) s[y] -= base;
+                    }
+                    if (i % FOLD != 0) {
+                        ok = ok && done(n_t - 1, false);
+#pragma unroll 1
+                        for (int e = 0; e < a.d; e += 8) {
+                            float o[8];
+                            tc::tmem_ld<8>(tm_o + e, o);
+#pragma unroll
+                            for (int y = 0; y < 8; ++y) o[y] *= f;
+                            tc::tmem_st<8>(tm_o + e, o);
+                        }
+                    }
+                    sum[0] = sum[1] = 0;
+                    weights(0), weights(1);
                 }
+                if (t >= mixed) {
+                    // this thread's row of V, a key: the boxes are shared out over the groups
+                    ok = ok && warp_wait(&st.v_ok, n_v & 1);
+                    ++n_v;
+                    const bool dead = t * KT + r >= w.s.len;
+                    for (int b = g; b < boxes && ok; b += QT) {
+                        int stage = st.v_stage + (b >> 1);
+                        if (stage >= stages) stage -= v_stages;
+                        uint4* row = reinterpret_cast<uint4*>(ring + stage * one_stage + (b & 1) * BOX_BYTES + r * 128);
+#pragma unroll
+                        for (int y = 0; y < 8; ++y) {
+                            const int c = y ^ (lane & 7);  // (an order without bank conflicts)
+                            if (dead) row[c] = make_uint4(0, 0, 0, 0);
+                            else if (kvt::has_odd<ST>(row[c])) row[c] = kvt::clear_odd<ST>(row[c]), st.odd[side] = 1;
+                        }
+                    }
+                    __threadfence_block();
+                    tc::fence_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&st.v_clean);
+                }
+                const auto publish = [&](int half) {
+                    st_wait();
+                    tc::fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&st.p_full[buf][half]);
+                };
+                publish(0);
+                weights(2), weights(3);
+                publish(1);
                 const float2 all = parts(add2(sum[0], sum[1]));
                 l += all.x + all.y;
             }
             if (!ok) break;
             // ------------------------------------------------------------ outputs
-            ok = done(n_t - 1) && warp_wait(&st.seg_loaded[side], (seg >> 1) & 1);
+            ok = done(n_t - 1, true) && warp_wait(&st.seg_loaded[side], (seg >> 1) & 1);
             if (!ok) break;
             const bool bad = st.bad[side], odd = st.odd[side], whole = w.whole(), fold = n > FOLD;
             const int32_t* table = a.page_table + (int64_t)w.s.slot * a.max_pages;
             const float back = folded == -INFINITY ? 1.f : kv_ex2((folded - m) * c2);
             const float inv = bad || l == 0.f ? 0.f : 1.f / l;
             const int64_t to = (int64_t)(w.s.first + tok) * a.Hq + w.h * a.G + (x - tok * a.G);
+            int64_t to4[4];  // where the rows of this lane's group of four go (-1: nowhere)
+#pragma unroll
+            for (int y = 0; y < 4; ++y) to4[y] = __shfl_sync(FULL_MASK, live ? to : -1, (lane & ~3) + y);
 #pragma unroll 1
             for (int e = 0; e < a.d; e += 32) {
                 float o[32];
-                __syncwarp();
-                tc::tmem_ld<32>(tm_o + e, o);
                 const int cols = min(32, a.d - e);
                 if (fold) {
+                    float old[32];
 #pragma unroll
-                    for (int y = 0; y < 32; ++y)
-                        if (y < cols) o[y] = fmaf(part[(int64_t)(e + y) * PLACES], back, o[y]);
+                    for (int y = 0; y < 32; ++y) old[y] = y < cols ? part[(e + y) * PLACES] : 0.f;
+                    tc::tmem_ld<32>(tm_o + e, o);
+#pragma unroll
+                    for (int y = 0; y < 32; ++y) o[y] = fmaf(old[y], back, o[y]);
+                } else {
+                    tc::tmem_ld<32>(tm_o + e, o);
                 }
-                if (!live) continue;
-                if (odd && !bad) add_odd<ST>(a, table, w.h, max(mixed, w.t0) * KT, min(last, w.t1 * KT - 1), e, o);
                 if (!whole) {
 #pragma unroll
                     for (int y = 0; y < 32; ++y)
-                        if (y < cols) part[(int64_t)(e + y) * PLACES] = bad ? 0.f : o[y];
+                        if (y < cols) part[(e + y) * PLACES] = bad ? 0.f : o[y];
                     continue;
                 }
-                ST* out = static_cast<ST*>(a.out) + to * a.d + e;
 #pragma unroll
-                for (int y = 0; y < 32; y += 8) {
-                    if (y >= cols) break;
-                    float z[8];
+                for (int y = 0; y < 32; ++y) o[y] = inv == 0.f ? 0.f : o[y] * inv;
+                if (vec) {
+                    uint4 z[4];
 #pragma unroll
-                    for (int q = 0; q < 8; ++q) z[q] = inv == 0.f ? 0.f : o[y + q] * inv;
-                    if (vec) *reinterpret_cast<uint4*>(out + y) = Store<ST>::pack(z);
-                    else
-                        for (int q = 0; q < 8; ++q) out[y + q] = H::round(z[q]);
+                    for (int y = 0; y < 4; ++y) z[y] = Store<ST>::pack(o + 8 * y);
+                    turn4(z, lane);
+                    const int at = e + (lane & 3) * 8;
+#pragma unroll
+                    for (int y = 0; y < 4; ++y)
+                        if (to4[y] >= 0 && at < a.d)
+                            *reinterpret_cast<uint4*>(static_cast<ST*>(a.out) + to4[y] * a.d + at) = z[y];
+                } else if (live) {
+#pragma unroll
+                    for (int y = 0; y < 32; ++y)
+                        if (y < cols) static_cast<ST*>(a.out)[to * a.d + e + y] = H::round(o[y]);
                 }
             }
             tc::fence_before();
@@ -567,6 +678,12 @@ __global__ void __launch_bounds__(kpt::threads(QT), 1)
                     a.lse[to] = bad || l == 0.f ? -INFINITY : (log2f(l) - nref) * LN2;
                 }
             }
+            if (odd && !bad) {
+                __syncwarp();  // (the row's outputs are other lanes' stores)
+                const int from = max(mixed, w.t0) * KT, end = min(last, w.t1 * KT - 1);
+                if (live && whole) add_odd<ST>(a, table, w.h, from, end, static_cast<ST*>(a.out) + to * a.d, 1, Store<ST>::code);
+                else if (live) add_odd<ST>(a, table, w.h, from, end, part, PLACES, GDN_F32);
+            }
             if (tid == 0 && w.t0 == 0 && !whole) kp_border(a, st.scan, w);
             __syncwarp();
             if (lane == 0) mbar_arrive(&st.seg_free[side]);
@@ -574,11 +691,11 @@ __global__ void __launch_bounds__(kpt::threads(QT), 1)
         } while (w.next());
         if (!ok && lane == 0) st.stopped = 1, set_error(a.dev_err, GDN_DEVERR_TIMEOUT);
     }
-    if (warp == S_WARP) kp_empty_rows(a, a.B <= KEEP ? st.scan.seq : nullptr, lane, 32);
+    }
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
-    if (warp == O_WARP)
+    if (warp == M_WARP)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(TM_COLS) : "memory");
     if (st.stopped) refuse_range<QT>(a, st);
 }

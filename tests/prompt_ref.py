@@ -70,10 +70,10 @@ def prompt_attention(k, v, table, lengths, slots, cu, q, scale):
 
 class Prompt:
     """A cache and packed prompts [(rows, entries before them)]. Entries past a length, pages that nobody holds and
-    rows of no sequence are NaN. written: the prompts' own entries are in the cache already."""
+    rows of no sequence are NaN. written: the prompts' own entries are in the cache already; blank: no entry's key and value is."""
 
     def __init__(self, seed, dtype, prompts, Hq, Hkv, d, page, kind="heads", pad=(), gap=0, spread=1.0, written=True,
-                 q_kind="plain"):
+                 q_kind="plain", blank=False):
         from hybrid_ssm_gated_gb300 import kv
 
         self.kv, r = kv, np.random.default_rng(seed)
@@ -101,7 +101,7 @@ class Prompt:
         dt = TORCH[dtype]
         k0, v0 = (torch.full((num_pages, Hkv, page, d), float("nan"), dtype=dt) for _ in range(2))
         for b in range(B):
-            if self.slots[b] >= 0:
+            if self.slots[b] >= 0 and not blank:
                 L = lens[b] if written else prompts[b][1]
                 for pool, s in ((k0, spread), (v0, 1.0)):
                     x = torch.from_numpy(r.normal(size=(L, Hkv, d)) * s).to(dt)
