@@ -53,7 +53,13 @@ using kvt::KT;
 constexpr int TILE = 128;  // rows of a tile
 constexpr int KEEP = 32;   // sequences that the scan keeps
 constexpr int MAX_STAGES = 12;
-constexpr int FOLD = 32;   // tiles of one sum in tensor memory
+constexpr float MOST = 32768.f;  // sum of the weights of half a tile, at most (each then fits fp16)
+// Tiles of one sum in tensor memory: what its products' cut-off costs (2^-21 of the sum a product of 16 keys at most)
+// stays under half of half a unit of the outputs' type.
+template <typename ST>
+__host__ __device__ constexpr int fold_of() { return sizeof(ST) == 2 ? 32 : 0; }
+template <>
+__host__ __device__ constexpr int fold_of<__nv_bfloat16>() { return 128; }
 __host__ __device__ constexpr int threads(int QT) { return (4 * QT + 4) * 32; }
 
 struct Maps {
@@ -190,6 +196,7 @@ __global__ void __launch_bounds__(kpt::threads(QT), 1)
     using kvt::idesc, kvt::warp_wait, kvt::tma_load;
     using kvt::Two, kvt::two, kvt::fma2, kvt::add2, kvt::parts, kvt::max3;
     using H = kvt::Half16<ST>;
+    constexpr int FOLD = fold_of<ST>();
     constexpr int NT = threads(QT), SM_WARPS = 4 * QT, PLACES = QT * TILE;
     constexpr int K_WARP = SM_WARPS, V_WARP = SM_WARPS + 1, M_WARP = SM_WARPS + 2;
     constexpr uint32_t TM_S = 0, TM_O = 256, TM_COLS = 512;
@@ -241,10 +248,10 @@ __global__ void __launch_bounds__(kpt::threads(QT), 1)
     // the first tile of the unit that some row sees a part of only
     const auto first_mixed = [&]() { return (w.s.len - w.s.n + w.r0() / a.G + 1) / KT; };
 
-    // (of two tiles' kernel) registers to the threads that hold a row of scores: 256 x 208 + 128 x 88 of the launch's
+    // (of two tiles' kernel) registers to the threads that hold a row of scores: 256 x 216 + 128 x 72 of the launch's
     // 384 x 168
     if (warp >= SM_WARPS) {
-    if constexpr (QT == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    if constexpr (QT == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     if ((warp == K_WARP || warp == V_WARP) && busy) {
         // ------------------------------------------------------------ loads
         const bool keys = warp == K_WARP;
@@ -453,7 +460,7 @@ __global__ void __launch_bounds__(kpt::threads(QT), 1)
     }
     if (warp == V_WARP) kp_empty_rows(a, a.B <= KEEP ? st.scan.seq : nullptr, lane, 32);
     } else {
-    if constexpr (QT == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    if constexpr (QT == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
     if (busy) {
         // ------------------------------------------------------------ softmax
         const int g = warp >> 2, quad = warp & 3, r = quad * 32 + lane;
@@ -482,7 +489,7 @@ __global__ void __launch_bounds__(kpt::threads(QT), 1)
             const int mixed = first_mixed();
             float* part = a.part + ((int64_t)blockIdx.x * 2 + w.later()) * kp_part_floats(PLACES, a.d) + g * TILE + r;
             float m = -INFINITY, nref = 0.f, l = 0.f, folded = -INFINITY;  // reference (unscaled), lift - c m, sum; m of the fold
-            bool big = false;
+            bool big = false, taken = false;
             ok = ok && warp_wait(&st.seg_open[side], (seg >> 1) & 1);
 #pragma unroll 1
             for (int i = 0; i < n && ok; ++i, ++n_t) {
@@ -521,17 +528,18 @@ __global__ void __launch_bounds__(kpt::threads(QT), 1)
                     }
                     folded = m;
                 }
-                // Exponents c s - m are fused, one rounding: exact enough while a product's own rounding is under one.
-                // Where a reference is larger, the rest of the segment takes it off the scores first.
+                // Exponents c s - m are fused, one rounding: exact enough while a product's own rounding is under one. A
+                // row whose reference became larger takes it off the scores first (`taken`; big: some row of the warp).
+                float from = nref;
                 if (big) {
-                    const float base = m == -INFINITY ? 0.f : m;
+                    const float base = taken ? m : 0.f;
+                    if (taken) from = H::lift;
 #pragma unroll
                     for (int y = 0; y < KT; ++y) s[y] -= base;
                 }
                 // weights: FP32 sums, rounded once to the cache's type for the product with the values
                 Two sum[2];
                 const auto weights = [&](int h) {  // of 32 keys
-                    const float from = big ? H::lift : nref;
                     const Two cc = two(c2, c2), nn = two(from, from);
                     uint32_t u[16];
 #pragma unroll
@@ -545,32 +553,33 @@ __global__ void __launch_bounds__(kpt::threads(QT), 1)
                 };
                 sum[0] = sum[1] = 0;
                 weights(0), weights(1);
+                // A new reference where the maximum has left the old one behind (not for places without a row: what they
+                // hold is anything). No weight is larger than their sum: the first half's largest need not be looked for.
                 float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                for (int y = 0; y < KT; y += 8)
+                for (int y = KT / 2; y < KT; y += 8)
 #pragma unroll
                     for (int z = 0; z < 4; ++z) top[z] = max3(top[z], s[y + 2 * z], s[y + 2 * z + 1]);
-                const float mx = max3(max3(top[0], top[1], top[2]), top[3], top[3]);
-                // a new reference where the maximum has left the old one behind (not for places without a row: what they
-                // hold is anything)
-                const bool need = live && mx > (big ? 0.f : m) &&
-                                  (m == -INFINITY || fmaf(mx, c2, big ? H::lift : nref) > kvt::REF_SLACK + H::lift);
+                const float upper = max3(max3(top[0], top[1], top[2]), top[3], top[3]);
+                const float2 half = parts(add2(sum[0], sum[1]));
+                const bool need = live && (m == -INFINITY || half.x + half.y > MOST ||
+                                           fmaf(upper, c2, from) > kvt::REF_SLACK + H::lift);
                 if (__any_sync(FULL_MASK, need)) {
-                    float f = 1.f;
-                    if (need) {
-                        const float to = big && m != -INFINITY ? m + mx : mx;
-                        f = m == -INFINITY ? 1.f : kv_ex2((big ? -mx : m - mx) * c2);
-                        m = to, nref = fmaf(-m, c2, H::lift), l *= f;
-                        if (big) {
+                    float f = 1.f, mx = upper;
 #pragma unroll
-                            for (int y = 0; y < KT; ++y) s[y] -= mx;
-                        }
+                    for (int y = 0; y < KT / 2; y += 2) mx = max3(mx, s[y], s[y + 1]);
+                    float shift = 0.f;
+                    if (need && mx > (taken ? 0.f : m)) {  // (a row's result depends on no other row)
+                        f = m == -INFINITY ? 1.f : kv_ex2((taken ? -mx : m - mx) * c2);
+                        m = taken ? m + mx : mx, nref = fmaf(-m, c2, H::lift), l *= f;
+                        if (taken) shift = mx;
                     }
-                    if (!big && __any_sync(FULL_MASK, fabsf(nref) > kvt::FUSED_MOST && m > -INFINITY)) {
+                    if (!taken && fabsf(nref) > kvt::FUSED_MOST) taken = true, shift = m;
+                    from = taken ? H::lift : nref;
+                    if (__any_sync(FULL_MASK, taken)) {
                         big = true;
-                        const float base = m == -INFINITY ? 0.f : m;
 #pragma unroll
-                        for (int y = 0; y < KT; ++y) s[y] -= base;
+                        for (int y = 0; y < KT; ++y) s[y] -= shift;
                     }
                     if (i % FOLD != 0) {
                         ok = ok && done(n_t - 1, false);
@@ -630,20 +639,23 @@ __global__ void __launch_bounds__(kpt::threads(QT), 1)
             const int64_t to = (int64_t)(w.s.first + tok) * a.Hq + w.h * a.G + (x - tok * a.G);
             int64_t to4[4];  // where the rows of this lane's group of four go (-1: nowhere)
 #pragma unroll
-            for (int y = 0; y < 4; ++y) to4[y] = __shfl_sync(FULL_MASK, live ? to : -1, (lane & ~3) + y);
+            for (int y = 0; y < 4; ++y) to4[y] = __shfl_sync(FULL_MASK, live ? to * a.d : -1, (lane & ~3) + y);
+            const bool none = inv == 0.f, some_none = __any_sync(FULL_MASK, none);
+            float old[32];
+            const auto folds = [&](int e) {  // of 32 outputs
+#pragma unroll
+                for (int y = 0; y < 32; ++y) old[y] = e + y < a.d ? part[(e + y) * PLACES] : 0.f;
+            };
+            if (fold) folds(0);
 #pragma unroll 1
             for (int e = 0; e < a.d; e += 32) {
                 float o[32];
                 const int cols = min(32, a.d - e);
+                tc::tmem_ld<32>(tm_o + e, o);
                 if (fold) {
-                    float old[32];
-#pragma unroll
-                    for (int y = 0; y < 32; ++y) old[y] = y < cols ? part[(e + y) * PLACES] : 0.f;
-                    tc::tmem_ld<32>(tm_o + e, o);
 #pragma unroll
                     for (int y = 0; y < 32; ++y) o[y] = fmaf(old[y], back, o[y]);
-                } else {
-                    tc::tmem_ld<32>(tm_o + e, o);
+                    if (e + 32 < a.d) folds(e + 32);
                 }
                 if (!whole) {
 #pragma unroll
@@ -652,17 +664,22 @@ __global__ void __launch_bounds__(kpt::threads(QT), 1)
                     continue;
                 }
 #pragma unroll
-                for (int y = 0; y < 32; ++y) o[y] = inv == 0.f ? 0.f : o[y] * inv;
+                for (int y = 0; y < 32; ++y) o[y] *= inv;
+                if (some_none) {
+#pragma unroll
+                    for (int y = 0; y < 32; ++y) o[y] = none ? 0.f : o[y];
+                }
                 if (vec) {
                     uint4 z[4];
 #pragma unroll
                     for (int y = 0; y < 4; ++y) z[y] = Store<ST>::pack(o + 8 * y);
                     turn4(z, lane);
                     const int at = e + (lane & 3) * 8;
+                    if (at < a.d) {
 #pragma unroll
-                    for (int y = 0; y < 4; ++y)
-                        if (to4[y] >= 0 && at < a.d)
-                            *reinterpret_cast<uint4*>(static_cast<ST*>(a.out) + to4[y] * a.d + at) = z[y];
+                        for (int y = 0; y < 4; ++y)
+                            if (to4[y] >= 0) *reinterpret_cast<uint4*>(static_cast<ST*>(a.out) + to4[y] + at) = z[y];
+                    }
                 } else if (live) {
 #pragma unroll
                     for (int y = 0; y < 32; ++y)
