@@ -11,7 +11,7 @@ namespace {
 template <typename ST, int QT>
 cudaError_t launch(const KvArgs& a, const kpt::Maps& maps, int boxes, int box_rows, const DeviceInfo& di, cudaStream_t stream) {
     auto kern = kv_prompt_tc_kernel<ST, QT>;
-    int stages = (di.smem_optin - kpt::smem_bytes<QT>(boxes, 0)) / kpt::stage_bytes(boxes);
+    int stages = (di.smem_optin - kpt::smem_bytes<QT>(boxes, 0)) / kpt::stage_bytes<QT>(boxes);
     if (stages > kpt::MAX_STAGES) stages = kpt::MAX_STAGES;
     // V waits for the weights: it gets the odd stage
     const int k_stages = stages / 2, v_stages = stages - k_stages, smem = kpt::smem_bytes<QT>(boxes, stages);
@@ -46,18 +46,18 @@ cudaError_t kv_prompt_tc_workspace(KvArgs& a, int64_t& bytes) {
 }
 
 cudaError_t launch_kv_prompt_tc(KvArgs& a, cudaStream_t stream) {
-    const int boxes = boxes_of(a.d), box_rows = box_rows_of(a.page_size), tokens = kpt::TILE / a.G;
+    const int boxes = boxes_of(a.d), tokens = kpt::TILE / a.G;
     if (a.total == 0) return cudaErrorNotSupported;  // (no row to describe)
+    DeviceInfo di;
+    cudaError_t e = device_info(di);
+    if (e != cudaSuccess) return e;
+    const int QT = tiles_of(a, di.sms), keys = kpt::keys_of(QT), most = box_rows_of(a.page_size), box_rows = most < keys ? most : keys;
     kpt::Maps maps{};
     if (!encoder() ||
         !encode(maps.k, a.dtype, a.k.p, a.d, a.page_size, a.k.token, a.Hkv, a.k.head, a.num_pages, a.k.page, box_rows) ||
         !encode(maps.v, a.dtype, a.v.p, a.d, a.page_size, a.v.token, a.Hkv, a.v.head, a.num_pages, a.v.page, box_rows) ||
         !encode(maps.q, a.dtype, a.q.p, a.d, a.Hq, a.q.head, a.total, a.q.node, 1, a.d, a.G, tokens))
         return cudaErrorNotSupported;
-    DeviceInfo di;
-    cudaError_t e = device_info(di);
-    if (e != cudaSuccess) return e;
-    const int QT = tiles_of(a, di.sms);
     a.tile_rows = tokens * a.G, a.tile_places = kpt::TILE, a.row_block = QT * a.tile_rows, a.part_rows = QT * kpt::TILE;
     a.border = reinterpret_cast<char*>(a.part) + kp_part_bytes(di.sms, a.part_rows, a.d);
     if (a.dtype == GDN_BF16)

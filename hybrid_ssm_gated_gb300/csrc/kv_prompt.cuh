@@ -50,7 +50,7 @@ __device__ __forceinline__ KpSeq kp_seq(const KvArgs& a, int b) {
 }
 
 constexpr int KP_EXTRA = 256;  // keys that a unit's start and end cost as much as
-constexpr int KP_LEAST = 512;  // keys of a CTA's range at least
+constexpr int KP_LEAST = 256;  // keys of a CTA's range at least
 
 // Blocks of a sequence, and the length of the line before block i of a key head.
 __device__ __forceinline__ int kp_blocks(const KvArgs& a, const KpSeq& s) {
@@ -104,9 +104,9 @@ __device__ __forceinline__ void kp_locate(const KvArgs& a, KpScan<NT, KEEP>& sc)
         if (w < warp) before += sc.warp_sum[w];
         total += sc.warp_sum[w];
     }
-    const long long most = total / ((long long)KP_LEAST * a.G);
+    const long long most = kv_div(total, (long long)KP_LEAST * a.G);
     const int parts = (int)(most < 1 ? 1 : most < gridDim.x ? most : gridDim.x);
-    const long long q = total / parts;
+    const long long q = kv_div(total, parts);
     const int r = (int)(total - q * parts), c = blockIdx.x;
     if (tid == 0) sc.q = q, sc.r = r, sc.parts = parts;
     for (int side = 0; side < 2; ++side) {
@@ -154,7 +154,7 @@ struct KpWalk {
         const KpSeq x = get(m.b);
         const int nb = kp_blocks(a, x);
         const long long one = kp_before(a, x, nb);
-        p.h = (int)(m.off / one);
+        p.h = (int)kv_div(m.off, one);
         const long long off = m.off - one * p.h;
         int lo = 0, hi = nb;  // the block that holds `off`
         while (hi - lo > 1) {
@@ -168,8 +168,10 @@ struct KpWalk {
     }
     // Tile that a point `off` of a unit is cut ahead of.
     __device__ __forceinline__ int tile_at(long long off, int n) const {
-        const long long t = (off - (long long)KP_EXTRA * a.G) / ((long long)KT * a.G);
-        return (int)(t < 0 ? 0 : t < n ? t : n - 1);  // (the last tile's CTA is the one that ends the unit)
+        const long long in = off - (long long)KP_EXTRA * a.G;
+        if (in < 0) return 0;
+        const long long t = kv_div(in, (long long)KT * a.G);
+        return (int)(t < n ? t : n - 1);  // (the last tile's CTA is the one that ends the unit)
     }
     __device__ __forceinline__ bool before_end() const {
         return b < end.b || (b == end.b && (h < end.h || (h == end.h && i <= end.i)));

@@ -2,7 +2,7 @@
 // tcgen05 tensor cores (16-bit caches whose pages hold a multiple of 8 entries and
 // whose rows the TMA engine can address; up to 128 query heads a key head).
 //
-// Mathematics. One pass over tiles of 128 keys for tiles of 128 query rows: S = Q K^T
+// Mathematics. One pass over tiles of 128 (QT = 1: 64) keys for tiles of 128 query rows: S = Q K^T
 // (128 x 128), P = 2^{c S - m} with a reference m a row, O += P V (128 x d). A thread
 // owns a row: its 128 scores of a tile come from tensor memory into its registers, and
 // maximum, sum and weights need no other thread. The weights go back to tensor memory,
@@ -19,7 +19,7 @@
 //     other one. Tensor memory: two S (P over them), two O.
 //   QT = 1 (d above 128, and calls with few units): one tile, two buffers of S in turn.
 //   softmax    four warps a tile of rows, thread = row = tensor-memory lane;
-//   K, V       a warp each: tiles by TMA into a ring of stages of 128 keys x 128
+//   K, V       a warp each: tiles by TMA into a ring of stages of a tile's keys x 128
 //              elements, boxes of as many keys as a page and the tile share;
 //              the V warp loads a unit's queries too, once the last one's products have
 //              read theirs (whole tokens: a tile of rows holds as many as have their G
@@ -48,18 +48,20 @@ namespace gdn {
 namespace kpt {
 
 using kvt::BOX;
-using kvt::BOX_BYTES;
-using kvt::KT;
 constexpr int TILE = 128;  // rows of a tile
+// Keys of a tile: at d = 256 a tile of 128 of keys and one of values leave room for no second one beside the queries, and
+// the next keys' way from L2 was the kernel's period (4700 cycles a tile); 64 leave two. (N = 64 costs a product of S 48
+// cycles instead of 32.)
+__host__ __device__ constexpr int keys_of(int QT) { return QT == 2 ? 128 : 64; }
 constexpr int KEEP = 32;   // sequences that the scan keeps
 constexpr int MAX_STAGES = 12;
 constexpr float MOST = 32768.f;  // sum of the weights of half a tile, at most (each then fits fp16)
-// Tiles of one sum in tensor memory: what its products' cut-off costs (2^-21 of the sum a product of 16 keys at most)
+// Entries of one sum in tensor memory: what its products' cut-off costs (2^-21 of the sum a product of 16 keys at most)
 // stays under half of half a unit of the outputs' type.
 template <typename ST>
-__host__ __device__ constexpr int fold_of() { return sizeof(ST) == 2 ? 32 : 0; }
+__host__ __device__ constexpr int fold_keys() { return 4096; }
 template <>
-__host__ __device__ constexpr int fold_of<__nv_bfloat16>() { return 128; }
+__host__ __device__ constexpr int fold_keys<__nv_bfloat16>() { return 16384; }
 __host__ __device__ constexpr int threads(int QT) { return (4 * QT + 4) * 32; }
 
 struct Maps {
@@ -80,10 +82,11 @@ struct __align__(16) State {
 #endif
 };
 
-__host__ __device__ constexpr int stage_bytes(int boxes) { return (boxes > 1 ? 2 : 1) * BOX_BYTES; }
+template <int QT>
+__host__ __device__ constexpr int stage_bytes(int boxes) { return (boxes > 1 ? 2 : 1) * keys_of(QT) * BOX * 2; }
 template <int QT>
 __host__ __device__ constexpr int smem_bytes(int boxes, int stages) {
-    return 1024 + QT * boxes * TILE * 128 + stages * stage_bytes(boxes) + (int)sizeof(State<QT>);
+    return 1024 + QT * boxes * TILE * 128 + stages * stage_bytes<QT>(boxes) + (int)sizeof(State<QT>);
 }
 
 // Operand descriptors of the 128-byte swizzle, 1024 bytes between groups of eight rows: the upper word is the same for
@@ -164,7 +167,7 @@ __device__ __forceinline__ void turn4(uint4 (&x)[4], int lane) {
 // What a CTA leaves whose waits ran out, by the whole block: the rows of its range as those of a refused sequence.
 template <int QT>
 __device__ __noinline__ void refuse_range(const KvArgs& a, const State<QT>& st) {
-    constexpr int NT = threads(QT), PLACES = QT * TILE;
+    constexpr int NT = threads(QT), PLACES = QT * TILE, KT = keys_of(QT);
     bool some;
     KpWalk<KT> w(a, st.scan, some);
     if (!some) return;
@@ -196,13 +199,13 @@ __global__ void __launch_bounds__(kpt::threads(QT), 1)
     using kvt::idesc, kvt::warp_wait, kvt::tma_load;
     using kvt::Two, kvt::two, kvt::fma2, kvt::add2, kvt::parts, kvt::max3;
     using H = kvt::Half16<ST>;
-    constexpr int FOLD = fold_of<ST>();
+    constexpr int KT = keys_of(QT), FOLD = fold_keys<ST>() / KT, BOX_BYTES = KT * BOX * 2, HALF = KT / 2;
     constexpr int NT = threads(QT), SM_WARPS = 4 * QT, PLACES = QT * TILE;
     constexpr int K_WARP = SM_WARPS, V_WARP = SM_WARPS + 1, M_WARP = SM_WARPS + 2;
     constexpr uint32_t TM_S = 0, TM_O = 256, TM_COLS = 512;
     extern __shared__ unsigned char smem_raw[];
     unsigned char* smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
-    const int pairs = (boxes + 1) >> 1, one_stage = stage_bytes(boxes), stages = k_stages + v_stages;
+    const int pairs = (boxes + 1) >> 1, one_stage = stage_bytes<QT>(boxes), stages = k_stages + v_stages;
     unsigned char* sQ = smem;
     unsigned char* ring = smem + QT * boxes * TILE * 128;
     State<QT>& st = *reinterpret_cast<State<QT>*>(ring + stages * one_stage);
@@ -429,10 +432,10 @@ __global__ void __launch_bounds__(kpt::threads(QT), 1)
                         for (int p = 0; p < pairs; ++p) {
                             const int nb = min(2, boxes - 2 * p), N = min(128, (a.d - p * 128 + 15) / 16 * 16);
                             const uint32_t id = idesc(H::type, false, true, N), to = tmem + TM_O + (QT == 2 ? j : p) * 128;
-                            const uint32_t from = tmem + TM_S + buf * KT + half * 32;
-                            const uint32_t db = desc_lo(aR + sp * one_stage + half * 4 * 2048, nb > 1 ? BOX_BYTES : 0);
+                            const uint32_t from = tmem + TM_S + buf * KT + half * (HALF / 2);
+                            const uint32_t db = desc_lo(aR + sp * one_stage + half * HALF * 128, nb > 1 ? BOX_BYTES : 0);
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) mma_ts(to, from + k * 8, db + k * (2048 >> 4), id, i % FOLD + half + k > 0);
+                            for (int k = 0; k < HALF / 16; ++k) mma_ts(to, from + k * 8, db + k * (2048 >> 4), id, i % FOLD + half + k > 0);
                             if (++sp == stages) sp = k_stages;
                         }
                     }
@@ -503,7 +506,7 @@ __global__ void __launch_bounds__(kpt::threads(QT), 1)
                 tc::fence_after();
                 float s[KT];
                 tc::tmem_ld<64>(tm_s, s);
-                tc::tmem_ld<64>(tm_s + 64, s + 64);
+                if constexpr (KT == 128) tc::tmem_ld<64>(tm_s + 64, s + 64);
                 if (flip) {
 #pragma unroll
                     for (int y = 0; y < KT; ++y) s[y] = -s[y];
@@ -551,13 +554,17 @@ __global__ void __launch_bounds__(kpt::threads(QT), 1)
                     }
                     st16(tm_s + h * 16, u);
                 };
+                const auto weights_of = [&](int half) {
+#pragma unroll
+                    for (int h = 0; h < HALF / 32; ++h) weights(half * (HALF / 32) + h);
+                };
                 sum[0] = sum[1] = 0;
-                weights(0), weights(1);
+                weights_of(0);
                 // A new reference where the maximum has left the old one behind (not for places without a row: what they
                 // hold is anything). No weight is larger than their sum: the first half's largest need not be looked for.
                 float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                for (int y = KT / 2; y < KT; y += 8)
+                for (int y = HALF; y < KT; y += 8)
 #pragma unroll
                     for (int z = 0; z < 4; ++z) top[z] = max3(top[z], s[y + 2 * z], s[y + 2 * z + 1]);
                 const float upper = max3(max3(top[0], top[1], top[2]), top[3], top[3]);
@@ -567,7 +574,7 @@ __global__ void __launch_bounds__(kpt::threads(QT), 1)
                 if (__any_sync(FULL_MASK, need)) {
                     float f = 1.f, mx = upper;
 #pragma unroll
-                    for (int y = 0; y < KT / 2; y += 2) mx = max3(mx, s[y], s[y + 1]);
+                    for (int y = 0; y < HALF; y += 2) mx = max3(mx, s[y], s[y + 1]);
                     float shift = 0.f;
                     if (need && mx > (taken ? 0.f : m)) {  // (a row's result depends on no other row)
                         f = m == -INFINITY ? 1.f : kv_ex2((taken ? -mx : m - mx) * c2);
@@ -593,22 +600,34 @@ __global__ void __launch_bounds__(kpt::threads(QT), 1)
                         }
                     }
                     sum[0] = sum[1] = 0;
-                    weights(0), weights(1);
+                    weights_of(0);
                 }
                 if (t >= mixed) {
-                    // this thread's row of V, a key: the boxes are shared out over the groups
+                    // rows of V, a key each: the boxes are shared out over the groups, four pieces of a row at a time
                     ok = ok && warp_wait(&st.v_ok, n_v & 1);
                     ++n_v;
-                    const bool dead = t * KT + r >= w.s.len;
-                    for (int b = g; b < boxes && ok; b += QT) {
+                    const int key = r % KT;
+                    const bool dead = t * KT + key >= w.s.len;
+#pragma unroll 1
+                    for (int b = ok ? g + r / KT : boxes; b < boxes; b += QT * (TILE / KT)) {
                         int stage = st.v_stage + (b >> 1);
                         if (stage >= stages) stage -= v_stages;
-                        uint4* row = reinterpret_cast<uint4*>(ring + stage * one_stage + (b & 1) * BOX_BYTES + r * 128);
+                        uint4* row = reinterpret_cast<uint4*>(ring + stage * one_stage + (b & 1) * BOX_BYTES + key * 128);
+#pragma unroll 1
+                        for (int c0 = 0; c0 < 8; c0 += 4) {  // (piece c ^ lane: an order without bank conflicts)
+                            uint4 v[4];
+                            bool bad_one = dead;
 #pragma unroll
-                        for (int y = 0; y < 8; ++y) {
-                            const int c = y ^ (lane & 7);  // (an order without bank conflicts)
-                            if (dead) row[c] = make_uint4(0, 0, 0, 0);
-                            else if (kvt::has_odd<ST>(row[c])) row[c] = kvt::clear_odd<ST>(row[c]), st.odd[side] = 1;
+                            for (int y = 0; y < 4; ++y) v[y] = row[(c0 + y) ^ (lane & 7)];
+#pragma unroll
+                            for (int y = 0; y < 4; ++y) bad_one = bad_one || kvt::has_odd<ST>(v[y]);
+                            if (!bad_one) continue;
+#pragma unroll 1
+                            for (int y = 0; y < 4; ++y) {
+                                uint4* at = &row[(c0 + y) ^ (lane & 7)];
+                                if (dead) *at = make_uint4(0, 0, 0, 0);
+                                else if (kvt::has_odd<ST>(*at)) *at = kvt::clear_odd<ST>(*at), st.odd[side] = 1;
+                            }
                         }
                     }
                     __threadfence_block();
@@ -623,7 +642,7 @@ __global__ void __launch_bounds__(kpt::threads(QT), 1)
                     if (lane == 0) mbar_arrive(&st.p_full[buf][half]);
                 };
                 publish(0);
-                weights(2), weights(3);
+                weights_of(1);
                 publish(1);
                 const float2 all = parts(add2(sum[0], sum[1]));
                 l += all.x + all.y;

@@ -237,15 +237,12 @@ struct Half16<__half> {
     __device__ static __forceinline__ __half round(float x) { return __float2half_rn(x); }
 };
 
-// Whether one of eight 16-bit values is not finite.
+// Whether one of eight 16-bit values is not finite: its exponent, all ones, carries into the sign's place.
 template <typename ST>
 __device__ __forceinline__ bool has_odd(const uint4& x) {
-    constexpr uint32_t e = Half16<ST>::exp_mask;
-    bool odd = false;
-    const uint32_t u[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) odd = odd || (u[i] & e) == e || (u[i] >> 16 & e) == e;
-    return odd;
+    constexpr uint32_t e = Half16<ST>::exp_mask * 0x10001u, one = (e & ~(e << 1)) & 0x7fff7fffu;
+    const uint32_t u = ((x.x & e) + one) | ((x.y & e) + one) | ((x.z & e) + one) | ((x.w & e) + one);
+    return (u & 0x80008000u) != 0;
 }
 
 // Eight 16-bit values with those that are not finite replaced by zero.
