@@ -24,12 +24,13 @@
 //              the V warp loads a unit's queries too, once the last one's products have
 //              read theirs (whole tokens: a tile of rows holds as many as have their G
 //              heads in it);
-//   products   a warp a tile of rows, an elected thread of which issues all of its
-//              products in order: with QT = 2 a tile's S is issued right behind the last
-//              product that reads the P it is written over, and waits for nobody. (A
-//              commit holds a thread up for 120 to 210 cycles, one right behind another
-//              for 12: a thread for both tiles took 4100 cycles a tile of keys where the
-//              products take 2048.)
+//   products   two warps, an elected thread of each. QT = 2: one a tile of rows, which
+//              issues all of its products in order: S right behind the last product that
+//              reads the P it is written over, waiting for nobody. QT = 1: one for S, one
+//              for O. (A commit holds a thread up for 120 to 210 cycles, one right behind
+//              another for 12: a thread for both tiles of rows took 4100 cycles a tile of
+//              keys where the products take 2048, one for S and O of one tile 2800 where
+//              they take 1280.)
 // A tile's chain is S, softmax, O, S ...: what bounds the kernel is its latency. So the
 // weights' first half is formed against the last tile's reference while the maximum is
 // still looked for (it is formed again where that moved the reference), and is given to
@@ -332,13 +333,13 @@ __global__ void __launch_bounds__(kpt::threads(QT), 1)
         if (!ok && lane == 0) st.stopped = 1, set_error(a.dev_err, GDN_DEVERR_TIMEOUT);
         kvt::landed(st.full, first, end, stage, round);
         if (asked) mbar_wait(&st.q_full, (asked - 1) & 1);
-    } else if (warp >= M_WARP && warp < M_WARP + QT && busy) {
+    } else if ((warp == M_WARP || warp == M_WARP + 1) && busy) {
         // ------------------------------------------------------------ products
         // (one thread, and one that the compiler knows to be alone: elsewhere a product took 107 cycles to issue, for
         // operands that might differ from thread to thread)
         if (elected()) {
             const int j = warp - M_WARP;
-            const uint32_t id_s = idesc(H::type, false, false, KT), aQ = smem_addr(sQ) + j * boxes * TILE * 128, aR = smem_addr(ring);
+            const uint32_t id_s = idesc(H::type, false, false, KT), aQ = smem_addr(sQ) + (QT == 2 ? j * boxes * TILE * 128 : 0), aR = smem_addr(ring);
             int ks = 0, vs = k_stages;  // the rings' next stages
             uint32_t k_round = 0, v_round = 0, n_t = 0, n_v = 0, seg = 0;
             bool ok = true;
@@ -393,23 +394,35 @@ __global__ void __launch_bounds__(kpt::threads(QT), 1)
             };
             do {
                 const int n = w.t1 - w.t0, t0 = w.t0, mixed = first_mixed();
-                ok = ok && mbar_wait(&st.q_full, seg & 1);
-                if (ok) k_there();
-                my_turn();
-                if (ok) {
-                    scores(QT == 2 ? j : n_t & 1);
-                    if (n == 1) tc::commit(&st.q_free);
+                if (QT == 2 || j == 0) ok = ok && mbar_wait(&st.q_full, seg & 1);
+                if constexpr (QT == 1) {
+                    if (j == 0) {
+#pragma unroll 1
+                        for (int i = 0; i < n && ok; ++i, ++n_t) {
+                            k_there();
+                            if (n_t >= 2) ok = ok && mbar_wait(&st.o_done[n_t & 1], ((n_t >> 1) - 1) & 1);
+                            if (!ok) break;
+                            tc::fence_after();
+                            scores(n_t & 1);
+                            if (i + 1 == n) tc::commit(&st.q_free);
+                        }
+                        ++seg;
+                        continue;
+                    }
+                } else {
+                    if (ok) k_there();
+                    my_turn();
+                    if (ok) {
+                        scores(j);
+                        if (n == 1) tc::commit(&st.q_free);
+                    }
                 }
 #pragma unroll 1
                 for (int i = 0; i < n && ok; ++i, ++n_t) {
                     const bool more = i + 1 < n;
                     const int buf = QT == 2 ? j : n_t & 1;
                     const uint32_t use = QT == 2 ? n_t : n_t >> 1;
-                    if (more) k_there();
-                    if (QT == 1 && more && ok) {
-                        scores((n_t + 1) & 1);
-                        if (i + 2 == n) tc::commit(&st.q_free);
-                    }
+                    if (QT == 2 && more) k_there();
                     int sp = vs;
                     uint32_t rp = v_round;
                     for (int p = 0; p < pairs && ok; ++p) {
@@ -417,7 +430,7 @@ __global__ void __launch_bounds__(kpt::threads(QT), 1)
                         if (++sp == stages) sp = k_stages, ++rp;
                     }
                     if (ok && t0 + i >= mixed) {  // the softmax threads look the values through
-                        if (j == 0) st.v_stage = vs, mbar_arrive(&st.v_ok);
+                        if (j == (QT == 2 ? 0 : 1)) st.v_stage = vs, mbar_arrive(&st.v_ok);
                         ok = mbar_wait(&st.v_clean, n_v & 1);
                         ++n_v;
                     }
