@@ -63,6 +63,7 @@ struct KvArgs {
     // prompts
     const int32_t* cu;  // row offsets of the packed sequences
     int total;
+    int extra;  // keys that a unit's start and end cost as much as
     int tile_rows, tile_places, part_rows;  // rows of a tile of a unit, places for them, places of a unit
 };
 
@@ -358,7 +359,7 @@ struct KvRotateArgs {
     int rot, axes, interleaved;
     int tokens;  // B T, or the rows of an append
     int T, Hq, Hkv, d, dtype;
-    int per_block;  // tokens of a block
+    int log_block;  // of the tokens of a block
 };
 
 // Compaction's workspace: held pages, a bit each; where each page above the border goes; the pages that move, in order.

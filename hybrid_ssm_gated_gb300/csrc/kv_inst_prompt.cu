@@ -33,7 +33,7 @@ cudaError_t wave(const KvArgs& a, int64_t& grid) {
 
 cudaError_t launch_kp_join(const KvArgs& a, int grid, cudaStream_t stream) {
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)(grid * kpj::SHARE)), cfg.blockDim = dim3(kpj::NT), cfg.stream = stream;
+    cfg.gridDim = dim3((unsigned)(grid * kpj::share(a.part_rows, a.d))), cfg.blockDim = dim3(kpj::NT), cfg.stream = stream;
     cudaLaunchAttribute pdl{};
     pdl.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     pdl.val.programmaticStreamSerializationAllowed = 1;
@@ -50,6 +50,7 @@ cudaError_t kv_prompt_workspace(KvArgs& a, int64_t& bytes) {
 
 cudaError_t launch_kv_prompt(KvArgs& a, bool vec, cudaStream_t stream) {
     int64_t grid = 0;
+    a.extra = 128;  // (two tiles)
     a.row_block = a.tile_rows = a.tile_places = a.part_rows = kpg::RB;
     cudaError_t e = wave(a, grid);
     if (e != cudaSuccess) return e;

@@ -34,10 +34,16 @@ cudaError_t launch_kv_rotate(KvRotateArgs& r, const KvArgs* cache, bool vec, cud
     vec = vec && r.d % kvr::LANE == 0 && (r.interleaved ? r.rot : r.rot / 2) % kvr::LANE == 0;
     const int lanes = !vec ? 0 : r.d <= 64 ? 8 : r.d <= 128 ? 16 : 32;
     // tokens of a block: as many as leave the device four blocks a SM, so that their angles' cost is spread
-    int per = r.tokens / (di.sms * 4);
-    if (per > kvr::MAX_TOKENS) per = kvr::MAX_TOKENS;
-    r.per_block = per < 1 ? 1 : per;
-    const unsigned grid = (unsigned)((r.tokens + r.per_block - 1) / r.per_block);
+    r.log_block = 0;
+    const int groups = lanes ? kvr::NT / lanes : kvr::MAX_TOKENS;
+    while (2 << r.log_block <= kvr::MAX_TOKENS && 2 << r.log_block <= groups && r.tokens >> (r.log_block + 1) >= di.sms * 4) ++r.log_block;
+    const unsigned grid = (unsigned)((r.tokens + (1 << r.log_block) - 1) >> r.log_block);
+    // tokens that one stride separates, of every row that is read and written
+    const auto flat = [&](const KvTurn& t) { return cache || !t.in || (t.in_seq == r.T * t.in_node && t.out_seq == r.T * t.out_node); };
+    if ((cache || r.T > 1) && flat(r.q) && flat(r.k)) {  // (an append's rows lie in strides of `node`)
+        r.T = 1;
+        for (KvTurn* t : {&r.q, &r.k, &r.v}) t->in_seq = t->in_node, t->out_seq = t->out_node;
+    }
     if (!cache) {
         choose<false>(r.dtype, lanes)<<<grid, kvr::NT, 0, stream>>>(r, KvArgs{});
         return cudaGetLastError();

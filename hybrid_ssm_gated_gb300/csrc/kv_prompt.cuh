@@ -6,7 +6,7 @@
 // row_block); its keys end behind its last token, so that blocks grow along a prompt.
 //
 // Division. All units in order (sequence, key head, block) make a line, a unit as
-// long as its keys and a few more (KP_EXTRA) that stand for what it costs beyond its
+// long as its keys and a few more (the call's extra) that stand for what it costs beyond its
 // tiles, and CTA c of `parts` takes [W c / parts, W (c + 1) / parts) of it: every CTA
 // has the same work, whatever the lengths, and neighbours read the same keys. In
 // units of a G-th key the length of block i is G (prefix + extra) + RB (i + 1), so
@@ -49,7 +49,6 @@ __device__ __forceinline__ KpSeq kp_seq(const KvArgs& a, int b) {
     return s;
 }
 
-constexpr int KP_EXTRA = 256;  // keys that a unit's start and end cost as much as
 constexpr int KP_LEAST = 256;  // keys of a CTA's range at least
 
 // Blocks of a sequence, and the length of the line before block i of a key head.
@@ -57,11 +56,16 @@ __device__ __forceinline__ int kp_blocks(const KvArgs& a, const KpSeq& s) {
     return s.slot < 0 ? 0 : (int)((uint32_t)(s.n * a.G + a.row_block - 1) / (uint32_t)a.row_block);
 }
 __device__ __forceinline__ long long kp_before(const KvArgs& a, const KpSeq& s, long long i) {
-    return i * ((long long)a.G * (s.len - s.n + KP_EXTRA)) + a.row_block * (i * (i + 1) / 2);
+    return i * ((long long)a.G * (s.len - s.n + a.extra)) + a.row_block * (i * (i + 1) / 2);
 }
 __device__ __forceinline__ long long kp_seq_cost(const KvArgs& a, const KpSeq& s) {
     return kp_before(a, s, kp_blocks(a, s)) * a.Hkv;
 }
+
+// A place between tiles: in sequence b, key head h, block i, ahead of tile t.
+struct KpPlace {
+    int b, h, i, t;
+};
 
 // What the scan over sequences leaves in shared memory: the CTA's range.
 struct KpMark {
@@ -74,12 +78,39 @@ struct KpScan {
     KpSeq seq[KEEP];  // the batch's sequences, where there are at most KEEP (which is at most NT)
     long long warp_sum[NT / 32];
     KpMark mark[2];  // beginning and end of the range
+    KpPlace place[2];  // and between which tiles they lie
     long long q;     // ranges: length, and how many are one longer
     int r, parts;
 };
 
+// Tiles of block `blk`: keys 0 .. prefix + last token.
+template <int KT>
+__device__ __forceinline__ int kp_tiles(const KvArgs& a, const KpSeq& x, int blk) {
+    const int rows = (int)min((long long)x.n * a.G, (long long)(blk + 1) * a.row_block);
+    return (x.len - x.n + (rows - 1) / a.G + KT) / KT;
+}
+// The place that a point of the line is cut at.
+template <int KT>
+__device__ __forceinline__ KpPlace kp_place(const KvArgs& a, const KpMark& m, const KpSeq& x) {
+    const int nb = kp_blocks(a, x);
+    const long long one = kp_before(a, x, nb);
+    KpPlace p{m.b, (int)kv_div(m.off, one), 0, 0};
+    const long long off = m.off - one * p.h;
+    int lo = 0, hi = nb;  // the block that holds `off`
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (kp_before(a, x, mid) <= off) lo = mid;
+        else hi = mid;
+    }
+    p.i = lo;
+    const long long in = off - kp_before(a, x, lo) - (long long)a.extra * a.G;
+    // (at the last tile at most: its CTA is the one that ends the unit)
+    if (in > 0) p.t = (int)min(kv_div(in, (long long)KT * a.G), (long long)kp_tiles<KT>(a, x, lo) - 1);
+    return p;
+}
+
 // By the whole block of NT threads: the division, and this CTA's range.
-template <int NT, int KEEP>
+template <int KT, int NT, int KEEP>
 __device__ __forceinline__ void kp_locate(const KvArgs& a, KpScan<NT, KEEP>& sc) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int run = a.B <= NT ? 1 : (a.B + NT - 1) / NT;
@@ -125,12 +156,13 @@ __device__ __forceinline__ void kp_locate(const KvArgs& a, KpScan<NT, KEEP>& sc)
         }
     }
     __syncthreads();
+    if (lane == 0 && warp < 2) {  // (beside one another: a place takes a search)
+        const KpMark m = sc.mark[warp];
+        if (m.b < a.B) sc.place[warp] = kp_place<KT>(a, m, a.B <= KEEP ? sc.seq[m.b] : kp_seq(a, m.b));
+        else sc.place[warp] = KpPlace{a.B, 0, 0, 0};
+    }
+    __syncthreads();
 }
-
-// A place between tiles: in sequence b, key head h, block i, ahead of tile t.
-struct KpPlace {
-    int b, h, i, t;
-};
 
 // A walk along a CTA's segments: runs of tiles of one unit.
 template <int KT>
@@ -142,37 +174,7 @@ struct KpWalk {
     KpSeq s;
     int nt, t0, t1;  // the unit's tiles, and the segment's
 
-    __device__ __forceinline__ int tiles(const KpSeq& x, int blk) const {
-        const int rows = (int)min((long long)x.n * a.G, (long long)(blk + 1) * a.row_block);
-        return (x.len - x.n + (rows - 1) / a.G + KT) / KT;  // keys 0 .. prefix + last token
-    }
     __device__ __forceinline__ KpSeq get(int x) const { return seq ? seq[x] : kp_seq(a, x); }
-    // The place that a point of the line is cut at.
-    __device__ __forceinline__ KpPlace place(const KpMark& m) const {
-        KpPlace p{m.b, 0, 0, 0};
-        if (m.b >= a.B) return p;
-        const KpSeq x = get(m.b);
-        const int nb = kp_blocks(a, x);
-        const long long one = kp_before(a, x, nb);
-        p.h = (int)kv_div(m.off, one);
-        const long long off = m.off - one * p.h;
-        int lo = 0, hi = nb;  // the block that holds `off`
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (kp_before(a, x, mid) <= off) lo = mid;
-            else hi = mid;
-        }
-        p.i = lo;
-        p.t = tile_at(off - kp_before(a, x, lo), tiles(x, lo));
-        return p;
-    }
-    // Tile that a point `off` of a unit is cut ahead of.
-    __device__ __forceinline__ int tile_at(long long off, int n) const {
-        const long long in = off - (long long)KP_EXTRA * a.G;
-        if (in < 0) return 0;
-        const long long t = kv_div(in, (long long)KT * a.G);
-        return (int)(t < n ? t : n - 1);  // (the last tile's CTA is the one that ends the unit)
-    }
     __device__ __forceinline__ bool before_end() const {
         return b < end.b || (b == end.b && (h < end.h || (h == end.h && i <= end.i)));
     }
@@ -183,7 +185,7 @@ struct KpWalk {
     // The segment of the current unit from tile t on; false if the range ends ahead of it.
     __device__ __forceinline__ bool segment(int t) {
         if (!before_end() || b >= a.B) return false;
-        nt = tiles(s, i), t0 = t;
+        nt = kp_tiles<KT>(a, s, i), t0 = t;
         t1 = b == end.b && h == end.h && i == end.i ? min(end.t, nt) : nt;
         return true;
     }
@@ -193,8 +195,8 @@ struct KpWalk {
         t0 = t1 = nt = 0;
         some = false;
         if ((int)blockIdx.x >= sc.parts) return;
-        const KpPlace from = place(sc.mark[0]);
-        end = place(sc.mark[1]);
+        const KpPlace from = sc.place[0];
+        end = sc.place[1];
         b = from.b, h = from.h, i = from.i;
         if (b >= a.B) return;
         load();

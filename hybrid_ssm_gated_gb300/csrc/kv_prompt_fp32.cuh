@@ -65,7 +65,7 @@ __global__ void __launch_bounds__(kpg::NT) kv_prompt_kernel(const __grid_constan
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4, pitch = L.pitch, d4 = L.dp / 4;
     const float c2 = a.scale * LOG2E;
     kv_grid_launch();
-    kp_locate(a, sc);
+    kp_locate<KT>(a, sc);
     bool busy;
     KpWalk<KT> w(a, sc, busy);
     kp_empty_rows(a, a.B <= NT ? sc.seq : nullptr, tid, NT);

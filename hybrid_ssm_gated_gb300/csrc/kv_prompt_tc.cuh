@@ -244,7 +244,7 @@ __global__ void __launch_bounds__(kpt::threads(QT), 1)
     }
     if (tid == 0) kp_no_border(a);
     tc::fence_before();
-    kp_locate(a, st.scan);
+    kp_locate<KT>(a, st.scan);
     tc::fence_after();
     const uint32_t tmem = st.tmem;
     bool busy;

@@ -105,160 +105,196 @@ __device__ __forceinline__ kvr::Place kv_place(const KvArgs& c, const int* cu, i
 
 // ST: element type; LP: lanes a row (eight elements a lane), or 0 for the scalar form; APPEND: c is the cache.
 template <typename ST, int LP, bool APPEND>
-__global__ void __launch_bounds__(kvr::NT) kv_rotate_kernel(const __grid_constant__ KvRotateArgs a, const __grid_constant__ KvArgs c) {
+__global__ void __launch_bounds__(kvr::NT, LP > 0 ? (APPEND ? 4 : 5) : 1) kv_rotate_kernel(const __grid_constant__ KvRotateArgs a, const __grid_constant__ KvArgs c) {
     using namespace kvr;
     __shared__ __align__(16) float s_cos[MAX_PAIRS], s_sin[MAX_PAIRS];
     __shared__ Place s_place[APPEND ? MAX_TOKENS : 1];
     __shared__ int s_cu[APPEND ? SEQS : 1];
     __shared__ float s_row[LP == 0 ? WARPS : 1][LP == 0 ? KV_MAX_D : 1];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int t0 = blockIdx.x * a.per_block, tokens = min(a.per_block, a.tokens - t0), half = a.rot / 2;
+    const int t0 = blockIdx.x << a.log_block, tokens = min(1 << a.log_block, a.tokens - t0), half = a.rot / 2;
+    // rows of a token: queries, keys, values; row r is that of token r % 2^log_block
+    const int nq = a.q.in ? a.Hq : 0, nk = a.k.in ? a.Hkv : 0, per = nq + nk + (a.v.in ? a.Hkv : 0), rows = per << a.log_block;
+    const auto side_of = [&](int y) { return y < nq ? 0 : y < nq + nk ? 1 : 2; };
+    const auto head_of = [&](int y, int side) { return y - (side == 0 ? 0 : side == 1 ? nq : nq + nk); };
+    const auto turn_of = [&](int side) -> const KvTurn& { return side == 0 ? a.q : side == 1 ? a.k : a.v; };
+    const auto offset = [&](int tok, int64_t seq, int64_t node) {
+        if (a.T == 1) return tok * seq;  // (tokens in one stride)
+        const int b = tok / a.T;
+        return b * seq + (tok - b * a.T) * node;
+    };
+    const auto in_of = [&](int r) {
+        const int y = r >> a.log_block, side = side_of(y);
+        const KvTurn& s = turn_of(side);
+        return static_cast<const ST*>(s.in) + offset(t0 + (r & ((1 << a.log_block) - 1)), s.in_seq, s.in_node) +
+               (int64_t)head_of(y, side) * s.in_head;
+    };
+    const auto there = [&](int r) { return r < rows && (r & ((1 << a.log_block) - 1)) < tokens; };
+
     if constexpr (APPEND) {
         kv_grid_launch();
         if (!kv_offsets_ok<NT>(c, s_cu, SEQS)) return;
         if (tid < tokens) s_place[tid] = kv_place(c, c.B < SEQS ? s_cu : c.cu, t0 + tid);
-        __syncthreads();
+        if (!a.positions) __syncthreads();
     }
     for (int i = tid; i < tokens * half; i += NT) {
         const int t = i / half, x = i - t * half;
         int ax = a.axis ? a.axis[x] : 0;
         if ((uint32_t)ax >= (uint32_t)a.axes) ax = 0;
         int pos;
-        if constexpr (APPEND) pos = a.positions ? a.positions[(int64_t)ax * a.tokens + t0 + t] : s_place[t].first;
-        else pos = a.positions[(int64_t)ax * a.tokens + t0 + t];
+        if (!APPEND || a.positions) pos = a.positions[(int64_t)ax * a.tokens + t0 + t];
+        else pos = s_place[t].first;
         const float2 cs = kv_cos_sin(a.turns[x], pos);
         s_cos[i] = cs.x, s_sin[i] = cs.y;
     }
     __syncthreads();
-    // rows of a token: queries, keys, values
-    const int nq = a.q.in ? a.Hq : 0, nk = a.k.in ? a.Hkv : 0, per = nq + nk + (a.v.in ? a.Hkv : 0), rows = tokens * per;
-    // row r: its token, kind and addresses (out NULL: nothing is written)
-    struct Row {
-        const ST* in;
-        ST* out;
-        const float* norm;
-        int t;
-        bool turn, zero;
-    };
-    const auto row_of = [&](int r) {
-        Row x;
-        x.t = r / per;
-        const int y = r - x.t * per, side = y < nq ? 0 : y < nq + nk ? 1 : 2, h = side == 0 ? y : side == 1 ? y - nq : y - nq - nk;
-        const KvTurn& s = side == 0 ? a.q : side == 1 ? a.k : a.v;
-        const int tok = t0 + x.t;
-        const int64_t b = APPEND ? 0 : tok / a.T, j = APPEND ? tok : tok - b * a.T;
-        x.in = static_cast<const ST*>(s.in) + b * s.in_seq + j * s.in_node + (int64_t)h * s.in_head;
-        x.norm = s.norm ? s.norm + (int64_t)h * s.norm_head : nullptr;
-        x.turn = side < 2 && (s.norm || half > 0), x.zero = false;  // (else it is moved as it is)
-        x.out = static_cast<ST*>(s.out) + b * s.out_seq + j * s.out_node + (int64_t)h * s.out_head;
+    // where row r goes (NULL: nowhere), and whether as zeros
+    const auto out_of = [&](int r, bool& zero) -> ST* {
+        const int y = r >> a.log_block, side = side_of(y), t = r & ((1 << a.log_block) - 1), h = head_of(y, side);
+        const KvTurn& s = turn_of(side);
+        ST* out = static_cast<ST*>(s.out) + (int64_t)h * s.out_head;
+        zero = false;
         if constexpr (APPEND) {
-            const Place& p = s_place[x.t];
-            if (side > 0)
-                x.out = p.live != 1 ? nullptr
-                                    : static_cast<ST*>(s.out) + (side == 1 ? p.k : p.v) + (int64_t)h * s.out_head;
-            else if (p.live < 0)
-                x.out = nullptr;
-            x.zero = p.live == 0;
+            const Place& p = s_place[t];
+            zero = p.live == 0;
+            if (side > 0) return p.live != 1 ? nullptr : out + (side == 1 ? p.k : p.v);
+            if (p.live < 0) return nullptr;
         }
-        return x;
+        return out + offset(t0 + t, s.out_seq, s.out_node);
     };
     if constexpr (LP > 0) {
+        // A group of lanes stays with one token of the block: places, angles and weights are in registers, and the next
+        // row is a step of whole heads away.
         constexpr int GROUPS = NT / LP, AHEAD = 2;
-        const int sub = tid % LP, e0 = sub * LANE;
-        const bool in = e0 < a.d, first = e0 < half, turned = e0 < a.rot;
+        const int sub = tid % LP, e0 = sub * LANE, group = tid / LP, t = group & ((1 << a.log_block) - 1), h0 = group >> a.log_block;
+        const int step = GROUPS >> a.log_block;  // (a block has no more tokens than groups)
+        const bool in = e0 < a.d && t < tokens, first = e0 < half, turned = e0 < a.rot;
         const int partner = first ? sub + half / LANE : turned ? sub - half / LANE : sub;
-        for (int r0 = tid / LP; r0 - tid / LP < rows; r0 += GROUPS * AHEAD) {  // (the same trips for every lane)
-            Row row[AHEAD];
-            Eight<ST> raw[AHEAD];
+        const float mean = 1.f / (float)a.d;
+        float co[LANE], si[LANE];  // of this lane's elements; interleaved: of its four pairs
 #pragma unroll
-            for (int y = 0; y < AHEAD; ++y) {
-                row[y] = row_of(min(r0 + y * GROUPS, rows - 1));
-                if (r0 + y * GROUPS >= rows) row[y].out = nullptr;
-                raw[y].clear();
-                if (in && row[y].out && !row[y].zero) raw[y].load(row[y].in + e0);
-            }
+        for (int e = 0; e < LANE; ++e) co[e] = 1.f, si[e] = 0.f;
+        if (turned && t < tokens) {
+            const int i = t * half + (a.interleaved ? e0 / 2 : first ? e0 : e0 - half);
 #pragma unroll
-            for (int y = 0; y < AHEAD; ++y) {
-                const Row& w = row[y];
-                float x[LANE];
-                raw[y].unpack(x);
-                float ss = 0.f;
-#pragma unroll
-                for (int e = 0; e < LANE; ++e) ss = fmaf(x[e], x[e], ss);
-                ss = group_sum<LP>(ss);
-                if (w.norm && in) {
-                    const float f = rsqrtf(ss / (float)a.d + a.eps);
-#pragma unroll
-                    for (int e = 0; e < LANE; e += 4) {
-                        const float4 g = *reinterpret_cast<const float4*>(w.norm + e0 + e);
-                        x[e] *= f * (g.x + a.offset), x[e + 1] *= f * (g.y + a.offset);
-                        x[e + 2] *= f * (g.z + a.offset), x[e + 3] *= f * (g.w + a.offset);
-                    }
-                }
-                if (a.interleaved) {
-                    if (turned && w.turn) {
-                        const int i = w.t * half + e0 / 2;
-                        const float4 co = *reinterpret_cast<const float4*>(s_cos + i), si = *reinterpret_cast<const float4*>(s_sin + i);
-                        const float c4[4] = {co.x, co.y, co.z, co.w}, s4[4] = {si.x, si.y, si.z, si.w};
-#pragma unroll
-                        for (int e = 0; e < LANE; e += 2) {
-                            const float p = x[e], q = x[e + 1];
-                            x[e] = p * c4[e / 2] - q * s4[e / 2], x[e + 1] = p * s4[e / 2] + q * c4[e / 2];
-                        }
-                    }
-                } else {
-                    const int i = w.t * half + e0 - (first || !turned ? 0 : half);
-#pragma unroll
-                    for (int e = 0; e < LANE; e += 4) {
-                        float o[4];
-#pragma unroll
-                        for (int z = 0; z < 4; ++z) o[z] = __shfl_sync(FULL_MASK, x[e + z], partner, LP);
-                        if (turned && w.turn) {
-                            const float4 co = *reinterpret_cast<const float4*>(s_cos + i + e);
-                            const float4 si = *reinterpret_cast<const float4*>(s_sin + i + e);
-                            const float c4[4] = {co.x, co.y, co.z, co.w}, s4[4] = {si.x, si.y, si.z, si.w};
-#pragma unroll
-                            for (int z = 0; z < 4; ++z)
-                                x[e + z] = x[e + z] * c4[z] + (first ? -o[z] : o[z]) * s4[z];
-                        }
-                    }
-                }
-                if (w.turn) raw[y].pack(x);
-                if (in && w.out) raw[y].store(w.out + e0);
+            for (int e = 0; e < LANE; e += 4) {
+                if (a.interleaved && e > 0) break;
+                const float4 x = *reinterpret_cast<const float4*>(s_cos + i + e), y = *reinterpret_cast<const float4*>(s_sin + i + e);
+                const float z = a.interleaved || !first ? 1.f : -1.f;  // (of halves: the other element's share, signed)
+                co[e] = x.x, co[e + 1] = x.y, co[e + 2] = x.z, co[e + 3] = x.w;
+                si[e] = z * y.x, si[e + 1] = z * y.y, si[e + 2] = z * y.z, si[e + 3] = z * y.w;
             }
         }
+        const auto rows_of = [&](const KvTurn& s, int heads, int side) {
+            const ST* from = static_cast<const ST*>(s.in) + offset(t0 + t, s.in_seq, s.in_node) + (int64_t)h0 * s.in_head + e0;
+            ST* to = static_cast<ST*>(s.out) + (int64_t)h0 * s.out_head + e0;
+            bool zero = false, write = in;
+            if constexpr (APPEND) {
+                const Place& p = s_place[t];
+                zero = p.live == 0, write = in && (side > 0 ? p.live == 1 : p.live >= 0);
+                if (side > 0) to += side == 1 ? p.k : p.v;
+            }
+            if (!APPEND || side == 0) to += offset(t0 + t, s.out_seq, s.out_node);
+            const int64_t from_step = step * s.in_head, to_step = step * s.out_head;
+            const bool norm = side < 2 && s.norm, turn = side < 2 && half > 0;
+            float w[LANE];
+            const auto weights = [&](int h) {
+#pragma unroll
+                for (int e = 0; e < LANE; e += 4) {
+                    float4 g = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (in && h < heads) g = *reinterpret_cast<const float4*>(s.norm + (int64_t)h * s.norm_head + e0 + e);
+                    w[e] = g.x + a.offset, w[e + 1] = g.y + a.offset, w[e + 2] = g.z + a.offset, w[e + 3] = g.w + a.offset;
+                }
+            };
+            if (norm) weights(h0);
+#pragma unroll 1
+            for (int i = 0; i * step < heads; i += AHEAD) {  // (the same trips for every lane)
+                Eight<ST> raw[AHEAD];
+#pragma unroll
+                for (int y = 0; y < AHEAD; ++y) {
+                    raw[y].clear();
+                    if (write && !zero && h0 + (i + y) * step < heads) raw[y].load(from);
+                    from += from_step;
+                }
+#pragma unroll
+                for (int y = 0; y < AHEAD; ++y) {
+                    const int h = h0 + (i + y) * step;
+                    if (norm || turn) {
+                        float x[LANE];
+                        raw[y].unpack(x);
+                        if (norm) {
+                            if (s.norm_head && i + y > 0) weights(h);
+                            float ss = 0.f;
+#pragma unroll
+                            for (int e = 0; e < LANE; ++e) ss = fmaf(x[e], x[e], ss);
+                            ss = group_sum<LP>(ss);
+                            const float f = rsqrtf(ss * mean + a.eps);
+#pragma unroll
+                            for (int e = 0; e < LANE; ++e) x[e] *= f * w[e];
+                        }
+                        if (turn && a.interleaved) {
+                            if (turned) {
+#pragma unroll
+                            for (int e = 0; e < LANE; e += 2) {
+                                const float p = x[e], q = x[e + 1];
+                                x[e] = p * co[e / 2] - q * si[e / 2], x[e + 1] = p * si[e / 2] + q * co[e / 2];
+                            }
+                            }
+                        } else if (turn) {
+#pragma unroll
+                            for (int e = 0; e < LANE; ++e) {
+                                const float o = __shfl_sync(FULL_MASK, x[e], partner, LP);
+                                if (turned) x[e] = fmaf(o, si[e], x[e] * co[e]);
+                            }
+                        }
+                        raw[y].pack(x);
+                    }
+                    if (zero) raw[y].clear();
+                    if (write && h < heads) raw[y].store(to);
+                    to += to_step;
+                }
+            }
+        };
+        if (nq) rows_of(a.q, a.Hq, 0);
+        if (nk) rows_of(a.k, a.Hkv, 1);
+        if (a.v.in) rows_of(a.v, a.Hkv, 2);
     } else {
         float* line = s_row[warp];
         for (int r = warp; r < rows; r += WARPS) {
-            const Row w = row_of(r);
-            if (!w.out) continue;
+            if (!there(r)) continue;
+            const int y = r >> a.log_block, side = side_of(y), t = r & ((1 << a.log_block) - 1);
+            const KvTurn& s = turn_of(side);
+            bool zero;
+            ST* out = out_of(r, zero);
+            if (!out) continue;
+            const ST* from = in_of(r);
+            if (zero || side == 2 || (!s.norm && half == 0)) {
+                for (int e = lane; e < a.d; e += 32) out[e] = zero ? ST(0.f) : from[e];
+                continue;
+            }
             float ss = 0.f;
             for (int e = lane; e < a.d; e += 32) {
-                const float x = w.zero ? 0.f : load_elem(w.in, e, Store<ST>::code);
+                const float x = load_elem(from, e, Store<ST>::code);
                 line[e] = x, ss = fmaf(x, x, ss);
             }
             ss = group_sum<32>(ss);
             __syncwarp();
-            if (!w.turn && !w.zero) {
-                for (int e = lane; e < a.d; e += 32) w.out[e] = w.in[e];
-                __syncwarp();
-                continue;
-            }
-            if (w.norm) {
+            if (s.norm) {
                 const float f = rsqrtf(ss / (float)a.d + a.eps);
-                for (int e = lane; e < a.d; e += 32) line[e] *= f * (w.norm[e] + a.offset);
+                const float* norm = s.norm + (int64_t)head_of(y, side) * s.norm_head;
+                for (int e = lane; e < a.d; e += 32) line[e] *= f * (norm[e] + a.offset);
                 __syncwarp();
             }
             for (int e = lane; e < a.d; e += 32) {
                 float z = line[e];
-                if (e < a.rot && !w.zero) {
+                if (e < a.rot) {
                     const bool one = a.interleaved ? (e & 1) == 0 : e < half;
                     const int i = a.interleaved ? e >> 1 : one ? e : e - half;
                     const float other = line[a.interleaved ? e ^ 1 : one ? e + half : e - half];
-                    const float co = s_cos[w.t * half + i], si = s_sin[w.t * half + i];
+                    const float co = s_cos[t * half + i], si = s_sin[t * half + i];
                     z = one ? z * co - other * si : other * si + z * co;
                 }
-                store_elem(w.out, e, Store<ST>::code, w.zero ? 0.f : z);
+                store_elem(out, e, Store<ST>::code, z);
             }
             __syncwarp();
         }
