@@ -28,7 +28,7 @@ NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2"
                      "-I", INCLUDE]
 
 
-STALL = ["kv_inst_tc.cu", "kv_inst_weights_tc.cu"]
+STALL = ["kv_inst_tc.cu", "kv_inst_weights_tc.cu", "kv_inst_prompt_tc.cu"]
 
 
 def nvcc() -> str:

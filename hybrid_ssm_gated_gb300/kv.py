@@ -290,48 +290,49 @@ class Rotary:
 
     def check(self, norm, heads: int, d: int) -> None:
         """That a side's weights are those of rows [heads, d]."""
-        if norm is not None and (norm.shape[-1] != d or (norm.dim() == 2 and norm.shape[0] != heads)):
+        if norm is not None and norm.shape != (d,) and norm.shape != (heads, d):
             raise ValueError(f"kv: a norm's weights must be [{d}] or [{heads}, {d}]")
 
 
-def _turned(x, out, name: str, like):
-    """kv_rows of a side of kv_norm_rotate [B, T, heads, d] and of its output; None for neither."""
+def _side(x, out, name: str, dtype, device: int, B: int, T: int, d: int):
+    """kv_rows of a side of kv_norm_rotate [B, T, heads, d] and of its output, and its heads; nothing for neither."""
     if x is None and out is None:
-        return None, None
-    if x is None or out is None or x.dim() != 4 or x.shape != out.shape or x.shape[:2] != like.shape[:2] or \
-            x.shape[3] != like.shape[3] or any(t.dtype is not like.dtype or t.get_device() != like.get_device()
-                                               or t.stride(3) != 1 for t in (x, out)):
-        raise ValueError(f"kv: {name} and {name}_out must be tensors [B, T, heads, d] of one dtype and device, with unit "
-                         "stride in d")
-    return tuple(kv_rows(t.data_ptr(), *t.stride()[:3]) for t in (x, out))
+        return None, None, 0
+    if x is not None and out is not None and x.dim() == 4:
+        shape, s, o = x.shape, x.stride(), out.stride()
+        if shape[0] == B and shape[1] == T and shape[3] == d and out.shape == shape and x.dtype is dtype and \
+                out.dtype is dtype and s[3] == 1 and o[3] == 1 and x.get_device() == device and out.get_device() == device:
+            return kv_rows(x.data_ptr(), s[0], s[1], s[2]), kv_rows(out.data_ptr(), o[0], o[1], o[2]), shape[2]
+    raise ValueError(f"kv: {name} and {name}_out must be tensors [B, T, heads, d] of one dtype on the rotary's device, with "
+                     "unit stride in d")
 
 
 def kv_norm_rotate(rotary: Rotary, positions, q=None, k=None, q_out=None, k_out=None, stream=None) -> None:
     """Norm and rotation of drafted tokens: q [B, T, Hq, d], k [B, T, Hkv, d] into q_out, k_out (which may be q
     and k); positions [axes, B, T] int32 ([B, T] with one axis; None where nothing is turned)."""
     like = q if q is not None else k
-    if like is None or like.dim() != 4 or like.dtype not in DTYPE_CODE or like.get_device() != rotary.device:
-        raise ValueError("kv: q or k must be a tensor [B, T, heads, d] on the rotary's device")
+    if like is None or like.dim() != 4 or like.dtype not in DTYPE_CODE:
+        raise ValueError("kv: q or k must be a tensor [B, T, heads, d] of a dtype of the cache's")
+    device, dtype = rotary.device, like.dtype
     B, T, _, d = like.shape
-    Hq, Hkv = (0 if t is None else t.shape[2] for t in (q, k))
-    rq, ro = _turned(q, q_out, "q", like)
-    rk, rp = _turned(k, k_out, "k", like)
-    if q is not None:
+    rq, ro, Hq = _side(q, q_out, "q", dtype, device, B, T, d)
+    rk, rp, Hkv = _side(k, k_out, "k", dtype, device, B, T, d)
+    if rq is not None:
         rotary.check(rotary.q_norm, Hq, d)
-    if k is not None:
+    if rk is not None:
         rotary.check(rotary.k_norm, Hkv, d)
-    shape = (B, T) if positions is not None and positions.dim() == 2 and rotary.axes == 1 else (rotary.axes, B, T)
+    shape = (B, T) if positions is not None and rotary.axes == 1 and positions.dim() == 2 else (rotary.axes, B, T)
     pos = _ints(positions, rotary, shape, "positions")
-    _check(_on_device(rotary, lib().kv_norm_rotate, rotary._ref, DTYPE_CODE[like.dtype], B, T, Hq, Hkv, d, pos, rq, ro,
-                      rk, rp, _stream(stream, rotary.device)))
+    _check(_on_device(rotary, lib().kv_norm_rotate, rotary._ref, DTYPE_CODE[dtype], B, T, Hq, Hkv, d, pos, rq, ro, rk, rp,
+                      _stream(stream, device)))
 
 
 def _packed(t, cache: KVCache, heads: int, total: int, name: str) -> kv_rows:
-    if t.dim() != 3 or t.shape != (total, heads, cache.d) or t.dtype is not cache.dtype or \
-            t.get_device() != cache.device or t.stride(2) != 1:
+    s = t.stride()
+    if t.shape != (total, heads, cache.d) or t.dtype is not cache.dtype or s[2] != 1 or t.get_device() != cache.device:
         raise ValueError(f"kv: {name} must be a tensor [{total}, {heads}, {cache.d}] of the cache's dtype on the cache's "
                          "device, with unit stride in d")
-    return kv_rows(t.data_ptr(), 0, t.stride(0), t.stride(1))
+    return kv_rows(t.data_ptr(), 0, s[0], s[1])
 
 
 def kv_append(cache: KVCache, slots, cu_seqlens, k, v, dev_err, rotary: Rotary | None = None, positions=None, q=None,
@@ -340,26 +341,26 @@ def kv_append(cache: KVCache, slots, cu_seqlens, k, v, dev_err, rotary: Rotary |
     (cu_seqlens [B + 1] int32, on the device). With `rotary`, keys are normed and turned on the way, and q
     [total, Hq, d] into q_out (which may be q); positions [axes, total] int32 ([total] with one axis), None:
     the sequence's count and on."""
-    B, total = slots.shape[0], k.shape[0]
-    rk, rv = _packed(k, cache, cache.Hkv, total, "k"), _packed(v, cache, cache.Hkv, total, "v")
-    rq = ro = None
-    Hq = 0
-    if (q is None) != (q_out is None) or (q is not None and rotary is None):
-        raise ValueError("kv: q, q_out and rotary come together")
-    if q is not None:
+    B, total, Hkv, d, device = slots.shape[0], k.shape[0], cache.Hkv, cache.d, cache.device
+    rk, rv = _packed(k, cache, Hkv, total, "k"), _packed(v, cache, Hkv, total, "v")
+    rq = ro = ref = None
+    Hq, axes = 0, 1
+    if rotary is not None:
+        if rotary.device != device:
+            raise ValueError("kv: the rotary must lie on the cache's device")
+        ref, axes = rotary._ref, rotary.axes
+        rotary.check(rotary.k_norm, Hkv, d)
+    if q is not None or q_out is not None:
+        if q is None or q_out is None or rotary is None:
+            raise ValueError("kv: q, q_out and rotary come together")
         Hq = q.shape[1]
         rq, ro = _packed(q, cache, Hq, total, "q"), _packed(q_out, cache, Hq, total, "q_out")
-        rotary.check(rotary.q_norm, Hq, cache.d)
-    if rotary is not None:
-        if rotary.device != cache.device:
-            raise ValueError("kv: the rotary must lie on the cache's device")
-        rotary.check(rotary.k_norm, cache.Hkv, cache.d)
-    axes = 1 if rotary is None else rotary.axes
-    shape = (total,) if positions is not None and positions.dim() == 1 and axes == 1 else (axes, total)
+        rotary.check(rotary.q_norm, Hq, d)
+    shape = (total,) if positions is not None and axes == 1 and positions.dim() == 1 else (axes, total)
     _check(_on_device(cache, lib().kv_append, cache._ref, B, total, Hq, _ints(slots, cache, (B,), "slots"),
-                      _ints(cu_seqlens, cache, (B + 1,), "cu_seqlens"), rk, rv, None if rotary is None else rotary._ref,
+                      _ints(cu_seqlens, cache, (B + 1,), "cu_seqlens"), rk, rv, ref,
                       _ints(positions, cache, shape, "positions"), rq, ro, _whole(dev_err, cache, "dev_err"),
-                      _stream(stream, cache.device)))
+                      _stream(stream, device)))
 
 
 def kv_prompt_workspace(cache: KVCache, B: int, q) -> torch.Tensor:
