@@ -10,13 +10,24 @@ namespace {
 
 using Kernel = void (*)(const KvArgs, const int);
 
-template <int NC>
-Kernel of_dtype(int dtype) {
-    return dtype == GDN_F32 ? kv_prompt_kernel<float, NC>
-                            : dtype == GDN_BF16 ? kv_prompt_kernel<__nv_bfloat16, NC> : kv_prompt_kernel<__half, NC>;
+// Blocks of 64 outputs, and whether up to 16 more are left over. (16-bit caches come here with odd sizes and
+// strides alone: for them the next whole block does.)
+template <int NC, bool TAIL>
+Kernel of_f32() {
+    return kv_prompt_kernel<float, NC, TAIL>;
+}
+template <typename ST>
+Kernel of_16(int d) {
+    return d <= 64 ? kv_prompt_kernel<ST, 1, false> : d <= 128 ? kv_prompt_kernel<ST, 2, false> : kv_prompt_kernel<ST, 4, false>;
 }
 Kernel choose(const KvArgs& a) {
-    return a.d <= 64 ? of_dtype<1>(a.dtype) : a.d <= 128 ? of_dtype<2>(a.dtype) : of_dtype<4>(a.dtype);
+    if (a.dtype == GDN_BF16) return of_16<__nv_bfloat16>(a.d);
+    if (a.dtype == GDN_F16) return of_16<__half>(a.d);
+    static const Kernel kernels[5][2] = {{of_f32<0, true>(), of_f32<0, true>()}, {of_f32<1, false>(), of_f32<1, true>()},
+                                         {of_f32<2, false>(), of_f32<2, true>()}, {of_f32<3, false>(), of_f32<3, true>()},
+                                         {of_f32<4, false>(), of_f32<4, false>()}};
+    const int left = a.d % 64;
+    return left > 16 ? kernels[a.d / 64 + 1][0] : kernels[a.d / 64][left > 0];
 }
 
 cudaError_t wave(const KvArgs& a, int64_t& grid) {

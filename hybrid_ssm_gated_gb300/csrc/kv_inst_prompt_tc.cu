@@ -22,11 +22,13 @@ cudaError_t launch(const KvArgs& a, const kpt::Maps& maps, int boxes, int box_ro
     return cudaGetLastError();
 }
 
-// Tiles of query rows a unit: two where their outputs fit tensor memory and there are units for every SM.
+// Tiles of query rows a unit: two where their outputs fit tensor memory, there are units for every SM, and the sequences
+// have rows for them in the mean.
 int tiles_of(const KvArgs& a, int sms) {
     if (a.d > 128) return 1;
     const int64_t tokens = 2 * (kpt::TILE / a.G);
-    return (a.total / tokens) * a.Hkv >= sms ? 2 : 1;
+    const int64_t units = a.total / tokens;
+    return units * a.Hkv >= sms && units >= a.B ? 2 : 1;
 }
 
 }  // namespace

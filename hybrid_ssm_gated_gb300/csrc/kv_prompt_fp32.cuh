@@ -8,14 +8,16 @@
 // then added to the rescaled outputs, so that long sums are not rounded to the steps
 // of what they have become.
 //
-// Shape: 256 threads, units of 64 rows, tiles of 64 keys, queries, keys, values and
-// weights in shared memory as FP32. Threads form a 16 x 16 grid: four rows by four
-// keys of the scores, then the same four rows by four outputs (of each 64 of d), so
-// that a row's maximum, sum and rescaling stay with its 16 threads. The keys of the
+// Shape: 128 threads, units of 64 rows, tiles of 64 keys, queries, keys, values and
+// weights in shared memory as FP32. Threads form a 16 x 8 grid: eight rows by four
+// keys of the scores, then the same eight rows by four outputs (of each 64 of d; by one
+// of up to 16 that are left over), so that a row's maximum, sum and rescaling stay with
+// its 16 threads. The keys of the
 // next tile are on their way (cp.async where the cache is FP32 and its rows allow
 // 16-byte copies) while weights and outputs form, the values while scores form.
-// Bound by the FP32 pipe and shared-memory loads (8 loads of 16 bytes for 64
-// products a thread).
+// Bound by the FP32 pipe and shared-memory loads (12 loads of 16 bytes for 128
+// products a thread; four rows by four keys of 256 threads, 8 for 64, took 192 us for
+// three prompts of up to 1200 rows (8 / 4 heads, d = 80, 3.4 GFLOP) where these take 176).
 #pragma once
 
 #include "kv_attn.cuh"
@@ -25,7 +27,7 @@ namespace gdn {
 
 namespace kpg {
 
-constexpr int RB = 64, KT = 64, NT = 256;
+constexpr int RB = 64, KT = 64, NT = 128, R = 8;  // R: rows of a thread
 
 struct Layout {
     int dp, pitch, off_k, off_v, off_p, off_at, off_q_at, off_scan, off_bad, bytes;
@@ -47,8 +49,8 @@ __host__ __device__ inline Layout layout(int d) {
 
 }  // namespace kpg
 
-// NC: blocks of 64 outputs.
-template <typename ST, int NC>
+// NC: blocks of 64 outputs; TAIL: and up to 16 more.
+template <typename ST, int NC, bool TAIL>
 __global__ void __launch_bounds__(kpg::NT) kv_prompt_kernel(const __grid_constant__ KvArgs a, const int vec) {
     using namespace kpg;
     extern __shared__ __align__(128) unsigned char smem[];
@@ -106,12 +108,13 @@ __global__ void __launch_bounds__(kpg::NT) kv_prompt_kernel(const __grid_constan
         load(sK, a.k, w.t0, 0);
         load(sV, a.v, w.t0, 1);
         look(w.t0 + 1);
-        int last[4];  // each row's last entry
-        float m[4], l[4], o[NC][4][4];
+        int last[R];  // each row's last entry
+        float m[R], l[R], o[NC > 0 ? NC : 1][R][4], ot[TAIL ? R : 1];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int x = r0 + min(ty * 4 + i, rows - 1);
+        for (int i = 0; i < R; ++i) {
+            const int x = r0 + min(ty * R + i, rows - 1);
             last[i] = prefix + x / a.G, m[i] = -INFINITY, l[i] = 0.f;
+            if (TAIL) ot[i] = 0.f;
 #pragma unroll
             for (int c = 0; c < NC; ++c)
 #pragma unroll
@@ -121,22 +124,22 @@ __global__ void __launch_bounds__(kpg::NT) kv_prompt_kernel(const __grid_constan
         for (int t = w.t0; t < w.t1; ++t) {
             cp_async_wait<1>();
             __syncthreads();
-            float s[4][4] = {};
+            float s[R][4] = {};
 #pragma unroll 2
             for (int e = 0; e < d4; ++e) {
-                float4 q[4], k[4];
+                float4 q[R], k[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) q[i] = *reinterpret_cast<const float4*>(sQ + (ty * 4 + i) * pitch + e * 4);
+                for (int i = 0; i < R; ++i) q[i] = *reinterpret_cast<const float4*>(sQ + (ty * R + i) * pitch + e * 4);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) k[j] = *reinterpret_cast<const float4*>(sK + (tx + 16 * j) * pitch + e * 4);
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
+                for (int i = 0; i < R; ++i)
 #pragma unroll
                     for (int j = 0; j < 4; ++j) kv_dot4(s[i][j], q[i], k[j]);
             }
-            float f[4];
+            float f[R];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < R; ++i) {
                 float top_s = -INFINITY;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
@@ -151,7 +154,7 @@ __global__ void __launch_bounds__(kpg::NT) kv_prompt_kernel(const __grid_constan
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     s[i][j] = kv_ex2(s[i][j] - base), sum += s[i][j];
-                    sP[(ty * 4 + i) * PP + tx + 16 * j] = s[i][j];
+                    sP[(ty * R + i) * PP + tx + 16 * j] = s[i][j];
                 }
 #pragma unroll
                 for (int x = 8; x; x >>= 1) sum += __shfl_xor_sync(FULL_MASK, sum, x);
@@ -177,19 +180,19 @@ __global__ void __launch_bounds__(kpg::NT) kv_prompt_kernel(const __grid_constan
 #pragma unroll
             for (int c = 0; c < NC; ++c) {
                 const int e = c * 64 + tx * 4;
-                float acc[4][4] = {};
+                float acc[R][4] = {};
                 if (e < L.dp) {
                     if (!odd) {
 #pragma unroll 2
                         for (int k = 0; k < KT; k += 4) {
-                            float4 p[4];
+                            float4 p[R];
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) p[i] = *reinterpret_cast<const float4*>(sP + (ty * 4 + i) * PP + k);
+                            for (int i = 0; i < R; ++i) p[i] = *reinterpret_cast<const float4*>(sP + (ty * R + i) * PP + k);
 #pragma unroll
                             for (int y = 0; y < 4; ++y) {
                                 const float4 v = *reinterpret_cast<const float4*>(sV + (k + y) * pitch + e);
 #pragma unroll
-                                for (int i = 0; i < 4; ++i) {
+                                for (int i = 0; i < R; ++i) {
                                     const float x = y == 0 ? p[i].x : y == 1 ? p[i].y : y == 2 ? p[i].z : p[i].w;
                                     acc[i][0] = fmaf(x, v.x, acc[i][0]), acc[i][1] = fmaf(x, v.y, acc[i][1]);
                                     acc[i][2] = fmaf(x, v.z, acc[i][2]), acc[i][3] = fmaf(x, v.w, acc[i][3]);
@@ -201,9 +204,9 @@ __global__ void __launch_bounds__(kpg::NT) kv_prompt_kernel(const __grid_constan
                         for (int k = 0; k < KT; ++k) {
                             const float4 v = *reinterpret_cast<const float4*>(sV + k * pitch + e);
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) {
+                            for (int i = 0; i < R; ++i) {
                                 if (t * KT + k > last[i]) continue;
-                                const float x = sP[(ty * 4 + i) * PP + k];
+                                const float x = sP[(ty * R + i) * PP + k];
                                 acc[i][0] = fmaf(x, v.x, acc[i][0]), acc[i][1] = fmaf(x, v.y, acc[i][1]);
                                 acc[i][2] = fmaf(x, v.z, acc[i][2]), acc[i][3] = fmaf(x, v.w, acc[i][3]);
                             }
@@ -211,9 +214,36 @@ __global__ void __launch_bounds__(kpg::NT) kv_prompt_kernel(const __grid_constan
                     }
                 }
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
+                for (int i = 0; i < R; ++i)
 #pragma unroll
                     for (int y = 0; y < 4; ++y) o[c][i][y] = fmaf(o[c][i][y], f[i], acc[i][y]);
+            }
+            if constexpr (TAIL) {
+                float acc[R] = {};
+                const int e = NC * 64 + tx;
+                if (e < L.dp) {
+                    if (!odd) {
+#pragma unroll 2
+                        for (int k = 0; k < KT; k += 4) {
+                            float v[4];
+#pragma unroll
+                            for (int y = 0; y < 4; ++y) v[y] = sV[(k + y) * pitch + e];
+#pragma unroll
+                            for (int i = 0; i < R; ++i) {
+                                const float4 p = *reinterpret_cast<const float4*>(sP + (ty * R + i) * PP + k);
+                                acc[i] = fmaf(p.x, v[0], fmaf(p.y, v[1], fmaf(p.z, v[2], fmaf(p.w, v[3], acc[i]))));
+                            }
+                        }
+                    } else {
+#pragma unroll 1
+                        for (int k = 0; k < KT; ++k)
+#pragma unroll
+                            for (int i = 0; i < R; ++i)
+                                if (t * KT + k <= last[i]) acc[i] = fmaf(sP[(ty * R + i) * PP + k], sV[k * pitch + e], acc[i]);
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < R; ++i) ot[i] = fmaf(ot[i], f[i], acc[i]);
             }
             __syncthreads();  // values and weights are read
             if (t + 1 < w.t1) load(sV, a.v, t + 1, 1);
@@ -224,32 +254,26 @@ __global__ void __launch_bounds__(kpg::NT) kv_prompt_kernel(const __grid_constan
         const bool bad = s_bad, whole = w.whole();
         float* part = a.part + ((int64_t)blockIdx.x * 2 + w.later()) * kp_part_floats(RB, a.d);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int r = ty * 4 + i;
+        for (int i = 0; i < R; ++i) {
+            const int r = ty * R + i;
             if (r >= rows) break;
-            if (whole) {
-                const bool none = bad || l[i] == 0.f;
-                const float inv = none ? 0.f : 1.f / l[i];
-                const int x = r0 + r, tok = x / a.G;
-                const int64_t to = (int64_t)(w.s.first + tok) * a.Hq + w.h * a.G + (x - tok * a.G);
+            const bool none = bad || l[i] == 0.f;
+            const float inv = none ? 0.f : 1.f / l[i];
+            const int x = r0 + r, tok = x / a.G;
+            const int64_t to = (int64_t)(w.s.first + tok) * a.Hq + w.h * a.G + (x - tok * a.G);
+            const auto put = [&](int e, float v) {
+                if (e >= a.d) return;
+                if (whole) store_elem(a.out, to * a.d + e, Store<ST>::code, none ? 0.f : v * inv);
+                else part[(int64_t)e * RB + r] = v;
+            };
 #pragma unroll
-                for (int c = 0; c < NC; ++c)
+            for (int c = 0; c < NC; ++c)
 #pragma unroll
-                    for (int y = 0; y < 4; ++y) {
-                        const int e = c * 64 + tx * 4 + y;
-                        if (e < a.d) store_elem(a.out, to * a.d + e, Store<ST>::code, none ? 0.f : o[c][i][y] * inv);
-                    }
-                if (tx == 0 && a.lse) a.lse[to] = none ? -INFINITY : (m[i] + log2f(l[i])) * LN2;
-            } else {
-#pragma unroll
-                for (int c = 0; c < NC; ++c)
-#pragma unroll
-                    for (int y = 0; y < 4; ++y) {
-                        const int e = c * 64 + tx * 4 + y;
-                        if (e < a.d) part[(int64_t)e * RB + r] = o[c][i][y];
-                    }
-                if (tx == 0) part[RB * a.d + r] = m[i], part[RB * a.d + RB + r] = bad ? -1.f : l[i];
-            }
+                for (int y = 0; y < 4; ++y) put(c * 64 + tx * 4 + y, o[c][i][y]);
+            if (TAIL) put(NC * 64 + tx, ot[i]);
+            if (tx != 0) continue;
+            if (!whole) part[RB * a.d + r] = m[i], part[RB * a.d + RB + r] = bad ? -1.f : l[i];
+            else if (a.lse) a.lse[to] = none ? -INFINITY : (m[i] + log2f(l[i])) * LN2;
         }
         if (tid == 0) {
             if (bad) set_error(a.dev_err, KV_DEVERR_PAGE);

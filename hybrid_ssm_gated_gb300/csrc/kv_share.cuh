@@ -17,6 +17,9 @@ constexpr int PLAN_NT = 1024;
 
 }  // namespace kvs
 
+// Pages of `len` entries (len + page_size may not fit 32 bits).
+__device__ __forceinline__ int kv_pages_of(int len, int page_size) { return len > 0 ? (len - 1) / page_size + 1 : 0; }
+
 // Entries 0 .. n - 1 of head h of page `from` to page `to`, by the whole block. Piece: what rows are copied by.
 template <typename Piece>
 __device__ __forceinline__ void kv_copy_head(const KvArgs& a, int from, int to, int h, int n) {
@@ -66,7 +69,7 @@ __global__ void __launch_bounds__(kvs::NT) kv_fork_kernel(const __grid_constant_
         len = a.lengths[from];
         if (len < 0 || (int64_t)len > (int64_t)a.max_pages * a.page_size) err = KV_DEVERR_LENGTH;
     }
-    const int pages = err ? 0 : (len + a.page_size - 1) / a.page_size;
+    const int pages = err ? 0 : kv_pages_of(len, a.page_size);
     const int32_t* old = a.page_table + (int64_t)from * a.max_pages;
     const int32_t* fresh = new_pages + (int64_t)i * a.max_pages;
     bool bad = false;
@@ -114,7 +117,7 @@ __global__ void __launch_bounds__(kvs::NT) kv_mark_kernel(const __grid_constant_
         const int len = a.lengths[s];
         int err = 0;
         if (len < 0 || (int64_t)len > (int64_t)a.max_pages * a.page_size) err = KV_DEVERR_LENGTH;
-        const int pages = err ? 0 : (len + a.page_size - 1) / a.page_size;
+        const int pages = err ? 0 : kv_pages_of(len, a.page_size);
         const int32_t* row = a.page_table + s * a.max_pages;
         for (int j = lane; j < pages; j += 32) {
             const int x = row[j];
@@ -190,7 +193,7 @@ __global__ void __launch_bounds__(kvs::NT) kv_pages_kernel(const __grid_constant
     const int lane = threadIdx.x & 31;
     const int64_t warps = (int64_t)(gridDim.x - copiers) * (NT / 32);
     for (int64_t s = (int64_t)(blockIdx.x - copiers) * (NT / 32) + (threadIdx.x >> 5); s < a.num_slots; s += warps) {
-        const int pages = (a.lengths[s] + a.page_size - 1) / a.page_size;
+        const int pages = kv_pages_of(a.lengths[s], a.page_size);
         int32_t* row = const_cast<int32_t*>(a.page_table) + s * a.max_pages;
         for (int j = lane; j < pages; j += 32) {
             const int x = row[j];
