@@ -26,7 +26,8 @@
 //              heads in it);
 //   products   two warps, an elected thread of each. QT = 2: one a tile of rows, which
 //              issues all of its products in order: S right behind the last product that
-//              reads the P it is written over, waiting for nobody. QT = 1: one for S, one
+//              reads the P it is written over, waiting for nobody (the tensor cores take a
+//              thread's products in the order of their issue). QT = 1: one for S, one
 //              for O. (A commit holds a thread up for 120 to 210 cycles, one right behind
 //              another for 12: a thread for both tiles of rows took 4100 cycles a tile of
 //              keys where the products take 2048, one for S and O of one tile 2800 where
@@ -35,6 +36,20 @@
 // weights' first half is formed against the last tile's reference while the maximum is
 // still looked for (it is formed again where that moved the reference), and is given to
 // the tensor cores while the second half is formed.
+// Bound and measurement (GB300, whole calls with the join). QT = 2: a tile of 256 rows by
+// 128 keys takes some 3300 cycles where its products take 2048: the two tiles' blocks
+// (O of one's last weights, then S of its next keys: 1100 to 1250 cycles) and the way
+// from one thread of products to the other, 300 each. 20000 tokens (32 / 8 heads, d =
+// 128, bf16, 3.28 TFLOP) take 2.27 ms, 1440 TFLOP/s or 0.74 of the measured rate (tensor
+// pipe 50% active at 6000 tokens); chunks of up to 512 tokens behind up to 8192 for 15
+// sequences (fp16, 0.40 TFLOP) 418 us, 950: half-filled last units, and 5 to 9 us a
+// unit's beginning and end. QT = 1: 8192 tokens of 16 / 2 heads, d = 256, 492 us, 1117
+// TFLOP/s. 700 of them 35 us: latency, of which the beginning (lengths, places, first
+// loads) is 6, a unit's end 3, the join 5.
+// Measured and not taken (20000 tokens): sixteen softmax warps, two threads a row (2700
+// us: 96 registers); one thread of products for both tiles (2690); the turn passed on
+// ahead of S (2630) or amid it (2300 to 2440); weights given over at once (2460) or in
+// three parts (2680); scalar instead of packed exponents' arithmetic (2640).
 // A tile of which some row sees a part ("mixed") has its values looked through by the
 // softmax threads: rows of V past the sequence's end become zero, and so does what is
 // not finite (0 x NaN would reach rows that do not see it); the epilogue adds the
