@@ -64,6 +64,7 @@ struct KvArgs {
     const int32_t* cu;  // row offsets of the packed sequences
     int total;
     int extra;  // keys that a unit's start and end cost as much as
+    int least;  // keys of a CTA's range at least: two tiles, and over a tile and a block's tokens
     int tile_rows, tile_places, part_rows;  // rows of a tile of a unit, places for them, places of a unit
 };
 

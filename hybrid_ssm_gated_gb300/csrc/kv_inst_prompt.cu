@@ -61,7 +61,7 @@ cudaError_t kv_prompt_workspace(KvArgs& a, int64_t& bytes) {
 
 cudaError_t launch_kv_prompt(KvArgs& a, bool vec, cudaStream_t stream) {
     int64_t grid = 0;
-    a.extra = 128;  // (two tiles)
+    a.extra = 128, a.least = 256;  // (two tiles; over 64 + 64)
     a.row_block = a.tile_rows = a.tile_places = a.part_rows = kpg::RB;
     cudaError_t e = wave(a, grid);
     if (e != cudaSuccess) return e;

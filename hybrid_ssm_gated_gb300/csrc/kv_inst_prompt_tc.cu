@@ -61,6 +61,7 @@ cudaError_t launch_kv_prompt_tc(KvArgs& a, cudaStream_t stream) {
         !encode(maps.q, a.dtype, a.q.p, a.d, a.Hq, a.q.head, a.total, a.q.node, 1, a.d, a.G, tokens))
         return cudaErrorNotSupported;
     a.extra = QT == 2 ? 512 : 384;  // (measured: 9 us where a tile of 128 takes 2, 5 to 6 where one of 64 takes 1)
+    a.least = QT == 2 ? 512 : 256;  // (over 128 + 256, 64 + 128)
     a.tile_rows = tokens * a.G, a.tile_places = kpt::TILE, a.row_block = QT * a.tile_rows, a.part_rows = QT * kpt::TILE;
     a.border = reinterpret_cast<char*>(a.part) + kp_part_bytes(di.sms, a.part_rows, a.d);
     if (a.dtype == GDN_BF16)

@@ -49,8 +49,6 @@ __device__ __forceinline__ KpSeq kp_seq(const KvArgs& a, int b) {
     return s;
 }
 
-constexpr int KP_LEAST = 256;  // keys of a CTA's range at least
-
 // Blocks of a sequence, and the length of the line before block i of a key head.
 __device__ __forceinline__ int kp_blocks(const KvArgs& a, const KpSeq& s) {
     return s.slot < 0 ? 0 : (int)((uint32_t)(s.n * a.G + a.row_block - 1) / (uint32_t)a.row_block);
@@ -135,7 +133,7 @@ __device__ __forceinline__ void kp_locate(const KvArgs& a, KpScan<NT, KEEP>& sc)
         if (w < warp) before += sc.warp_sum[w];
         total += sc.warp_sum[w];
     }
-    const long long most = kv_div(total, (long long)KP_LEAST * a.G);
+    const long long most = kv_div(total, (long long)a.least * a.G);
     const int parts = (int)(most < 1 ? 1 : most < gridDim.x ? most : gridDim.x);
     const long long q = kv_div(total, parts);
     const int r = (int)(total - q * parts), c = blockIdx.x;
@@ -246,7 +244,8 @@ __device__ __forceinline__ void kp_border(const KvArgs& a, const KpScan<NT, KEEP
     const long long size = kp_before(a, w.s, w.i + 1) - kp_before(a, w.s, w.i), at = sc.mark[1].off - u0;
     const auto start = [&](int x) { return sc.q * x + min(x, sc.r); };
     const int c = blockIdx.x;
-    // a range is longer than two tiles: each CTA whose range begins inside the unit has one of its tiles
+    // each CTA whose range begins inside the unit has one of its tiles: a range is as long as two tiles, and longer than
+    // the last tile and what the line counts behind it (a block's rows that the sequence has no more)
     for (int x = c + 1; x < sc.parts; ++x) {
         ++k.n;
         if (at + start(x + 1) - start(c + 1) >= size) break;

@@ -28,10 +28,12 @@ __device__ __forceinline__ int kv_pages_of(int len, int page_size) { return len 
 template <typename Piece>
 __device__ __forceinline__ void kv_copy_head(const KvArgs& a, int from, int to, int h, int n) {
     using namespace kvs;
-    const int per = a.d * dtype_size(a.dtype) / (int)sizeof(Piece), esz = dtype_size(a.dtype), rows = 2 * n;
+    const int per = a.d * dtype_size(a.dtype) / (int)sizeof(Piece), esz = dtype_size(a.dtype);
+    const uint32_t rows = 2u * n;
     // piece i: row i / per (keys, then values), and NT pieces further each time
     const int dr = NT / per, dc = NT - dr * per;
-    int r = (int)threadIdx.x / per, c = (int)threadIdx.x - r * per;
+    uint32_t r = threadIdx.x / per;
+    int c = (int)(threadIdx.x - r * per);
     while (r < rows) {
         Piece x[AHEAD];
         Piece* out[AHEAD];
@@ -39,7 +41,7 @@ __device__ __forceinline__ void kv_copy_head(const KvArgs& a, int from, int to, 
         for (int y = 0; y < AHEAD; ++y) {
             out[y] = nullptr;
             if (r < rows) {
-                const bool val = r >= n;
+                const bool val = r >= (uint32_t)n;
                 const KvPages& p = val ? a.v : a.k;
                 const int64_t at = (int64_t)h * p.head + (int64_t)(val ? r - n : r) * p.token;
                 char* base = static_cast<char*>(const_cast<void*>(p.p));
