@@ -49,10 +49,15 @@ cudaError_t launch_kv_compact(const KvArgs& a, int32_t* ws, int32_t* used, bool 
         return blocks < 1 ? 1 : blocks < top ? blocks : top;
     };
     const int64_t slots = (a.num_slots + kvs::NT / 32 - 1) / (kvs::NT / 32);
-    kv_clear_kernel<<<(unsigned)most((p.words + 8 + kvs::NT - 1) / kvs::NT, 4), kvs::NT, 0, stream>>>(ws, p.words);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    if ((e = behind(kv_mark_kernel, most(slots, 4), kvs::NT, stream, a, p)) != cudaSuccess) return e;
-    if ((e = behind(kv_plan_kernel, 1, kvs::PLAN_NT, stream, p, a.num_pages, used)) != cudaSuccess) return e;
+    if (a.num_pages <= KV_SMALL_PAGES && a.num_slots * a.max_pages <= KV_SMALL_ENTRIES) {
+        kv_plan_kernel<true><<<1, kvs::PLAN_NT, 0, stream>>>(a, p, used);
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    } else {
+        kv_clear_kernel<<<(unsigned)most((p.words + 8 + kvs::NT - 1) / kvs::NT, 4), kvs::NT, 0, stream>>>(ws, p.words);
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        if ((e = behind(kv_mark_kernel, most(slots, 4), kvs::NT, stream, a, p)) != cudaSuccess) return e;
+        if ((e = behind(kv_plan_kernel<false>, 1, kvs::PLAN_NT, stream, a, p, used)) != cudaSuccess) return e;
+    }
     // (no more than half of the pages can move)
     const int copiers = (int)most(a.num_pages / 2 * a.Hkv, 7), tables = (int)most(slots, 1);
     return behind(vec ? kv_pages_kernel<uint4> : kv_pages_kernel<uint16_t>, copiers + tables, kvs::NT, stream, a, p, copiers);

@@ -262,3 +262,16 @@ def test_captured_compaction_behind_a_fork():
         g.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(getattr(p, n), x) for n, x in want.items()) and int(used) == 13 and int(p.err) == 0
+
+
+@pytest.mark.parametrize("extra_slots,spare", [(6, 50), (4000, 50), (6, (1 << 18) + 5)])
+def test_compact_forms(extra_slots, spare):
+    """Tables and pools that one block marks, and those that a grid marks: many slots, many pages."""
+    lens = [0 if i % 3 == 2 else 3 + 7 * i for i in range(40)]
+    p = Pool(69, "bf16", lens, Hkv=1, d=8, page=4, spare=spare, extra_slots=extra_slots)
+    assert compact(p)[1] > 0
+    p.lengths[p.slots[5]] = -4
+    p.sync()
+    used = torch.zeros(1, dtype=torch.int32, device="cuda")
+    kv.kv_compact(p.cache, used, p.err, kv.kv_compact_workspace(p.cache))
+    assert int(used.item()) == -1 and int(p.err.item()) == kv.DEVERR_LENGTH
