@@ -6,7 +6,7 @@
 // is one head of one page: its keys, values, weights and stamps, eight 16-byte pieces in
 // flight a thread. 32 forks with pages of their own (fp16, 0.69 GB read and written) take
 // 119 us, 5.8 TB/s or 0.85 of the measured copy bandwidth; a compaction that moves 0.31 GB
-// 67 us, of which 12 are the four kernels' beginnings and the plan; a fork that shares
+// 66 us, of which 12 are the kernels' beginnings and the plan; a fork that shares
 // all pages but the last 5 us.
 #pragma once
 
@@ -139,7 +139,8 @@ __global__ void __launch_bounds__(kvs::NT) kv_mark_kernel(const __grid_constant_
 }
 
 // One block: the number of held pages U, then the lists of holes below U and of held pages from U on. SMALL: it marks the
-// pages too, in shared memory, where tables and pool are small (two kernels less ahead of it: 11.2 -> 9.7 us for 4 sequences of 700 entries).
+// pages too, in shared memory, where tables and pool are small (two kernels less ahead of it: 9.7 us instead of 11.2 for
+// 4 sequences of 700 entries).
 constexpr int KV_SMALL_PAGES = 1 << 18, KV_SMALL_ENTRIES = 1 << 14;
 template <bool SMALL>
 __global__ void __launch_bounds__(kvs::PLAN_NT) kv_plan_kernel(const __grid_constant__ KvArgs a, const KvPlan p, int32_t* used) {
