@@ -1,10 +1,11 @@
 // kv_prompt_join.cuh -- joins the partial results of prompt units that the ranges of
 // several CTAs share: with m = max m_c, out = sum_c 2^{m_c - m} O_c / sum_c 2^{m_c - m} l_c.
 //
-// Bound by latency: a few megabytes, read once, in three dependent loads (the border's
-// record; maxima and sums; outputs). So a block is 32 rows by 64 outputs of one border, a
-// warp 16 of these, a lane a row, with all 16 loads of a part in flight. (Four jobs of 8
-// outputs a warp, one after another, took 12 to 15 us behind a call of 20.)
+// Bound by latency: a few tens of megabytes at most, read once, in two dependent loads (the
+// border's record; maxima, sums and outputs of two parts at a time, over a running
+// maximum). So a warp is 32 rows, a lane each, by eight outputs, with few registers, that
+// many of them hide each other's waits: 7 us behind 700 tokens of d = 256, 11 behind 152 CTAs with 256 rows of d = 128 each (40 MB). (Sixteen outputs behind maxima of all
+// parts, 96 registers: 29 us there.)
 #pragma once
 
 #include "kv_prompt.cuh"
@@ -13,13 +14,13 @@ namespace gdn {
 
 namespace kpj {
 
-constexpr int NT = 128, COLS = 64, MINE = COLS / (NT / 32);
+constexpr int NT = 128, MINE = 8, COLS = MINE * (NT / 32);
 // Blocks of a border.
 __host__ __device__ inline int share(int places, int d) { return places / 32 * ((d + COLS - 1) / COLS); }
 
 }  // namespace kpj
 
-__global__ void __launch_bounds__(kpj::NT) kp_join_kernel(const __grid_constant__ KvArgs a) {
+__global__ void __launch_bounds__(kpj::NT, 10) kp_join_kernel(const __grid_constant__ KvArgs a) {
     using namespace kpj;
     const int RB = a.part_rows, cols = (a.d + COLS - 1) / COLS, each = RB / 32 * cols;
     const int c = blockIdx.x / each, x = blockIdx.x - c * each, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -28,23 +29,22 @@ __global__ void __launch_bounds__(kpj::NT) kp_join_kernel(const __grid_constant_
     kv_grid_wait();
     const KpBorder k = static_cast<const KpBorder*>(a.border)[c];
     if (k.n == 0 || in_tile >= a.tile_rows || of_unit >= k.rows || e0 >= a.d) return;
-    const int64_t size = kp_part_floats(RB, a.d);
-    const auto part = [&](int j) { return a.part + ((int64_t)(c + j) * 2 + (j == 0)) * size + r; };
-    const int64_t stat = (int64_t)RB * a.d;
-    float m = -INFINITY, l = 0.f;
+    const int64_t size = kp_part_floats(RB, a.d), stat = (int64_t)RB * a.d;
+    const float* p = a.part + ((int64_t)c * 2 + 1) * size + r;  // (the first part is its CTA's second, the others their CTAs' first)
+    const int mine = min(MINE, a.d - e0);
+    float m = -INFINITY, l = 0.f, o[MINE] = {};
     bool refused = false;
-#pragma unroll 4
-    for (int j = 0; j < k.n; ++j) m = fmaxf(m, part(j)[stat]);
-    const float base = m == -INFINITY ? 0.f : m;
-    float o[MINE] = {};
 #pragma unroll 2
-    for (int j = 0; j < k.n; ++j) {
-        const float* p = part(j);
-        const float sum = p[stat + RB], f = kv_ex2(p[stat] - base);
-        l = fmaf(sum, f, l), refused = refused || sum == -1.f;
+    for (int j = 0; j < k.n; ++j, p += j == 1 ? size : 2 * size) {
+        const float mj = p[stat], sum = p[stat + RB];
+        float x[MINE];
+        const float* q = p + (int64_t)e0 * RB;
 #pragma unroll
-        for (int e = 0; e < MINE; ++e)
-            if (e0 + e < a.d) o[e] = fmaf(p[(int64_t)(e0 + e) * RB], f, o[e]);
+        for (int e = 0; e < MINE; ++e) x[e] = e < mine ? q[e * RB] : 0.f;
+        const float top = fmaxf(m, mj), base = top == -INFINITY ? 0.f : top, f = kv_ex2(m - base), g = kv_ex2(mj - base);
+        l = fmaf(l, f, sum * g), m = top, refused = refused || sum == -1.f;
+#pragma unroll
+        for (int e = 0; e < MINE; ++e) o[e] = fmaf(o[e], f, x[e] * g);
     }
     if (refused) l = 0.f;
     const float inv = l == 0.f ? 0.f : 1.f / l;
