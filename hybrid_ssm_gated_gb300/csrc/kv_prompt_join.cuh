@@ -4,8 +4,9 @@
 // Bound by latency: a few tens of megabytes at most, read once, in two dependent loads (the
 // border's record; maxima, sums and outputs of two parts at a time, over a running
 // maximum). So a warp is 32 rows, a lane each, by eight outputs, with few registers, that
-// many of them hide each other's waits: 7 us behind 700 tokens of d = 256, 11 behind 152 CTAs with 256 rows of d = 128 each (40 MB). (Sixteen outputs behind maxima of all
-// parts, 96 registers: 29 us there.)
+// many of them hide each other's waits: 7 us behind 700 tokens of d = 256, 11 behind 152
+// CTAs with 256 rows of d = 128 each (40 MB). (Sixteen outputs behind maxima of all parts,
+// 96 registers: 29 us there.)
 #pragma once
 
 #include "kv_prompt.cuh"
