@@ -40,12 +40,12 @@
 // 128 keys takes some 3300 cycles where its products take 2048: the two tiles' blocks
 // (O of one's last weights, then S of its next keys: 1100 to 1250 cycles) and the way
 // from one thread of products to the other, 300 each. 20000 tokens (32 / 8 heads, d =
-// 128, bf16, 3.28 TFLOP) take 2.27 ms, 1440 TFLOP/s or 0.74 of the measured rate (tensor
+// 128, bf16, 3.28 TFLOP) take 2.23 ms, 1470 TFLOP/s or 0.75 of the measured rate (tensor
 // pipe 50% active at 6000 tokens); chunks of up to 512 tokens behind up to 8192 for 15
-// sequences (fp16, 0.40 TFLOP) 418 us, 950: half-filled last units, and 5 to 9 us a
+// sequences (fp16, 0.40 TFLOP) 403 us, 990: half-filled last units, and 5 to 9 us a
 // unit's beginning and end. QT = 1: 8192 tokens of 16 / 2 heads, d = 256, 492 us, 1117
-// TFLOP/s. 700 of them 35 us: latency, of which the beginning (lengths, places, first
-// loads) is 6, a unit's end 3, the join 5.
+// TFLOP/s. 700 of them 30 us: latency, of which the beginning (lengths, places, first
+// loads) is 6, a unit's end 3, the join 7.
 // Measured and not taken (20000 tokens): sixteen softmax warps, two threads a row (2700
 // us: 96 registers); one thread of products for both tiles (2690); the turn passed on
 // ahead of S (2630) or amid it (2300 to 2440); weights given over at once (2460) or in
