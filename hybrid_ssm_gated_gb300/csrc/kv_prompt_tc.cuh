@@ -43,7 +43,7 @@
 // 128, bf16, 3.28 TFLOP) take 2.23 ms, 1470 TFLOP/s or 0.75 of the measured rate (tensor
 // pipe 50% active at 6000 tokens); chunks of up to 512 tokens behind up to 8192 for 15
 // sequences (fp16, 0.40 TFLOP) 403 us, 990: half-filled last units, and 5 to 9 us a
-// unit's beginning and end. QT = 1: 8192 tokens of 16 / 2 heads, d = 256, 492 us, 1117
+// unit's beginning and end. QT = 1: 8192 tokens of 16 / 2 heads, d = 256, 492 to 510 us, 1077 to 1117
 // TFLOP/s. 700 of them 30 us: latency, of which the beginning (lengths, places, first
 // loads) is 6, a unit's end 3, the join 7.
 // Measured and not taken (20000 tokens): sixteen softmax warps, two threads a row (2700
