@@ -346,9 +346,11 @@ int kv_append(const kv_cache* cache, int32_t B, int32_t total, int32_t Hq, const
     if ((rc = check_call(fn, slots, dev_err))) return rc;
     if (!cu_seqlens) return fail(GDN_ERR_NULL, "%s: cu_seqlens is NULL", fn);
     if (!aligned_to(cu_seqlens, 4) || !aligned_to(positions, 4)) return fail(GDN_ERR_ALIGN, "%s: cu_seqlens or positions misaligned", fn);
-    if ((rc = check_rows(fn, "k", k, cache->dtype)) || (rc = check_rows(fn, "v", v, cache->dtype))) return rc;
-    for (const kv_rows* r : {q, q_out})
-        if (r && (rc = check_rows(fn, "q or q_out", r, cache->dtype))) return rc;
+    if (total > 0) {  // (without a row none has an address; slots, lengths and offsets are looked at all the same)
+        if ((rc = check_rows(fn, "k", k, cache->dtype)) || (rc = check_rows(fn, "v", v, cache->dtype))) return rc;
+        for (const kv_rows* r : {q, q_out})
+            if (r && (rc = check_rows(fn, "q or q_out", r, cache->dtype))) return rc;
+    }
     if (cache->stamps && !cache->counts) return fail(GDN_ERR_NULL, "%s: a cache with stamps needs counts", fn);
     gdn::KvArgs c = args_of(cache, B, slots, dev_err);
     c.cu = cu_seqlens, c.total = total;
@@ -395,14 +397,16 @@ int kv_prompt_attention(const kv_cache* cache, int32_t B, int32_t total, int32_t
     if ((rc = check_heads(fn, cache, Hq, scale)) || (rc = check_prompt(fn, cache, B, total, Hq))) return rc;
     if (B == 0) return GDN_OK;
     if ((rc = check_call(fn, slots, dev_err))) return rc;
-    if (!cu_seqlens || !out || !workspace) return fail(GDN_ERR_NULL, "%s: cu_seqlens, out or workspace is NULL", fn);
-    if ((rc = check_rows(fn, "q", q, cache->dtype))) return rc;
+    if (!cu_seqlens || (total > 0 && !out) || !workspace)
+        return fail(GDN_ERR_NULL, "%s: cu_seqlens, out or workspace is NULL", fn);
+    if (total > 0 && (rc = check_rows(fn, "q", q, cache->dtype))) return rc;
     if (!aligned_to(cu_seqlens, 4) || !aligned_to(lse, 4) || !aligned_to(workspace, 16) ||
         !aligned_to(out, gdn::dtype_size(cache->dtype)))
         return fail(GDN_ERR_ALIGN, "%s: cu_seqlens, out, lse or workspace misaligned", fn);
     gdn::KvArgs a = args_of(cache, B, slots, dev_err);
     a.cu = cu_seqlens, a.total = total, a.Hq = Hq, a.G = Hq / cache->Hkv;
-    a.q = rows_of(q), a.scale = scale, a.out = out, a.lse = lse, a.part = static_cast<float*>(workspace);
+    if (total > 0) a.q = rows_of(q);
+    a.scale = scale, a.out = out, a.lse = lse, a.part = static_cast<float*>(workspace);
     int64_t need = 0;
     cudaError_t e = prompt_workspace(a, need);
     if (e != cudaSuccess) return launched(e, fn);

@@ -179,7 +179,9 @@ int64_t kv_evict_workspace(const kv_cache* cache, int32_t B, int32_t budget);
  * cu_seqlens[b] .. cu_seqlens[b+1]-1 of [total][heads][d] activations, whose
  * kv_rows take `node` as the stride of a row (`seq` is not looked at).
  * cu_seqlens [B + 1] int32 (device), 0 <= cu_seqlens[b] <= cu_seqlens[b+1] <=
- * total. Rows of no sequence are neither read nor written.
+ * total. Rows of no sequence are neither read nor written. total may be 0 (a
+ * step in which no sequence has a row): q, k, v and the outputs are not looked
+ * at then, slots, lengths and offsets are.
  */
 
 /*
