@@ -314,6 +314,8 @@ def kv_norm_rotate(rotary: Rotary, positions, q=None, k=None, q_out=None, k_out=
     if like is None or like.dim() != 4 or like.dtype not in DTYPE_CODE:
         raise ValueError("kv: q or k must be a tensor [B, T, heads, d] of a dtype of the cache's")
     device, dtype = rotary.device, like.dtype
+    if device < 0:  # (tensors of the host would pass the checks of one device below)
+        raise ValueError("kv: the rotary must lie on a CUDA device")
     B, T, _, d = like.shape
     rq, ro, Hq = _side(q, q_out, "q", dtype, device, B, T, d)
     rk, rp, Hkv = _side(k, k_out, "k", dtype, device, B, T, d)
