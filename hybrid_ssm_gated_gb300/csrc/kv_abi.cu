@@ -340,7 +340,9 @@ int kv_append(const kv_cache* cache, int32_t B, int32_t total, int32_t Hq, const
     if (rc) return rc;
     if (total < 0 || total > 0x7fffff00) return fail(GDN_ERR_SHAPE, "%s: total=%d", fn, total);
     if (!q != !q_out || (q && !rotary)) return fail(GDN_ERR_NULL, "%s: q, q_out and rotary come together", fn);
-    if (q && (Hq < 1 || Hq > 1 << 24)) return fail(GDN_ERR_SHAPE, "%s: Hq=%d", fn, Hq);
+    // (rows of a block, up to 16 tokens' heads, are counted in 32 bits)
+    if ((q && (Hq < 1 || Hq > 1 << 24)) || cache->Hkv > 1 << 24)
+        return fail(GDN_ERR_SHAPE, "%s: Hq=%d, Hkv=%d", fn, Hq, cache->Hkv);
     if (rotary && (rc = check_rotary(fn, rotary, cache->d, true))) return rc;
     if (B == 0) return GDN_OK;
     if ((rc = check_call(fn, slots, dev_err))) return rc;

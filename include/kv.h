@@ -219,7 +219,7 @@ typedef struct kv_rotary {
  * decode step's single ones too), ahead of kv_tree_attention.
  * q, q_out   [B][T][Hq][d], k, k_out [B][T][Hkv][d], of `dtype`; q or k may be
  *            NULL with its output. An output may be its input (the same rows),
- *            else they must not overlap.
+ *            else they must not overlap. Hq and Hkv at most 2^24.
  * positions  [axes][B][T] int32; NULL where rot is 0.
  */
 int kv_norm_rotate(const kv_rotary* rotary, int32_t dtype, int32_t B, int32_t T, int32_t Hq, int32_t Hkv, int32_t d,
@@ -238,7 +238,8 @@ int kv_norm_rotate(const kv_rotary* rotary, int32_t dtype, int32_t B, int32_t T,
  * lacks one (KV_DEVERR_PAGE) keeps its length and count, and what its other
  * new entries' places held is lost. q_out rows of padding and of sequences
  * refused for their slot or length are zero. Offsets that decrease or pass
- * `total` anywhere (GDN_DEVERR_SEQLEN) refuse the whole call.
+ * `total` anywhere (GDN_DEVERR_SEQLEN) refuse the whole call. Hq and Hkv are
+ * at most 2^24.
  */
 int kv_append(const kv_cache* cache, int32_t B, int32_t total, int32_t Hq, const int32_t* slots,
               const int32_t* cu_seqlens, const kv_rows* k, const kv_rows* v, const kv_rotary* rotary,
