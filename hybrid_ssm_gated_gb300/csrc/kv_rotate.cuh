@@ -3,8 +3,8 @@
 //
 // Mathematics. y = x rsqrt(mean x^2 + eps) (w + offset); pairs of y turned by
 // position times a frequency. The frequency is a 64-bit fraction of a turn, so
-// that the product's low 64 bits are the angle modulo a turn, off by 2^-65 turns
-// a position; its upper 32 bits, as a signed number, go to sincospif.
+// that the product's low 64 bits are that fraction's angle modulo a turn, exactly;
+// its upper 32 bits, as a signed number, go to sincospif.
 //
 // Shape: a block takes a few tokens. Their angles' cosines and sines are formed
 // once, into shared memory (rot / 2 pairs a token serve all its heads), beside the

@@ -193,7 +193,8 @@ int64_t kv_evict_workspace(const kv_cache* cache, int32_t B, int32_t budget);
  *     z_1 = y_1 cos a - y_2 sin a,  z_2 = y_1 sin a + y_2 cos a
  * Pairs are elements i and i + rot / 2, or 2i and 2i + 1 (interleaved). FP32
  * arithmetic, one rounding at the end; angles are formed in whole numbers
- * modulo a turn, so that far positions lose nothing.
+ * modulo a turn, so that far positions lose nothing of what `turns` says (which
+ * is off by 2^-65 turns a position where it is the nearest to a frequency).
  * q_norm, k_norm       FP32 weights of queries and keys, head h's at p + h *
  *                      head stride (0: one row for all heads), d of them;
  *                      NULL: that side is not normed.
