@@ -24,7 +24,7 @@ cudaError_t launch(const KvArgs& a, const kpt::Maps& maps, int boxes, int box_ro
 
 // Tiles of query rows a unit: two where their outputs fit tensor memory, there are units for every SM, and the sequences
 // have rows for them in the mean. (32 / 8 heads, d = 128: 2048 tokens, 256 units of two tiles, take 61 us so and 70 with
-// one; 512 tokens, 64 such units, 25 and 22.)
+// one; 1024 tokens, 128 such units, 35.3 and 34.9; 512 tokens, 64, 25 and 22.)
 int tiles_of(const KvArgs& a, int sms) {
     if (a.d > 128) return 1;
     const int64_t tokens = 2 * (kpt::TILE / a.G);

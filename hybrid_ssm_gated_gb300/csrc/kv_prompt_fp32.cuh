@@ -15,9 +15,15 @@
 // its 16 threads. The keys of the
 // next tile are on their way (cp.async where the cache is FP32 and its rows allow
 // 16-byte copies) while weights and outputs form, the values while scores form.
-// Bound by the FP32 pipe and shared-memory loads (12 loads of 16 bytes for 128
-// products a thread; four rows by four keys of 256 threads, 8 for 64, took 192 us for
-// three prompts of up to 1200 rows (8 / 4 heads, d = 80, 3.4 GFLOP) where these take 176).
+// Bound by latency at two warps a scheduler (199 registers and 82 KB at d = 80: two CTAs
+// a SM): 47% of issue slots, 34% of the FP32 pipe and 38% of shared memory's are used; for
+// each instruction that it issues a warp waits 0.74 cycles for shared-memory loads, 0.56
+// for its last instruction and 0.32 for the next one's code. Three prompts of up to 1200 rows (8 / 4 heads, d = 80, 3.4
+// GFLOP) take 176 us, 19 TFLOP/s, where four rows by four keys of 256 threads took 192;
+// 2000 tokens take 164 us at d = 64, 249 at 96, 343 at 128, 748 at 256 (22 to 25 TFLOP/s).
+// What 16-bit caches that TMA cannot address cost: 1200 tokens of 8 / 4 heads, d = 128,
+// 166 us in pages of 4 entries and 22 on the tensor cores in pages of 16. (255 registers
+// from d = 81 on; above 208 they spill 176 bytes.)
 #pragma once
 
 #include "kv_attn.cuh"

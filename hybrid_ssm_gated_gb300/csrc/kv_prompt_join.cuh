@@ -7,6 +7,9 @@
 // many of them hide each other's waits: 7 us behind 700 tokens of d = 256, 11 behind 152
 // CTAs with 256 rows of d = 128 each (40 MB). (Sixteen outputs behind maxima of all parts,
 // 96 registers: 29 us there.)
+// Maxima are scaled scores rounded to FP32, as the scores of any FP32 softmax: past 2^24
+// two parts whose maxima differ are weighed by a difference of numbers in steps of two and
+// more, while within a part a row's reference is taken off the unscaled scores first.
 #pragma once
 
 #include "kv_prompt.cuh"

@@ -42,10 +42,15 @@
 // from one thread of products to the other, 300 each. 20000 tokens (32 / 8 heads, d =
 // 128, bf16, 3.28 TFLOP) take 2.23 ms, 1470 TFLOP/s or 0.75 of the measured rate (tensor
 // pipe 50% active at 6000 tokens); chunks of up to 512 tokens behind up to 8192 for 15
-// sequences (fp16, 0.40 TFLOP) 403 us, 990: half-filled last units, and 5 to 9 us a
-// unit's beginning and end. QT = 1: 8192 tokens of 16 / 2 heads, d = 256, 492 to 510 us, 1077 to 1117
-// TFLOP/s. 700 of them 30 us: latency, of which the beginning (lengths, places, first
-// loads) is 6, a unit's end 3, the join 7.
+// sequences (fp16, 0.40 TFLOP) 403 to 407 us, 990: half-filled last units (whose empty
+// second tile is computed all the same), and 5 to 9 us a unit's beginning and end. The
+// chain does not shorten with d: 8192 tokens of 32 / 8 heads take 427 us at d = 128 (1289
+// TFLOP/s), 401 at 96, 394 at 80, 378 at 64 (726). QT = 1: 8192 tokens of 16 / 2 heads,
+// d = 256, 492 to 510 us, 1077 to 1117 TFLOP/s; 16000 of them 1773 us, 1183; 8192 at d =
+// 192 415 us (995), at 136 414. 700 of d = 256 30 us: latency, of which the beginning
+// (lengths, places, first loads) is 6, a unit's end 3, the join 7.
+// Registers: QT = 2 spills 644 bytes a thread of stores and 552 of loads at its 168,
+// 1.2% of the instructions that 6000 tokens issue. QT = 1 (200 registers) spills nothing.
 // Measured and not taken (20000 tokens): sixteen softmax warps, two threads a row (2700
 // us: 96 registers); one thread of products for both tiles (2690); the turn passed on
 // ahead of S (2630) or amid it (2300 to 2440); weights given over at once (2460) or in

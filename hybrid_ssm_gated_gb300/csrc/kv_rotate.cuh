@@ -17,7 +17,12 @@
 // 128, bf16, 0.41 GB) take 78.5 us, 5.2 TB/s or 0.77 of the measured copy bandwidth; an
 // append of 37000 tokens of 8 prompts with queries (fp16, 0.93 GB) 182 us, 5.1 TB/s. (A
 // row's token, side and head found anew for each row took 267 instructions a warp and
-// row, and 127 us; places, angles and weights now stay with a group of lanes.)
+// row, and 127 us; places, angles and weights now stay with a group of lanes.) In halves
+// they take 86 us, in fp32 139 (5.9 TB/s). The rotation's 48 registers (for a fifth block
+// a SM) spill 76 bytes of stores and 96 of loads a thread, 1.7% of its instructions.
+// The scalar form is bound by its instructions, a 2-byte load and store an element of a
+// lane: 20000 tokens take 427 us at d = 96 with 24 turned and 418 at d = 80 with 40, 0.7
+// and 0.6 TB/s, where the vector form of the same rows takes 81 and 78 with all turned.
 #pragma once
 
 #include "kv_common.cuh"

@@ -256,9 +256,10 @@ class Rotary:
 
     inv_freq: radians a position of each turned pair (rot / 2 numbers, taken in 64 bits; their fractions of a
     turn are formed in doubles, off by 1.37 x 2^-53 of themselves at most: one radian a position is off by
-    2^-36 turns at position 2^19, by 2^-24 at the end of the positions' type), or None for no rotation; axis: which of the `axes` positions each pair follows (None: the first); interleaved: pairs
-    are neighbours, else elements i and i + rot / 2. q_norm, k_norm: None, or FP32 weights [d], or [heads, d]
-    of each head, to which `offset` is added (1 for weights stored about zero).
+    2^-36 turns at position 2^19, by 2^-24 at the end of the positions' type), or None for no rotation; axis:
+    which of the `axes` positions each pair follows (None: the first); interleaved: pairs are neighbours, else
+    elements i and i + rot / 2. q_norm, k_norm: None, or FP32 weights [d], or [heads, d] of each head, to which
+    `offset` is added (1 for weights stored about zero).
     """
 
     def __init__(self, inv_freq=None, axis=None, axes: int = 1, interleaved: bool = False, q_norm=None, k_norm=None,
@@ -343,7 +344,7 @@ def kv_append(cache: KVCache, slots, cu_seqlens, k, v, dev_err, rotary: Rotary |
     """The prompts' keys and values into the cache: k, v [total, Hkv, d], sequence b's rows cu_seqlens[b] on
     (cu_seqlens [B + 1] int32, on the device). With `rotary`, keys are normed and turned on the way, and q
     [total, Hq, d] into q_out (which may be q); positions [axes, total] int32 ([total] with one axis), None:
-    the sequence's count and on."""
+    the sequence's count and on. total may be 0."""
     B, total, Hkv, d, device = slots.shape[0], k.shape[0], cache.Hkv, cache.d, cache.device
     rk, rv = _packed(k, cache, Hkv, total, "k"), _packed(v, cache, Hkv, total, "v")
     rq = ro = ref = None
@@ -375,7 +376,7 @@ def kv_prompt_workspace(cache: KVCache, B: int, q) -> torch.Tensor:
 def kv_prompt_attention(cache: KVCache, slots, cu_seqlens, q, out, dev_err, workspace, lse=None, scale=None,
                         stream=None) -> None:
     """Causal attention of packed prompts over the cache, after kv_append of the same rows: q [total, Hq, d]; out
-    [total, Hq, d]; lse None or [total, Hq] fp32; workspace from kv_prompt_workspace."""
+    [total, Hq, d]; lse None or [total, Hq] fp32; workspace from kv_prompt_workspace. total may be 0."""
     total, Hq = q.shape[:2]
     B = slots.shape[0]
     rq = _packed(q, cache, Hq, total, "q")

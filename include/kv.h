@@ -262,7 +262,8 @@ int kv_append(const kv_cache* cache, int32_t B, int32_t total, int32_t Hq, const
  * decrease or pass `total` set GDN_DEVERR_SEQLEN, and the sequence is skipped
  * (its rows are not written). Rows whose entries lie in a page outside the
  * pool are zero, as those of the rows of their block.
- * The tensor cores run what they run in kv_tree_attention.
+ * The tensor cores run what they run in kv_tree_attention, where a key head has
+ * at most 128 query heads; above that the FP32 pipe does.
  */
 int kv_prompt_attention(const kv_cache* cache, int32_t B, int32_t total, int32_t Hq, const int32_t* slots,
                         const int32_t* cu_seqlens, const kv_rows* q, float scale, void* out, float* lse,
