@@ -244,10 +244,10 @@ __global__ void __launch_bounds__(kvr::NT, LP > 0 ? (APPEND ? 4 : 5) : 1) kv_rot
                         if (turn && a.interleaved) {
                             if (turned) {
 #pragma unroll
-                            for (int e = 0; e < LANE; e += 2) {
-                                const float p = x[e], q = x[e + 1];
-                                x[e] = p * co[e / 2] - q * si[e / 2], x[e + 1] = p * si[e / 2] + q * co[e / 2];
-                            }
+                                for (int e = 0; e < LANE; e += 2) {
+                                    const float p = x[e], q = x[e + 1];
+                                    x[e] = p * co[e / 2] - q * si[e / 2], x[e + 1] = p * si[e / 2] + q * co[e / 2];
+                                }
                             }
                         } else if (turn) {
 #pragma unroll
